@@ -9,8 +9,9 @@ is no fallback path, and a missing library raises ``RuntimeError``.
 Every call that takes a workspace (and the static-scratch call) accepts
 ``check=True``: after the launch it reads the device status word
 (synchronising the stream) and raises ``CpaError`` when the GPU recorded a bad
-page id, a bad prefix length, a bad tree parent or a pipeline timeout.  The
-outputs of such a call are undefined.
+page id, a bad length, a bad tree parent or a pipeline timeout, or a bad row, a
+bad count or a lack of free pages in a page operation.  The outputs of such a
+call are undefined unless include/cpa.h says what they are.
 """
 from __future__ import annotations
 
@@ -44,6 +45,16 @@ __all__ = [
     "cpa_tree_verify_workspace_size",
     "cpa_tree_verify",
     "cpa_tree_pass_b",
+    "cpa_decode_workspace_size",
+    "cpa_decode",
+    "cpa_decode_fp8",
+    "cpa_window_prefill_workspace_size",
+    "cpa_window_prefill",
+    "cpa_cache_fork_workspace_size",
+    "cpa_cache_fork",
+    "cpa_cache_free",
+    "cpa_cache_copy_pages",
+    "cpa_cache_compact",
     "cpa_get_device_status",
     "cpa_noalloc_device_status",
     "cpa_debug_wait_timeout",
@@ -62,7 +73,8 @@ PREFILL_FULL, PREFILL_RECT, PREFILL_TRI = 0, 1, 2
 _STATUS = {0: "CPA_OK", 1: "CPA_ERR_INVALID_ARG", 2: "CPA_ERR_UNSUPPORTED",
            3: "CPA_ERR_WORKSPACE", 4: "CPA_ERR_LAUNCH", 5: "CPA_ERR_BAD_PAGE",
            6: "CPA_ERR_TIMEOUT", 7: "CPA_ERR_CUDA", 8: "CPA_ERR_BAD_LENGTH",
-           9: "CPA_ERR_BAD_TREE"}
+           9: "CPA_ERR_BAD_TREE", 10: "CPA_ERR_BAD_ROW", 11: "CPA_ERR_NO_PAGE",
+           12: "CPA_ERR_BAD_COUNT"}
 
 
 class CpaError(RuntimeError):
@@ -73,6 +85,7 @@ class CpaError(RuntimeError):
 
 
 _lib: Optional[ctypes.CDLL] = None
+_STATUS_BYTES = 256  # cpa_status_workspace_size()
 
 
 def build_library(force: bool = False) -> str:
@@ -119,6 +132,18 @@ def lib() -> ctypes.CDLL:
         "cpa_tree_verify": (I, [P, P, P, P, I, P, I, P, P, I, I, I, I, I, I, I, I, F, P, P, P, SZ,
                                 P]),
         "cpa_tree_pass_b": (I, [P, P, P, P, I, P, I, I, I, I, I, I, I, F, P, P, P, SZ, P]),
+        "cpa_decode_workspace_size": (SZ, [I, I, I, I, I]),
+        "cpa_decode": (I, [P, P, P, P, I, P, I, I, I, I, I, I, I, I, I, F, P, P, P, SZ, P]),
+        "cpa_decode_fp8": (I, [P, P, P, P, P, I, P, I, P, I, I, I, I, I, I, I, I, I, F, P, P, P,
+                               SZ, P]),
+        "cpa_window_prefill_workspace_size": (SZ, [I, I, I, I, I, I, I]),
+        "cpa_window_prefill": (I, [P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, I, I, F, P, P,
+                                   P, SZ, P]),
+        "cpa_cache_fork_workspace_size": (SZ, [I]),
+        "cpa_cache_fork": (I, [P, I, I, P, P, P, I, P, I, I, P, P, P, SZ, P]),
+        "cpa_cache_free": (I, [P, I, I, P, P, P, I, P, I, P, SZ, P]),
+        "cpa_cache_copy_pages": (I, [P, P, P, P, I, I, SZ, P, SZ, P]),
+        "cpa_cache_compact": (I, [P, P, P, I, I, P, P, I, P, P, I, P, I, I, I, SZ, P, SZ, P]),
         "cpa_get_device_status": (I, [P, ctypes.POINTER(ctypes.c_uint32), P]),
         "cpa_noalloc_device_status": (I, [ctypes.POINTER(ctypes.c_uint32), P]),
         "cpa_debug_wait_timeout": (I, [P, SZ, I, P]),
@@ -642,6 +667,286 @@ def cpa_tree_pass_b(q, k_pages, v_pages, tree_page_table, tree_parents,
     if check:
         _check_device("cpa_tree_pass_b", ws, stream)
     return o_b, lse_b
+
+
+# ---------------------------------------------------------------- decode, windowed prefill, page operations
+def _on(ref: torch.Tensor, *tensors):
+    """All tensors are on the device of `ref`."""
+    for t in tensors:
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"tensors are on different devices: {ref.device} and {t.device}")
+
+
+def _shape(t: torch.Tensor, name: str, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _run(name: str, device: torch.device, stream, workspace, nbytes: int, check: bool, call):
+    """Run `call(workspace, bytes, stream)` with `device` current.  Without a workspace from
+    the caller each call gets its own, from PyTorch's allocator on the call's stream: calls on
+    several streams, or in several captured graphs, then share nothing."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _run(name, device, stream, workspace, nbytes, check, call)
+    if workspace is None:
+        with torch.cuda.stream(stream):  # (None: the current stream)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    s = torch.cuda.current_stream() if stream is None else stream
+    _check(name, call(workspace.data_ptr(), workspace.numel(), s.cuda_stream))
+    if check:
+        _check_device(name, workspace, stream)
+
+
+def _need_workspace(workspace, ref):
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+        _on(ref, workspace)
+
+
+def cpa_decode_workspace_size(B, H_q, H_kv, head_dim, page_size) -> int:
+    return lib().cpa_decode_workspace_size(B, H_q, H_kv, head_dim, page_size)
+
+
+def _decode(name, q, k_pages, v_pages, scales, page_table, seq_lens, max_seq_len, window, sinks,
+            sm_scale, o, lse, workspace, stream, check):
+    kv = torch.uint8 if scales else torch.bfloat16
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_pages, "k_pages", kv, 4)
+    _need(v_pages, "v_pages", kv, 4)
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    num_pages, P, H_kv, d = k_pages.shape
+    B, H_q, dq = q.shape
+    if dq != d or seq_lens.shape[0] != B or page_table.shape[0] != B:
+        raise ValueError("inconsistent decode shapes")
+    sc = ()
+    if scales:
+        for t, n in zip(scales, ("k_scale", "v_scale")):
+            _need(t, n, torch.float32)
+            if t.numel() not in (1, H_kv * d) or t.numel() != scales[0].numel():
+                raise ValueError("k_scale / v_scale must hold 1 or H_kv * head_dim values each")
+        sc = (scales[0].data_ptr(), scales[1].data_ptr(), int(scales[0].numel() > 1))
+    if max_seq_len is None:
+        max_seq_len = page_table.shape[1] * P
+    if o is None or lse is None:
+        with torch.cuda.stream(stream):
+            o = torch.empty_like(q) if o is None else o
+            lse = torch.empty(B, H_q, dtype=torch.float32, device=q.device) if lse is None else lse
+    _need(o, "o", torch.bfloat16)
+    _need(lse, "lse", torch.float32)
+    _shape(o, "o", q.shape)
+    _shape(lse, "lse", (B, H_q))
+    _need_workspace(workspace, q)
+    _on(q, k_pages, v_pages, page_table, seq_lens, o, lse, *scales)
+    fn = getattr(lib(), name)
+    nbytes = 0 if workspace is not None else cpa_decode_workspace_size(B, H_q, H_kv, d, P)
+    _run(name, q.device, stream, workspace, nbytes, check, lambda ws, n, s: fn(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), *sc, page_table.data_ptr(),
+        page_table.shape[1], seq_lens.data_ptr(), B, H_q, H_kv, d, P, num_pages,
+        int(max_seq_len), int(window), int(sinks), float(d ** -0.5 if sm_scale is None else sm_scale),
+        o.data_ptr(), lse.data_ptr(), ws, n, s))
+    return o, lse
+
+
+def cpa_decode(q, k_pages, v_pages, page_table, seq_lens, max_seq_len: Optional[int] = None,
+               window: int = 0, sinks: int = 0, sm_scale: Optional[float] = None, o=None,
+               lse=None, workspace=None, stream=None, check: bool = False):
+    """Attention of one new token per request.  Returns (o bf16, lse fp32).
+
+    Row b of ``q`` [B, H_q, 128] is the token at position ``seq_lens[b] - 1``; it
+    sees every key, or with ``window`` > 0 the last ``window`` (itself among
+    them) and the first ``sinks``.
+    """
+    return _decode("cpa_decode", q, k_pages, v_pages, (), page_table, seq_lens, max_seq_len,
+                   window, sinks, sm_scale, o, lse, workspace, stream, check)
+
+
+def cpa_decode_fp8(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
+                   max_seq_len: Optional[int] = None, window: int = 0, sinks: int = 0,
+                   sm_scale: Optional[float] = None, o=None, lse=None, workspace=None,
+                   stream=None, check: bool = False):
+    """cpa_decode over FP8 E4M3 pages (pools and scales as for cpa_cascade_verify_fp8)."""
+    return _decode("cpa_decode_fp8", q, k_pages, v_pages, (k_scale, v_scale), page_table,
+                   seq_lens, max_seq_len, window, sinks, sm_scale, o, lse, workspace, stream,
+                   check)
+
+
+def cpa_window_prefill_workspace_size(B, T, H_q, H_kv, head_dim, page_size, max_new) -> int:
+    return lib().cpa_window_prefill_workspace_size(B, T, H_q, H_kv, head_dim, page_size, max_new)
+
+
+def cpa_window_prefill(q, k_pages, v_pages, page_table, q_start, seq_lens,
+                       max_new: Optional[int] = None, max_seq_len: Optional[int] = None,
+                       window: int = 0, sinks: int = 0, sm_scale: Optional[float] = None, o=None,
+                       lse=None, workspace=None, stream=None, check: bool = False):
+    """Causal prefill of ragged prompt chunks, with a sliding window and sinks.
+
+    Request b has the new tokens ``q_start[b] .. q_start[b+1]-1`` of ``q``
+    [T, H_q, 128], the last ones of its ``seq_lens[b]`` tokens.  Returns (o bf16,
+    lse fp32); rows that belong to no request are not written.
+    """
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_pages, "k_pages", torch.bfloat16, 4)
+    _need(v_pages, "v_pages", torch.bfloat16, 4)
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(q_start, "q_start", torch.int32, 1)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    num_pages, P, H_kv, d = k_pages.shape
+    T, H_q, dq = q.shape
+    B = seq_lens.shape[0]
+    if dq != d or q_start.shape[0] != B + 1 or page_table.shape[0] != B:
+        raise ValueError("inconsistent prefill shapes")
+    if max_new is None:
+        max_new = T
+    if max_seq_len is None:
+        max_seq_len = page_table.shape[1] * P
+    if o is None or lse is None:
+        with torch.cuda.stream(stream):
+            o = torch.empty_like(q) if o is None else o
+            lse = torch.empty(T, H_q, dtype=torch.float32, device=q.device) if lse is None else lse
+    _need(o, "o", torch.bfloat16)
+    _need(lse, "lse", torch.float32)
+    _shape(o, "o", q.shape)
+    _shape(lse, "lse", (T, H_q))
+    _need_workspace(workspace, q)
+    _on(q, k_pages, v_pages, page_table, q_start, seq_lens, o, lse)
+    fn = lib().cpa_window_prefill
+    nbytes = 0 if workspace is not None else cpa_window_prefill_workspace_size(
+        B, T, H_q, H_kv, d, P, int(max_new))
+    _run("cpa_window_prefill", q.device, stream, workspace, nbytes, check, lambda ws, n, s: fn(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        page_table.shape[1], q_start.data_ptr(), seq_lens.data_ptr(), B, T, H_q, H_kv, d, P,
+        num_pages, int(max_new), int(max_seq_len), int(window), int(sinks),
+        float(d ** -0.5 if sm_scale is None else sm_scale), o.data_ptr(), lse.data_ptr(), ws, n,
+        s))
+    return o, lse
+
+
+def cpa_cache_fork_workspace_size(num_pages) -> int:
+    return lib().cpa_cache_fork_workspace_size(num_pages)
+
+
+def cpa_cache_fork(page_table, seq_lens, parents, children, refcounts, page_size: int,
+                   copy_src=None, copy_dst=None, workspace=None, stream=None,
+                   check: bool = False):
+    """Row ``children[i]`` of ``page_table`` becomes a copy of row ``parents[i]``: whole pages
+    shared, a partly filled last one replaced by a free page (count 0 in ``refcounts``).
+
+    Returns (copy_src, copy_dst), the page pairs for ``cpa_cache_copy_pages`` (-1, -1 where
+    there is none).  ``page_table``, ``seq_lens`` and ``refcounts`` change in place.
+    """
+    _need(page_table, "page_table", torch.int32, 2)
+    for t, n in ((seq_lens, "seq_lens"), (parents, "parents"), (children, "children"),
+                 (refcounts, "refcounts")):
+        _need(t, n, torch.int32, 1)
+    n_rows, stride = page_table.shape
+    n = parents.shape[0]
+    _shape(seq_lens, "seq_lens", (n_rows,))
+    _shape(children, "children", (n,))
+    if copy_src is None or copy_dst is None:
+        with torch.cuda.stream(stream):
+            copy_src = torch.empty_like(parents) if copy_src is None else copy_src
+            copy_dst = torch.empty_like(parents) if copy_dst is None else copy_dst
+    for t, name in ((copy_src, "copy_src"), (copy_dst, "copy_dst")):
+        _need(t, name, torch.int32, 1)
+        _shape(t, name, (n,))
+    _need_workspace(workspace, page_table)
+    _on(page_table, seq_lens, parents, children, refcounts, copy_src, copy_dst)
+    fn, num_pages = lib().cpa_cache_fork, refcounts.shape[0]
+    nbytes = 0 if workspace is not None else cpa_cache_fork_workspace_size(num_pages)
+    _run("cpa_cache_fork", page_table.device, stream, workspace, nbytes, check,
+         lambda ws, nb, s: fn(page_table.data_ptr(), stride, n_rows, seq_lens.data_ptr(),
+                              parents.data_ptr(), children.data_ptr(), n, refcounts.data_ptr(),
+                              int(page_size), num_pages, copy_src.data_ptr(),
+                              copy_dst.data_ptr(), ws, nb, s))
+    return copy_src, copy_dst
+
+
+def cpa_cache_free(page_table, rows, first, last, refcounts, workspace=None, stream=None,
+                   check: bool = False) -> None:
+    """Give back entries ``first[i] .. last[i]-1`` of row ``rows[i]``: the pages' counts are
+    lowered and the entries become -1."""
+    _need(page_table, "page_table", torch.int32, 2)
+    for t, n in ((rows, "rows"), (first, "first"), (last, "last"), (refcounts, "refcounts")):
+        _need(t, n, torch.int32, 1)
+    n_rows, stride = page_table.shape
+    n = rows.shape[0]
+    _shape(first, "first", (n,))
+    _shape(last, "last", (n,))
+    _need_workspace(workspace, page_table)
+    _on(page_table, rows, first, last, refcounts)
+    fn = lib().cpa_cache_free
+    _run("cpa_cache_free", page_table.device, stream, workspace, _STATUS_BYTES, check,
+         lambda ws, nb, s: fn(page_table.data_ptr(), stride, n_rows, rows.data_ptr(),
+                              first.data_ptr(), last.data_ptr(), n, refcounts.data_ptr(),
+                              refcounts.shape[0], ws, nb, s))
+
+
+def _any_pools(k_pages, v_pages):
+    """K and V pools of any element type; returns (num_pages, page_size, bytes of one token)."""
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _need(t, n, getattr(k_pages, "dtype", None), 4)
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    num_pages, P, H_kv, d = k_pages.shape
+    return num_pages, P, H_kv * d * k_pages.element_size()
+
+
+def cpa_cache_copy_pages(k_pages, v_pages, copy_src, copy_dst, workspace=None, stream=None,
+                         check: bool = False) -> None:
+    """Page ``copy_dst[i]`` of both pools becomes a copy of page ``copy_src[i]``; pairs of two
+    -1 are passed over."""
+    num_pages, P, token = _any_pools(k_pages, v_pages)
+    for t, n in ((copy_src, "copy_src"), (copy_dst, "copy_dst")):
+        _need(t, n, torch.int32, 1)
+    _shape(copy_dst, "copy_dst", copy_src.shape)
+    _need_workspace(workspace, k_pages)
+    _on(k_pages, v_pages, copy_src, copy_dst)
+    fn = lib().cpa_cache_copy_pages
+    _run("cpa_cache_copy_pages", k_pages.device, stream, workspace, _STATUS_BYTES, check,
+         lambda ws, nb, s: fn(k_pages.data_ptr(), v_pages.data_ptr(), copy_src.data_ptr(),
+                              copy_dst.data_ptr(), copy_src.shape[0], num_pages, P * token, ws,
+                              nb, s))
+
+
+def cpa_cache_compact(k_pages, v_pages, src_page_table, src_pos, n_keep, dst_page_table=None,
+                      dst_start=None, src_rows=None, workspace=None, stream=None,
+                      check: bool = False) -> None:
+    """Move the kept tokens of each request together: position ``src_pos[b, i]`` of row
+    ``src_rows[b]`` (default b) of ``src_page_table`` goes to position ``dst_start[b] + i`` of row
+    b of ``dst_page_table``, for i < ``n_keep[b]``.  Without ``dst_page_table`` the move is within
+    the source row, whose positions ascend."""
+    num_pages, P, token = _any_pools(k_pages, v_pages)
+    _need(src_page_table, "src_page_table", torch.int32, 2)
+    _need(src_pos, "src_pos", torch.int32, 2)
+    _need(n_keep, "n_keep", torch.int32, 1)
+    _need(dst_start, "dst_start", torch.int32, 1)
+    B, max_keep = src_pos.shape
+    _shape(n_keep, "n_keep", (B,))
+    _shape(dst_start, "dst_start", (B,))
+    if src_rows is not None:
+        _need(src_rows, "src_rows", torch.int32, 1)
+        _shape(src_rows, "src_rows", (B,))
+    dst, dst_stride = None, 0
+    if dst_page_table is not None:
+        _need(dst_page_table, "dst_page_table", torch.int32, 2)
+        if dst_page_table.shape[0] != B:
+            raise ValueError("dst_page_table must have a row for each request")
+        dst, dst_stride = dst_page_table.data_ptr(), dst_page_table.shape[1]
+    _need_workspace(workspace, k_pages)
+    _on(k_pages, v_pages, src_page_table, src_pos, n_keep, dst_page_table, dst_start, src_rows)
+    fn = lib().cpa_cache_compact
+    _run("cpa_cache_compact", k_pages.device, stream, workspace, _STATUS_BYTES, check,
+         lambda ws, nb, s: fn(k_pages.data_ptr(), v_pages.data_ptr(), src_page_table.data_ptr(),
+                              src_page_table.shape[1], src_page_table.shape[0],
+                              None if src_rows is None else src_rows.data_ptr(),
+                              src_pos.data_ptr(), max_keep, n_keep.data_ptr(), dst, dst_stride,
+                              dst_start.data_ptr(), B, P, num_pages, token, ws, nb, s))
 
 
 def cpa_get_device_status(workspace: torch.Tensor, stream=None) -> tuple[int, int]:

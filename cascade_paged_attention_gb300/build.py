@@ -1,6 +1,6 @@
 """Build libcpa.so (the CUDA kernels and the C ABI) in-tree for sm_103a.
 
-Two translation units are compiled in parallel with nvcc and linked into
+The translation units are compiled in parallel with nvcc and linked into
 ``cascade_paged_attention_gb300/libcpa.so`` against the shared CUDA runtime,
 so the library and PyTorch share one runtime instance in a process.
 """
@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libcpa.so")
 # Diagnostic variant with the kernels' trace hooks compiled in (-DCPA_TRACE);
 # never loaded unless CPA_LIBRARY names it.
 TRACE_LIB = os.path.join(HERE, "libcpa_trace.so")
-SOURCES = ["cpa_api.cu", "cpa_small.cu"]
+SOURCES = ["cpa_api.cu", "cpa_small.cu", "cpa_decode.cu", "cpa_window.cu", "cpa_cache.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

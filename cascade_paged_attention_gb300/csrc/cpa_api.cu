@@ -6,17 +6,16 @@
 
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
 #include "cpa.h"
 #include "cpa_attn.cuh"
+#include "cpa_checks.h"
 #include "cpa_host.h"
 #include "cpa_small.h"
 
 namespace cpa {
 namespace {
 
-constexpr size_t kStatusBytes = 256;
 constexpr int kMaxSmemOptin = 232448;  // 227 KB per CTA on sm_100-class parts
 
 // ---------------------------------------------------------------- device facts
@@ -28,45 +27,7 @@ int smem_optin() {
     return n;
 }
 
-int sm_count() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n;
-}
-
 // ---------------------------------------------------------------- tensor maps
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// bf16 tensor [dim2][dim1][128] seen as (d, dim1, dim2), 128-B swizzled boxes
-// of {64, box1, box2}.
-bool make_map(CUtensorMap* map, const void* base, uint64_t dim1, uint64_t dim2, uint32_t box1,
-              uint32_t box2) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {128, dim1, dim2};
-    cuuint64_t strides[2] = {128 * 2, dim1 * 128 * 2};
-    cuuint32_t box[3] = {64, box1, box2};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-                    strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 // uint8 tensor (FP8 E4M3 codes) [dim2][dim1][128] seen as (d, dim1, dim2),
 // 128-B swizzled boxes of {128, box1, box2}: one box row is a whole 128-code row.
 bool make_map_u8(CUtensorMap* map, const void* base, uint64_t dim1, uint64_t dim2,
@@ -85,11 +46,6 @@ bool make_map_u8(CUtensorMap* map, const void* base, uint64_t dim1, uint64_t dim
                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-bool page_size_ok(int P) { return P >= 8 && P <= 256 && pow2(P); }
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // ---------------------------------------------------------------- workspace layout
 struct WsLayout {
@@ -427,6 +383,9 @@ const char* cpa_status_string(cpa_status s) {
         case CPA_ERR_CUDA: return "CUDA runtime error";
         case CPA_ERR_BAD_LENGTH: return "prefix length out of range";
         case CPA_ERR_BAD_TREE: return "tree parent index out of range";
+        case CPA_ERR_BAD_ROW: return "table row out of range or named twice";
+        case CPA_ERR_NO_PAGE: return "no free page left";
+        case CPA_ERR_BAD_COUNT: return "page count below zero";
     }
     return "unknown status";
 }
@@ -821,9 +780,13 @@ cpa_status cpa_get_device_status(const void* workspace, uint32_t* status_out,
     if (cudaStreamSynchronize(s) != cudaSuccess) return CPA_ERR_CUDA;
     *status_out = v;
     if (v & CPA_DEV_TIMEOUT) return CPA_ERR_TIMEOUT;
+    // (a page or length read through a wrong row says nothing of its own)
+    if (v & CPA_DEV_BAD_ROW) return CPA_ERR_BAD_ROW;
     if (v & CPA_DEV_BAD_PAGE) return CPA_ERR_BAD_PAGE;
     if (v & CPA_DEV_BAD_LENGTH) return CPA_ERR_BAD_LENGTH;
     if (v & CPA_DEV_BAD_TREE) return CPA_ERR_BAD_TREE;
+    if (v & CPA_DEV_BAD_COUNT) return CPA_ERR_BAD_COUNT;
+    if (v & CPA_DEV_NO_PAGE) return CPA_ERR_NO_PAGE;
     return CPA_OK;
 }
 

@@ -83,7 +83,10 @@ typedef enum cpa_status {
     CPA_ERR_TIMEOUT = 6,      /* device pipeline wait exceeded its limit */
     CPA_ERR_CUDA = 7,         /* a CUDA runtime call failed */
     CPA_ERR_BAD_LENGTH = 8,   /* device saw a prefix length outside [0, max_prefix_len] */
-    CPA_ERR_BAD_TREE = 9      /* device saw a tree parent index outside [-1, i) */
+    CPA_ERR_BAD_TREE = 9,     /* device saw a tree parent index outside [-1, i) */
+    CPA_ERR_BAD_ROW = 10,     /* device saw a table row out of range, or named twice */
+    CPA_ERR_NO_PAGE = 11,     /* the pool had fewer free pages than were asked for */
+    CPA_ERR_BAD_COUNT = 12    /* a page was given back more often than it was taken */
 } cpa_status;
 
 /* Bits of the device status word (first 4 bytes of a workspace). */
@@ -91,6 +94,9 @@ typedef enum cpa_status {
 #define CPA_DEV_TIMEOUT 0x2u
 #define CPA_DEV_BAD_LENGTH 0x4u
 #define CPA_DEV_BAD_TREE 0x8u
+#define CPA_DEV_BAD_ROW 0x10u
+#define CPA_DEV_NO_PAGE 0x20u
+#define CPA_DEV_BAD_COUNT 0x40u
 
 /* Largest draft tree cpa_tree_verify accepts (one 64-bit ancestor mask per node). */
 #define CPA_MAX_TREE_NODES 64
@@ -382,10 +388,175 @@ cpa_status cpa_tree_pass_b(const void* q, const void* k_pages, const void* v_pag
                            cpa_stream_t stream);
 
 /*
+ * Decode: attention of one new token per request over the paged cache.  Row b
+ * of q is the token at position seq_lens[b] - 1; its own K/V is already in the
+ * cache, as are those of every earlier token that it sees.  It sees key j when
+ *     j < seq_lens[b]  and  (window == 0, or j >= seq_lens[b] - window,
+ *                            or j < sinks):
+ * all keys, or the last `window` (itself among them) and the first `sinks`.
+ * Keys that are not seen are not read, nor are their table entries: the pages
+ * a window has left behind may have been given back (cpa_cache_free).
+ *   q           bf16 [B, H_q, head_dim]
+ *   page_table  int32 [B, pt_stride], pt_stride >= ceil(max_seq_len / page_size)
+ *   seq_lens    int32 [B] on the device, 0 <= seq_lens[b] <= max_seq_len; a
+ *               request of length 0 gets o = 0, lse = -inf
+ *   o, lse      bf16 [B, H_q, head_dim], fp32 [B, H_q]
+ * The work is split over the visible length and joined, in a fixed order: the
+ * result of a call depends on its inputs and the device's SM count alone.
+ * Supported: head_dim 128; page_size in {8,16,32,64,128,256}; any H_q that is a
+ * multiple of H_kv.
+ */
+size_t cpa_decode_workspace_size(int B, int H_q, int H_kv, int head_dim, int page_size);
+
+cpa_status cpa_decode(const void* q, const void* k_pages, const void* v_pages,
+                      const int32_t* page_table, int pt_stride, const int32_t* seq_lens, int B,
+                      int H_q, int H_kv, int head_dim, int page_size, int num_pages,
+                      int max_seq_len, int window, int sinks, float sm_scale, void* o, float* lse,
+                      void* workspace, size_t workspace_bytes, cpa_stream_t stream);
+
+/*
+ * Decode over FP8 E4M3 pages: cpa_decode with the pools and scales of
+ * cpa_cascade_verify_fp8.  Codes are widened exactly to f16 (a NaN code that a
+ * row sees gives NaN), q x k_scale is rounded to f16 once, so it must stay
+ * below 65504 in magnitude, and P is f16; sums are fp32.
+ */
+cpa_status cpa_decode_fp8(const void* q, const void* k_pages, const void* v_pages,
+                          const float* k_scale, const float* v_scale, int scale_per_channel,
+                          const int32_t* page_table, int pt_stride, const int32_t* seq_lens,
+                          int B, int H_q, int H_kv, int head_dim, int page_size, int num_pages,
+                          int max_seq_len, int window, int sinks, float sm_scale, void* o,
+                          float* lse, void* workspace, size_t workspace_bytes,
+                          cpa_stream_t stream);
+
+/*
+ * Prefill of prompt chunks of unequal length, causal, with an optional sliding
+ * window and sinks.  Request b has the new tokens q_start[b] .. q_start[b+1]-1
+ * of q, m_b of them; they are the last m_b tokens of its sequence of
+ * seq_lens[b] tokens, whose K/V (the new tokens' among them) is in the cache.
+ * New token i is at position p = seq_lens[b] - m_b + i and sees key j when
+ *     j <= p  and  (window == 0, or j > p - window, or j < sinks).
+ * Pages that no new token sees are not read, nor are their table entries.
+ *   q           bf16 [T, H_q, head_dim]
+ *   page_table  int32 [B, pt_stride], pt_stride >= ceil(max_seq_len / page_size)
+ *   q_start     int32 [B + 1] on the device, ascending, 0 <= q_start[0] and
+ *               q_start[B] <= T; rows of o and lse before q_start[0] or at and
+ *               past q_start[B] are left as they were
+ *   seq_lens    int32 [B] on the device, m_b <= seq_lens[b] <= max_seq_len
+ *   max_new     host-side upper bound of every m_b
+ *   o, lse      bf16 [T, H_q, head_dim], fp32 [T, H_q]
+ * A q_start that is not ascending or leaves [0, T], an m_b above max_new or
+ * above seq_lens[b], or a length above max_seq_len sets CPA_DEV_BAD_LENGTH.
+ * Supported: head_dim 128; page_size in {8,16,32,64,128,256}; H_q / H_kv <= 128.
+ */
+size_t cpa_window_prefill_workspace_size(int B, int T, int H_q, int H_kv, int head_dim,
+                                         int page_size, int max_new);
+
+cpa_status cpa_window_prefill(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* page_table, int pt_stride, const int32_t* q_start,
+                              const int32_t* seq_lens, int B, int T, int H_q, int H_kv,
+                              int head_dim, int page_size, int num_pages, int max_new,
+                              int max_seq_len, int window, int sinks, float sm_scale, void* o,
+                              float* lse, void* workspace, size_t workspace_bytes,
+                              cpa_stream_t stream);
+
+/*
+ * The page operations of the cache.  A page of the pool is free when its count
+ * is 0: refcounts is int32 [num_pages] on the device, the number of table
+ * entries that hold the page, and the caller keeps it (a page taken by the
+ * caller's own means has count 1).  Tables and counts serve every layer, so
+ * forking and freeing touch them alone; copying and compacting move K and V of
+ * one layer's pools.
+ *
+ * cpa_cache_fork: sequence children[i] becomes a copy of sequence parents[i]
+ * (rows of one page_table [n_rows, pt_stride] and of seq_lens [n_rows]).  The
+ * parent's whole pages are shared, their counts raised by one each.  A last,
+ * partly filled page is not shared: the child gets the lowest free page that no
+ * earlier i got, with count 1, and (copy_src[i], copy_dst[i]) names the two
+ * pages, for cpa_cache_copy_pages to copy in every layer.  Where there is
+ * nothing to copy both are -1.  Entries past the child's last page become -1.
+ * The entries that row children[i] held before are not given back: free them
+ * first.
+ *   parents, children  int32 [n] on the device.  A parent may have many
+ *                      children; a child may not be named twice, nor be a
+ *                      parent in the same call (CPA_DEV_BAD_ROW: such children
+ *                      are left as they were, their pairs -1).
+ *   copy_src, copy_dst int32 [n] on the device, output.
+ * With too few free pages (CPA_DEV_NO_PAGE) the children that got none have -1
+ * as their last page and their pair; all else is as described, so freeing the
+ * row undoes the fork.  n >= 1.
+ */
+size_t cpa_cache_fork_workspace_size(int num_pages);
+
+cpa_status cpa_cache_fork(int32_t* page_table, int pt_stride, int n_rows, int32_t* seq_lens,
+                          const int32_t* parents, const int32_t* children, int n,
+                          int32_t* refcounts, int page_size, int num_pages, int32_t* copy_src,
+                          int32_t* copy_dst, void* workspace, size_t workspace_bytes,
+                          cpa_stream_t stream);
+
+/*
+ * cpa_cache_free: for each i, entries first[i] .. last[i]-1 of row rows[i] are
+ * given back: the page's count is lowered by one and the entry becomes -1.
+ * Entries that are -1 already are passed over, so that naming an entry twice
+ * gives it back once.  0 .. pt_stride frees a whole sequence; a window of W
+ * tokens with S sinks over L tokens has left the pages ceil(S / page_size) ..
+ * max(L - W, 0) / page_size behind (seq_lens does not change).  A count that is
+ * 0 already stays 0 and sets CPA_DEV_BAD_COUNT; bounds outside [0, pt_stride]
+ * set CPA_DEV_BAD_LENGTH, a row outside [0, n_rows) CPA_DEV_BAD_ROW, and
+ * nothing of that i is given back.  Workspace: cpa_status_workspace_size().
+ */
+cpa_status cpa_cache_free(int32_t* page_table, int pt_stride, int n_rows, const int32_t* rows,
+                          const int32_t* first, const int32_t* last, int n, int32_t* refcounts,
+                          int num_pages, void* workspace, size_t workspace_bytes,
+                          cpa_stream_t stream);
+
+/*
+ * cpa_cache_copy_pages: page copy_dst[i] of both pools becomes a copy of page
+ * copy_src[i], for each of the n pairs; pairs of two -1 are passed over.  No
+ * page may be the destination of two pairs, nor the source of one and the
+ * destination of another: the contents of such pages are undefined.  page_bytes
+ * (one page of one pool) is a multiple of 16.  Workspace:
+ * cpa_status_workspace_size().
+ */
+cpa_status cpa_cache_copy_pages(void* k_pages, void* v_pages, const int32_t* copy_src,
+                                const int32_t* copy_dst, int n, int num_pages,
+                                size_t page_bytes, void* workspace, size_t workspace_bytes,
+                                cpa_stream_t stream);
+
+/*
+ * cpa_cache_compact: the kept tokens of a sequence move together.  For request
+ * b and i < n_keep[b], K and V of position src_pos[b][i] of row src_rows[b] of
+ * src_table move to position dst_start[b] + i of row b of dst_table.  After a
+ * verify step that is how accepted drafts join the prefix: src_table the
+ * draft (or tree) table, src_pos the accepted path, dst_table the prefix table
+ * and dst_start the prefix lengths.
+ *   src_table   int32 [n_src_rows, src_stride]
+ *   src_rows    int32 [B] on the device, or NULL: row b
+ *   src_pos     int32 [B, max_keep];  n_keep int32 [B], 0 <= n_keep[b] <= max_keep
+ *   dst_table   int32 [B, dst_stride], or NULL: the move is within the source
+ *               row, whose positions have to be ascending with dst_start[b] + i
+ *               <= src_pos[b][i] (a history pruned in place), and no row may be
+ *               named twice
+ *   dst_start   int32 [B] on the device
+ *   token_bytes K (or V) of one token: H_kv x head_dim x element size, a
+ *               multiple of 16
+ * With a dst_table no slot may be both read and written by the call, or written
+ * twice.  A row outside [0, n_src_rows) sets CPA_DEV_BAD_ROW; a count or
+ * position outside its table, or one that breaks the order in place,
+ * CPA_DEV_BAD_LENGTH.  Workspace: cpa_status_workspace_size().
+ */
+cpa_status cpa_cache_compact(void* k_pages, void* v_pages, const int32_t* src_table,
+                             int src_stride, int n_src_rows, const int32_t* src_rows,
+                             const int32_t* src_pos, int max_keep, const int32_t* n_keep,
+                             const int32_t* dst_table, int dst_stride, const int32_t* dst_start,
+                             int B, int page_size, int num_pages, size_t token_bytes,
+                             void* workspace, size_t workspace_bytes, cpa_stream_t stream);
+
+/*
  * Read the device status word of `workspace` (written by the last call that
  * used it) into *status_out (host).  SYNCHRONISES `stream`.  Returns CPA_OK
  * when the word is 0, otherwise the status matching its most serious bit
- * (TIMEOUT, then BAD_PAGE, then BAD_LENGTH, then BAD_TREE).
+ * (TIMEOUT, then BAD_ROW, BAD_PAGE, BAD_LENGTH, BAD_TREE, BAD_COUNT and
+ * NO_PAGE).
  */
 cpa_status cpa_get_device_status(const void* workspace, uint32_t* status_out,
                                   cpa_stream_t stream);

@@ -1,0 +1,175 @@
+"""Windowed prefill of ragged chunks against a 64-bit reference."""
+import pytest
+import torch
+
+import cascade_paged_attention_gb300 as cpa
+from tests import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def make(news, lens, H_q, H_kv, P, seed, lead=0, trail=0):
+    g = ref.gen(seed)
+    table, pool = ref.table_of(lens, P, g)
+    start = [lead]
+    for m in news:
+        start.append(start[-1] + m)
+    T = start[-1] + trail
+    q = torch.randn(T, H_q, 128, generator=g, device="cuda").to(torch.bfloat16)
+    k, v = ref.pool_of(pool, P, H_kv, g), ref.pool_of(pool, P, H_kv, g)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    return q, k, v, table, i32(start), i32(lens), start
+
+
+def check(news, lens, H_q, H_kv, P, window=0, sinks=0, seed=0, lead=0, trail=0, hide=True, **kw):
+    q, k, v, table, qs, dl, start = make(news, lens, H_q, H_kv, P, seed, lead, trail)
+    full = table.clone()
+    masks = [ref.seen(range(L - m, L), L, window, sinks, "cuda") for m, L in zip(news, lens)]
+    if hide:
+        ref.hide_unseen(k, v, table, lens, [m.any(0) for m in masks], P)
+    o = torch.full_like(q, 7.0)
+    lse = torch.full((q.shape[0], H_q), 7.0, device="cuda")
+    cpa.cpa_window_prefill(q, k, v, table, qs, dl, window=window, sinks=sinks, o=o, lse=lse,
+                           check=True, **kw)
+    if hide:
+        for x in (k, v):
+            x.nan_to_num_(0.0)
+    for b, (m, L) in enumerate(zip(news, lens)):
+        a = start[b]
+        K, V = ref.dense(k, full[b], L, P), ref.dense(v, full[b], L, P)
+        for i0 in range(0, m, 256):
+            i1 = min(m, i0 + 256)
+            want = ref.attend(q[a + i0:a + i1], K, V, masks[b][i0:i1], 128 ** -0.5, ref.E_P_BF16)
+            ref.close(o[a + i0:a + i1], lse[a + i0:a + i1], want)
+    for r in (slice(0, lead), slice(start[-1], q.shape[0])):  # rows of no request
+        assert bool((o[r] == 7).all()) and bool((lse[r] == 7).all())
+
+
+@pytest.mark.parametrize("H_q,H_kv,P", [(32, 8, 16), (8, 8, 8), (5, 1, 64), (12, 4, 32), (16, 1, 256),
+                                        (64, 8, 128), (1, 1, 16), (128, 1, 16), (100, 2, 16)])
+def test_ragged_chunks(H_q, H_kv, P):
+    check([1, 2, 0, 17, 64, 65, 128, 31], [1, 300, 5, 17, 200, 129, 128, 1000], H_q, H_kv, P,
+          seed=H_q, lead=3, trail=5)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 2), (5, 3), (64, 4), (100, 130), (128, 0),
+                                          (129, 16), (255, 128), (1000, 4), (3, 5000)])
+@pytest.mark.parametrize("P", [8, 64])
+def test_windows_and_sinks(window, sinks, P):
+    check([300, 1, 70, 129], [300, 600, 1200, 129], 8, 2, P, window, sinks, seed=window + P, trail=1)
+
+
+@pytest.mark.parametrize("news,lens,window,sinks", [
+    ([1], [1], 0, 0), ([1], [5000], 0, 0), ([7], [9000], 0, 0), ([3, 1, 2], [4000, 1, 2500], 1500, 4),
+    ([1500], [1500], 0, 0), ([1100], [2000], 700, 16), ([513, 700], [513, 3333], 512, 64),
+    ([0, 0], [10, 0], 0, 0), ([2000], [2000], 128, 4)])
+def test_short_and_long(news, lens, window, sinks):
+    check(news, lens, 32, 8, 16, window, sinks, seed=sum(news), hide=False)
+    check(news, lens, 4, 1, 32, window, sinks, seed=sum(news) + 1, hide=False)
+
+
+def test_bounds_given_and_repeat():
+    """max_new and max_seq_len as tight as they may be; the same call twice gives the same bits."""
+    news, lens = [40, 3, 200], [1000, 3, 900]
+    check(news, lens, 16, 4, 16, 300, 4, seed=2, max_new=200, max_seq_len=1000)
+    q, k, v, table, qs, dl, _ = make(news, lens, 16, 4, 16, 2)
+    ws = torch.full((cpa.cpa_window_prefill_workspace_size(3, q.shape[0], 16, 4, 128, 16, 200),),
+                    0xA5, dtype=torch.uint8, device="cuda")
+    kw = dict(max_new=200, max_seq_len=1000, workspace=ws)
+    o, lse = cpa.cpa_window_prefill(q, k, v, table, qs, dl, **kw)
+    ws.fill_(0x5A)
+    o2, lse2 = cpa.cpa_window_prefill(q, k, v, table, qs, dl, **kw)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_scores_that_grow():
+    """Scores that climb along the keys by far more than 2^8: the running maximum moves often."""
+    q, k, v, table, qs, dl, _ = make([300], [900], 4, 1, 16, 5)
+    pos = torch.arange(900, device="cuda")
+    q.copy_(q[:1, :1].expand_as(q))
+    k[table[0].long()[pos // 16], pos % 16] = \
+        (q[0, 0] / 12).to(torch.bfloat16)[None, None] * (pos / 20).to(torch.bfloat16)[:, None, None]
+    o, lse = cpa.cpa_window_prefill(q, k, v, table, qs, dl, window=500, sinks=2, check=True)
+    want = ref.attend(q, ref.dense(k, table[0], 900, 16), ref.dense(v, table[0], 900, 16),
+                      ref.seen(range(600, 900), 900, 500, 2, "cuda"), 128 ** -0.5, ref.E_P_BF16)
+    ref.close(o, lse, want)
+
+
+def test_nan_that_is_seen_and_one_that_is_not():
+    q, k, v, table, qs, dl, _ = make([200], [400], 4, 2, 16, 11)
+    at = 350
+    v[table[0, at // 16].long(), at % 16, 1, 9] = float("nan")
+    o, lse = cpa.cpa_window_prefill(q, k, v, table, qs, dl, window=30, check=True)
+    bad = torch.isnan(o)
+    pos = torch.arange(200, 400, device="cuda")
+    hit = (pos >= at) & (pos < at + 30)
+    assert bool(bad[hit][:, 2:, 9].all()) and bool(torch.isfinite(lse).all())
+    assert int(bad.sum()) == 2 * int(hit.sum())
+
+
+def test_bad_starts_lengths_and_pages_are_reported():
+    q, k, v, table, qs, dl, _ = make([30, 40], [100, 200], 8, 2, 16, 13)
+    call = lambda **kw: cpa.cpa_window_prefill(q, k, v, table, qs, dl, check=True, **kw)  # noqa: E731
+    call()
+    for where, bad, status in ((qs, [0, 30, 71], 8), (qs, [-1, 30, 70], 8), (qs, [0, 80, 70], 8),
+                               (qs, [0, 31, 30], 8), (dl, [29, 200], 8), (dl, [100, 209], 8),
+                               (dl, [-1, 200], 8), (qs, [0, -2 ** 31, 70], 8),
+                               (dl, [2 ** 31 - 1, 200], 8)):
+        good = where.clone()
+        where.copy_(torch.tensor(bad, dtype=torch.int32))
+        with pytest.raises(cpa.CpaError) as e:
+            call()
+        assert e.value.status == status, bad
+        where.copy_(good)
+    with pytest.raises(cpa.CpaError) as e:
+        call(max_new=39)
+    assert e.value.status == 8
+    for bad in (-1, k.shape[0], 2 ** 31 - 1):
+        good = table[1, 3].clone()
+        table[1, 3] = bad
+        with pytest.raises(cpa.CpaError) as e:
+            call()
+        assert e.value.status == 5
+        call(window=64)  # positions 160 - 63 and on: page 3 (48..63) is not seen
+        table[1, 3] = good
+    call()
+
+
+def test_graph_replay_and_streams():
+    """A captured call serves other lengths and chunks; two streams at once share nothing."""
+    q, k, v, table, qs, dl, _ = make([100, 60], [600, 500], 16, 4, 16, 17)
+    o, lse = torch.empty_like(q), torch.empty(160, 16, device="cuda")
+    kw = dict(max_new=120, window=200, sinks=4)
+    cpa.cpa_window_prefill(q, k, v, table, qs, dl, o=o, lse=lse, **kw)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        cpa.cpa_window_prefill(q, k, v, table, qs, dl, o=o, lse=lse, **kw)
+    for news, lens in (([100, 60], [600, 500]), ([40, 120], [44, 480]), ([1, 0], [3, 200])):
+        qs.copy_(torch.tensor([0, news[0], sum(news)], dtype=torch.int32))
+        dl.copy_(torch.tensor(lens, dtype=torch.int32))
+        gr.replay()
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            o2, lse2 = cpa.cpa_window_prefill(q, k, v, table, qs, dl, **kw)
+        o3, lse3 = cpa.cpa_window_prefill(q, k, v, table, qs, dl, **kw)
+        torch.cuda.synchronize()
+        n = sum(news)
+        assert torch.equal(o[:n], o2[:n]) and torch.equal(o[:n], o3[:n])
+        a = 0
+        for b, (m, L) in enumerate(zip(news, lens)):
+            want = ref.attend(q[a:a + m], ref.dense(k, table[b], L, 16), ref.dense(v, table[b], L, 16),
+                              ref.seen(range(L - m, L), L, 200, 4, "cuda"), 128 ** -0.5, ref.E_P_BF16)
+            ref.close(o[a:a + m], lse[a:a + m], want)
+            a += m
+
+
+def test_agrees_with_prefill_hit():
+    """One length for all and no window is cpa_prefill_hit's case."""
+    q, k, v, table, qs, dl, _ = make([190, 190], [500, 500], 32, 8, 16, 23)
+    o, lse = cpa.cpa_window_prefill(q, k, v, table, qs, dl, check=True)
+    o2, lse2 = cpa.cpa_prefill_hit(q, k, v, table, 2, 500, 310, check=True)
+    # each within 2^-8 (|o| + sum w |v|) of the exact value, |o| < 1 here
+    assert float((o.float() - o2.float()).abs().max()) <= 2e-2
+    assert float((lse - lse2).abs().max()) <= 1e-3
