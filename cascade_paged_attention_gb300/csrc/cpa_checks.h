@@ -52,6 +52,7 @@ inline bool make_map(CUtensorMap* map, const void* base, uint64_t dim1, uint64_t
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 inline bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 inline bool page_size_ok(int P) { return P >= 8 && P <= 256 && pow2(P); }
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

@@ -404,7 +404,7 @@ cpa_status cpa_tree_pass_b(const void* q, const void* k_pages, const void* v_pag
  * The work is split over the visible length and joined, in a fixed order: the
  * result of a call depends on its inputs and the device's SM count alone.
  * Supported: head_dim 128; page_size in {8,16,32,64,128,256}; any H_q that is a
- * multiple of H_kv.
+ * multiple of H_kv; k_pages and v_pages 32-byte aligned.
  */
 size_t cpa_decode_workspace_size(int B, int H_q, int H_kv, int head_dim, int page_size);
 
