@@ -1,9 +1,912 @@
 // cpa_window.cu -- prefill of ragged prompt chunks over the paged cache, causal,
-// with an optional sliding window and sinks.
+// with an optional sliding window and sinks, on the tensor cores (tcgen05).
+//
+// Unit: two tiles of up to 128 query rows of one request and KV head (a row is a
+// (token, head of the group) pair), against the key tiles (128 keys) that any of
+// its rows sees: the tiles of the sinks, then those from the first row's window
+// to the last row's position.  Tiles between are not visited.
+//
+// Both query tiles meet each K/V tile while it is in shared memory, and take
+// turns on the tensor cores: while one's scores go through the softmax, the
+// other's products run.  The order of the products is
+//     PV0(i-1) S0(i) PV1(i-1) S1(i)   for key tile i,
+// S and its weights P share TMEM (P overwrites the scores that it came from, and
+// S(i+1) is issued after PV(i)), so S0, S1, O0 and O1 fill the 512 columns.
+//
+// Warps (12): 0-3 softmax and output of query tile 0, 4-7 of tile 1 (one thread a
+// row: its 128 scores in registers, no exchange between threads), 8 loads Q and
+// K, 9 loads V, 10 issues the products, 11 allocates TMEM.
+//
+// What bounds it: the tensor cores for long chunks (4 H_q d flops a visible
+// pair); the chain softmax -> PV -> S -> softmax of one query tile when the
+// softmax takes longer than the other tile's products.
+//
+// Split.  As in decode the key tiles of all units lie end to end and every block
+// takes an equal range, so unequal requests, causal triangles and short batches
+// over long caches are balanced alike; a unit cut by a range's end is joined by
+// a second kernel in the order of its parts.
+//
+// Values that are not numbers.  A masked key has weight 0, but 0 times a NaN in V
+// is a NaN in a matrix product.  A row whose result is not finite is therefore
+// done again, key by key over what it sees, by its warp: exact, slow, and never
+// taken by finite caches.  (Slots past a sequence's end may hold anything: their
+// V rows are cleared in shared memory.)
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
 #include <cmath>
 
+#include "cpa.h"
 #include "cpa_checks.h"
-#include "cpa_rows.cuh"
+#include "cpa_device.cuh"
+#include "cpa_host.h"
+
+namespace cpa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 256;       // rows of a unit
+constexpr int kKStages = 3, kVStages = 2;
+constexpr uint32_t kHalf = 128u * 128u;    // 64 columns of a 128-row tile: 16 KB
+constexpr uint32_t kTileBytes = 2 * kHalf; // 128 rows of 256 bytes
+constexpr uint32_t kOffQ = 1024;
+constexpr uint32_t kOffK = kOffQ + 2 * kTileBytes;
+constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
+constexpr uint32_t kSmem = kOffV + kVStages * kTileBytes + 1024;  // (aligned up inside)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
+// A wait that lasts this long means a broken pipeline.  (Longer than elsewhere:
+// rows that are not finite are done again key by key while the other warps wait.)
+constexpr uint64_t kLimitNs = 4ull * 1000 * 1000 * 1000;
+static_assert(kSmem <= 232448, "shared memory of one block");
+
+struct WindowParams {
+    CUtensorMap qmap, kmap, vmap;
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k_pages;
+    const __nv_bfloat16* v_pages;
+    const int32_t* table;
+    const int32_t* q_start;
+    const int32_t* lens;
+    __nv_bfloat16* o;
+    float* lse;
+    uint32_t* status;
+    uint32_t* bad;    // [n_cta] what each block found wrong
+    int4* desc;       // [n_cta] (request, KV head, query tile, parts) of the unit that starts
+                      // in the block's range and goes on past it; request -1: none
+    float* part_lse;  // [2 n_cta][kRows], log2 units
+    float4* part_o;   // [2 n_cta][32 groups of 4 columns][kRows]
+    int stride, B, T, H_q, H_kv, G, TSB, lp, boxr, num_pages, max_new, max_len, window, sinks;
+    int n_cta, min_tiles;
+    float scale_log2;
+};
+
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                        uint32_t* bad) {
+    return mbar_wait(bar, parity, abort_flag, bad, kLimitNs);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity,
+                                          volatile uint32_t* abort_flag, uint32_t* bad) {
+    return __all_sync(0xffffffffu, wait_on(bar, parity, abort_flag, bad));
+}
+
+__device__ __forceinline__ float ninf_f() { return __int_as_float(0xff800000); }
+
+// One request: its new tokens and their place; m = 0 where nothing is to be done.
+struct Request {
+    int t0, m, L;
+};
+__device__ __forceinline__ Request request_of(const WindowParams& p, int b, uint32_t& bad) {
+    Request r;
+    const int s0 = __ldg(p.q_start + b), s1 = __ldg(p.q_start + b + 1);
+    r.L = __ldg(p.lens + b);
+    r.t0 = s0;
+    r.m = 0;
+    if (s0 < 0 || s1 < s0 || s1 > p.T || r.L < 0 || r.L > p.max_len || s1 - s0 > p.max_new ||
+        s1 - s0 > r.L)
+        bad |= CPA_DEV_BAD_LENGTH;
+    else
+        r.m = s1 - s0;
+    return r;
+}
+
+struct Unit {
+    int b, hk, qt;
+    int t0, ntok;       // first query token (row of q) and tokens of the unit
+    int p0;             // position of the first token
+    int L;
+    int lo, sink;       // keys [0, sink) and [lo, p0 + ntok) are seen by some row
+    int n_sink, w0;     // tiles 0 .. n_sink-1 are key tiles 0 ..; then key tiles w0 ..
+    int n_tiles;
+};
+
+__device__ __forceinline__ void unit_tiles(const WindowParams& p, const Request& r, int qt, Unit& x) {
+    const int TS = 2 * p.TSB;
+    x.ntok = min(TS, r.m - qt * TS);
+    x.p0 = r.L - r.m + qt * TS;
+    x.lo = p.window > 0 && x.p0 + 1 > p.window ? x.p0 + 1 - p.window : 0;
+    x.sink = min(p.sinks, x.lo);
+    const int st = (x.sink + 127) >> 7, end = (x.p0 + x.ntok + 127) >> 7;
+    x.w0 = x.lo >> 7;
+    x.n_sink = st;
+    if (x.w0 <= st) x.w0 = x.n_sink = 0;  // one run of tiles from 0
+    x.n_tiles = x.n_sink + end - x.w0;
+}
+
+__device__ __forceinline__ Unit unit_of(const WindowParams& p, int b, int hk, int qt) {
+    uint32_t bad = 0;
+    const Request r = request_of(p, b, bad);
+    Unit x;
+    unit_tiles(p, r, qt, x);
+    x.b = b;
+    x.hk = hk;
+    x.qt = qt;
+    x.t0 = r.t0 + qt * 2 * p.TSB;
+    x.L = r.L;
+    return x;
+}
+
+__device__ __forceinline__ int key0_of(const Unit& x, int j) {
+    return (j < x.n_sink ? j : j - x.n_sink + x.w0) << 7;
+}
+
+struct Ctrl {
+    uint64_t q_full, q_empty;
+    uint64_t k_full[kKStages], k_empty[kKStages];
+    uint64_t v_full[kVStages], v_empty[kVStages];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    uint32_t abort_flag;
+    uint32_t bad;
+    long long scan[kWarps];
+    long long t0, left, per, off;  // this block's range, and where its first unit starts
+    long long sum_q;               // tiles of one KV head of the first unit's request
+    int b, hk, qt, j;
+};
+static_assert(sizeof(Ctrl) <= kOffQ, "control block");
+
+// Tiles of one KV head of request b, by one warp.
+__device__ __forceinline__ long long head_tiles(const WindowParams& p, const Request& r) {
+    const int TS = 2 * p.TSB, lane = threadIdx.x & 31;
+    const int nq = (r.m + TS - 1) / TS;
+    int s = 0;  // (a request's tiles fit: 2^24 query tiles' worth of rows at most)
+    long long sum = 0;
+    for (int qt = lane; qt < nq; qt += 32) {
+        Unit x;
+        unit_tiles(p, r, qt, x);
+        s = x.n_tiles;
+        sum += s;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+// Every thread: the problem's tiles, this block's range, and the unit and tile
+// where it begins.  Each warp sums whole requests; then all walk the warps' sums.
+__device__ void schedule(const WindowParams& p, Ctrl* c) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t bad = 0;
+    long long mine = 0;
+    for (int b = warp; b < p.B; b += kWarps)
+        mine += head_tiles(p, request_of(p, b, bad)) * p.H_kv;
+    if (bad && lane == 0) atomicOr(&c->bad, bad);
+    if (lane == 0) c->scan[warp] = mine;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        long long total = 0;
+        for (int w = 0; w < kWarps; ++w) total += c->scan[w];
+        long long per = (total + p.n_cta - 1) / p.n_cta;
+        if (per < p.min_tiles) per = p.min_tiles;
+        c->per = per;
+        c->t0 = per * blockIdx.x;
+        c->left = c->t0 < total ? min(per, total - c->t0) : 0;
+    }
+    __syncthreads();
+    if (c->left == 0) return;
+    // the request that holds tile t0: a round of kWarps requests at a time
+    long long run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kWarps) {
+        const int b = b0 + warp;
+        long long per_head = 0;
+        if (b < p.B) per_head = head_tiles(p, request_of(p, b, bad));
+        __syncthreads();
+        if (lane == 0) c->scan[warp] = per_head * p.H_kv;
+        __syncthreads();
+        long long before = run, all = run;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += c->scan[w];
+            all += c->scan[w];
+        }
+        if (before <= c->t0 && c->t0 < before + per_head * p.H_kv) {
+            // this warp's request: the head, then the query tile
+            const Request r = request_of(p, b, bad);
+            long long off = c->t0 - before;
+            const int hk = (int)(off / per_head);
+            off -= hk * per_head;
+            const int TS = 2 * p.TSB, nq = (r.m + TS - 1) / TS;
+            long long at = 0;
+            for (int q0 = 0; q0 < nq; q0 += 32) {
+                Unit x;
+                x.n_tiles = 0;
+                if (q0 + lane < nq) unit_tiles(p, r, q0 + lane, x);
+                long long incl = x.n_tiles;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                const long long ex = at + incl - x.n_tiles;
+                if (ex <= off && off < ex + x.n_tiles) {
+                    c->b = b;
+                    c->hk = hk;
+                    c->qt = q0 + lane;
+                    c->j = (int)(off - ex);
+                }
+                at += __shfl_sync(0xffffffffu, incl, 31);
+                if (at > off) break;
+            }
+        }
+        run = all;
+        if (run > c->t0) break;
+    }
+    __syncthreads();
+}
+
+// Walks the pieces (unit, tiles [j0, j1)) of this block's range.
+struct Walker {
+    Unit x;
+    long long left;
+    int j0, j1;
+    __device__ __forceinline__ void cut() {
+        j1 = (int)min((long long)x.n_tiles, (long long)j0 + left);
+    }
+    __device__ __forceinline__ void init(const WindowParams& p, const Ctrl* c) {
+        left = c->left;
+        if (left == 0) return;
+        x = unit_of(p, c->b, c->hk, c->qt);
+        j0 = c->j;
+        cut();
+    }
+    __device__ __forceinline__ void next(const WindowParams& p) {
+        left -= j1 - j0;
+        if (left == 0) return;
+        int b = x.b, hk = x.hk, qt = x.qt + 1;
+        uint32_t bad = 0;
+        Request r = request_of(p, b, bad);
+        if (qt * 2 * p.TSB >= r.m) {
+            qt = 0;
+            if (++hk == p.H_kv) {
+                hk = 0;
+                do {
+                    ++b;
+                    r = request_of(p, b, bad);
+                } while (r.m == 0);  // (tiles are left, so a request with tokens is)
+            }
+        }
+        x = unit_of(p, b, hk, qt);
+        j0 = 0;
+        cut();
+    }
+    // query tiles that hold tokens
+    __device__ __forceinline__ int tiles_q(const WindowParams& p) const {
+        return x.ntok > p.TSB ? 2 : 1;
+    }
+};
+
+// 128 TMEM columns of this warp's lanes, loaded and waited for.
+#define W8(i) "=r"(r[i + 0]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
+              "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+__device__ __forceinline__ void tmem_ld_x128(uint32_t taddr, uint32_t (&r)[128]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
+        "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+        "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
+        "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+        "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, "
+        "[%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : W8(0), W8(8), W8(16), W8(24), W8(32), W8(40), W8(48), W8(56), W8(64), W8(72), W8(80),
+          W8(88), W8(96), W8(104), W8(112), W8(120)
+        : "r"(taddr)
+        : "memory");
+}
+#undef W8
+
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// One row over tiles [j0, j1) of its unit, by a whole warp, key by key: what the
+// row does not see is not touched.  Lane l ends up with dimensions 4 l .. 4 l + 3
+// of o (normalised); returns the log-sum-exp in log2 units.
+__device__ __noinline__ float slow_row(const WindowParams& p, const Unit& x, int j0, int j1,
+                                       size_t qrow, int pos, float (&o)[4]) {
+    const int lane = threadIdx.x & 31;
+    const uint2 qr = __ldg(reinterpret_cast<const uint2*>(p.q + qrow * 128) + lane);
+    const float q0 = __uint_as_float(qr.x << 16), q1 = __uint_as_float(qr.x & 0xFFFF0000u);
+    const float q2 = __uint_as_float(qr.y << 16), q3 = __uint_as_float(qr.y & 0xFFFF0000u);
+    const int32_t* trow = p.table + (size_t)x.b * p.stride;
+    float m = ninf_f(), l = 0.f;
+    o[0] = o[1] = o[2] = o[3] = 0.f;
+    // four keys at a time, so that their loads and sums overlap
+    for (int j = j0; j < j1; ++j) {
+        const int key0 = key0_of(x, j), stop = min(key0 + 128, pos + 1);
+        for (int k4 = key0; k4 < stop; k4 += 4) {
+            float s[4], v[4][4];
+            bool on[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int key = k4 + u;
+                on[u] = key < stop && (p.window == 0 || key > pos - p.window || key < p.sinks);
+                const int pg = on[u] ? __ldg(trow + (key >> p.lp)) : -1;
+                on[u] = on[u] && pg >= 0 && pg < p.num_pages;
+                uint2 kr = make_uint2(0u, 0u), vr = kr;
+                if (on[u]) {
+                    const size_t off =
+                        ((((size_t)pg << p.lp) + (key & ((1 << p.lp) - 1))) * p.H_kv + x.hk) * 128 +
+                        lane * 4;
+                    kr = __ldg(reinterpret_cast<const uint2*>(p.k_pages + off));
+                    vr = __ldg(reinterpret_cast<const uint2*>(p.v_pages + off));
+                }
+                s[u] = q0 * __uint_as_float(kr.x << 16) + q1 * __uint_as_float(kr.x & 0xFFFF0000u) +
+                       q2 * __uint_as_float(kr.y << 16) + q3 * __uint_as_float(kr.y & 0xFFFF0000u);
+                v[u][0] = __uint_as_float(vr.x << 16);
+                v[u][1] = __uint_as_float(vr.x & 0xFFFF0000u);
+                v[u][2] = __uint_as_float(vr.y << 16);
+                v[u][3] = __uint_as_float(vr.y & 0xFFFF0000u);
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], d);
+            float mn = m;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                s[u] = on[u] ? s[u] * p.scale_log2 : ninf_f();
+                mn = fmaxf(mn, s[u]);
+            }
+            const float r = mn == ninf_f() ? 0.f : mn, f = ex2(m - r);
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] *= f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (!on[u]) continue;
+                const float e = ex2(s[u] - r);
+                l += e;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] += e * v[u][i];
+            }
+            m = mn;
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= inv;
+    return l == 0.f ? ninf_f() : m + lg2(l);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_constant__ WindowParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile uint32_t* abort_flag = &ctrl->abort_flag;
+    uint32_t* const bad_word = &ctrl->bad;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (threadIdx.x == 0) {
+        mbar_init(&ctrl->q_full, 1);
+        mbar_init(&ctrl->q_empty, 1);
+        for (int i = 0; i < kKStages; ++i) {
+            mbar_init(&ctrl->k_full[i], 1);
+            mbar_init(&ctrl->k_empty[i], 1);
+        }
+        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(&ctrl->v_full[i], 1);
+            mbar_init(&ctrl->v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctrl->s_full[i], 1);
+            mbar_init(&ctrl->p_full[i], 4);  // one arrival per softmax warp
+            mbar_init(&ctrl->o_full[i], 1);
+        }
+        mbar_init(&ctrl->mma_done, 1);
+        ctrl->abort_flag = 0;
+        ctrl->bad = 0;
+        fence_barrier_init();
+        prefetch_tmap(&p.qmap);
+        prefetch_tmap(&p.kmap);
+        prefetch_tmap(&p.vmap);
+    }
+    if (warp == 11) {
+        tmem_alloc(&ctrl->tmem_base, 512);
+        tmem_relinquish();
+    }
+    // V rows that a tile does not load keep what was there: begin with zeros
+    for (uint32_t i = threadIdx.x; i < kVStages * kTileBytes / 16; i += kThreads)
+        *reinterpret_cast<uint4*>(smem + kOffV + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    schedule(p, ctrl);
+    const uint32_t tmem = ctrl->tmem_base;
+    int4 desc = make_int4(-1, 0, 0, 0);
+
+    if (ctrl->left > 0) {
+        if (warp == 8 || warp == 9) {
+            // ============================== loads: warp 8 Q and K, warp 9 V
+            const bool is_k = warp == 8;
+            const CUtensorMap* map = is_k ? &p.kmap : &p.vmap;
+            uint64_t* const full = is_k ? ctrl->k_full : ctrl->v_full;
+            uint64_t* const empty = is_k ? ctrl->k_empty : ctrl->v_empty;
+            const int n_stages = is_k ? kKStages : kVStages;
+            uint8_t* const ring = smem + (is_k ? kOffK : kOffV);
+            const uint64_t pol = l2_policy_evict_normal();
+            const int NB = 128 / p.boxr;
+            const uint32_t q_bytes = (uint32_t)(p.G * p.TSB) * 128u;  // one half of one query tile
+            long long g = 0;
+            int st = 0, piece = 0, q_loads = 0;
+            uint32_t par = 1;  // parity of the ring's previous round
+            bool ok = true;
+            Walker w;
+            w.init(p, ctrl);
+            for (; w.left > 0 && ok; w.next(p), ++piece) {
+                const Unit& x = w.x;
+                const int end = x.p0 + x.ntok;
+                const int32_t* trow = p.table + (size_t)x.b * p.stride;
+                // lane bi: the page of box bi of a tile, or -1 where no row sees any of it
+                auto page_of = [&](int j) -> int {
+                    const int pos = key0_of(x, j) + lane * p.boxr;
+                    if (lane >= NB || j >= w.j1 || pos >= end ||
+                        (pos + p.boxr <= x.lo && pos >= x.sink))
+                        return -1;
+                    const int pg = __ldg(trow + (pos >> p.lp));
+                    if (pg < 0 || pg >= p.num_pages) {
+                        atomicOr(bad_word, CPA_DEV_BAD_PAGE);
+                        return -1;
+                    }
+                    return pg;
+                };
+                int page = page_of(w.j0);
+                if (is_k) {
+                    if (piece > 0)
+                        ok = wait_warp(&ctrl->q_empty, (uint32_t)((piece - 1) & 1), abort_flag,
+                                            bad_word);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const int nq = w.tiles_q(p);
+                        mbar_arrive_expect_tx(&ctrl->q_full, (uint32_t)nq * 2u * q_bytes);
+                        for (int mt = 0; mt < nq; ++mt)
+                            for (int h = 0; h < 2; ++h)
+                                tma_load_3d(smem + kOffQ + mt * kTileBytes + h * kHalf, &p.qmap, h * 64,
+                                            x.hk * p.G, x.t0 + mt * p.TSB, &ctrl->q_full, pol);
+                    }
+                    __syncwarp();
+                    ++q_loads;
+                }
+                for (int j = w.j0; j < w.j1; ++j, ++g) {
+                    const int next_page = page_of(j + 1);
+                    if (g >= n_stages) {
+                        ok = wait_warp(&empty[st], par, abort_flag, bad_word);
+                        if (!ok) break;
+                    }
+                    const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(mask) * 2u * p.boxr * 128u);
+                    __syncwarp();
+                    uint8_t* dst = ring + (uint32_t)st * kTileBytes;
+                    const int key0 = key0_of(x, j);
+                    for (int t0 = 0; t0 < 2 * NB; t0 += 32) {
+                        const int t = t0 + lane, bi = (t < 2 * NB ? t : 0) >> 1, h = t & 1;
+                        const int pg = __shfl_sync(0xffffffffu, page, bi & 31);
+                        if (t < 2 * NB && pg >= 0)
+                            tma_load_3d(dst + h * kHalf + bi * p.boxr * 128, map, h * 64, x.hk,
+                                        (int)(((uint32_t)pg << p.lp) +
+                                              (uint32_t)((key0 + bi * p.boxr) & ((1 << p.lp) - 1))),
+                                        &full[st], pol);
+                    }
+                    page = next_page;
+                    if (++st == n_stages) {
+                        st = 0;
+                        par ^= 1u;
+                    }
+                }
+            }
+            // no copy may be in flight when the block leaves
+            for (int s = 0; s < n_stages; ++s)
+                if (s < g) {
+                    const long long last = s + (g - 1 - s) / n_stages * n_stages;
+                    wait_on(&full[s], (uint32_t)((last / n_stages) & 1), abort_flag, bad_word);
+                }
+            if (q_loads > 0)
+                wait_on(&ctrl->q_full, (uint32_t)((q_loads - 1) & 1), abort_flag, bad_word);
+            __syncwarp();
+        } else if (warp == 10) {
+            // ============================== products
+            if (lane == 0) {
+                const uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
+                const uint32_t idesc_o = idesc_bf16_f32(128, 128, true);
+                int ks = 0, vs = 0, piece = 0;
+                uint32_t kpar = 0, vpar = 0, ppar[2] = {0u, 0u};
+                bool ok = true;
+                Walker w;
+                w.init(p, ctrl);
+                auto wait = [&](uint64_t* bar, uint32_t par) {
+                    if (ok) ok = wait_on(bar, par, abort_flag, bad_word);
+                    return ok;
+                };
+                auto issue_s = [&](int mt) {
+                    const uint32_t qa = sbase + kOffQ + mt * kTileBytes;
+                    const uint32_t kb = sbase + kOffK + (uint32_t)ks * kTileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
+                        umma_bf16_ss(tmem + mt * 128u, sdesc_sw128(qa + o, 16, 1024),
+                                     sdesc_sw128(kb + o, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit(&ctrl->s_full[mt]);
+                };
+                auto issue_pv = [&](int mt, bool first) {
+                    const uint32_t vb = sbase + kOffV + (uint32_t)vs * kTileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_bf16_ts(tmem + 256u + mt * 128u, tmem + mt * 128u + kk * 8u,
+                                     sdesc_sw128(vb + kk * 16 * 128, kHalf, 1024), idesc_o,
+                                     first && kk == 0 ? 0u : 1u);
+                };
+                for (; w.left > 0 && ok; w.next(p), ++piece) {
+                    const int nq = w.tiles_q(p), n = w.j1 - w.j0;
+                    if (!wait(&ctrl->q_full, (uint32_t)(piece & 1))) break;
+                    for (int i = 0; i <= n && ok; ++i) {
+                        // tile i's scores and tile i - 1's values
+                        if (i < n && !wait(&ctrl->k_full[ks], kpar)) break;
+                        if (i > 0 && !wait(&ctrl->v_full[vs], vpar)) break;
+                        for (int mt = 0; mt < nq && ok; ++mt) {
+                            if (i > 0) {
+                                if (!wait(&ctrl->p_full[mt], ppar[mt])) break;
+                                ppar[mt] ^= 1u;
+                                tc_fence_after_sync();
+                                issue_pv(mt, i == 1);
+                                if (i == n) umma_commit(&ctrl->o_full[mt]);
+                            }
+                            if (i < n) issue_s(mt);
+                        }
+                        if (!ok) break;
+                        if (i < n) {
+                            umma_commit(&ctrl->k_empty[ks]);
+                            if (i == n - 1) umma_commit(&ctrl->q_empty);
+                            if (++ks == kKStages) {
+                                ks = 0;
+                                kpar ^= 1u;
+                            }
+                        }
+                        if (i > 0) {
+                            umma_commit(&ctrl->v_empty[vs]);
+                            if (++vs == kVStages) {
+                                vs = 0;
+                                vpar ^= 1u;
+                            }
+                        }
+                    }
+                }
+                umma_commit(&ctrl->mma_done);
+                wait_on(&ctrl->mma_done, 0, abort_flag, bad_word);
+            }
+            __syncwarp();
+        } else if (warp < 8) {
+            // ============================== softmax and output
+            const int mt = warp >> 2;
+            const int r = (warp & 3) * 32 + lane, R = mt * 128 + r;
+            const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t s_addr = tmem + lane_addr + mt * 128u;
+            const uint32_t o_addr = tmem + lane_addr + 256u + mt * 128u;
+            const int it = r / p.G, gq = r - it * p.G;
+            uint32_t spar = 0, opar = 0;
+            long long g = 0;  // key tiles of this block so far (V's ring)
+            bool ok = true;
+            Walker w;
+            w.init(p, ctrl);
+            for (; w.left > 0 && ok; w.next(p)) {
+                const Unit& x = w.x;
+                if (mt >= w.tiles_q(p)) {
+                    g += w.j1 - w.j0;
+                    continue;
+                }
+                const int tok = mt * p.TSB + it;
+                const bool active = it < p.TSB && tok < x.ntok;
+                const int pos = x.p0 + tok;
+                // positions of this query tile's first and last token
+                const int p_min = x.p0 + mt * p.TSB;
+                const int p_max = x.p0 + min(x.ntok, (mt + 1) * p.TSB) - 1;
+                float m_used = ninf_f(), l = 0.f;
+                for (int j = w.j0; j < w.j1; ++j, ++g) {
+                    const int key0 = key0_of(x, j);
+                    const bool whole = key0 + 127 <= p_min &&
+                                       (p.window == 0 || key0 > p_max - p.window ||
+                                        key0 + 128 <= p.sinks);
+                    ok = wait_warp(&ctrl->s_full[mt], spar, abort_flag, bad_word);
+                    if (!ok) break;
+                    spar ^= 1u;
+                    tc_fence_after_sync();
+                    uint32_t s[128];
+                    tmem_ld_x128(s_addr, s);
+                    if (!whole) {
+                        // columns [a, z) by position, and those below sk as sinks
+                        const int a = p.window > 0 ? pos + 1 - p.window - key0 : 0;
+                        const int z = pos + 1 - key0, sk = min(p.sinks - key0, z);
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4) {
+                            const uint32_t bits =
+                                (bits_below(z - 32 * q4) & ~bits_below(a - 32 * q4)) |
+                                bits_below(sk - 32 * q4);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(bits >> c & 1u)) s[32 * q4 + c] = 0xff800000u;
+                        }
+                    }
+                    float m4[4] = {ninf_f(), ninf_f(), ninf_f(), ninf_f()};
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        m4[c & 3] = fmax3(m4[c & 3],
+                                          fmax3(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1]),
+                                                __uint_as_float(s[4 * c + 2])),
+                                          __uint_as_float(s[4 * c + 3]));
+                    const float tmax =
+                        fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+                    // O holds every earlier tile of this unit: PV(j - 1) was issued before
+                    // S(j), whose completion s_full told
+                    const bool need = active && m_used != ninf_f() && tmax > m_used + kRescale;
+                    if (__any_sync(0xffffffffu, need)) {
+                        const float f = need ? ex2(m_used - tmax) : 1.f;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 128; c0 += 8) {
+                            uint32_t v[8];
+                            tmem_ld_x8(o_addr + c0, v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                            asm volatile(
+                                "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], "
+                                "{%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(o_addr + c0),
+                                "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+                                "r"(v[6]), "r"(v[7])
+                                : "memory");
+                        }
+                        if (need) {
+                            l *= f;
+                            m_used = tmax;
+                        }
+                    }
+                    if (m_used == ninf_f()) m_used = tmax;
+                    const float mref = m_used == ninf_f() ? 0.f : m_used;
+                    // P = 2^(s * scale - m) in bf16 over the first 64 columns of the scores
+                    // (a weight's rounding of 2^-9 is of the size of the output's own; the
+                    // sum is of the unrounded weights in 32 bits)
+                    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+                    const float2 nm2 = make_float2(-mref, -mref);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float2 t = __ffma2_rn(
+                                make_float2(__uint_as_float(s[32 * q4 + 2 * c]),
+                                            __uint_as_float(s[32 * q4 + 2 * c + 1])),
+                                sc2, nm2);
+                            const float ea = ex2(t.x), eb = ex2(t.y);
+                            sum[c & 1] = __fadd2_rn(sum[c & 1], make_float2(ea, eb));
+                            pk[c] = pack_bf16x2(ea, eb);
+                        }
+                        tmem_st_x16_nowait(s_addr + 16u * q4, pk);
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    // slots past the sequence's end in the last loaded box: their V rows are
+                    // cleared (by query tile 0, whose products come first)
+                    if (mt == 0 && j == x.n_tiles - 1 &&
+                        ((x.p0 + x.ntok + p.boxr - 1) & ~(p.boxr - 1)) > x.L) {
+                        const int st = (int)(g % kVStages);
+                        ok = wait_warp(&ctrl->v_full[st], (uint32_t)((g / kVStages) & 1),
+                                            abort_flag, bad_word);
+                        if (!ok) break;
+                        const int first = x.L - key0;
+                        const int stop = min(128, (first + p.boxr - 1) & ~(p.boxr - 1));
+                        uint8_t* vb = smem + kOffV + (uint32_t)st * kTileBytes;
+                        for (int i = r; i < 16 * (stop - first); i += 128)
+                            *reinterpret_cast<uint4*>(vb + (i & 1) * kHalf + first * 128 + (i >> 1) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                    }
+                    tmem_wait_st();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctrl->p_full[mt]);
+                }
+                if (!ok) break;
+
+                // ---- output: the row, or its part of a unit cut by the block's range
+                ok = wait_warp(&ctrl->o_full[mt], opar, abort_flag, bad_word);
+                if (!ok) break;
+                opar ^= 1u;
+                tc_fence_after_sync();
+                const bool split = w.j0 > 0 || w.j1 < x.n_tiles;
+                const size_t slot = 2 * (size_t)blockIdx.x + (w.j0 > 0 ? 0 : 1);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float lse2 = l == 0.f ? ninf_f() : m_used + lg2(l);
+                const size_t row = (size_t)(x.t0 + (active ? tok : 0)) * p.H_q + x.hk * p.G +
+                                   (active ? gq : 0);
+                float check = lse2 == ninf_f() ? 0.f : lse2;
+                float4* po = p.part_o + slot * 32 * kRows + R;
+                uint4* out = reinterpret_cast<uint4*>(p.o + row * 128);
+#pragma unroll 1
+                for (int c0 = 0; c0 < 128; c0 += 32) {
+                    uint32_t v[32];
+                    tmem_ld_x32(o_addr + c0, v);
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        f[i] = __uint_as_float(v[i]) * inv;
+                        check = fmaf(f[i], 0.f, check);  // NaN once any is not finite
+                    }
+                    if (!active) continue;
+                    if (split) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            po[(size_t)(c0 / 4 + i) * kRows] =
+                                make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            out[c0 / 8 + i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]),
+                                                         pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
+                                                         pack_bf16x2(f[8 * i + 4], f[8 * i + 5]),
+                                                         pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+                    }
+                }
+                if (active) {
+                    if (split) p.part_lse[slot * kRows + R] = lse2;
+                    else p.lse[row] = lse2 == ninf_f() ? lse2 : lse2 * kLn2;
+                }
+                tc_fence_before_sync();  // O may be written again after this warp's next P
+                __syncwarp();
+                uint32_t again = __ballot_sync(0xffffffffu, active && !isfinite(check));
+                for (; again != 0u; again &= again - 1u) {
+                    const int src = __ffs((int)again) - 1;
+                    const size_t row_a = __shfl_sync(0xffffffffu, (unsigned long long)row, src);
+                    const int pos_a = __shfl_sync(0xffffffffu, pos, src);
+                    const int R_a = __shfl_sync(0xffffffffu, R, src);
+                    float f[4];
+                    const float z = slow_row(p, x, w.j0, w.j1, row_a, pos_a, f);
+                    if (split) {
+                        p.part_o[(slot * 32 + lane) * kRows + R_a] = make_float4(f[0], f[1], f[2], f[3]);
+                        if (lane == 0) p.part_lse[slot * kRows + R_a] = z;
+                    } else {
+                        reinterpret_cast<uint2*>(p.o + row_a * 128)[lane] =
+                            make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+                        if (lane == 0) p.lse[row_a] = z == ninf_f() ? z : z * kLn2;
+                    }
+                }
+            }
+        } else {
+            // warp 11: the unit that this block leaves unfinished, for the join
+            Walker w;
+            w.init(p, ctrl);
+            for (; w.left > 0; w.next(p))
+                if (w.j0 == 0 && w.j1 < w.x.n_tiles) {
+                    const long long first = ctrl->t0 + ctrl->left - w.left;
+                    desc = make_int4(w.x.b, w.x.hk, w.x.qt,
+                                     (int)((first + w.x.n_tiles - 1) / ctrl->per - blockIdx.x) + 1);
+                }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 11) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+        if (lane == 0) {
+            p.desc[blockIdx.x] = desc;
+            p.bad[blockIdx.x] = ctrl->bad;
+        }
+    }
+}
+
+// Joins the unit that starts in block c's range and goes on past its end: its
+// parts are block c's second slot and the first slots of the blocks after it, in
+// that order.  A block does 32 rows (grid.y), a thread 4 columns of a row at a
+// time.  Block (0, 0) gathers the status word.
+__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WindowParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        __shared__ uint32_t all;
+        if (threadIdx.x == 0) all = 0;
+        __syncthreads();
+        uint32_t bad = 0;
+        for (int i = threadIdx.x; i < p.n_cta; i += 256) bad |= __ldcg(p.bad + i);
+        if (bad) atomicOr(&all, bad);
+        __syncthreads();
+        if (threadIdx.x == 0) *p.status = all;
+    }
+    const int4 d = __ldcg(p.desc + blockIdx.x);
+    if (d.x < 0) return;
+    const Unit x = unit_of(p, d.x, d.y, d.z);
+    const int np = d.w;
+    const int R = blockIdx.y * 32 + (threadIdx.x & 31), r = R & 127;
+    const int it = r / p.G, gq = r - it * p.G;
+    const int tok = (R >> 7) * p.TSB + it;
+    if (it >= p.TSB || tok >= x.ntok) return;
+    const size_t row = (size_t)(x.t0 + tok) * p.H_q + x.hk * p.G + gq;
+    auto slot = [&](int i) -> size_t { return 2 * ((size_t)blockIdx.x + i) + (i == 0 ? 1 : 0); };
+    float mx = ninf_f();
+    for (int i = 0; i < np; ++i) mx = fmaxf(mx, __ldcg(p.part_lse + slot(i) * kRows + R));
+    const float ref = mx == ninf_f() ? 0.f : mx;
+    float sum = 0.f;
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int g0 = threadIdx.x >> 5;  // column groups g0, g0 + 8, g0 + 16, g0 + 24
+#pragma unroll 2
+    for (int i = 0; i < np; ++i) {
+        const float f = ex2(__ldcg(p.part_lse + slot(i) * kRows + R) - ref);
+        sum += f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = __ldcg(p.part_o + (slot(i) * 32 + g0 + 8 * k) * kRows + R);
+            acc[k].x += f * v.x;
+            acc[k].y += f * v.y;
+            acc[k].z += f * v.z;
+            acc[k].w += f * v.w;
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        reinterpret_cast<uint2*>(p.o + row * 128)[g0 + 8 * k] =
+            make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
+                       pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    if (g0 == 0) p.lse[row] = sum == 0.f ? ninf_f() : (ref + lg2(sum)) * kLn2;
+}
+
+struct WindowWs {
+    size_t bad, desc, part_lse, part_o, total;
+};
+WindowWs window_ws(int n_cta) {
+    WindowWs w;
+    w.bad = kStatusBytes;
+    w.desc = align_up(w.bad + (size_t)n_cta * 4, 256);
+    w.part_lse = align_up(w.desc + (size_t)n_cta * 16, 256);
+    w.part_o = align_up(w.part_lse + (size_t)2 * n_cta * kRows * 4, 256);
+    w.total = align_up(w.part_o + (size_t)2 * n_cta * kRows * 128 * 4, 256);
+    return w;
+}
+
+cudaError_t raise_smem_once() {
+    static PerDevice<int> state;
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return (cudaError_t)state.run(dev, (int)cudaErrorInvalidDevice, [](int&) {
+        return (int)cudaFuncSetAttribute(window_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmem);
+    });
+}
+
+}  // namespace
+}  // namespace cpa
 
 using namespace cpa;
 
@@ -14,7 +917,8 @@ size_t cpa_window_prefill_workspace_size(int B, int T, int H_q, int H_kv, int he
     if (B < 1 || T < 0 || max_new < 0 || H_q < 1 || H_kv < 1 || H_q % H_kv ||
         H_q / H_kv > 128 || head_dim != 128 || !page_size_ok(page_size))
         return 0;
-    return kStatusBytes;
+    const int n_sm = sm_count();
+    return n_sm <= 0 ? 0 : window_ws(n_sm).total;
 }
 
 cpa_status cpa_window_prefill(const void* q, const void* k_pages, const void* v_pages,
@@ -41,32 +945,61 @@ cpa_status cpa_window_prefill(const void* q, const void* k_pages, const void* v_
     if (!workspace || workspace_bytes < kStatusBytes) return CPA_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return CPA_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(workspace, 0, 4, s) != cudaSuccess) return CPA_ERR_CUDA;
-    if (T == 0) return CPA_OK;
-    RowParams p = {};
+    if (T == 0) return cudaMemsetAsync(workspace, 0, 4, s) == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
+    const int n_sm = sm_count();
+    if (n_sm <= 0) return CPA_ERR_CUDA;
+    const WindowWs w = window_ws(n_sm);
+    if (workspace_bytes < w.total) return CPA_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    WindowParams p = {};
     p.q = static_cast<const __nv_bfloat16*>(q);
-    p.k_pages = k_pages;
-    p.v_pages = v_pages;
+    p.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
+    p.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
     p.table = page_table;
     p.q_start = q_start;
     p.lens = seq_lens;
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
-    p.status = static_cast<uint32_t*>(workspace);
+    p.status = reinterpret_cast<uint32_t*>(ws);
+    p.bad = reinterpret_cast<uint32_t*>(ws + w.bad);
+    p.desc = reinterpret_cast<int4*>(ws + w.desc);
+    p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+    p.part_o = reinterpret_cast<float4*>(ws + w.part_o);
     p.stride = pt_stride;
     p.B = B;
     p.T = T;
     p.H_q = H_q;
     p.H_kv = H_kv;
+    p.G = H_q / H_kv;
+    p.TSB = 128 / p.G;
     p.lp = 31 - __builtin_clz((unsigned)page_size);
+    p.boxr = page_size < 128 ? page_size : 128;
     p.num_pages = num_pages;
     p.max_new = max_new;
     p.max_len = max_seq_len;
     p.window = window;
     p.sinks = sinks;
-    p.scale_log2 = sm_scale * 1.4426950408889634f;
-    rows_kernel<false><<<(unsigned)(((long long)T * H_q + 7) / 8), 256, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? CPA_OK : CPA_ERR_LAUNCH;
+    p.n_cta = n_sm;
+    p.min_tiles = 2;
+    p.scale_log2 = sm_scale * kLog2e;
+    const uint64_t slots = (uint64_t)num_pages * page_size;
+    if (!make_map(&p.qmap, q, H_q, (uint64_t)T, p.G, p.TSB) ||
+        !make_map(&p.kmap, k_pages, H_kv, slots, 1, p.boxr) ||
+        !make_map(&p.vmap, v_pages, H_kv, slots, 1, p.boxr))
+        return CPA_ERR_CUDA;
+    if (raise_smem_once() != cudaSuccess) return CPA_ERR_CUDA;
+    window_kernel<<<n_sm, kThreads, kSmem, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return CPA_ERR_LAUNCH;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)n_sm, kRows / 32);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, window_join_kernel, p) == cudaSuccess ? CPA_OK : CPA_ERR_LAUNCH;
 }
 
 }  // extern "C"
