@@ -13,9 +13,12 @@
 // S and its weights P share TMEM (P overwrites the scores that it came from, and
 // S(i+1) is issued after PV(i)), so S0, S1, O0 and O1 fill the 512 columns.
 //
+// The order goes on from a unit into the next, so that the first scores of a unit
+// run while the last weights of the one before are still being made.
+//
 // Warps (12): 0-3 softmax and output of query tile 0, 4-7 of tile 1 (one thread a
-// row: its 128 scores in registers, no exchange between threads), 8 loads Q and
-// K, 9 loads V, 10 issues the products, 11 allocates TMEM.
+// row: its 128 scores in registers, no exchange between threads), 8 loads K, 9
+// loads V, 10 issues the products, 11 loads Q and holds the TMEM allocation.
 //
 // What bounds it: the tensor cores for long chunks (4 H_q d flops a visible
 // pair); the chain softmax -> PV -> S -> softmax of one query tile when the
@@ -154,10 +157,10 @@ __device__ __forceinline__ int key0_of(const Unit& x, int j) {
 }
 
 struct Ctrl {
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t k_full[kKStages], k_empty[kKStages];
     uint64_t v_full[kVStages], v_empty[kVStages];
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: weights of keys 0..63, 64..127
     uint64_t mma_done;
     uint32_t tmem_base;
     uint32_t abort_flag;
@@ -325,6 +328,52 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
     return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r));
+    return r;
+}
+// The products and commits of cpa_device.cuh, issued by the lane whose `lead` is set.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
 // One row over tiles [j0, j1) of its unit, by a whole warp, key by key: what the
 // row does not see is not touched.  Lane l ends up with dimensions 4 l .. 4 l + 3
 // of o (normalised); returns the log-sum-exp in log2 units.
@@ -407,8 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (threadIdx.x == 0) {
-        mbar_init(&ctrl->q_full, 1);
-        mbar_init(&ctrl->q_empty, 1);
         for (int i = 0; i < kKStages; ++i) {
             mbar_init(&ctrl->k_full[i], 1);
             mbar_init(&ctrl->k_empty[i], 1);
@@ -418,8 +465,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             mbar_init(&ctrl->v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctrl->q_full[i], 1);
+            mbar_init(&ctrl->q_empty[i], 1);
             mbar_init(&ctrl->s_full[i], 1);
-            mbar_init(&ctrl->p_full[i], 4);  // one arrival per softmax warp
+            mbar_init(&ctrl->p_full[i][0], 4);  // one arrival per softmax warp
+            mbar_init(&ctrl->p_full[i][1], 4);
             mbar_init(&ctrl->o_full[i], 1);
         }
         mbar_init(&ctrl->mma_done, 1);
@@ -447,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 
     if (ctrl->left > 0) {
         if (warp == 8 || warp == 9) {
-            // ============================== loads: warp 8 Q and K, warp 9 V
+            // ============================== loads: warp 8 K, warp 9 V
             const bool is_k = warp == 8;
             const CUtensorMap* map = is_k ? &p.kmap : &p.vmap;
             uint64_t* const full = is_k ? ctrl->k_full : ctrl->v_full;
@@ -456,14 +506,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             uint8_t* const ring = smem + (is_k ? kOffK : kOffV);
             const uint64_t pol = l2_policy_evict_normal();
             const int NB = 128 / p.boxr;
-            const uint32_t q_bytes = (uint32_t)(p.G * p.TSB) * 128u;  // one half of one query tile
             long long g = 0;
-            int st = 0, piece = 0, q_loads = 0;
+            int st = 0;
             uint32_t par = 1;  // parity of the ring's previous round
             bool ok = true;
             Walker w;
             w.init(p, ctrl);
-            for (; w.left > 0 && ok; w.next(p), ++piece) {
+            for (; w.left > 0 && ok; w.next(p)) {
                 const Unit& x = w.x;
                 const int end = x.p0 + x.ntok;
                 const int32_t* trow = p.table + (size_t)x.b * p.stride;
@@ -481,22 +530,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     return pg;
                 };
                 int page = page_of(w.j0);
-                if (is_k) {
-                    if (piece > 0)
-                        ok = wait_warp(&ctrl->q_empty, (uint32_t)((piece - 1) & 1), abort_flag,
-                                            bad_word);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        const int nq = w.tiles_q(p);
-                        mbar_arrive_expect_tx(&ctrl->q_full, (uint32_t)nq * 2u * q_bytes);
-                        for (int mt = 0; mt < nq; ++mt)
-                            for (int h = 0; h < 2; ++h)
-                                tma_load_3d(smem + kOffQ + mt * kTileBytes + h * kHalf, &p.qmap, h * 64,
-                                            x.hk * p.G, x.t0 + mt * p.TSB, &ctrl->q_full, pol);
-                    }
-                    __syncwarp();
-                    ++q_loads;
-                }
                 for (int j = w.j0; j < w.j1; ++j, ++g) {
                     const int next_page = page_of(j + 1);
                     if (g >= n_stages) {
@@ -531,81 +564,95 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     const long long last = s + (g - 1 - s) / n_stages * n_stages;
                     wait_on(&full[s], (uint32_t)((last / n_stages) & 1), abort_flag, bad_word);
                 }
-            if (q_loads > 0)
-                wait_on(&ctrl->q_full, (uint32_t)((q_loads - 1) & 1), abort_flag, bad_word);
             __syncwarp();
         } else if (warp == 10) {
             // ============================== products
-            if (lane == 0) {
-                const uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
-                const uint32_t idesc_o = idesc_bf16_f32(128, 128, true);
-                int ks = 0, vs = 0, piece = 0;
-                uint32_t kpar = 0, vpar = 0, ppar[2] = {0u, 0u};
-                bool ok = true;
-                Walker w;
-                w.init(p, ctrl);
-                auto wait = [&](uint64_t* bar, uint32_t par) {
-                    if (ok) ok = wait_on(bar, par, abort_flag, bad_word);
-                    return ok;
-                };
-                auto issue_s = [&](int mt) {
-                    const uint32_t qa = sbase + kOffQ + mt * kTileBytes;
-                    const uint32_t kb = sbase + kOffK + (uint32_t)ks * kTileBytes;
+            // All lanes run the loop, so that addresses and descriptors stay uniform
+            // across the warp; one elected lane's predicate issues.
+            const uint32_t lead = elect_one();
+            const uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
+            const uint32_t idesc_o = idesc_bf16_f32(128, 128, true);
+            const uint64_t q_desc = sdesc_sw128(sbase + kOffQ, 16, 1024);
+            const uint64_t k_desc = sdesc_sw128(sbase + kOffK, 16, 1024);
+            const uint64_t v_desc = sdesc_sw128(sbase + kOffV, kHalf, 1024);
+            int ks = 0, vs = 0;  // stage of the tile whose scores / values are next
+            uint32_t kpar = 0, vpar = 0, qpar[2] = {0u, 0u}, ppar[2] = {0u, 0u};
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t par) {
+                ok = ok && wait_warp(bar, par, abort_flag, bad_word);
+                return ok;
+            };
+            auto issue_s = [&](int mt) {
+                const uint64_t a = q_desc + mt * (kTileBytes >> 4);
+                const uint64_t b = k_desc + (uint32_t)ks * (kTileBytes >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        umma_bf16_ss(tmem + mt * 128u, sdesc_sw128(qa + o, 16, 1024),
-                                     sdesc_sw128(kb + o, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                    mma_ss(lead, tmem + mt * 128u, a + o, b + o, idesc_s, kk > 0 ? 1u : 0u);
+                }
+                commit(lead, &ctrl->s_full[mt]);
+            };
+            // half of PV: 64 keys
+            auto issue_pv = [&](int mt, int half, bool first) {
+                const uint64_t b = v_desc + (uint32_t)vs * (kTileBytes >> 4);
+#pragma unroll
+                for (int k4 = 0; k4 < 4; ++k4) {
+                    const int kk = half * 4 + k4;
+                    mma_ts(lead, tmem + 256u + mt * 128u, tmem + mt * 128u + kk * 8u,
+                           b + ((kk * 16 * 128) >> 4), idesc_o, first && kk == 0 ? 0u : 1u);
+                }
+            };
+            // what the tile before the current one was
+            int nq_prev = 0;
+            bool first_prev = false, last_prev = false;
+            // tile by tile, one more round after the last: PV of the tile before, S of
+            // this one
+            auto round = [&](int nq, bool first, bool last) {
+                if (nq_prev && !wait(&ctrl->v_full[vs], vpar)) return;
+                if (nq && !wait(&ctrl->k_full[ks], kpar)) return;
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    if (mt < nq_prev) {
+                        if (!wait(&ctrl->p_full[mt][0], ppar[mt])) return;
+                        tc_fence_after_sync();
+                        issue_pv(mt, 0, first_prev);
+                        if (!wait(&ctrl->p_full[mt][1], ppar[mt])) return;
+                        tc_fence_after_sync();
+                        issue_pv(mt, 1, false);
+                        ppar[mt] ^= 1u;
+                        if (last_prev) commit(lead, &ctrl->o_full[mt]);
+                        if (mt == nq_prev - 1) commit(lead, &ctrl->v_empty[vs]);
                     }
-                    umma_commit(&ctrl->s_full[mt]);
-                };
-                auto issue_pv = [&](int mt, bool first) {
-                    const uint32_t vb = sbase + kOffV + (uint32_t)vs * kTileBytes;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16_ts(tmem + 256u + mt * 128u, tmem + mt * 128u + kk * 8u,
-                                     sdesc_sw128(vb + kk * 16 * 128, kHalf, 1024), idesc_o,
-                                     first && kk == 0 ? 0u : 1u);
-                };
-                for (; w.left > 0 && ok; w.next(p), ++piece) {
-                    const int nq = w.tiles_q(p), n = w.j1 - w.j0;
-                    if (!wait(&ctrl->q_full, (uint32_t)(piece & 1))) break;
-                    for (int i = 0; i <= n && ok; ++i) {
-                        // tile i's scores and tile i - 1's values
-                        if (i < n && !wait(&ctrl->k_full[ks], kpar)) break;
-                        if (i > 0 && !wait(&ctrl->v_full[vs], vpar)) break;
-                        for (int mt = 0; mt < nq && ok; ++mt) {
-                            if (i > 0) {
-                                if (!wait(&ctrl->p_full[mt], ppar[mt])) break;
-                                ppar[mt] ^= 1u;
-                                tc_fence_after_sync();
-                                issue_pv(mt, i == 1);
-                                if (i == n) umma_commit(&ctrl->o_full[mt]);
-                            }
-                            if (i < n) issue_s(mt);
+                    if (mt < nq) {
+                        if (first) {
+                            if (!wait(&ctrl->q_full[mt], qpar[mt])) return;
+                            qpar[mt] ^= 1u;
                         }
-                        if (!ok) break;
-                        if (i < n) {
-                            umma_commit(&ctrl->k_empty[ks]);
-                            if (i == n - 1) umma_commit(&ctrl->q_empty);
-                            if (++ks == kKStages) {
-                                ks = 0;
-                                kpar ^= 1u;
-                            }
-                        }
-                        if (i > 0) {
-                            umma_commit(&ctrl->v_empty[vs]);
-                            if (++vs == kVStages) {
-                                vs = 0;
-                                vpar ^= 1u;
-                            }
-                        }
+                        issue_s(mt);
+                        if (last) commit(lead, &ctrl->q_empty[mt]);
+                        if (mt == nq - 1) commit(lead, &ctrl->k_empty[ks]);
                     }
                 }
-                umma_commit(&ctrl->mma_done);
-                wait_on(&ctrl->mma_done, 0, abort_flag, bad_word);
-            }
-            __syncwarp();
+                if (nq_prev && ++vs == kVStages) {
+                    vs = 0;
+                    vpar ^= 1u;
+                }
+                if (nq && ++ks == kKStages) {
+                    ks = 0;
+                    kpar ^= 1u;
+                }
+                nq_prev = nq;
+                first_prev = first;
+                last_prev = last;
+            };
+            Walker w;
+            w.init(p, ctrl);
+            for (; w.left > 0 && ok; w.next(p))
+                for (int j = w.j0; j < w.j1 && ok; ++j)
+                    round(w.tiles_q(p), j == w.j0, j == w.j1 - 1);
+            if (ok) round(0, false, false);
+            commit(lead, &ctrl->mma_done);
+            wait_warp(&ctrl->mma_done, 0, abort_flag, bad_word);
         } else if (warp < 8) {
             // ============================== softmax and output
             const int mt = warp >> 2;
@@ -652,6 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                             const uint32_t bits =
                                 (bits_below(z - 32 * q4) & ~bits_below(a - 32 * q4)) |
                                 bits_below(sk - 32 * q4);
+                            // (most groups of an edge tile are whole for the whole warp)
+                            if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
                                 if (!(bits >> c & 1u)) s[32 * q4 + c] = 0xff800000u;
@@ -692,6 +741,22 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     }
                     if (m_used == ninf_f()) m_used = tmax;
                     const float mref = m_used == ninf_f() ? 0.f : m_used;
+                    // slots past the sequence's end in the last loaded box: their V rows are
+                    // cleared (by query tile 0, whose products come first)
+                    if (mt == 0 && j == x.n_tiles - 1 &&
+                        ((x.p0 + x.ntok + p.boxr - 1) & ~(p.boxr - 1)) > x.L) {
+                        const int st = (int)(g % kVStages);
+                        ok = wait_warp(&ctrl->v_full[st], (uint32_t)((g / kVStages) & 1),
+                                            abort_flag, bad_word);
+                        if (!ok) break;
+                        const int first = x.L - key0;
+                        const int stop = min(128, (first + p.boxr - 1) & ~(p.boxr - 1));
+                        uint8_t* vb = smem + kOffV + (uint32_t)st * kTileBytes;
+                        for (int i = r; i < 16 * (stop - first); i += 128)
+                            *reinterpret_cast<uint4*>(vb + (i & 1) * kHalf + first * 128 + (i >> 1) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                    }
                     // P = 2^(s * scale - m) in bf16 over the first 64 columns of the scores
                     // (a weight's rounding of 2^-9 is of the size of the output's own; the
                     // sum is of the unrounded weights in 32 bits)
@@ -712,28 +777,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                             pk[c] = pack_bf16x2(ea, eb);
                         }
                         tmem_st_x16_nowait(s_addr + 16u * q4, pk);
+                        if (q4 & 1) {  // 64 keys: their products may begin
+                            tmem_wait_st();
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&ctrl->p_full[mt][q4 >> 1]);
+                        }
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    // slots past the sequence's end in the last loaded box: their V rows are
-                    // cleared (by query tile 0, whose products come first)
-                    if (mt == 0 && j == x.n_tiles - 1 &&
-                        ((x.p0 + x.ntok + p.boxr - 1) & ~(p.boxr - 1)) > x.L) {
-                        const int st = (int)(g % kVStages);
-                        ok = wait_warp(&ctrl->v_full[st], (uint32_t)((g / kVStages) & 1),
-                                            abort_flag, bad_word);
-                        if (!ok) break;
-                        const int first = x.L - key0;
-                        const int stop = min(128, (first + p.boxr - 1) & ~(p.boxr - 1));
-                        uint8_t* vb = smem + kOffV + (uint32_t)st * kTileBytes;
-                        for (int i = r; i < 16 * (stop - first); i += 128)
-                            *reinterpret_cast<uint4*>(vb + (i & 1) * kHalf + first * 128 + (i >> 1) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                    }
-                    tmem_wait_st();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctrl->p_full[mt]);
                 }
                 if (!ok) break;
 
@@ -801,15 +852,44 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 }
             }
         } else {
-            // warp 11: the unit that this block leaves unfinished, for the join
+            // ============================== warp 11: Q, and the unit that this block
+            // leaves unfinished, for the join
+            const uint32_t bytes = (uint32_t)(p.G * p.TSB) * 2u * 128u;  // of one query tile
+            const uint64_t pol = l2_policy_evict_normal();
+            uint32_t loads[2] = {0u, 0u};
+            bool ok = true;
             Walker w;
             w.init(p, ctrl);
-            for (; w.left > 0; w.next(p))
-                if (w.j0 == 0 && w.j1 < w.x.n_tiles) {
+            while (w.left > 0 && ok) {
+                const Unit x = w.x;
+                const int nq = w.tiles_q(p);
+                if (w.j0 == 0 && w.j1 < x.n_tiles) {
                     const long long first = ctrl->t0 + ctrl->left - w.left;
-                    desc = make_int4(w.x.b, w.x.hk, w.x.qt,
-                                     (int)((first + w.x.n_tiles - 1) / ctrl->per - blockIdx.x) + 1);
+                    desc = make_int4(x.b, x.hk, x.qt,
+                                     (int)((first + x.n_tiles - 1) / ctrl->per - blockIdx.x) + 1);
                 }
+                for (int mt = 0; mt < nq && ok; ++mt) {
+                    if (loads[mt] > 0)
+                        ok = wait_warp(&ctrl->q_empty[mt], (loads[mt] - 1) & 1u, abort_flag, bad_word);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&ctrl->q_full[mt], bytes);
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_3d(smem + kOffQ + mt * kTileBytes + h * kHalf, &p.qmap, h * 64,
+                                        x.hk * p.G, x.t0 + mt * p.TSB, &ctrl->q_full[mt], pol);
+                    }
+                    __syncwarp();
+                    ++loads[mt];
+                }
+                w.next(p);
+                // the next unit's Q into L2: its load is then short
+                if (ok && w.left > 0 && lane < 2 * w.tiles_q(p))
+                    prefetch_3d(&p.qmap, (lane & 1) * 64, w.x.hk * p.G, w.x.t0 + (lane >> 1) * p.TSB);
+            }
+            for (int mt = 0; mt < 2; ++mt)  // no copy may be in flight when the block leaves
+                if (loads[mt] > 0)
+                    wait_on(&ctrl->q_full[mt], (loads[mt] - 1) & 1u, abort_flag, bad_word);
+            __syncwarp();
         }
     }
 
