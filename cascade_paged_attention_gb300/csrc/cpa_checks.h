@@ -12,6 +12,7 @@
 namespace cpa {
 
 constexpr size_t kStatusBytes = 256;
+constexpr int kMaxLength = 1 << 30;  // tokens of a sequence (sums of a length and a tile fit an int)
 
 inline int sm_count() {
     int dev = 0;

@@ -653,6 +653,7 @@ cpa_status decode_common(const void* q, const void* k_pages, const void* v_pages
         return CPA_ERR_INVALID_ARG;
     if ((long long)num_pages * page_size > (1ll << 31)) return CPA_ERR_UNSUPPORTED;
     if ((long long)B * H_q > (1ll << 31) / 128) return CPA_ERR_UNSUPPORTED;
+    if (max_seq_len > kMaxLength) return CPA_ERR_UNSUPPORTED;
     if (!workspace) return CPA_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return CPA_ERR_INVALID_ARG;
     const int G = H_q / H_kv;

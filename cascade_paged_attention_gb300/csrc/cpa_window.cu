@@ -18,7 +18,11 @@
 //
 // Warps (12): 0-3 softmax and output of query tile 0, 4-7 of tile 1 (one thread a
 // row: its 128 scores in registers, no exchange between threads), 8 loads K, 9
-// loads V, 10 issues the products, 11 loads Q and holds the TMEM allocation.
+// loads Q and V, 10 issues the products of query tile 0, 11 those of tile 1.  Two
+// issuing warps, because a warp that has issued products goes on only when they
+// have left its queue: the other one waits for its weights and loads meanwhile,
+// and hands the turn on as soon as it has issued (one warp alone left the tensor
+// cores idle for 0.3 of the time).
 //
 // What bounds it: the tensor cores for long chunks (4 H_q d flops a visible
 // pair); the chain softmax -> PV -> S -> softmax of one query tile when the
@@ -51,13 +55,14 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 256;       // rows of a unit
-constexpr int kKStages = 3, kVStages = 2;
+constexpr int kKStages = 2, kVStages = 2;
 constexpr uint32_t kHalf = 128u * 128u;    // 64 columns of a 128-row tile: 16 KB
 constexpr uint32_t kTileBytes = 2 * kHalf; // 128 rows of 256 bytes
 constexpr uint32_t kOffQ = 1024;
 constexpr uint32_t kOffK = kOffQ + 2 * kTileBytes;
 constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
-constexpr uint32_t kSmem = kOffV + kVStages * kTileBytes + 1024;  // (aligned up inside)
+constexpr uint32_t kOffOut = kOffV + kVStages * kTileBytes;  // 4 KB a softmax warp
+constexpr uint32_t kSmem = kOffOut + 8 * 4096 + 1024;        // (aligned up inside)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
@@ -93,6 +98,8 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
 }
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity,
                                           volatile uint32_t* abort_flag, uint32_t* bad) {
+    // (the first look by itself: most waits find the phase complete)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, wait_on(bar, parity, abort_flag, bad));
 }
 
@@ -161,14 +168,14 @@ struct Ctrl {
     uint64_t k_full[kKStages], k_empty[kKStages];
     uint64_t v_full[kVStages], v_empty[kVStages];
     uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: weights of keys 0..63, 64..127
+    uint64_t turn[2];   // the issuing warps' turns
     uint64_t mma_done;
     uint32_t tmem_base;
     uint32_t abort_flag;
     uint32_t bad;
     long long scan[kWarps];
-    long long t0, left, per, off;  // this block's range, and where its first unit starts
-    long long sum_q;               // tiles of one KV head of the first unit's request
-    int b, hk, qt, j;
+    long long t0, left, per;  // this block's range of tiles
+    int b, hk, qt, j;         // where it begins
 };
 static_assert(sizeof(Ctrl) <= kOffQ, "control block");
 
@@ -176,13 +183,11 @@ static_assert(sizeof(Ctrl) <= kOffQ, "control block");
 __device__ __forceinline__ long long head_tiles(const WindowParams& p, const Request& r) {
     const int TS = 2 * p.TSB, lane = threadIdx.x & 31;
     const int nq = (r.m + TS - 1) / TS;
-    int s = 0;  // (a request's tiles fit: 2^24 query tiles' worth of rows at most)
     long long sum = 0;
     for (int qt = lane; qt < nq; qt += 32) {
         Unit x;
         unit_tiles(p, r, qt, x);
-        s = x.n_tiles;
-        sum += s;
+        sum += x.n_tiles;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -458,11 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         for (int i = 0; i < kKStages; ++i) {
             mbar_init(&ctrl->k_full[i], 1);
-            mbar_init(&ctrl->k_empty[i], 1);
+            mbar_init(&ctrl->k_empty[i], 2);  // the two issuing warps
         }
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&ctrl->v_full[i], 1);
-            mbar_init(&ctrl->v_empty[i], 1);
+            mbar_init(&ctrl->v_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctrl->q_full[i], 1);
@@ -471,8 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             mbar_init(&ctrl->p_full[i][0], 4);  // one arrival per softmax warp
             mbar_init(&ctrl->p_full[i][1], 4);
             mbar_init(&ctrl->o_full[i], 1);
+            mbar_init(&ctrl->turn[i], 1);
         }
-        mbar_init(&ctrl->mma_done, 1);
+        mbar_init(&ctrl->mma_done, 2);
         ctrl->abort_flag = 0;
         ctrl->bad = 0;
         fence_barrier_init();
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 
     if (ctrl->left > 0) {
         if (warp == 8 || warp == 9) {
-            // ============================== loads: warp 8 K, warp 9 V
+            // ============================== loads: warp 8 K, warp 9 Q and V
             const bool is_k = warp == 8;
             const CUtensorMap* map = is_k ? &p.kmap : &p.vmap;
             uint64_t* const full = is_k ? ctrl->k_full : ctrl->v_full;
@@ -506,6 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             uint8_t* const ring = smem + (is_k ? kOffK : kOffV);
             const uint64_t pol = l2_policy_evict_normal();
             const int NB = 128 / p.boxr;
+            const uint32_t q_bytes = (uint32_t)(p.G * p.TSB) * 2u * 128u;  // of one query tile
+            uint32_t q_loads[2] = {0u, 0u};
             long long g = 0;
             int st = 0;
             uint32_t par = 1;  // parity of the ring's previous round
@@ -530,6 +538,31 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     return pg;
                 };
                 int page = page_of(w.j0);
+                if (is_k) {
+                    // the unit that this block leaves unfinished, for the join
+                    if (w.j0 == 0 && w.j1 < x.n_tiles) {
+                        const long long first = ctrl->t0 + ctrl->left - w.left;
+                        desc = make_int4(x.b, x.hk, x.qt,
+                                         (int)((first + x.n_tiles - 1) / ctrl->per - blockIdx.x) + 1);
+                    }
+                } else {
+                    const int nq = w.tiles_q(p);
+                    for (int mt = 0; mt < nq && ok; ++mt) {
+                        if (q_loads[mt] > 0)
+                            ok = wait_warp(&ctrl->q_empty[mt], (q_loads[mt] - 1) & 1u, abort_flag,
+                                           bad_word);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&ctrl->q_full[mt], q_bytes);
+                            for (int h = 0; h < 2; ++h)
+                                tma_load_3d(smem + kOffQ + mt * kTileBytes + h * kHalf, &p.qmap, h * 64,
+                                            x.hk * p.G, x.t0 + mt * p.TSB, &ctrl->q_full[mt], pol);
+                        }
+                        __syncwarp();
+                        ++q_loads[mt];
+                    }
+                    if (!ok) break;
+                }
                 for (int j = w.j0; j < w.j1; ++j, ++g) {
                     const int next_page = page_of(j + 1);
                     if (g >= n_stages) {
@@ -556,8 +589,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                         st = 0;
                         par ^= 1u;
                     }
+                    if (!is_k && j == w.j0) {
+                        // the next unit's Q into L2: its load is then short
+                        Walker y = w;
+                        y.next(p);
+                        if (y.left > 0 && lane < 2 * y.tiles_q(p))
+                            prefetch_3d(&p.qmap, (lane & 1) * 64, y.x.hk * p.G,
+                                        y.x.t0 + (lane >> 1) * p.TSB);
+                    }
                 }
             }
+            for (int mt = 0; mt < 2; ++mt)
+                if (q_loads[mt] > 0)
+                    wait_on(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u, abort_flag, bad_word);
             // no copy may be in flight when the block leaves
             for (int s = 0; s < n_stages; ++s)
                 if (s < g) {
@@ -565,74 +609,79 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     wait_on(&full[s], (uint32_t)((last / n_stages) & 1), abort_flag, bad_word);
                 }
             __syncwarp();
-        } else if (warp == 10) {
-            // ============================== products
+        } else if (warp >= 10) {
+            // ============================== products of query tile mt
             // All lanes run the loop, so that addresses and descriptors stay uniform
             // across the warp; one elected lane's predicate issues.
+            const int mt = warp - 10;
             const uint32_t lead = elect_one();
             const uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
             const uint32_t idesc_o = idesc_bf16_f32(128, 128, true);
             const uint64_t q_desc = sdesc_sw128(sbase + kOffQ, 16, 1024);
             const uint64_t k_desc = sdesc_sw128(sbase + kOffK, 16, 1024);
             const uint64_t v_desc = sdesc_sw128(sbase + kOffV, kHalf, 1024);
+            const uint64_t a_desc = q_desc + mt * (kTileBytes >> 4);
+            const uint32_t s_col = tmem + mt * 128u, o_col = tmem + 256u + mt * 128u;
             int ks = 0, vs = 0;  // stage of the tile whose scores / values are next
-            uint32_t kpar = 0, vpar = 0, qpar[2] = {0u, 0u}, ppar[2] = {0u, 0u};
+            uint32_t kpar = 0, vpar = 0, qpar = 0, ppar = 0, tpar = mt == 0 ? 1u : 0u;
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t par) {
                 ok = ok && wait_warp(bar, par, abort_flag, bad_word);
                 return ok;
             };
-            auto issue_s = [&](int mt) {
-                const uint64_t a = q_desc + mt * (kTileBytes >> 4);
-                const uint64_t b = k_desc + (uint32_t)ks * (kTileBytes >> 4);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                    mma_ss(lead, tmem + mt * 128u, a + o, b + o, idesc_s, kk > 0 ? 1u : 0u);
-                }
-                commit(lead, &ctrl->s_full[mt]);
-            };
             // half of PV: 64 keys
-            auto issue_pv = [&](int mt, int half, bool first) {
+            auto issue_pv = [&](int half, bool first) {
                 const uint64_t b = v_desc + (uint32_t)vs * (kTileBytes >> 4);
 #pragma unroll
                 for (int k4 = 0; k4 < 4; ++k4) {
                     const int kk = half * 4 + k4;
-                    mma_ts(lead, tmem + 256u + mt * 128u, tmem + mt * 128u + kk * 8u,
-                           b + ((kk * 16 * 128) >> 4), idesc_o, first && kk == 0 ? 0u : 1u);
+                    mma_ts(lead, o_col, s_col + kk * 8u, b + ((kk * 16 * 128) >> 4), idesc_o,
+                           first && kk == 0 ? 0u : 1u);
                 }
             };
             // what the tile before the current one was
             int nq_prev = 0;
             bool first_prev = false, last_prev = false;
-            // tile by tile, one more round after the last: PV of the tile before, S of
-            // this one
+            // A round: PV of the tile before, S of this one (after the last tile there is
+            // one more round).  Everything is waited for before the turn; the turn is
+            // handed on when all is issued.
             auto round = [&](int nq, bool first, bool last) {
-                if (nq_prev && !wait(&ctrl->v_full[vs], vpar)) return;
-                if (nq && !wait(&ctrl->k_full[ks], kpar)) return;
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    if (mt < nq_prev) {
-                        if (!wait(&ctrl->p_full[mt][0], ppar[mt])) return;
-                        tc_fence_after_sync();
-                        issue_pv(mt, 0, first_prev);
-                        if (!wait(&ctrl->p_full[mt][1], ppar[mt])) return;
-                        tc_fence_after_sync();
-                        issue_pv(mt, 1, false);
-                        ppar[mt] ^= 1u;
-                        if (last_prev) commit(lead, &ctrl->o_full[mt]);
-                        if (mt == nq_prev - 1) commit(lead, &ctrl->v_empty[vs]);
-                    }
-                    if (mt < nq) {
-                        if (first) {
-                            if (!wait(&ctrl->q_full[mt], qpar[mt])) return;
-                            qpar[mt] ^= 1u;
-                        }
-                        issue_s(mt);
-                        if (last) commit(lead, &ctrl->q_empty[mt]);
-                        if (mt == nq - 1) commit(lead, &ctrl->k_empty[ks]);
-                    }
+                const bool pv = mt < nq_prev, sc = mt < nq;
+                if (pv && !(wait(&ctrl->v_full[vs], vpar) && wait(&ctrl->p_full[mt][0], ppar))) return;
+                if (sc && !wait(&ctrl->k_full[ks], kpar)) return;
+                if (sc && first) {
+                    if (!wait(&ctrl->q_full[mt], qpar)) return;
+                    qpar ^= 1u;
                 }
+                if (!wait(&ctrl->turn[mt], tpar)) return;
+                tpar ^= 1u;
+                tc_fence_after_sync();
+                if (pv) {
+                    issue_pv(0, first_prev);
+                    if (!wait(&ctrl->p_full[mt][1], ppar)) return;
+                    ppar ^= 1u;
+                    tc_fence_after_sync();
+                    issue_pv(1, false);
+                    if (last_prev) commit(lead, &ctrl->o_full[mt]);
+                    commit(lead, &ctrl->v_empty[vs]);
+                } else if (nq_prev && lead) {
+                    mbar_arrive(&ctrl->v_empty[vs]);
+                }
+                if (sc) {
+                    const uint64_t b = k_desc + (uint32_t)ks * (kTileBytes >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                        mma_ss(lead, s_col, a_desc + o, b + o, idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    commit(lead, &ctrl->s_full[mt]);
+                    if (last) commit(lead, &ctrl->q_empty[mt]);
+                    commit(lead, &ctrl->k_empty[ks]);
+                } else if (nq && lead) {
+                    mbar_arrive(&ctrl->k_empty[ks]);
+                }
+                if (lead) mbar_arrive(&ctrl->turn[mt ^ 1]);
+                __syncwarp();
                 if (nq_prev && ++vs == kVStages) {
                     vs = 0;
                     vpar ^= 1u;
@@ -742,8 +791,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     if (m_used == ninf_f()) m_used = tmax;
                     const float mref = m_used == ninf_f() ? 0.f : m_used;
                     // slots past the sequence's end in the last loaded box: their V rows are
-                    // cleared (by query tile 0, whose products come first)
-                    if (mt == 0 && j == x.n_tiles - 1 &&
+                    // cleared (by both query tiles, each before its own products)
+                    if (j == x.n_tiles - 1 &&
                         ((x.p0 + x.ntok + p.boxr - 1) & ~(p.boxr - 1)) > x.L) {
                         const int st = (int)(g % kVStages);
                         ok = wait_warp(&ctrl->v_full[st], (uint32_t)((g / kVStages) & 1),
@@ -797,34 +846,57 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 const size_t slot = 2 * (size_t)blockIdx.x + (w.j0 > 0 ? 0 : 1);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const float lse2 = l == 0.f ? ninf_f() : m_used + lg2(l);
-                const size_t row = (size_t)(x.t0 + (active ? tok : 0)) * p.H_q + x.hk * p.G +
-                                   (active ? gq : 0);
+                const int row = (x.t0 + (active ? tok : 0)) * p.H_q + x.hk * p.G + (active ? gq : 0);
                 float check = lse2 == ninf_f() ? 0.f : lse2;
                 float4* po = p.part_o + slot * 32 * kRows + R;
-                uint4* out = reinterpret_cast<uint4*>(p.o + row * 128);
+                uint8_t* stage = smem + kOffOut + warp * 4096;
+                const int row_or = active ? row : -1;
 #pragma unroll 1
-                for (int c0 = 0; c0 < 128; c0 += 32) {
-                    uint32_t v[32];
-                    tmem_ld_x32(o_addr + c0, v);
-                    float f[32];
+                for (int h = 0; h < 2; ++h) {
+                    // 64 columns; finished rows go through shared memory (32 rows of 128
+                    // bytes, 16-byte chunks swizzled), so that 8 lanes write a row's 128
+                    // bytes together
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        f[i] = __uint_as_float(v[i]) * inv;
-                        check = fmaf(f[i], 0.f, check);  // NaN once any is not finite
+                    for (int c0 = 0; c0 < 64; c0 += 32) {
+                        uint32_t v[32];
+                        tmem_ld_x32(o_addr + h * 64 + c0, v);
+                        float f[32];
+                        float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            f[i] = __uint_as_float(v[i]) * inv;
+                            z[i & 3] = fmaf(f[i], 0.f, z[i & 3]);  // NaN once any is not finite
+                        }
+                        check += (z[0] + z[1]) + (z[2] + z[3]);
+                        if (split) {
+                            if (active)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    po[(size_t)(h * 16 + c0 / 4 + i) * kRows] =
+                                        make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<uint4*>(
+                                    stage + lane * 128 + (((c0 / 8 + i) ^ (lane & 7)) << 4)) =
+                                    make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]),
+                                               pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
+                                               pack_bf16x2(f[8 * i + 4], f[8 * i + 5]),
+                                               pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+                        }
                     }
-                    if (!active) continue;
-                    if (split) {
+                    if (!split) {
+                        __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            po[(size_t)(c0 / 4 + i) * kRows] =
-                                make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            out[c0 / 8 + i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]),
-                                                         pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
-                                                         pack_bf16x2(f[8 * i + 4], f[8 * i + 5]),
-                                                         pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+                        for (int i = 0; i < 8; ++i) {
+                            const int rr = i * 4 + (lane >> 3), ch = lane & 7;
+                            const int to = __shfl_sync(0xffffffffu, row_or, rr);
+                            const uint4 x4 = *reinterpret_cast<const uint4*>(
+                                stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                            if (to >= 0)
+                                reinterpret_cast<uint4*>(p.o + (size_t)to * 128)[h * 8 + ch] = x4;
+                        }
+                        __syncwarp();
                     }
                 }
                 if (active) {
@@ -836,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 uint32_t again = __ballot_sync(0xffffffffu, active && !isfinite(check));
                 for (; again != 0u; again &= again - 1u) {
                     const int src = __ffs((int)again) - 1;
-                    const size_t row_a = __shfl_sync(0xffffffffu, (unsigned long long)row, src);
+                    const size_t row_a = (size_t)__shfl_sync(0xffffffffu, row, src);
                     const int pos_a = __shfl_sync(0xffffffffu, pos, src);
                     const int R_a = __shfl_sync(0xffffffffu, R, src);
                     float f[4];
@@ -851,45 +923,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     }
                 }
             }
-        } else {
-            // ============================== warp 11: Q, and the unit that this block
-            // leaves unfinished, for the join
-            const uint32_t bytes = (uint32_t)(p.G * p.TSB) * 2u * 128u;  // of one query tile
-            const uint64_t pol = l2_policy_evict_normal();
-            uint32_t loads[2] = {0u, 0u};
-            bool ok = true;
-            Walker w;
-            w.init(p, ctrl);
-            while (w.left > 0 && ok) {
-                const Unit x = w.x;
-                const int nq = w.tiles_q(p);
-                if (w.j0 == 0 && w.j1 < x.n_tiles) {
-                    const long long first = ctrl->t0 + ctrl->left - w.left;
-                    desc = make_int4(x.b, x.hk, x.qt,
-                                     (int)((first + x.n_tiles - 1) / ctrl->per - blockIdx.x) + 1);
-                }
-                for (int mt = 0; mt < nq && ok; ++mt) {
-                    if (loads[mt] > 0)
-                        ok = wait_warp(&ctrl->q_empty[mt], (loads[mt] - 1) & 1u, abort_flag, bad_word);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&ctrl->q_full[mt], bytes);
-                        for (int h = 0; h < 2; ++h)
-                            tma_load_3d(smem + kOffQ + mt * kTileBytes + h * kHalf, &p.qmap, h * 64,
-                                        x.hk * p.G, x.t0 + mt * p.TSB, &ctrl->q_full[mt], pol);
-                    }
-                    __syncwarp();
-                    ++loads[mt];
-                }
-                w.next(p);
-                // the next unit's Q into L2: its load is then short
-                if (ok && w.left > 0 && lane < 2 * w.tiles_q(p))
-                    prefetch_3d(&p.qmap, (lane & 1) * 64, w.x.hk * p.G, w.x.t0 + (lane >> 1) * p.TSB);
-            }
-            for (int mt = 0; mt < 2; ++mt)  // no copy may be in flight when the block leaves
-                if (loads[mt] > 0)
-                    wait_on(&ctrl->q_full[mt], (loads[mt] - 1) & 1u, abort_flag, bad_word);
-            __syncwarp();
         }
     }
 
@@ -898,10 +931,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     if (warp == 11) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
-        if (lane == 0) {
-            p.desc[blockIdx.x] = desc;
-            p.bad[blockIdx.x] = ctrl->bad;
-        }
+    }
+    if (warp == 8 && lane == 0) {
+        p.desc[blockIdx.x] = desc;
+        p.bad[blockIdx.x] = ctrl->bad;
     }
 }
 
@@ -1022,6 +1055,7 @@ cpa_status cpa_window_prefill(const void* q, const void* k_pages, const void* v_
         return CPA_ERR_INVALID_ARG;
     if ((long long)num_pages * page_size > (1ll << 31)) return CPA_ERR_UNSUPPORTED;
     if ((long long)T * H_q > (1ll << 31) / 128) return CPA_ERR_UNSUPPORTED;
+    if (max_seq_len > kMaxLength) return CPA_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < kStatusBytes) return CPA_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return CPA_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
