@@ -146,9 +146,8 @@ __device__ __forceinline__ void unit_tiles(const WindowParams& p, const Request&
     x.n_tiles = x.n_sink + end - x.w0;
 }
 
-__device__ __forceinline__ Unit unit_of(const WindowParams& p, int b, int hk, int qt) {
-    uint32_t bad = 0;
-    const Request r = request_of(p, b, bad);
+__device__ __forceinline__ Unit unit_of(const WindowParams& p, const Request& r, int b, int hk,
+                                       int qt) {
     Unit x;
     unit_tiles(p, r, qt, x);
     x.b = b;
@@ -177,7 +176,8 @@ struct Ctrl {
     long long t0, left, per;  // this block's range of tiles
     int b, hk, qt, j;         // where it begins
 };
-static_assert(sizeof(Ctrl) <= kOffQ, "control block");
+constexpr uint32_t kOffWalk = 384;  // the softmax warps' walkers
+static_assert(sizeof(Ctrl) <= kOffWalk, "control block");
 
 // Tiles of one KV head of request b, by one warp.
 __device__ __forceinline__ long long head_tiles(const WindowParams& p, const Request& r) {
@@ -268,6 +268,7 @@ __device__ void schedule(const WindowParams& p, Ctrl* c) {
 // Walks the pieces (unit, tiles [j0, j1)) of this block's range.
 struct Walker {
     Unit x;
+    Request r;  // x's request
     long long left;
     int j0, j1;
     __device__ __forceinline__ void cut() {
@@ -276,7 +277,9 @@ struct Walker {
     __device__ __forceinline__ void init(const WindowParams& p, const Ctrl* c) {
         left = c->left;
         if (left == 0) return;
-        x = unit_of(p, c->b, c->hk, c->qt);
+        uint32_t bad = 0;
+        r = request_of(p, c->b, bad);
+        x = unit_of(p, r, c->b, c->hk, c->qt);
         j0 = c->j;
         cut();
     }
@@ -284,19 +287,16 @@ struct Walker {
         left -= j1 - j0;
         if (left == 0) return;
         int b = x.b, hk = x.hk, qt = x.qt + 1;
-        uint32_t bad = 0;
-        Request r = request_of(p, b, bad);
         if (qt * 2 * p.TSB >= r.m) {
             qt = 0;
             if (++hk == p.H_kv) {
                 hk = 0;
-                do {
-                    ++b;
-                    r = request_of(p, b, bad);
-                } while (r.m == 0);  // (tiles are left, so a request with tokens is)
+                uint32_t bad = 0;
+                do r = request_of(p, ++b, bad);
+                while (r.m == 0);  // (tiles are left, so a request with tokens is)
             }
         }
-        x = unit_of(p, b, hk, qt);
+        x = unit_of(p, r, b, hk, qt);
         j0 = 0;
         cut();
     }
@@ -305,6 +305,8 @@ struct Walker {
         return x.ntok > p.TSB ? 2 : 1;
     }
 };
+
+static_assert(kOffWalk + 8 * sizeof(Walker) <= kOffQ, "control block");
 
 // 128 TMEM columns of this warp's lanes, loaded and waited for.
 #define W8(i) "=r"(r[i + 0]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
@@ -382,7 +384,7 @@ __device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int c0, int 
 // One row over tiles [j0, j1) of its unit, by a whole warp, key by key: what the
 // row does not see is not touched.  Lane l ends up with dimensions 4 l .. 4 l + 3
 // of o (normalised); returns the log-sum-exp in log2 units.
-__device__ __noinline__ float slow_row(const WindowParams& p, const Unit& x, int j0, int j1,
+__device__ __forceinline__ float slow_row(const WindowParams& p, const Unit& x, int j0, int j1,
                                        size_t qrow, int pos, float (&o)[4]) {
     const int lane = threadIdx.x & 31;
     const uint2 qr = __ldg(reinterpret_cast<const uint2*>(p.q + qrow * 128) + lane);
@@ -643,11 +645,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             int nq_prev = 0;
             bool first_prev = false, last_prev = false;
             // A round: PV of the tile before, S of this one (after the last tile there is
-            // one more round).  Everything is waited for before the turn; the turn is
-            // handed on when all is issued.
+            // one more round).  The weights are waited for last, as what comes last; the
+            // turn is handed on when all is issued.
             auto round = [&](int nq, bool first, bool last) {
                 const bool pv = mt < nq_prev, sc = mt < nq;
-                if (pv && !(wait(&ctrl->v_full[vs], vpar) && wait(&ctrl->p_full[mt][0], ppar))) return;
+                if (pv && !wait(&ctrl->v_full[vs], vpar)) return;
                 if (sc && !wait(&ctrl->k_full[ks], kpar)) return;
                 if (sc && first) {
                     if (!wait(&ctrl->q_full[mt], qpar)) return;
@@ -655,8 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 }
                 if (!wait(&ctrl->turn[mt], tpar)) return;
                 tpar ^= 1u;
-                tc_fence_after_sync();
                 if (pv) {
+                    if (!wait(&ctrl->p_full[mt][0], ppar)) return;
+                    tc_fence_after_sync();
                     issue_pv(0, first_prev);
                     if (!wait(&ctrl->p_full[mt][1], ppar)) return;
                     ppar ^= 1u;
@@ -668,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     mbar_arrive(&ctrl->v_empty[vs]);
                 }
                 if (sc) {
+                    tc_fence_after_sync();
                     const uint64_t b = k_desc + (uint32_t)ks * (kTileBytes >> 4);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
@@ -713,26 +717,36 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             uint32_t spar = 0, opar = 0;
             long long g = 0;  // key tiles of this block so far (V's ring)
             bool ok = true;
-            Walker w;
+            // The walk of this warp, in shared memory: registers are for the scores.  (All
+            // lanes write the same values.)
+            Walker& w = reinterpret_cast<Walker*>(smem + kOffWalk)[warp];
             w.init(p, ctrl);
-            for (; w.left > 0 && ok; w.next(p)) {
+            __syncwarp();
+            while (w.left > 0 && ok) {
                 const Unit& x = w.x;
                 if (mt >= w.tiles_q(p)) {
                     g += w.j1 - w.j0;
+                    w.next(p);
+                    __syncwarp();
                     continue;
                 }
                 const int tok = mt * p.TSB + it;
                 const bool active = it < p.TSB && tok < x.ntok;
                 const int pos = x.p0 + tok;
+                const int jend = w.j1, n_sink = x.n_sink, skip = x.w0 - x.n_sink;
                 // positions of this query tile's first and last token
                 const int p_min = x.p0 + mt * p.TSB;
-                const int p_max = x.p0 + min(x.ntok, (mt + 1) * p.TSB) - 1;
+                // keys up to here are hidden from its last token, unless they are sinks
+                const int hidden = p.window > 0
+                                       ? x.p0 + min(x.ntok, (mt + 1) * p.TSB) - 1 - p.window
+                                       : -1;
+                // tile whose loaded box goes on past the sequence's end
+                const int tail = ((x.p0 + x.ntok + p.boxr - 1) & ~(p.boxr - 1)) > x.L ? x.n_tiles - 1 : -1;
                 float m_used = ninf_f(), l = 0.f;
-                for (int j = w.j0; j < w.j1; ++j, ++g) {
-                    const int key0 = key0_of(x, j);
-                    const bool whole = key0 + 127 <= p_min &&
-                                       (p.window == 0 || key0 > p_max - p.window ||
-                                        key0 + 128 <= p.sinks);
+                for (int j = w.j0; j < jend; ++j, ++g) {
+                    const int key0 = (j < n_sink ? j : j + skip) << 7;
+                    const bool whole =
+                        key0 + 127 <= p_min && (key0 > hidden || key0 + 128 <= p.sinks);
                     ok = wait_warp(&ctrl->s_full[mt], spar, abort_flag, bad_word);
                     if (!ok) break;
                     spar ^= 1u;
@@ -792,8 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     const float mref = m_used == ninf_f() ? 0.f : m_used;
                     // slots past the sequence's end in the last loaded box: their V rows are
                     // cleared (by both query tiles, each before its own products)
-                    if (j == x.n_tiles - 1 &&
-                        ((x.p0 + x.ntok + p.boxr - 1) & ~(p.boxr - 1)) > x.L) {
+                    if (j == tail) {
                         const int st = (int)(g % kVStages);
                         ok = wait_warp(&ctrl->v_full[st], (uint32_t)((g / kVStages) & 1),
                                             abort_flag, bad_word);
@@ -922,6 +935,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                         if (lane == 0) p.lse[row_a] = z == ninf_f() ? z : z * kLn2;
                     }
                 }
+                __syncwarp();
+                w.next(p);
+                __syncwarp();
             }
         }
     }
@@ -956,7 +972,8 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
     }
     const int4 d = __ldcg(p.desc + blockIdx.x);
     if (d.x < 0) return;
-    const Unit x = unit_of(p, d.x, d.y, d.z);
+    uint32_t bad = 0;
+    const Unit x = unit_of(p, request_of(p, d.x, bad), d.x, d.y, d.z);
     const int np = d.w;
     const int R = blockIdx.y * 32 + (threadIdx.x & 31), r = R & 127;
     const int it = r / p.G, gq = r - it * p.G;
