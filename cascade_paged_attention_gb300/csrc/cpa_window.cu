@@ -65,6 +65,10 @@ constexpr uint32_t kOffOut = kOffV + kVStages * kTileBytes;  // 4 KB a softmax w
 constexpr uint32_t kSmem = kOffOut + 8 * 4096 + 1024;        // (aligned up inside)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// What a unit costs besides its tiles, in tiles: its first scores, masked edge
+// tiles and output.  Ranges are cut by this cost (equal numbers of tiles alone left
+// the median block waiting 10 % of the time for those with many short units).
+constexpr int kUnitCost = 3;
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
 // A wait that lasts this long means a broken pipeline.  (Longer than elsewhere:
 // rows that are not finite are done again key by key while the other warps wait.)
@@ -173,35 +177,35 @@ struct Ctrl {
     uint32_t abort_flag;
     uint32_t bad;
     long long scan[kWarps];
-    long long t0, left, per;  // this block's range of tiles
-    int b, hk, qt, j;         // where it begins
+    long long t0, left, per;  // this block's range, in tiles of cost
+    int b, hk, qt, off;       // where it begins: a unit, and how far into its cost
 };
 constexpr uint32_t kOffWalk = 384;  // the softmax warps' walkers
 static_assert(sizeof(Ctrl) <= kOffWalk, "control block");
 
-// Tiles of one KV head of request b, by one warp.
-__device__ __forceinline__ long long head_tiles(const WindowParams& p, const Request& r) {
+// Cost of one KV head of request r, by one warp.
+__device__ __forceinline__ long long head_cost(const WindowParams& p, const Request& r) {
     const int TS = 2 * p.TSB, lane = threadIdx.x & 31;
     const int nq = (r.m + TS - 1) / TS;
     long long sum = 0;
     for (int qt = lane; qt < nq; qt += 32) {
         Unit x;
         unit_tiles(p, r, qt, x);
-        sum += x.n_tiles;
+        sum += x.n_tiles + kUnitCost;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
 }
 
-// Every thread: the problem's tiles, this block's range, and the unit and tile
-// where it begins.  Each warp sums whole requests; then all walk the warps' sums.
+// Every thread: the problem's cost, this block's range, and the unit where it
+// begins.  Each warp sums whole requests; then all walk the warps' sums.
 __device__ void schedule(const WindowParams& p, Ctrl* c) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t bad = 0;
     long long mine = 0;
     for (int b = warp; b < p.B; b += kWarps)
-        mine += head_tiles(p, request_of(p, b, bad)) * p.H_kv;
+        mine += head_cost(p, request_of(p, b, bad)) * p.H_kv;
     if (bad && lane == 0) atomicOr(&c->bad, bad);
     if (lane == 0) c->scan[warp] = mine;
     __syncthreads();
@@ -209,19 +213,19 @@ __device__ void schedule(const WindowParams& p, Ctrl* c) {
         long long total = 0;
         for (int w = 0; w < kWarps; ++w) total += c->scan[w];
         long long per = (total + p.n_cta - 1) / p.n_cta;
-        if (per < p.min_tiles) per = p.min_tiles;
+        if (per < p.min_tiles + kUnitCost) per = p.min_tiles + kUnitCost;
         c->per = per;
         c->t0 = per * blockIdx.x;
         c->left = c->t0 < total ? min(per, total - c->t0) : 0;
     }
     __syncthreads();
     if (c->left == 0) return;
-    // the request that holds tile t0: a round of kWarps requests at a time
+    // the request that holds position t0: a round of kWarps requests at a time
     long long run = 0;
     for (int b0 = 0; b0 < p.B; b0 += kWarps) {
         const int b = b0 + warp;
         long long per_head = 0;
-        if (b < p.B) per_head = head_tiles(p, request_of(p, b, bad));
+        if (b < p.B) per_head = head_cost(p, request_of(p, b, bad));
         __syncthreads();
         if (lane == 0) c->scan[warp] = per_head * p.H_kv;
         __syncthreads();
@@ -240,20 +244,23 @@ __device__ void schedule(const WindowParams& p, Ctrl* c) {
             long long at = 0;
             for (int q0 = 0; q0 < nq; q0 += 32) {
                 Unit x;
-                x.n_tiles = 0;
-                if (q0 + lane < nq) unit_tiles(p, r, q0 + lane, x);
-                long long incl = x.n_tiles;
+                int cost = 0;
+                if (q0 + lane < nq) {
+                    unit_tiles(p, r, q0 + lane, x);
+                    cost = x.n_tiles + kUnitCost;
+                }
+                long long incl = cost;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
                     if (lane >= o) incl += y;
                 }
-                const long long ex = at + incl - x.n_tiles;
-                if (ex <= off && off < ex + x.n_tiles) {
+                const long long ex = at + incl - cost;
+                if (ex <= off && off < ex + cost) {
                     c->b = b;
                     c->hk = hk;
                     c->qt = q0 + lane;
-                    c->j = (int)(off - ex);
+                    c->off = (int)(off - ex);
                 }
                 at += __shfl_sync(0xffffffffu, incl, 31);
                 if (at > off) break;
@@ -265,27 +272,32 @@ __device__ void schedule(const WindowParams& p, Ctrl* c) {
     __syncthreads();
 }
 
-// Walks the pieces (unit, tiles [j0, j1)) of this block's range.
+// Walks the pieces (unit, tiles [j0, j1)) of this block's range; j0 == j1 past the
+// last.  A unit's own cost counts as lying before its first tile.
 struct Walker {
     Unit x;
-    Request r;  // x's request
-    long long left;
+    Request r;       // x's request
+    long long left;  // cost of the range after this piece
     int j0, j1;
-    __device__ __forceinline__ void cut() {
-        j1 = (int)min((long long)x.n_tiles, (long long)j0 + left);
+    __device__ __forceinline__ void cut(int off) {
+        const int take = (int)min((long long)x.n_tiles + kUnitCost - off, left);
+        left -= take;
+        j0 = max(0, off - kUnitCost);
+        j1 = max(0, off + take - kUnitCost);  // (0: the range ends before the first tile)
     }
+    __device__ __forceinline__ bool more() const { return j0 < j1; }
     __device__ __forceinline__ void init(const WindowParams& p, const Ctrl* c) {
         left = c->left;
-        if (left == 0) return;
         uint32_t bad = 0;
         r = request_of(p, c->b, bad);
         x = unit_of(p, r, c->b, c->hk, c->qt);
-        j0 = c->j;
-        cut();
+        cut(c->off);
     }
     __device__ __forceinline__ void next(const WindowParams& p) {
-        left -= j1 - j0;
-        if (left == 0) return;
+        if (left == 0) {
+            j0 = j1;
+            return;
+        }
         int b = x.b, hk = x.hk, qt = x.qt + 1;
         if (qt * 2 * p.TSB >= r.m) {
             qt = 0;
@@ -293,12 +305,11 @@ struct Walker {
                 hk = 0;
                 uint32_t bad = 0;
                 do r = request_of(p, ++b, bad);
-                while (r.m == 0);  // (tiles are left, so a request with tokens is)
+                while (r.m == 0);  // (cost is left, so a request with tokens is)
             }
         }
         x = unit_of(p, r, b, hk, qt);
-        j0 = 0;
-        cut();
+        cut(0);
     }
     // query tiles that hold tokens
     __device__ __forceinline__ int tiles_q(const WindowParams& p) const {
@@ -522,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             bool ok = true;
             Walker w;
             w.init(p, ctrl);
-            for (; w.left > 0 && ok; w.next(p)) {
+            for (; w.more() && ok; w.next(p)) {
                 const Unit& x = w.x;
                 const int end = x.p0 + x.ntok;
                 const int32_t* trow = p.table + (size_t)x.b * p.stride;
@@ -543,9 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 if (is_k) {
                     // the unit that this block leaves unfinished, for the join
                     if (w.j0 == 0 && w.j1 < x.n_tiles) {
-                        const long long first = ctrl->t0 + ctrl->left - w.left;
-                        desc = make_int4(x.b, x.hk, x.qt,
-                                         (int)((first + x.n_tiles - 1) / ctrl->per - blockIdx.x) + 1);
+                        // (it ends with this piece, which ends with the range)
+                        const long long last = ctrl->t0 + ctrl->left + x.n_tiles - w.j1 - 1;
+                        desc = make_int4(x.b, x.hk, x.qt, (int)(last / ctrl->per - blockIdx.x) + 1);
                     }
                 } else {
                     const int nq = w.tiles_q(p);
@@ -595,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                         // the next unit's Q into L2: its load is then short
                         Walker y = w;
                         y.next(p);
-                        if (y.left > 0 && lane < 2 * y.tiles_q(p))
+                        if (y.more() && lane < 2 * y.tiles_q(p))
                             prefetch_3d(&p.qmap, (lane & 1) * 64, y.x.hk * p.G,
                                         y.x.t0 + (lane >> 1) * p.TSB);
                     }
@@ -700,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             };
             Walker w;
             w.init(p, ctrl);
-            for (; w.left > 0 && ok; w.next(p))
+            for (; w.more() && ok; w.next(p))
                 for (int j = w.j0; j < w.j1 && ok; ++j)
                     round(w.tiles_q(p), j == w.j0, j == w.j1 - 1);
             if (ok) round(0, false, false);
@@ -722,8 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             Walker& w = reinterpret_cast<Walker*>(smem + kOffWalk)[warp];
             w.init(p, ctrl);
             __syncwarp();
-            while (w.left > 0 && ok) {
-                const Unit& x = w.x;
+            while (w.more() && ok) {
+                const Unit& xs = w.x;
                 if (mt >= w.tiles_q(p)) {
                     g += w.j1 - w.j0;
                     w.next(p);
@@ -731,17 +742,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     continue;
                 }
                 const int tok = mt * p.TSB + it;
-                const bool active = it < p.TSB && tok < x.ntok;
-                const int pos = x.p0 + tok;
-                const int jend = w.j1, n_sink = x.n_sink, skip = x.w0 - x.n_sink;
+                const bool active = it < p.TSB && tok < xs.ntok;
+                const int pos = xs.p0 + tok;
+                const int jend = w.j1, n_sink = xs.n_sink, skip = xs.w0 - xs.n_sink;
                 // positions of this query tile's first and last token
-                const int p_min = x.p0 + mt * p.TSB;
+                const int p_min = xs.p0 + mt * p.TSB;
                 // keys up to here are hidden from its last token, unless they are sinks
                 const int hidden = p.window > 0
-                                       ? x.p0 + min(x.ntok, (mt + 1) * p.TSB) - 1 - p.window
+                                       ? xs.p0 + min(xs.ntok, (mt + 1) * p.TSB) - 1 - p.window
                                        : -1;
                 // tile whose loaded box goes on past the sequence's end
-                const int tail = ((x.p0 + x.ntok + p.boxr - 1) & ~(p.boxr - 1)) > x.L ? x.n_tiles - 1 : -1;
+                const int tail = ((xs.p0 + xs.ntok + p.boxr - 1) & ~(p.boxr - 1)) > xs.L ? xs.n_tiles - 1 : -1;
                 float m_used = ninf_f(), l = 0.f;
                 for (int j = w.j0; j < jend; ++j, ++g) {
                     const int key0 = (j < n_sink ? j : j + skip) << 7;
@@ -811,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                         ok = wait_warp(&ctrl->v_full[st], (uint32_t)((g / kVStages) & 1),
                                             abort_flag, bad_word);
                         if (!ok) break;
-                        const int first = x.L - key0;
+                        const int first = xs.L - key0;
                         const int stop = min(128, (first + p.boxr - 1) & ~(p.boxr - 1));
                         uint8_t* vb = smem + kOffV + (uint32_t)st * kTileBytes;
                         for (int i = r; i < 16 * (stop - first); i += 128)
@@ -850,13 +861,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 }
                 if (!ok) break;
 
-                // ---- output: the row, or its part of a unit cut by the block's range
+                // ---- output: the row, or its part of a unit cut by the block's range.  The
+                // walk goes on first, while the last products run.
+                const Unit x = w.x;
+                const int j0 = w.j0, j1 = w.j1;
+                __syncwarp();
+                w.next(p);
+                __syncwarp();
                 ok = wait_warp(&ctrl->o_full[mt], opar, abort_flag, bad_word);
                 if (!ok) break;
                 opar ^= 1u;
                 tc_fence_after_sync();
-                const bool split = w.j0 > 0 || w.j1 < x.n_tiles;
-                const size_t slot = 2 * (size_t)blockIdx.x + (w.j0 > 0 ? 0 : 1);
+                const bool split = j0 > 0 || j1 < x.n_tiles;
+                const size_t slot = 2 * (size_t)blockIdx.x + (j0 > 0 ? 0 : 1);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const float lse2 = l == 0.f ? ninf_f() : m_used + lg2(l);
                 const int row = (x.t0 + (active ? tok : 0)) * p.H_q + x.hk * p.G + (active ? gq : 0);
@@ -925,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     const int pos_a = __shfl_sync(0xffffffffu, pos, src);
                     const int R_a = __shfl_sync(0xffffffffu, R, src);
                     float f[4];
-                    const float z = slow_row(p, x, w.j0, w.j1, row_a, pos_a, f);
+                    const float z = slow_row(p, x, j0, j1, row_a, pos_a, f);
                     if (split) {
                         p.part_o[(slot * 32 + lane) * kRows + R_a] = make_float4(f[0], f[1], f[2], f[3]);
                         if (lane == 0) p.part_lse[slot * kRows + R_a] = z;
@@ -935,9 +952,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                         if (lane == 0) p.lse[row_a] = z == ninf_f() ? z : z * kLn2;
                     }
                 }
-                __syncwarp();
-                w.next(p);
-                __syncwarp();
             }
         }
     }
