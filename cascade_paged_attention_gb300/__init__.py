@@ -670,38 +670,60 @@ def cpa_tree_pass_b(q, k_pages, v_pages, tree_page_table, tree_parents,
 
 
 # ---------------------------------------------------------------- decode, windowed prefill, page operations
-def _on(ref: torch.Tensor, *tensors):
-    """All tensors are on the device of `ref`."""
-    for t in tensors:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"tensors are on different devices: {ref.device} and {t.device}")
+def _want(t, name: str, dtype, ndim: int, dev: int):
+    """`_need`, and on device `dev`.  (The calls below are a few microseconds of GPU work at their
+    smallest: one pass over what nearly every call gets right, the messages apart.)"""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim
+            and t.get_device() == dev and t.is_contiguous()):
+        return
+    _need(t, name, dtype, ndim)
+    raise ValueError(f"{name} is on {t.device}: the call's tensors must be on one device")
+
+
+def _device(t, name: str, dtype=None) -> int:
+    """The device of the call: that of its first tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return t.get_device()
 
 
 def _shape(t: torch.Tensor, name: str, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _run(name: str, device: torch.device, stream, workspace, nbytes: int, check: bool, call):
-    """Run `call(workspace, bytes, stream)` with `device` current.  Without a workspace from
-    the caller each call gets its own, from PyTorch's allocator on the call's stream: calls on
-    several streams, or in several captured graphs, then share nothing."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _run(name, device, stream, workspace, nbytes, check, call)
+def _new(shape, dtype, dev: int, stream):
+    """An output that the caller did not give, from PyTorch's allocator on the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _launch(name: str, args, dev: int, stream, workspace, nbytes, check: bool):
+    """Call entry point `name` with `args`, workspace and stream on device `dev`.  Without a
+    workspace from the caller each call gets its own (`nbytes()` of it), from PyTorch's
+    allocator on the call's stream: calls on several streams, or in several captured graphs,
+    then share nothing."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(name, args, dev, stream, workspace, nbytes, check)
     if workspace is None:
-        with torch.cuda.stream(stream):  # (None: the current stream)
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    s = torch.cuda.current_stream() if stream is None else stream
-    _check(name, call(workspace.data_ptr(), workspace.numel(), s.cuda_stream))
+        workspace = _new(nbytes(), torch.uint8, dev, stream)
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8
+              and workspace.get_device() == dev and workspace.is_contiguous()):
+        _need(workspace, "workspace", torch.uint8)
+        raise ValueError("workspace is on another device than the call's tensors")
+    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    st = getattr(_lib or lib(), name)(*args, workspace.data_ptr(), workspace.numel(), raw)
+    if st != 0:
+        raise CpaError(name, st)
     if check:
         _check_device(name, workspace, stream)
-
-
-def _need_workspace(workspace, ref):
-    if workspace is not None:
-        _need(workspace, "workspace", torch.uint8)
-        _on(ref, workspace)
 
 
 def cpa_decode_workspace_size(B, H_q, H_kv, head_dim, page_size) -> int:
@@ -710,44 +732,42 @@ def cpa_decode_workspace_size(B, H_q, H_kv, head_dim, page_size) -> int:
 
 def _decode(name, q, k_pages, v_pages, scales, page_table, seq_lens, max_seq_len, window, sinks,
             sm_scale, o, lse, workspace, stream, check):
+    dev = _device(q, "q", torch.bfloat16)
     kv = torch.uint8 if scales else torch.bfloat16
-    _need(q, "q", torch.bfloat16, 3)
-    _need(k_pages, "k_pages", kv, 4)
-    _need(v_pages, "v_pages", kv, 4)
-    _need(page_table, "page_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _want(q, "q", torch.bfloat16, 3, dev)
+    _want(k_pages, "k_pages", kv, 4, dev)
+    _want(v_pages, "v_pages", kv, 4, dev)
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    _want(seq_lens, "seq_lens", torch.int32, 1, dev)
     if k_pages.shape != v_pages.shape:
         raise ValueError("k_pages and v_pages must have the same shape")
     num_pages, P, H_kv, d = k_pages.shape
     B, H_q, dq = q.shape
-    if dq != d or seq_lens.shape[0] != B or page_table.shape[0] != B:
+    rows, stride = page_table.shape
+    if dq != d or seq_lens.shape[0] != B or rows != B:
         raise ValueError("inconsistent decode shapes")
     sc = ()
     if scales:
-        for t, n in zip(scales, ("k_scale", "v_scale")):
-            _need(t, n, torch.float32)
-            if t.numel() not in (1, H_kv * d) or t.numel() != scales[0].numel():
+        n = scales[0].numel() if isinstance(scales[0], torch.Tensor) else 0
+        for t, nm in zip(scales, ("k_scale", "v_scale")):
+            _want(t, nm, torch.float32, t.dim() if isinstance(t, torch.Tensor) else 1, dev)
+            if t.numel() != n or n not in (1, H_kv * d):
                 raise ValueError("k_scale / v_scale must hold 1 or H_kv * head_dim values each")
-        sc = (scales[0].data_ptr(), scales[1].data_ptr(), int(scales[0].numel() > 1))
-    if max_seq_len is None:
-        max_seq_len = page_table.shape[1] * P
-    if o is None or lse is None:
-        with torch.cuda.stream(stream):
-            o = torch.empty_like(q) if o is None else o
-            lse = torch.empty(B, H_q, dtype=torch.float32, device=q.device) if lse is None else lse
-    _need(o, "o", torch.bfloat16)
-    _need(lse, "lse", torch.float32)
+        sc = (scales[0].data_ptr(), scales[1].data_ptr(), int(n > 1))
+    if o is None:
+        o = _new(q.shape, torch.bfloat16, dev, stream)
+    if lse is None:
+        lse = _new((B, H_q), torch.float32, dev, stream)
+    _want(o, "o", torch.bfloat16, 3, dev)
+    _want(lse, "lse", torch.float32, 2, dev)
     _shape(o, "o", q.shape)
     _shape(lse, "lse", (B, H_q))
-    _need_workspace(workspace, q)
-    _on(q, k_pages, v_pages, page_table, seq_lens, o, lse, *scales)
-    fn = getattr(lib(), name)
-    nbytes = 0 if workspace is not None else cpa_decode_workspace_size(B, H_q, H_kv, d, P)
-    _run(name, q.device, stream, workspace, nbytes, check, lambda ws, n, s: fn(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), *sc, page_table.data_ptr(),
-        page_table.shape[1], seq_lens.data_ptr(), B, H_q, H_kv, d, P, num_pages,
-        int(max_seq_len), int(window), int(sinks), float(d ** -0.5 if sm_scale is None else sm_scale),
-        o.data_ptr(), lse.data_ptr(), ws, n, s))
+    args = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), *sc, page_table.data_ptr(),
+            stride, seq_lens.data_ptr(), B, H_q, H_kv, d, P, num_pages,
+            stride * P if max_seq_len is None else int(max_seq_len), int(window), int(sinks),
+            d ** -0.5 if sm_scale is None else float(sm_scale), o.data_ptr(), lse.data_ptr())
+    _launch(name, args, dev, stream, workspace,
+            lambda: cpa_decode_workspace_size(B, H_q, H_kv, d, P), check)
     return o, lse
 
 
@@ -788,42 +808,36 @@ def cpa_window_prefill(q, k_pages, v_pages, page_table, q_start, seq_lens,
     [T, H_q, 128], the last ones of its ``seq_lens[b]`` tokens.  Returns (o bf16,
     lse fp32); rows that belong to no request are not written.
     """
-    _need(q, "q", torch.bfloat16, 3)
-    _need(k_pages, "k_pages", torch.bfloat16, 4)
-    _need(v_pages, "v_pages", torch.bfloat16, 4)
-    _need(page_table, "page_table", torch.int32, 2)
-    _need(q_start, "q_start", torch.int32, 1)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
+    dev = _device(q, "q", torch.bfloat16)
+    _want(q, "q", torch.bfloat16, 3, dev)
+    _want(k_pages, "k_pages", torch.bfloat16, 4, dev)
+    _want(v_pages, "v_pages", torch.bfloat16, 4, dev)
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    _want(q_start, "q_start", torch.int32, 1, dev)
+    _want(seq_lens, "seq_lens", torch.int32, 1, dev)
     if k_pages.shape != v_pages.shape:
         raise ValueError("k_pages and v_pages must have the same shape")
     num_pages, P, H_kv, d = k_pages.shape
     T, H_q, dq = q.shape
     B = seq_lens.shape[0]
-    if dq != d or q_start.shape[0] != B + 1 or page_table.shape[0] != B:
+    rows, stride = page_table.shape
+    if dq != d or q_start.shape[0] != B + 1 or rows != B:
         raise ValueError("inconsistent prefill shapes")
-    if max_new is None:
-        max_new = T
-    if max_seq_len is None:
-        max_seq_len = page_table.shape[1] * P
-    if o is None or lse is None:
-        with torch.cuda.stream(stream):
-            o = torch.empty_like(q) if o is None else o
-            lse = torch.empty(T, H_q, dtype=torch.float32, device=q.device) if lse is None else lse
-    _need(o, "o", torch.bfloat16)
-    _need(lse, "lse", torch.float32)
+    max_new = T if max_new is None else int(max_new)
+    if o is None:
+        o = _new(q.shape, torch.bfloat16, dev, stream)
+    if lse is None:
+        lse = _new((T, H_q), torch.float32, dev, stream)
+    _want(o, "o", torch.bfloat16, 3, dev)
+    _want(lse, "lse", torch.float32, 2, dev)
     _shape(o, "o", q.shape)
     _shape(lse, "lse", (T, H_q))
-    _need_workspace(workspace, q)
-    _on(q, k_pages, v_pages, page_table, q_start, seq_lens, o, lse)
-    fn = lib().cpa_window_prefill
-    nbytes = 0 if workspace is not None else cpa_window_prefill_workspace_size(
-        B, T, H_q, H_kv, d, P, int(max_new))
-    _run("cpa_window_prefill", q.device, stream, workspace, nbytes, check, lambda ws, n, s: fn(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-        page_table.shape[1], q_start.data_ptr(), seq_lens.data_ptr(), B, T, H_q, H_kv, d, P,
-        num_pages, int(max_new), int(max_seq_len), int(window), int(sinks),
-        float(d ** -0.5 if sm_scale is None else sm_scale), o.data_ptr(), lse.data_ptr(), ws, n,
-        s))
+    args = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), stride,
+            q_start.data_ptr(), seq_lens.data_ptr(), B, T, H_q, H_kv, d, P, num_pages, max_new,
+            stride * P if max_seq_len is None else int(max_seq_len), int(window), int(sinks),
+            d ** -0.5 if sm_scale is None else float(sm_scale), o.data_ptr(), lse.data_ptr())
+    _launch("cpa_window_prefill", args, dev, stream, workspace,
+            lambda: cpa_window_prefill_workspace_size(B, T, H_q, H_kv, d, P, max_new), check)
     return o, lse
 
 
@@ -840,30 +854,29 @@ def cpa_cache_fork(page_table, seq_lens, parents, children, refcounts, page_size
     Returns (copy_src, copy_dst), the page pairs for ``cpa_cache_copy_pages`` (-1, -1 where
     there is none).  ``page_table``, ``seq_lens`` and ``refcounts`` change in place.
     """
-    _need(page_table, "page_table", torch.int32, 2)
-    for t, n in ((seq_lens, "seq_lens"), (parents, "parents"), (children, "children"),
-                 (refcounts, "refcounts")):
-        _need(t, n, torch.int32, 1)
+    dev = _device(page_table, "page_table", torch.int32)
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    _want(seq_lens, "seq_lens", torch.int32, 1, dev)
+    _want(parents, "parents", torch.int32, 1, dev)
+    _want(children, "children", torch.int32, 1, dev)
+    _want(refcounts, "refcounts", torch.int32, 1, dev)
     n_rows, stride = page_table.shape
-    n = parents.shape[0]
+    n, num_pages = parents.shape[0], refcounts.shape[0]
     _shape(seq_lens, "seq_lens", (n_rows,))
     _shape(children, "children", (n,))
-    if copy_src is None or copy_dst is None:
-        with torch.cuda.stream(stream):
-            copy_src = torch.empty_like(parents) if copy_src is None else copy_src
-            copy_dst = torch.empty_like(parents) if copy_dst is None else copy_dst
-    for t, name in ((copy_src, "copy_src"), (copy_dst, "copy_dst")):
-        _need(t, name, torch.int32, 1)
-        _shape(t, name, (n,))
-    _need_workspace(workspace, page_table)
-    _on(page_table, seq_lens, parents, children, refcounts, copy_src, copy_dst)
-    fn, num_pages = lib().cpa_cache_fork, refcounts.shape[0]
-    nbytes = 0 if workspace is not None else cpa_cache_fork_workspace_size(num_pages)
-    _run("cpa_cache_fork", page_table.device, stream, workspace, nbytes, check,
-         lambda ws, nb, s: fn(page_table.data_ptr(), stride, n_rows, seq_lens.data_ptr(),
-                              parents.data_ptr(), children.data_ptr(), n, refcounts.data_ptr(),
-                              int(page_size), num_pages, copy_src.data_ptr(),
-                              copy_dst.data_ptr(), ws, nb, s))
+    if copy_src is None:
+        copy_src = _new((n,), torch.int32, dev, stream)
+    if copy_dst is None:
+        copy_dst = _new((n,), torch.int32, dev, stream)
+    _want(copy_src, "copy_src", torch.int32, 1, dev)
+    _want(copy_dst, "copy_dst", torch.int32, 1, dev)
+    _shape(copy_src, "copy_src", (n,))
+    _shape(copy_dst, "copy_dst", (n,))
+    args = (page_table.data_ptr(), stride, n_rows, seq_lens.data_ptr(), parents.data_ptr(),
+            children.data_ptr(), n, refcounts.data_ptr(), int(page_size), num_pages,
+            copy_src.data_ptr(), copy_dst.data_ptr())
+    _launch("cpa_cache_fork", args, dev, stream, workspace,
+            lambda: cpa_cache_fork_workspace_size(num_pages), check)
     return copy_src, copy_dst
 
 
@@ -871,47 +884,43 @@ def cpa_cache_free(page_table, rows, first, last, refcounts, workspace=None, str
                    check: bool = False) -> None:
     """Give back entries ``first[i] .. last[i]-1`` of row ``rows[i]``: the pages' counts are
     lowered and the entries become -1."""
-    _need(page_table, "page_table", torch.int32, 2)
-    for t, n in ((rows, "rows"), (first, "first"), (last, "last"), (refcounts, "refcounts")):
-        _need(t, n, torch.int32, 1)
+    dev = _device(page_table, "page_table", torch.int32)
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    _want(rows, "rows", torch.int32, 1, dev)
+    _want(first, "first", torch.int32, 1, dev)
+    _want(last, "last", torch.int32, 1, dev)
+    _want(refcounts, "refcounts", torch.int32, 1, dev)
     n_rows, stride = page_table.shape
     n = rows.shape[0]
     _shape(first, "first", (n,))
     _shape(last, "last", (n,))
-    _need_workspace(workspace, page_table)
-    _on(page_table, rows, first, last, refcounts)
-    fn = lib().cpa_cache_free
-    _run("cpa_cache_free", page_table.device, stream, workspace, _STATUS_BYTES, check,
-         lambda ws, nb, s: fn(page_table.data_ptr(), stride, n_rows, rows.data_ptr(),
-                              first.data_ptr(), last.data_ptr(), n, refcounts.data_ptr(),
-                              refcounts.shape[0], ws, nb, s))
+    args = (page_table.data_ptr(), stride, n_rows, rows.data_ptr(), first.data_ptr(),
+            last.data_ptr(), n, refcounts.data_ptr(), refcounts.shape[0])
+    _launch("cpa_cache_free", args, dev, stream, workspace, lambda: _STATUS_BYTES, check)
 
 
 def _any_pools(k_pages, v_pages):
-    """K and V pools of any element type; returns (num_pages, page_size, bytes of one token)."""
+    """K and V pools of any element type; returns (device, num_pages, page_size, bytes of a token)."""
+    dev = _device(k_pages, "k_pages")
     for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _need(t, n, getattr(k_pages, "dtype", None), 4)
+        _want(t, n, k_pages.dtype, 4, dev)
     if k_pages.shape != v_pages.shape:
         raise ValueError("k_pages and v_pages must have the same shape")
     num_pages, P, H_kv, d = k_pages.shape
-    return num_pages, P, H_kv * d * k_pages.element_size()
+    return dev, num_pages, P, H_kv * d * k_pages.element_size()
 
 
 def cpa_cache_copy_pages(k_pages, v_pages, copy_src, copy_dst, workspace=None, stream=None,
                          check: bool = False) -> None:
     """Page ``copy_dst[i]`` of both pools becomes a copy of page ``copy_src[i]``; pairs of two
     -1 are passed over."""
-    num_pages, P, token = _any_pools(k_pages, v_pages)
-    for t, n in ((copy_src, "copy_src"), (copy_dst, "copy_dst")):
-        _need(t, n, torch.int32, 1)
+    dev, num_pages, P, token = _any_pools(k_pages, v_pages)
+    _want(copy_src, "copy_src", torch.int32, 1, dev)
+    _want(copy_dst, "copy_dst", torch.int32, 1, dev)
     _shape(copy_dst, "copy_dst", copy_src.shape)
-    _need_workspace(workspace, k_pages)
-    _on(k_pages, v_pages, copy_src, copy_dst)
-    fn = lib().cpa_cache_copy_pages
-    _run("cpa_cache_copy_pages", k_pages.device, stream, workspace, _STATUS_BYTES, check,
-         lambda ws, nb, s: fn(k_pages.data_ptr(), v_pages.data_ptr(), copy_src.data_ptr(),
-                              copy_dst.data_ptr(), copy_src.shape[0], num_pages, P * token, ws,
-                              nb, s))
+    args = (k_pages.data_ptr(), v_pages.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(),
+            copy_src.shape[0], num_pages, P * token)
+    _launch("cpa_cache_copy_pages", args, dev, stream, workspace, lambda: _STATUS_BYTES, check)
 
 
 def cpa_cache_compact(k_pages, v_pages, src_page_table, src_pos, n_keep, dst_page_table=None,
@@ -921,32 +930,28 @@ def cpa_cache_compact(k_pages, v_pages, src_page_table, src_pos, n_keep, dst_pag
     ``src_rows[b]`` (default b) of ``src_page_table`` goes to position ``dst_start[b] + i`` of row
     b of ``dst_page_table``, for i < ``n_keep[b]``.  Without ``dst_page_table`` the move is within
     the source row, whose positions ascend."""
-    num_pages, P, token = _any_pools(k_pages, v_pages)
-    _need(src_page_table, "src_page_table", torch.int32, 2)
-    _need(src_pos, "src_pos", torch.int32, 2)
-    _need(n_keep, "n_keep", torch.int32, 1)
-    _need(dst_start, "dst_start", torch.int32, 1)
+    dev, num_pages, P, token = _any_pools(k_pages, v_pages)
+    _want(src_page_table, "src_page_table", torch.int32, 2, dev)
+    _want(src_pos, "src_pos", torch.int32, 2, dev)
+    _want(n_keep, "n_keep", torch.int32, 1, dev)
+    _want(dst_start, "dst_start", torch.int32, 1, dev)
     B, max_keep = src_pos.shape
     _shape(n_keep, "n_keep", (B,))
     _shape(dst_start, "dst_start", (B,))
     if src_rows is not None:
-        _need(src_rows, "src_rows", torch.int32, 1)
+        _want(src_rows, "src_rows", torch.int32, 1, dev)
         _shape(src_rows, "src_rows", (B,))
     dst, dst_stride = None, 0
     if dst_page_table is not None:
-        _need(dst_page_table, "dst_page_table", torch.int32, 2)
+        _want(dst_page_table, "dst_page_table", torch.int32, 2, dev)
         if dst_page_table.shape[0] != B:
             raise ValueError("dst_page_table must have a row for each request")
         dst, dst_stride = dst_page_table.data_ptr(), dst_page_table.shape[1]
-    _need_workspace(workspace, k_pages)
-    _on(k_pages, v_pages, src_page_table, src_pos, n_keep, dst_page_table, dst_start, src_rows)
-    fn = lib().cpa_cache_compact
-    _run("cpa_cache_compact", k_pages.device, stream, workspace, _STATUS_BYTES, check,
-         lambda ws, nb, s: fn(k_pages.data_ptr(), v_pages.data_ptr(), src_page_table.data_ptr(),
-                              src_page_table.shape[1], src_page_table.shape[0],
-                              None if src_rows is None else src_rows.data_ptr(),
-                              src_pos.data_ptr(), max_keep, n_keep.data_ptr(), dst, dst_stride,
-                              dst_start.data_ptr(), B, P, num_pages, token, ws, nb, s))
+    args = (k_pages.data_ptr(), v_pages.data_ptr(), src_page_table.data_ptr(),
+            src_page_table.shape[1], src_page_table.shape[0],
+            None if src_rows is None else src_rows.data_ptr(), src_pos.data_ptr(), max_keep,
+            n_keep.data_ptr(), dst, dst_stride, dst_start.data_ptr(), B, P, num_pages, token)
+    _launch("cpa_cache_compact", args, dev, stream, workspace, lambda: _STATUS_BYTES, check)
 
 
 def cpa_get_device_status(workspace: torch.Tensor, stream=None) -> tuple[int, int]:
