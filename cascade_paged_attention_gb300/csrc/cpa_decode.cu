@@ -61,6 +61,7 @@ struct DecodeParams {
     float* part_o;    // [2 n_cta][heads of a unit][128]
     int stride, B, H_q, H_kv, G, chunks, lp, num_pages, max_len, window, sinks, n_cta;
     int per_channel;
+    int wh;         // KV heads of a unit (the first kernel's WH)
     int min_tiles;  // fewest tiles of a block
     float scale_log2;
 };
@@ -70,7 +71,6 @@ struct Cfg {
     static constexpr int kHeads = 8 * NG;            // query heads of a unit
     static constexpr int kBlocks = FP8 ? 2 : 1;      // 16-key blocks of a warp's step
     static constexpr int kKeys = 16 * kBlocks;       // keys of a warp's step: 8 KB of K and V
-    static constexpr int kTile = kKeys * kWarps;     // keys of a block's step
     static constexpr int kRowBytes = FP8 ? 128 : 256;
     static constexpr int kKWords = kRowBytes / 16;   // 32-bit words of a K row in one lane
     static constexpr int kVWords = kRowBytes / 32;   // of a V row
@@ -98,10 +98,10 @@ __device__ __forceinline__ void load32(const uint8_t* ptr, uint32_t* r) {
           "=r"(r[7])
         : "l"(ptr));
 }
-__device__ __forceinline__ void load16(const uint8_t* ptr, uint32_t* r) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+__device__ __forceinline__ void load16(const uint8_t* ptr, uint32_t* r, uint64_t policy) {
+    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.b32 {%0,%1,%2,%3}, [%4], %5;"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "l"(ptr));
+                 : "l"(ptr), "l"(policy));
 }
 
 // d += a (16x16) * b (16x8), fp32 accumulators.
@@ -151,7 +151,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* ws, long
     return base + x - v;
 }
 
-template <bool FP8, int NG>
+template <bool FP8, int NG, int WH>
 __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(DecodeParams p) {
     using C = Cfg<FP8, NG>;
     constexpr int KB = C::kBlocks, KW = C::kKWords, VW = C::kVWords;
@@ -164,13 +164,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int U = p.H_kv * p.chunks;  // units of a request
+    const int wa = warp % WH, wb = warp / WH;          // this warp's head, and its place in the keys
+    constexpr int tile = C::kKeys * (kWarps / WH);    // keys of a block's step
+    const int U = p.H_kv / WH * p.chunks;             // units of a request
     uint32_t bad = 0;
+    const uint64_t once = FP8 ? l2_policy_evict_first() : 0;  // K and V are read once
 
     // ---- this block's range of tiles
     auto unit_tiles = [&](int b) -> int {
         const int n = seen_of(p, __ldg(p.lens + b)).n;
-        return n <= C::kTile ? 1 : (n + C::kTile - 1) / C::kTile;
+        return n <= tile ? 1 : (n + tile - 1) / tile;
     };
     long long total = 0, v0 = 0, ex0 = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
             const Seen see = seen_of(p, __ldg(p.lens + b));
             nt = unit_tiles(b);
             const int j1 = (int)min((long long)nt, (long long)j + left);
-            const int hk = u / p.chunks, chunk = u % p.chunks;
+            const int chunk = u % p.chunks, hk = u / p.chunks * WH + wa;
             const int h0 = chunk * C::kHeads;           // first head of the unit in its group
             const int nh = min(C::kHeads, p.G - h0);    // its heads
             const size_t row0 = (size_t)b * p.H_q + (size_t)hk * p.G + h0;
@@ -267,15 +270,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
             // lane l < kKeys follows key l of the warp's step: its table entry one
             // step ahead of its row, its row one step ahead of its products
             const int n_it = j1 - j;
-            const int v_base = j * C::kTile + warp * C::kKeys + lane;
+            const int v_base = j * tile + wb * C::kKeys + lane;
             auto entry = [&](int it, int& pos) -> int {
-                const int v = v_base + it * C::kTile;
+                const int v = v_base + it * tile;
                 pos = v < see.n_sink ? v : v + see.shift;
                 return (lane < C::kKeys && it < n_it && v < see.n) ? __ldg(trow + (pos >> p.lp))
                                                                   : -1;
             };
             auto to_row = [&](int it, int e, int pos) -> int {
-                const int v = v_base + it * C::kTile;
+                const int v = v_base + it * tile;
                 if (!(lane < C::kKeys && it < n_it && v < see.n)) return -1;
                 if (e < 0 || e >= p.num_pages) {
                     bad |= CPA_DEV_BAD_PAGE;
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
                         const int key = kb * 16 + 2 * c + (i & 1) + (i >> 1) * 8;
                         const int r = max(0, __shfl_sync(0xffffffffu, row, key));
                         const uint8_t* src = vbase + (size_t)r * row_bytes;
-                        if (FP8) load16(src, vr[kb][i]);
+                        if (FP8) load16(src, vr[kb][i], once);
                         else load32(src, vr[kb][i]);
                     }
             };
@@ -473,17 +476,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
             __syncthreads();
             const bool split = j > 0 || j1 < nt;
             const size_t slot = 2 * (size_t)blockIdx.x + (j > 0 ? 0 : 1);
-            for (int x = tid; x < C::kHeads * 16; x += kThreads) {
-                const int head = x >> 4, d = (x & 15) * 8;
+            for (int x = tid; x < WH * C::kHeads * 16; x += kThreads) {
+                const int a = x / (C::kHeads * 16), head = (x >> 4) % C::kHeads, d = (x & 15) * 8;
                 if (head >= nh) continue;
+                const int hka = u / p.chunks * WH + a;
+                const size_t row = (size_t)b * p.H_q + (size_t)hka * p.G + h0 + head;
                 float mx = ninf_f();
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][head]);
+                for (int w = a; w < kWarps; w += WH) mx = fmaxf(mx, sm_m[w][head]);
                 float sum = 0.f, acc[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[i] = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
+                for (int w = a; w < kWarps; w += WH) {
                     const float mw = sm_m[w][head];
                     const float f = mw == ninf_f() ? 0.f : ex2(mw - mx);
                     sum += f * sm_l[w][head];
@@ -504,18 +509,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     acc[i] *= inv;
-                    if (FP8) acc[i] *= __ldg(p.v_scale + (p.per_channel ? hk * 128 + d + i : 0));
+                    if (FP8) acc[i] *= __ldg(p.v_scale + (p.per_channel ? hka * 128 + d + i : 0));
                 }
                 if (split) {
-                    float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * C::kHeads + head) * 128 + d);
+                    float4* dst = reinterpret_cast<float4*>(p.part_o + ((slot * WH + a) * C::kHeads + head) * 128 + d);
                     dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
                     dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-                    if (d == 0) p.part_lse[slot * C::kHeads + head] = lse2;
+                    if (d == 0) p.part_lse[(slot * WH + a) * C::kHeads + head] = lse2;
                 } else {
-                    *reinterpret_cast<uint4*>(p.o + (row0 + head) * 128 + d) =
+                    *reinterpret_cast<uint4*>(p.o + row * 128 + d) =
                         make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
                                    pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
-                    if (d == 0) p.lse[row0 + head] = lse2 == ninf_f() ? lse2 : lse2 * kLn2;
+                    if (d == 0) p.lse[row] = lse2 == ninf_f() ? lse2 : lse2 * kLn2;
                 }
             }
             __syncthreads();
@@ -543,14 +548,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
 
 // Joins the unit that starts in block c's range and goes on past its end: its
 // parts are block c's second slot and the first slots of the blocks after it.
-// Warp w joins heads w, w + 8; a lane holds 4 dimensions.  Block 0 also gathers
-// what the first kernel's blocks found wrong into the status word, which
-// therefore needs no clearing.
+// grid (blocks, heads of a unit / 8), a warp per head, a lane per 4 dimensions.
+// Block (0, 0) also gathers what the first kernel's blocks found wrong into the
+// status word, which therefore needs no clearing.
 template <int NG>
 __global__ void __launch_bounds__(256) join_kernel(DecodeParams p) {
     constexpr int NH = 8 * NG;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
         uint32_t bad = 0;
         for (int i = threadIdx.x; i < p.n_cta; i += 256) bad |= __ldcg(p.bad + i);
         uint32_t all = __syncthreads_or((int)(bad & CPA_DEV_BAD_PAGE)) ? CPA_DEV_BAD_PAGE : 0u;
@@ -559,52 +564,76 @@ __global__ void __launch_bounds__(256) join_kernel(DecodeParams p) {
     }
     const int2 desc = __ldcg(p.desc + blockIdx.x);
     if (desc.x < 0) return;
-    const int U = p.H_kv * p.chunks;
+    const int U = p.H_kv / p.wh * p.chunks;
     const int b = desc.x / U, u = desc.x % U, np = desc.y;
-    const int hk = u / p.chunks, h0 = (u % p.chunks) * NH;
-    const int nh = min(NH, p.G - h0);
+    const int h0 = (u % p.chunks) * NH;
     const int lane = threadIdx.x & 31;
-    const size_t s0 = 2 * (size_t)blockIdx.x + 1, s1 = 2 * (size_t)blockIdx.x;
-    for (int head = threadIdx.x >> 5; head < nh; head += 8) {
-        // slot of part i: s0 for the first, s1 + 2 i after
-        float mx = ninf_f();
-        for (int i = lane; i < np; i += 32)
-            mx = fmaxf(mx, __ldcg(p.part_lse + (i ? s1 + 2 * i : s0) * NH + head));
+    const int x = blockIdx.y * 8 + (threadIdx.x >> 5), nw = p.wh * NH;  // head of the slot
+    const int a = x / NH, head = x % NH;
+    if (head >= p.G - h0) return;
+    // row of part i: block c's second slot for the first, the first slots of the
+    // blocks after it for the others
+    const size_t base = 2 * (size_t)blockIdx.x;
+    auto row_of = [&](int i) -> size_t { return (i ? base + 2 * i : base + 1) * nw + x; };
+    float m = ninf_f(), sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < np; i0 += 8) {  // eight parts' loads in flight at a time
+        float4 y[8];
+        float z[8], mx = m;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float r = mx == ninf_f() ? 0.f : mx;
-        float sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < np; ++i) {
-            const size_t at = (i ? s1 + 2 * i : s0) * NH + head;
-            const float w = ex2(__ldcg(p.part_lse + at) - r);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * 128) + lane);
-            sum += w;
-            acc.x += w * x.x;
-            acc.y += w * x.y;
-            acc.z += w * x.z;
-            acc.w += w * x.w;
+        for (int i = 0; i < 8; ++i) {
+            const size_t at = row_of(min(i0 + i, np - 1));
+            y[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * 128) + lane);
+            z[i] = __ldcg(p.part_lse + at);
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const size_t row = (size_t)b * p.H_q + (size_t)hk * p.G + h0 + head;
-        reinterpret_cast<uint2*>(p.o + row * 128)[lane] =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (lane == 0) p.lse[row] = sum == 0.f ? ninf_f() : (r + lg2(sum)) * kLn2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i0 + i >= np) z[i] = ninf_f();
+            mx = fmaxf(mx, z[i]);
+        }
+        const float r = mx == ninf_f() ? 0.f : mx, f = ex2(m - r);
+        sum *= f;
+        acc.x *= f;
+        acc.y *= f;
+        acc.z *= f;
+        acc.w *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i0 + i >= np) break;
+            const float w = ex2(z[i] - r);
+            sum += w;
+            acc.x += w * y[i].x;
+            acc.y += w * y[i].y;
+            acc.z += w * y[i].z;
+            acc.w += w * y[i].w;
+        }
+        m = mx;
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t row = (size_t)b * p.H_q + (size_t)(u / p.chunks * p.wh + a) * p.G + h0 + head;
+    reinterpret_cast<uint2*>(p.o + row * 128)[lane] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0)
+        p.lse[row] = sum == 0.f ? ninf_f() : ((m == ninf_f() ? 0.f : m) + lg2(sum)) * kLn2;
 }
 
 // Groups of up to 8 query heads fill one operand of N = 8; wider ones take two
 // at a time, so K and V are read ceil(G / 16) times.
 int groups_of(int G) { return G <= 8 ? 1 : 2; }
 
+// KV heads that a block's warps take side by side.  A row of one head is 128 bytes
+// in FP8 pages: two heads together read 256 contiguous bytes (109 -> 101 us for 64
+// requests of 512 to 8192 tokens; four heads: 102).  In bf16 pages a row is 256 bytes
+// by itself, and two heads only mean more parts to join (84.6 -> 85.7 us).
+int heads_of(bool fp8, int H_kv) { return fp8 && H_kv % 2 == 0 ? 2 : 1; }
+
 int blocks_of(int G, int n_sm) { return n_sm * (groups_of(G) == 1 ? 3 : 2); }
 
 struct DecodeWs {
     size_t bad, desc, part_lse, part_o, total;
 };
-DecodeWs decode_ws(int G, int n_cta) {
-    const size_t slots = 2 * (size_t)n_cta * 8 * groups_of(G);
+DecodeWs decode_ws(int G, int wh, int n_cta) {
+    const size_t slots = 2 * (size_t)n_cta * wh * 8 * groups_of(G);
     DecodeWs w;
     w.bad = kStatusBytes;
     w.desc = align_up(w.bad + (size_t)n_cta * 4, 256);
@@ -614,16 +643,16 @@ DecodeWs decode_ws(int G, int n_cta) {
     return w;
 }
 
-template <bool FP8, int NG>
+template <bool FP8, int NG, int WH>
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
-    decode_kernel<FP8, NG><<<p.n_cta, kThreads, 0, stream>>>(p);
+    decode_kernel<FP8, NG, WH><<<p.n_cta, kThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.n_cta);
+    cfg.gridDim = dim3((unsigned)p.n_cta, (unsigned)(p.wh * NG));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cfg.attrs = at;
@@ -662,7 +691,8 @@ cpa_status decode_common(const void* q, const void* k_pages, const void* v_pages
     if (n_sm <= 0) return CPA_ERR_CUDA;
     DecodeParams p = {};
     p.n_cta = blocks_of(G, n_sm);
-    const DecodeWs w = decode_ws(G, p.n_cta);
+    p.wh = heads_of(fp8, H_kv);
+    const DecodeWs w = decode_ws(G, p.wh, p.n_cta);
     if (workspace_bytes < w.total) return CPA_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.status = reinterpret_cast<uint32_t*>(ws);
@@ -693,12 +723,14 @@ cpa_status decode_common(const void* q, const void* k_pages, const void* v_pages
     p.sinks = sinks;
     p.min_tiles = 1;
     p.scale_log2 = sm_scale * kLog2e;
+    const bool one = groups_of(G) == 1;
     cudaError_t e;
-    if (fp8)
-        e = groups_of(G) == 1 ? launch_decode<true, 1>(p, stream) : launch_decode<true, 2>(p, stream);
+    if (!fp8)
+        e = one ? launch_decode<false, 1, 1>(p, stream) : launch_decode<false, 2, 1>(p, stream);
+    else if (p.wh == 2)
+        e = one ? launch_decode<true, 1, 2>(p, stream) : launch_decode<true, 2, 2>(p, stream);
     else
-        e = groups_of(G) == 1 ? launch_decode<false, 1>(p, stream)
-                              : launch_decode<false, 2>(p, stream);
+        e = one ? launch_decode<true, 1, 1>(p, stream) : launch_decode<true, 2, 1>(p, stream);
     return e == cudaSuccess ? CPA_OK : CPA_ERR_LAUNCH;
 }
 
@@ -715,7 +747,7 @@ size_t cpa_decode_workspace_size(int B, int H_q, int H_kv, int head_dim, int pag
     const int n_sm = sm_count();
     if (n_sm <= 0) return 0;
     const int G = H_q / H_kv;
-    return decode_ws(G, blocks_of(G, n_sm)).total;
+    return decode_ws(G, heads_of(true, H_kv), blocks_of(G, n_sm)).total;  // (either call's)
 }
 
 cpa_status cpa_decode(const void* q, const void* k_pages, const void* v_pages,
