@@ -12,7 +12,7 @@ namespace cpa {
 namespace {
 
 constexpr int kForkThreads = 256;
-constexpr int kChunkPages = 4096;  // pages of one word group of the free-page map
+constexpr int kChunkPages = 1024;  // pages of a chunk of the free-page map
 constexpr int kChunkWords = kChunkPages / 32;
 
 __device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) { atomicOr(status, bit); }
@@ -42,22 +42,30 @@ __device__ __forceinline__ int scan_block(int v, int* ws, int& total) {
 
 // ---------------------------------------------------------------- fork
 // A fork runs as two kernels: this one takes down which pages are free (a bit
-// per page, and a count per chunk of 4096 pages) before the second changes any
-// count, so that every child finds its page without waiting for another.
+// per page, and a count per chunk of 1024 pages, a block each with one load a lane
+// in flight per word) before the second changes any count, so that every child
+// finds its page without waiting for another.  The second is launched while the
+// first runs and waits for it on the device.
 __global__ void __launch_bounds__(kForkThreads)
     free_map_kernel(const int32_t* __restrict__ refcounts, int num_pages, uint32_t* map,
                     int32_t* chunk_free, uint32_t* status) {
     __shared__ int ws[kForkThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
+    constexpr int kPerWarp = kChunkWords / (kForkThreads / 32);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long base = (long long)blockIdx.x * kChunkPages;
-    int mine = 0;
-    for (int w = warp; w < kChunkWords; w += kForkThreads / 32) {
-        const long long pg = base + w * 32 + lane;
-        const bool is_free = pg < num_pages && __ldg(refcounts + pg) == 0;
-        const uint32_t bits = __ballot_sync(0xffffffffu, is_free);
+    int count[kPerWarp], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPerWarp; ++i) {
+        const long long pg = base + (warp * kPerWarp + i) * 32 + lane;
+        count[i] = pg < num_pages ? __ldg(refcounts + pg) : 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kPerWarp; ++i) {
+        const uint32_t bits = __ballot_sync(0xffffffffu, count[i] == 0);
         if (lane == 0) {
-            map[(size_t)blockIdx.x * kChunkWords + w] = bits;
+            map[(size_t)blockIdx.x * kChunkWords + warp * kPerWarp + i] = bits;
             mine += __popc(bits);
         }
     }
@@ -74,8 +82,8 @@ struct ForkParams {
     int32_t* refcounts;
     int32_t* copy_src;
     int32_t* copy_dst;
-    const uint32_t* map;
-    const int32_t* chunk_free;
+    const uint32_t* map;         // written by the kernel before (not through the
+    const int32_t* chunk_free;   // read-only cache)
     uint32_t* status;
     int stride, n_rows, n, P, num_pages, n_chunks;
 };
@@ -97,6 +105,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p) {
     __shared__ int ws[kForkThreads / 32];
     __shared__ int found;
     const int i = blockIdx.x, tid = threadIdx.x;
+    // (what the first kernel does not write is read before it is done)
     const int r = __ldg(p.parents + i), c = __ldg(p.children + i);
     bool ok = r >= 0 && r < p.n_rows && c >= 0 && c < p.n_rows;
     // is this child named twice, or a parent of this call?
@@ -104,6 +113,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p) {
     for (int j = tid; j < p.n; j += kForkThreads)
         twice |= (j != i && __ldg(p.children + j) == c) || __ldg(p.parents + j) == c;
     ok = !__syncthreads_or(twice || !ok);
+    // nothing is changed before the map is complete
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!ok) {
         if (tid == 0) {
             flag(p.status, CPA_DEV_BAD_ROW);
@@ -135,7 +146,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p) {
         int passed = 0, chunk = -1;
         for (int k0 = 0; k0 < p.n_chunks && chunk < 0; k0 += kForkThreads) {
             const int k = k0 + tid;
-            const int v = k < p.n_chunks ? __ldg(p.chunk_free + k) : 0;
+            const int v = k < p.n_chunks ? __ldcg(p.chunk_free + k) : 0;
             int sum;
             const int at = passed + scan_block(v, ws, sum);
             if (at <= rank && rank < at + v) found = k;
@@ -155,7 +166,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p) {
         if (chunk >= 0) {
             const int want = rank - passed;
             const uint32_t bits =
-                tid < kChunkWords ? __ldg(p.map + (size_t)chunk * kChunkWords + tid) : 0u;
+                tid < kChunkWords ? __ldcg(p.map + (size_t)chunk * kChunkWords + tid) : 0u;
             int sum;
             const int at = scan_block(__popc(bits), ws, sum);
             if (at <= want && want < at + __popc(bits)) {
@@ -406,7 +417,7 @@ ForkWs fork_ws(int num_pages) {
     w.n_chunks = (num_pages + kChunkPages - 1) / kChunkPages;
     w.chunk_free = kStatusBytes;
     w.map = align_up(w.chunk_free + (size_t)w.n_chunks * 4, 256);
-    w.total = align_up(w.map + (size_t)w.n_chunks * kChunkWords * 4, 256);
+    w.total = w.map + align_up((size_t)w.n_chunks * kChunkWords * 4, 512);
     return w;
 }
 
@@ -478,8 +489,16 @@ cpa_status cpa_cache_fork(int32_t* page_table, int pt_stride, int n_rows, int32_
         reinterpret_cast<int32_t*>(ws + w.chunk_free), p.status);
     const cpa_status st = launched();
     if (st != CPA_OK) return st;
-    fork_kernel<<<n, kForkThreads, 0, s>>>(p);
-    return launched();
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)n);
+    cfg.blockDim = dim3(kForkThreads);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fork_kernel, p) == cudaSuccess ? CPA_OK : CPA_ERR_LAUNCH;
 }
 
 cpa_status cpa_cache_free(int32_t* page_table, int pt_stride, int n_rows, const int32_t* rows,
