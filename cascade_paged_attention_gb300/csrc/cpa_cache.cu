@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(256)
 }
 
 struct CompactParams {
-    uint8_t* pools[2];
+    uint8_t* k_pages;
+    uint8_t* v_pages;
     const int32_t* src_table;
     const int32_t* src_rows;
     const int32_t* src_pos;
@@ -346,23 +347,25 @@ __global__ void __launch_bounds__(256) compact_kernel(CompactParams p) {
         const long long d = slot_of(p, p.dst_table + (size_t)b * p.dst_stride, p.dst_stride,
                                     (long long)__ldg(p.dst_start + b) + i);
         if (s < 0 || d < 0) continue;
-        for (int e0 = 0; e0 < 2 * p.token16; e0 += 32 * kUnroll) {
-            uint4 x[kUnroll];
+        const size_t from = (size_t)s * p.token16, to = (size_t)d * p.token16;
+        const uint4* ks = reinterpret_cast<const uint4*>(p.k_pages) + from;
+        const uint4* vs = reinterpret_cast<const uint4*>(p.v_pages) + from;
+        uint4* kd = reinterpret_cast<uint4*>(p.k_pages) + to;
+        uint4* vd = reinterpret_cast<uint4*>(p.v_pages) + to;
+        for (int e0 = lane; e0 < p.token16; e0 += 32 * kUnroll / 2) {
+            uint4 x[kUnroll / 2], y[kUnroll / 2];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int e = e0 + u * 32 + lane, v = e >= p.token16;
-                if (e < 2 * p.token16)
-                    x[u] = __ldcs(reinterpret_cast<const uint4*>(p.pools[v]) +
-                                  s * p.token16 + (e - v * p.token16));
-            }
+            for (int u = 0; u < kUnroll / 2; ++u)
+                if (e0 + u * 32 < p.token16) {
+                    x[u] = __ldcs(ks + e0 + u * 32);
+                    y[u] = __ldcs(vs + e0 + u * 32);
+                }
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int e = e0 + u * 32 + lane, v = e >= p.token16;
-                if (e < 2 * p.token16)
-                    __stcs(reinterpret_cast<uint4*>(p.pools[v]) + d * p.token16 +
-                               (e - v * p.token16),
-                           x[u]);
-            }
+            for (int u = 0; u < kUnroll / 2; ++u)
+                if (e0 + u * 32 < p.token16) {
+                    __stcs(kd + e0 + u * 32, x[u]);
+                    __stcs(vd + e0 + u * 32, y[u]);
+                }
         }
     }
 }
@@ -376,8 +379,9 @@ __global__ void __launch_bounds__(128) compact_in_place_kernel(CompactParams p) 
     const int e = blockIdx.y * blockDim.x + threadIdx.x;
     int row, keep;
     if (e >= 2 * p.token16 || !compact_row(p, b, row, keep)) return;
-    const int v = e >= p.token16;
-    uint4* pool = reinterpret_cast<uint4*>(p.pools[v]) + (e - v * p.token16);
+    const bool v = e >= p.token16;
+    uint4* pool = v ? reinterpret_cast<uint4*>(p.v_pages) + (e - p.token16)
+                    : reinterpret_cast<uint4*>(p.k_pages) + e;
     const int32_t* trow = p.src_table + (size_t)row * p.src_stride;
     const int32_t* pos = p.src_pos + (size_t)b * p.max_keep;
     const long long start = __ldg(p.dst_start + b);
@@ -564,8 +568,8 @@ cpa_status cpa_cache_compact(void* k_pages, void* v_pages, const int32_t* src_ta
     const int n_sm = sm_count();
     if (n_sm <= 0) return CPA_ERR_CUDA;
     CompactParams p;
-    p.pools[0] = static_cast<uint8_t*>(k_pages);
-    p.pools[1] = static_cast<uint8_t*>(v_pages);
+    p.k_pages = static_cast<uint8_t*>(k_pages);
+    p.v_pages = static_cast<uint8_t*>(v_pages);
     p.src_table = src_table;
     p.src_rows = src_rows;
     p.src_pos = src_pos;
@@ -586,8 +590,11 @@ cpa_status cpa_cache_compact(void* k_pages, void* v_pages, const int32_t* src_ta
         if (grid.y > 65535u) return CPA_ERR_UNSUPPORTED;
         compact_in_place_kernel<<<grid, 128, 0, s>>>(p);
     } else {
+        // a warp per token, in more blocks than run at a time: those of short requests
+        // end at once (78.3 us with 4 blocks an SM, 72.1 with 8, 71.3 with 64, for 400
+        // MB read and written)
         long long blocks = ((long long)B * max_keep + 7) / 8;
-        if (blocks > (long long)n_sm * 8) blocks = (long long)n_sm * 8;
+        if (blocks > (long long)n_sm * 64) blocks = (long long)n_sm * 64;
         compact_kernel<<<(unsigned)blocks, 256, 0, s>>>(p);
     }
     return launched();
