@@ -229,7 +229,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
             const uint8_t* vbase = p.v_pages + (size_t)hk * C::kRowBytes + g * (C::kRowBytes / 8);
 
             // Q: head g (and g + 8) of the unit, the dimensions of this lane's K words
+            // (FP8: q x k_scale as two f16 terms, because one alone would leave 2^-12 of
+            // every product in the scores; the second waits in this warp's part of sm_o,
+            // which is free until the output)
             uint32_t qf[NG][16];
+            uint4* q_low = reinterpret_cast<uint4*>(&sm_o[warp][0][0]) + lane;
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const bool on = n * 8 + g < nh;
@@ -241,18 +245,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
                     const int at = FP8 ? 4 * c + i : (i >> 1) * 8 + 2 * c + (i & 1);
                     const uint4 w = on ? __ldg(src + at) : make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t low[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t x = ww[e];
                         if (FP8) {
                             const int d = at * 8 + 2 * e + (p.per_channel ? hk * 128 : 0);
-                            const float s0 = __ldg(p.k_scale + (p.per_channel ? d : 0));
-                            const float s1 = __ldg(p.k_scale + (p.per_channel ? d + 1 : 0));
-                            x = pack_f16x2(__uint_as_float(x << 16) * s0,
-                                           __uint_as_float(x & 0xFFFF0000u) * s1);
+                            const float x0 = __uint_as_float(x << 16) *
+                                             __ldg(p.k_scale + (p.per_channel ? d : 0));
+                            const float x1 = __uint_as_float(x & 0xFFFF0000u) *
+                                             __ldg(p.k_scale + (p.per_channel ? d + 1 : 0));
+                            const __half2 hi = __floats2half2_rn(x0, x1);
+                            x = *reinterpret_cast<const uint32_t*>(&hi);
+                            low[e] = pack_f16x2(x0 - __low2float(hi), x1 - __high2float(hi));
                         }
                         qf[n][4 * i + e] = x;
                     }
+                    if (FP8) q_low[(n * 4 + i) * 32] = make_uint4(low[0], low[1], low[2], low[3]);
                 }
             }
 
@@ -341,8 +350,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
                             a3 = kr[kb][1][(2 * ks + 1) % KW];
                         }
 #pragma unroll
-                        for (int n = 0; n < NG; ++n)
+                        for (int n = 0; n < NG; ++n) {
                             mma<FP8>(s[kb][n], a0, a1, a2, a3, qf[n][2 * ks], qf[n][2 * ks + 1]);
+                            if (FP8) {
+                                const uint2 ql = reinterpret_cast<const uint2*>(
+                                    q_low + (n * 4 + ks / 2) * 32)[ks & 1];
+                                mma<FP8>(s[kb][n], a0, a1, a2, a3, ql.x, ql.y);
+                            }
+                        }
                     }
                 }
                 // the next step's rows, and its K into the registers just read

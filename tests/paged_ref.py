@@ -26,7 +26,8 @@ D = 128
 U_BF16 = 2.0 ** -8
 E_P_BF16 = 2.0 ** -8      # a weight rounded to bf16
 E_P_SPLIT = 2.0 ** -15    # a weight held as two bf16 terms
-E_F16 = 2.0 ** -11        # a weight, or an element of q x k_scale, rounded to f16
+E_F16 = 2.0 ** -11        # a weight rounded to f16
+E_Q_SPLIT = 2.0 ** -20    # an element of q x k_scale held as two f16 terms
 
 
 def gen(seed, device="cuda"):

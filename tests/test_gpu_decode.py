@@ -48,7 +48,7 @@ def check(lens, H_q, H_kv, P, window=0, sinks=0, seed=0, fp8=False, per_channel=
         K = ref.dense(k, full[b], L, P, ks)
         V = ref.dense(v, full[b], L, P, vs)
         want = ref.attend(q[b:b + 1], K, V, masks[b][None], 128 ** -0.5,
-                          ref.E_F16 if fp8 else ref.E_P_SPLIT, ref.E_F16 if fp8 else 0.0)
+                          ref.E_F16 if fp8 else ref.E_P_SPLIT, ref.E_Q_SPLIT if fp8 else 0.0)
         ref.close(o[b:b + 1], lse[b:b + 1], want)
 
 
