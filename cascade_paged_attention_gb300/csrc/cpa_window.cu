@@ -34,10 +34,11 @@
 // a second kernel in the order of its parts.
 //
 // Values that are not numbers.  A masked key has weight 0, but 0 times a NaN in V
-// is a NaN in a matrix product.  A row whose result is not finite is therefore
-// done again, key by key over what it sees, by its warp: exact, slow, and never
-// taken by finite caches.  (Slots past a sequence's end may hold anything: their
-// V rows are cleared in shared memory.)
+// is a NaN in a matrix product.  A row whose weights are finite and whose result is
+// not is therefore done again, key by key over what it sees, by its warp: exact,
+// slow (hundreds of times when every row of a call is), and never taken by finite
+// caches.  (Slots past a sequence's end may hold anything: their V rows are cleared
+// in shared memory.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -935,7 +936,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 }
                 tc_fence_before_sync();  // O may be written again after this warp's next P
                 __syncwarp();
-                uint32_t again = __ballot_sync(0xffffffffu, active && !isfinite(check));
+                // (a sum that is not a number comes from a seen score: the row's result is
+                // that, in every column)
+                uint32_t again =
+                    __ballot_sync(0xffffffffu, active && isfinite(l) && !isfinite(check));
                 for (; again != 0u; again &= again - 1u) {
                     const int src = __ffs((int)again) - 1;
                     const size_t row_a = (size_t)__shfl_sync(0xffffffffu, row, src);
