@@ -320,6 +320,13 @@ struct Walker {
 
 static_assert(kOffWalk + 8 * sizeof(Walker) <= kOffQ, "control block");
 
+// The next piece of a walker in shared memory: one lane walks.
+__device__ __forceinline__ void advance(Walker& w, const WindowParams& p) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) w.next(p);
+    __syncwarp();
+}
+
 // 128 TMEM columns of this warp's lanes, loaded and waited for.
 #define W8(i) "=r"(r[i + 0]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
               "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
@@ -729,17 +736,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             uint32_t spar = 0, opar = 0;
             long long g = 0;  // key tiles of this block so far (V's ring)
             bool ok = true;
-            // The walk of this warp, in shared memory: registers are for the scores.  (All
-            // lanes write the same values.)
+            // the walk of this warp, in shared memory: registers are for the scores
             Walker& w = reinterpret_cast<Walker*>(smem + kOffWalk)[warp];
-            w.init(p, ctrl);
+            if (lane == 0) w.init(p, ctrl);
             __syncwarp();
             while (w.more() && ok) {
                 const Unit& xs = w.x;
                 if (mt >= w.tiles_q(p)) {
                     g += w.j1 - w.j0;
-                    w.next(p);
-                    __syncwarp();
+                    advance(w, p);
                     continue;
                 }
                 const int tok = mt * p.TSB + it;
@@ -866,9 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 // walk goes on first, while the last products run.
                 const Unit x = w.x;
                 const int j0 = w.j0, j1 = w.j1;
-                __syncwarp();
-                w.next(p);
-                __syncwarp();
+                advance(w, p);
                 ok = wait_warp(&ctrl->o_full[mt], opar, abort_flag, bad_word);
                 if (!ok) break;
                 opar ^= 1u;
