@@ -31,11 +31,15 @@ import cpa_synth  # noqa: E402
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--case", choices=["cascade", "naive", "pass_a", "pass_b", "prefill", "tree",
-                                       "tree_pass_b", "shared", "cascade_fp8"],
+                                       "tree_pass_b", "shared", "cascade_fp8", "decode",
+                                       "decode_fp8", "window", "copy_pages"],
                     default="cascade")
     ap.add_argument("--config", default="pages_example")
     ap.add_argument("--hit", type=float, default=0.5, help="prefill: cached fraction h")
     ap.add_argument("--scales", default="channel", help="cascade_fp8: tensor or channel")
+    ap.add_argument("--window", type=int, default=0,
+                    help="decode, decode_fp8, window: the last tokens seen (0: all)")
+    ap.add_argument("--sinks", type=int, default=0, help="the first tokens that stay seen")
     ap.add_argument("--batch", type=int, default=0, help="override B")
     ap.add_argument("--warmup", type=int, default=2)
     ap.add_argument("--iters", type=int, default=3)
@@ -70,6 +74,53 @@ def main():
         def call():
             cpa.cpa_prefill_hit(q, kp, vp, pt, wl.B, wl.N, wl.H)
         work = f"prefill B={wl.B} N={wl.N} H={wl.H}: {wl.visible_pairs() * wl.B * wl.H_q} pairs"
+    elif args.case == "window":
+        c = dict(cpa_synth.PREFILL_CONFIG)
+        c.pop("hits")
+        if args.batch:
+            c["B"] = args.batch
+        wl = cpa_synth.make_prefill(H=0, **c)
+        q, kp, vp, pt = bf(wl.q), bf(wl.k_pages), bf(wl.v_pages), i32(wl.page_table)
+        start, lens = i32(np.arange(wl.B + 1) * wl.N), i32(np.full(wl.B, wl.N))
+
+        def call():
+            cpa.cpa_window_prefill(q, kp, vp, pt, start, lens, window=args.window,
+                                   sinks=args.sinks)
+        work = f"B={wl.B} N={wl.N} window={args.window} sinks={args.sinks}"
+    elif args.case in ("decode", "decode_fp8"):
+        cfg = dict(cpa_synth.VERIFY_CONFIGS[args.config], topk=1, S=1)
+        if args.batch:
+            cfg["B"] = args.batch
+        fp8 = args.case == "decode_fp8"
+        wl = cpa_synth.make_verify_fp8(scales=args.scales, **cfg) if fp8 else \
+            cpa_synth.make_verify(**cfg)
+        q, pt, lens = bf(wl.q), i32(wl.prefix_page_table), i32(wl.prefix_lens)
+        kw = dict(max_seq_len=wl.max_prefix_len, window=args.window, sinks=args.sinks)
+        if fp8:
+            kp, vp, ks, vs = (torch.from_numpy(np.ascontiguousarray(a)).to(dev) for a in (
+                wl.k_pages, wl.v_pages, wl.k_scale.astype(np.float32),
+                wl.v_scale.astype(np.float32)))
+
+            def call():
+                cpa.cpa_decode_fp8(q, kp, vp, ks, vs, pt, lens, **kw)
+        else:
+            kp, vp = bf(wl.k_pages), bf(wl.v_pages)
+
+            def call():
+                cpa.cpa_decode(q, kp, vp, pt, lens, **kw)
+        work = (f"{args.config} window={args.window}: KV "
+                f"{int(wl.prefix_lens.sum()) * wl.kv_bytes_per_token() / 1e6:.1f} MB")
+    elif args.case == "copy_pages":
+        cfg = dict(cpa_synth.VERIFY_CONFIGS[args.config])
+        wl = cpa_synth.make_verify(**cfg)
+        kp, vp = bf(wl.k_pages), bf(wl.v_pages)
+        order = np.random.default_rng(1).permutation(wl.num_pages)
+        n = wl.num_pages // 2
+        src, dst = i32(order[:n]), i32(order[n:2 * n])
+
+        def call():
+            cpa.cpa_cache_copy_pages(kp, vp, src, dst)
+        work = f"{n} pages, {2 * 2 * n * kp[0].numel() * 2 / 1e6:.1f} MB read and written"
     elif args.case == "cascade_fp8":
         cfg = dict(cpa_synth.VERIFY_CONFIGS[args.config])
         if args.batch:
