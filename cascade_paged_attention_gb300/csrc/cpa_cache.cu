@@ -587,7 +587,6 @@ cpa_status cpa_cache_compact(void* k_pages, void* v_pages, const int32_t* src_ta
     p.token16 = (int)(token_bytes / 16);
     if (!dst_table) {
         const dim3 grid((unsigned)B, (unsigned)((2 * p.token16 + 127) / 128));
-        if (grid.y > 65535u) return CPA_ERR_UNSUPPORTED;
         compact_in_place_kernel<<<grid, 128, 0, s>>>(p);
     } else {
         // a warp per token, in more blocks than run at a time: those of short requests

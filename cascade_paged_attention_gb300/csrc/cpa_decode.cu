@@ -175,40 +175,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
         const int n = seen_of(p, __ldg(p.lens + b)).n;
         return n <= tile ? 1 : (n + tile - 1) / tile;
     };
-    long long total = 0, v0 = 0, ex0 = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        long long v = 0;
-        if (b < p.B) {
-            const int L = __ldg(p.lens + b);
+    // each thread sums a run of requests; one scan over the block follows
+    const int per_thread = (p.B + kThreads - 1) / kThreads, b0 = tid * per_thread;
+    long long mine = 0, total;
+#pragma unroll 4
+    for (int i = 0; i < per_thread; ++i)
+        if (b0 + i < p.B) {
+            const int L = __ldg(p.lens + b0 + i);
             if (L < 0 || L > p.max_len) bad |= CPA_DEV_BAD_LENGTH;
-            v = (long long)U * unit_tiles(b);
+            mine += (long long)U * unit_tiles(b0 + i);
         }
-        long long sum;
-        ex0 = block_scan(v, scan, sum);
-        v0 = v;
-        total += sum;
-    }
+    long long before = block_scan(mine, scan, total);
     long long per = (total + p.n_cta - 1) / p.n_cta;
     if (per < p.min_tiles) per = p.min_tiles;
     const long long t0 = per * blockIdx.x;
     long long left = t0 < total ? min(per, total - t0) : 0;
     int2 desc = make_int2(-1, 0);
     if (left > 0) {
-        long long run = 0;
-        for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-            const int b = b0 + tid;
-            long long v = v0, ex = ex0, sum = total;
-            if (p.B > kThreads) {
-                v = b < p.B ? (long long)U * unit_tiles(b) : 0;
-                ex = block_scan(v, scan, sum);
+        if (before <= t0 && t0 < before + mine) {
+            int b = b0;
+            for (;; ++b) {
+                const long long v = (long long)U * unit_tiles(b);
+                if (t0 < before + v) break;
+                before += v;
             }
-            if (run + ex <= t0 && t0 < run + ex + v) {
-                s_b = b;
-                s_off = t0 - (run + ex);
-            }
-            run += sum;
-            if (run > t0) break;
+            s_b = b;
+            s_off = t0 - before;
         }
         __syncthreads();
         int b = s_b;

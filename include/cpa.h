@@ -41,18 +41,19 @@
  *     workspace; the library never allocates, frees or synchronises (except
  *     cpa_get_device_status and cpa_noalloc_device_status, which say so).
  *     Calls are asynchronous on `stream` (NULL = legacy default stream) and
- *     launch nothing when they return an error, with one exception:
- *     cpa_cascade_verify_shared launches two kernels when its shared prefix
- *     ends inside a page, and checks every argument before the first, so only
- *     CPA_ERR_LAUNCH or CPA_ERR_CUDA from the second launch can follow a
- *     launch already made.
+ *     launch nothing when they return an error, except the calls that launch
+ *     two kernels (cpa_cascade_verify_shared when its shared prefix ends inside
+ *     a page, the cpa_decode calls, cpa_window_prefill, cpa_cache_fork): they
+ *     check every argument before the first, so only CPA_ERR_LAUNCH or
+ *     CPA_ERR_CUDA from the second launch can follow a launch already made.
  *   - Errors: arguments that can be checked on the host return a status
  *     before any launch.  Problems only the GPU can see (a page id outside
  *     [0, num_pages), a prefix length outside [0, max_prefix_len], a pipeline
  *     wait that exceeded its time limit) set bits in a status word at the
  *     start of the workspace, which cpa_get_device_status reads.  Each
  *     workspace-taking call clears that word and the merge counters it uses
- *     (an asynchronous memset on `stream`).  Nothing crosses the ABI as an
+ *     (an asynchronous memset on `stream`) or has its kernels write the word
+ *     whole.  Nothing crosses the ABI as an
  *     exception, and no kernel traps, asserts or prints.
  *   - When the device status word has any bit set after a call, that call's
  *     outputs are undefined (they may be partial, stale or computed from a

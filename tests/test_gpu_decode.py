@@ -219,3 +219,30 @@ def test_agrees_with_cascade_verify_of_one_token():
     # both round o to bf16 once; verify's weights are bf16 (2^-8 each way)
     assert float((o.float() - o2.float()).abs().max()) <= 1e-2
     assert float((lse - lse2).abs().max()) <= 1e-3
+
+
+def test_many_requests_and_a_stream_of_ones_own():
+    """Thousands of short requests (several a thread in the split of the work), on a stream given
+    by argument."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 40, (3001,), generator=g).tolist()
+    q, k, v, _, _, table, dl = make(lens, 8, 2, 8, 41)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o, lse = cpa.cpa_decode(q, k, v, table, dl, stream=side, check=True)
+    torch.cuda.current_stream().wait_stream(side)
+    pos = torch.arange(40, device="cuda")
+    idx = table.long()[:, pos // 8].clamp(min=0)
+    K, V = k[idx, pos % 8].double(), v[idx, pos % 8].double()
+    seen = pos[None] < dl[:, None]
+    x = torch.einsum("bhgd,bjhd->bhgj", q.double().view(-1, 2, 4, 128), K) * 128 ** -0.5
+    x = x.masked_fill(~seen[:, None, None], float("-inf"))
+    want = torch.logsumexp(x, -1)
+    w = torch.exp(x - torch.where(want == float("-inf"), 0.0, want)[..., None])
+    wo = torch.einsum("bhgj,bjhd->bhgd", w, V)
+    none = (dl == 0)
+    assert bool((o[none] == 0).all()) and bool((lse[none] == float("-inf")).all())
+    # half a step of bf16, and weights to 2^-15 (see tests/paged_ref.py)
+    tol = 2.0 ** -8 * wo.abs() + 2.0 ** -14 * torch.einsum("bhgj,bjhd->bhgd", w, V.abs())
+    assert bool(((o.double().view_as(wo) - wo).abs() <= tol).all())
+    assert float((lse.double().view_as(want) - want)[~none].abs().max()) <= 1e-4

@@ -173,3 +173,64 @@ def test_agrees_with_prefill_hit():
     # each within 2^-8 (|o| + sum w |v|) of the exact value, |o| < 1 here
     assert float((o.float() - o2.float()).abs().max()) <= 2e-2
     assert float((lse - lse2).abs().max()) <= 1e-3
+
+
+def test_many_requests_some_long_some_empty():
+    """More requests than threads, lengths from none to several units, on a stream given by
+    argument; rows of the reference by the decode call, whose keys a last token sees alike."""
+    g = torch.Generator().manual_seed(5)
+    n = 1100
+    news = [int(x) for x in torch.randint(0, 4, (n,), generator=g)]
+    news[700] = 900
+    news[3] = 300
+    lens = [m + int(x) for m, x in zip(news, torch.randint(0, 60, (n,), generator=g))]
+    q, k, v, table, qs, dl, start = make(news, lens, 8, 2, 8, 6)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o, lse = cpa.cpa_window_prefill(q, k, v, table, qs, dl, window=50, sinks=2, stream=side, check=True)
+    torch.cuda.current_stream().wait_stream(side)
+    # the last token of each request that has one
+    some = torch.tensor([b for b in range(n) if news[b]], device="cuda")
+    last = (qs[1:].long() - 1)[some]
+    o1, lse1 = cpa.cpa_decode(q[last], k, v, table[some].contiguous(), dl[some].contiguous(), window=50,
+                              sinks=2, check=True)
+    # weights to 2^-8 here, to 2^-15 there; |o| and the mean |v| stay below 5
+    assert float((o[last].float() - o1.float()).abs().max()) <= 3 * 2.0 ** -8 * 5
+    assert float((lse[last] - lse1).abs().max()) <= 1e-4
+    for b in (3, 700):
+        a, m, L = start[b], news[b], lens[b]
+        want = ref.attend(q[a:a + m], ref.dense(k, table[b], L, 8), ref.dense(v, table[b], L, 8),
+                          ref.seen(range(L - m, L), L, 50, 2, "cuda"), 128 ** -0.5, ref.E_P_BF16)
+        ref.close(o[a:a + m], lse[a:a + m], want)
+
+
+def test_values_that_are_not_numbers_only_where_they_are_seen():
+    """NaN and infinity among K and V, in whole and in cut units: rows that see them have what
+    the definition gives, the others are as if they were not there."""
+    news, lens = [700, 30], [1500, 4000]
+    q, k, v, table, qs, dl, start = make(news, lens, 4, 1, 16, 8)
+    clean = (k.clone(), v.clone())
+    hits = [(0, 900, "v", float("inf")), (0, 1200, "k", float("nan")), (1, 3985, "v", float("nan"))]
+    for b, at, which, x in hits:
+        pool = k if which == "k" else v
+        pool[table[b, at // 16].long(), at % 16, 0, 5] = x
+    o, lse = cpa.cpa_window_prefill(q, k, v, table, qs, dl, window=100, check=True)
+    for b in range(2):
+        a, m, L = start[b], news[b], lens[b]
+        pos = torch.arange(L - m, L, device="cuda")
+        sick = torch.zeros(m, dtype=torch.bool, device="cuda")
+        for hb, at, which, x in hits:
+            if hb != b:
+                continue
+            sees = (pos >= at) & (pos < at + 100)
+            rows = o[a:a + m][sees]
+            if which == "k":
+                assert bool(torch.isnan(rows).all()) and bool(torch.isnan(lse[a:a + m][sees]).all())
+            else:
+                assert bool((~torch.isfinite(rows[:, :, 5])).all())
+                assert bool(torch.isfinite(lse[a:a + m][sees & ~sick]).all())
+            sick |= sees
+        want = ref.attend(q[a:a + m], ref.dense(clean[0], table[b], L, 16),
+                          ref.dense(clean[1], table[b], L, 16),
+                          ref.seen(range(L - m, L), L, 100, 0, "cuda"), 128 ** -0.5, ref.E_P_BF16)
+        ref.close(o[a:a + m][~sick], lse[a:a + m][~sick], [t[~sick] for t in want])
