@@ -17,6 +17,9 @@
 // mma.sync and not tcgen05: with 8 heads as N = 8 and 16 keys as M = 16 nothing
 // is padded for G = 8 and the operands are the loaded registers themselves; the
 // 128-row tile of tcgen05 would have to be fed through shared memory or TMEM.
+// Whole calls: 64 requests of 2000 tokens (32/8 heads, 525 MB) 83.7 us, 0.92 of the
+// measured copy rate; 16 of 1024 to 32768 (64/8 heads, 1.2 GB) 184 us, 0.97; FP8
+// pages, 64 of 512 to 8192 (572 MB) 104 us, 0.81.
 //
 // Split.  The tiles (64 or 128 keys) of all units (request, KV head, up to 8 or
 // 16 of its query heads) are laid end to end and cut into equal ranges, one per
