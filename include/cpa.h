@@ -405,7 +405,8 @@ cpa_status cpa_tree_pass_b(const void* q, const void* k_pages, const void* v_pag
  * The work is split over the visible length and joined, in a fixed order: the
  * result of a call depends on its inputs and the device's SM count alone.
  * Supported: head_dim 128; page_size in {8,16,32,64,128,256}; any H_q that is a
- * multiple of H_kv; k_pages and v_pages 32-byte aligned.
+ * multiple of H_kv; B * H_q up to 2^24; max_seq_len up to 2^30; k_pages and v_pages
+ * 32-byte aligned.
  */
 size_t cpa_decode_workspace_size(int B, int H_q, int H_kv, int head_dim, int page_size);
 
@@ -447,7 +448,10 @@ cpa_status cpa_decode_fp8(const void* q, const void* k_pages, const void* v_page
  *   o, lse      bf16 [T, H_q, head_dim], fp32 [T, H_q]
  * A q_start that is not ascending or leaves [0, T], an m_b above max_new or
  * above seq_lens[b], or a length above max_seq_len sets CPA_DEV_BAD_LENGTH.
- * Supported: head_dim 128; page_size in {8,16,32,64,128,256}; H_q / H_kv <= 128.
+ * A NaN or an infinity in V reaches the rows that see it and no others; a call
+ * with many rows beside such values is exact, and slow.
+ * Supported: head_dim 128; page_size in {8,16,32,64,128,256}; H_q / H_kv <= 128;
+ * T * H_q up to 2^24; max_seq_len up to 2^30.
  */
 size_t cpa_window_prefill_workspace_size(int B, int T, int H_q, int H_kv, int head_dim,
                                          int page_size, int max_new);
@@ -484,7 +488,7 @@ cpa_status cpa_window_prefill(const void* q, const void* k_pages, const void* v_
  *   copy_src, copy_dst int32 [n] on the device, output.
  * With too few free pages (CPA_DEV_NO_PAGE) the children that got none have -1
  * as their last page and their pair; all else is as described, so freeing the
- * row undoes the fork.  n >= 1.
+ * row undoes the fork.  n may be 0.
  */
 size_t cpa_cache_fork_workspace_size(int num_pages);
 
@@ -535,8 +539,8 @@ cpa_status cpa_cache_copy_pages(void* k_pages, void* v_pages, const int32_t* cop
  *   src_pos     int32 [B, max_keep];  n_keep int32 [B], 0 <= n_keep[b] <= max_keep
  *   dst_table   int32 [B, dst_stride], or NULL: the move is within the source
  *               row, whose positions have to be ascending with dst_start[b] + i
- *               <= src_pos[b][i] (a history pruned in place), and no row may be
- *               named twice
+ *               <= src_pos[b][i] (a history pruned in place); no row may be named
+ *               twice, and a page that another sequence holds too changes for both
  *   dst_start   int32 [B] on the device
  *   token_bytes K (or V) of one token: H_kv x head_dim x element size, a
  *               multiple of 16

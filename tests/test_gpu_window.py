@@ -234,3 +234,28 @@ def test_values_that_are_not_numbers_only_where_they_are_seen():
                           ref.dense(clean[1], table[b], L, 16),
                           ref.seen(range(L - m, L), L, 100, 0, "cuda"), 128 ** -0.5, ref.E_P_BF16)
         ref.close(o[a:a + m][~sick], lse[a:a + m][~sick], [t[~sick] for t in want])
+
+
+@pytest.mark.parametrize("M", [1, 40, 129])
+def test_against_the_oracle(M):
+    """The library's own fp64 oracle (plain C) on its seeded workloads, slots past the end NaN."""
+    import numpy as np
+
+    import cpa_synth
+    import oracle
+    from tests.gpu_util import dev_bf16, dev_i32
+
+    wl = cpa_synth.make_prefill(B=3, N=300, H=300 - M, H_q=16, H_kv=4, page_size=32, seed=M,
+                                pad_fill="nan")
+    ref_o, ref_lse = oracle.prefill_wl(wl)
+    kv = (dev_bf16(wl.k_pages), dev_bf16(wl.v_pages), dev_i32(wl.page_table))
+    q, lens = dev_bf16(wl.q), dev_i32([300] * 3)
+    outs = [cpa.cpa_window_prefill(q, *kv, dev_i32(np.arange(4) * M), lens, check=True)]
+    if M == 1:
+        outs.append(cpa.cpa_decode(q, *kv, lens, check=True))
+    for o, lse in outs:
+        o = o.double().cpu().numpy().reshape(ref_o.shape)
+        # half a step of bf16 for the output, as much for the weights: sum w |v| is about 0.8 over
+        # the 170 keys and more that a row sees
+        assert np.all(np.abs(o - ref_o) <= 2.0 ** -8 * (np.abs(ref_o) + 1.0) + 1e-4)
+        assert float(np.abs(lse.double().cpu().numpy().reshape(ref_lse.shape) - ref_lse).max()) <= 1e-4
