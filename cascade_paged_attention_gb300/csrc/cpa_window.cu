@@ -62,14 +62,13 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 256;       // rows of a unit
-constexpr int kKStages = 2, kVStages = 2;
+constexpr int kKStages = 3, kVStages = 2;
 constexpr uint32_t kHalf = 128u * 128u;    // 64 columns of a 128-row tile: 16 KB
 constexpr uint32_t kTileBytes = 2 * kHalf; // 128 rows of 256 bytes
 constexpr uint32_t kOffQ = 1024;
 constexpr uint32_t kOffK = kOffQ + 2 * kTileBytes;
 constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
-constexpr uint32_t kOffOut = kOffV + kVStages * kTileBytes;  // 4 KB a softmax warp
-constexpr uint32_t kSmem = kOffOut + 8 * 4096 + 1024;        // (aligned up inside)
+constexpr uint32_t kSmem = kOffV + kVStages * kTileBytes + 1024;  // (aligned up inside)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // What a unit costs besides its tiles, in tiles: its first scores, masked edge
@@ -388,6 +387,13 @@ __device__ __forceinline__ void tmem_ld_x128(uint32_t taddr, uint32_t (&r)[128])
 
 __device__ __forceinline__ uint32_t bits_below(int n) {
     return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// 32 bytes, 32-byte aligned.
+__device__ __forceinline__ void store32(uint32_t* ptr, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(ptr), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t elect_one() {
@@ -919,54 +925,37 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 const int row = (x.t0 + (active ? tok : 0)) * p.H_q + x.hk * p.G + (active ? gq : 0);
                 float check = lse2 == ninf_f() ? 0.f : lse2;
                 float4* po = p.part_o + slot * 32 * kRows + R;
-                uint8_t* stage = smem + kOffOut + warp * 4096;
-                const int row_or = active ? row : -1;
+                // (a lane writes its own row, 32 bytes at a time: whole sectors.  Through shared
+                // memory 8 lanes would write 128 bytes of a row together, at the same speed
+                // and for 32 KB that the third K stage needs more)
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    // 64 columns; finished rows go through shared memory (32 rows of 128
-                    // bytes, 16-byte chunks swizzled), so that 8 lanes write a row's 128
-                    // bytes together
+                for (int c0 = 0; c0 < 128; c0 += 32) {
+                    uint32_t v[32];
+                    tmem_ld_x32(o_addr + c0, v);
+                    float f[32];
+                    float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int c0 = 0; c0 < 64; c0 += 32) {
-                        uint32_t v[32];
-                        tmem_ld_x32(o_addr + h * 64 + c0, v);
-                        float f[32];
-                        float z[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            f[i] = __uint_as_float(v[i]) * inv;
-                            z[i & 3] = fmaf(f[i], 0.f, z[i & 3]);  // NaN once any is not finite
-                        }
-                        check += (z[0] + z[1]) + (z[2] + z[3]);
-                        if (split) {
-                            if (active)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    po[(size_t)(h * 16 + c0 / 4 + i) * kRows] =
-                                        make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<uint4*>(
-                                    stage + lane * 128 + (((c0 / 8 + i) ^ (lane & 7)) << 4)) =
-                                    make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]),
-                                               pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
-                                               pack_bf16x2(f[8 * i + 4], f[8 * i + 5]),
-                                               pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
-                        }
+                    for (int i = 0; i < 32; ++i) {
+                        f[i] = __uint_as_float(v[i]) * inv;
+                        z[i & 3] = fmaf(f[i], 0.f, z[i & 3]);  // NaN once any is not finite
                     }
-                    if (!split) {
-                        __syncwarp();
+                    check += (z[0] + z[1]) + (z[2] + z[3]);
+                    if (!active) continue;
+                    if (split) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int rr = i * 4 + (lane >> 3), ch = lane & 7;
-                            const int to = __shfl_sync(0xffffffffu, row_or, rr);
-                            const uint4 x4 = *reinterpret_cast<const uint4*>(
-                                stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
-                            if (to >= 0)
-                                reinterpret_cast<uint4*>(p.o + (size_t)to * 128)[h * 8 + ch] = x4;
+                        for (int i = 0; i < 8; ++i)
+                            po[(size_t)(c0 / 4 + i) * kRows] =
+                                make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                    } else {
+                        uint32_t* out = reinterpret_cast<uint32_t*>(p.o + (size_t)row * 128 + c0);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                w[e] = pack_bf16x2(f[16 * i + 2 * e], f[16 * i + 2 * e + 1]);
+                            store32(out + 8 * i, w);
                         }
-                        __syncwarp();
                     }
                 }
                 if (active) {
@@ -1121,7 +1110,7 @@ cpa_status cpa_window_prefill(const void* q, const void* k_pages, const void* v_
         max_seq_len < 0 || window < 0 || sinks < 0)
         return CPA_ERR_INVALID_ARG;
     if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return CPA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o))
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned32(o))
         return CPA_ERR_INVALID_ARG;
     if (head_dim != 128 || !page_size_ok(page_size) || H_q / H_kv > 128)
         return CPA_ERR_UNSUPPORTED;

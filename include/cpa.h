@@ -451,7 +451,7 @@ cpa_status cpa_decode_fp8(const void* q, const void* k_pages, const void* v_page
  * A NaN or an infinity in V reaches the rows that see it and no others; a call
  * with many rows beside such values is exact, and slow.
  * Supported: head_dim 128; page_size in {8,16,32,64,128,256}; H_q / H_kv <= 128;
- * T * H_q up to 2^24; max_seq_len up to 2^30.
+ * T * H_q up to 2^24; max_seq_len up to 2^30; o 32-byte aligned.
  */
 size_t cpa_window_prefill_workspace_size(int B, int T, int H_q, int H_kv, int head_dim,
                                          int page_size, int max_new);
