@@ -704,6 +704,11 @@ def _new(shape, dtype, dev: int, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+# PyTorch's current stream of a device as an integer (the first without making a Stream of it)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _launch(name: str, args, dev: int, stream, workspace, nbytes, check: bool):
     """Call entry point `name` with `args`, workspace and stream on device `dev`.  Without a
     workspace from the caller each call gets its own (`nbytes()` of it), from PyTorch's
@@ -718,7 +723,7 @@ def _launch(name: str, args, dev: int, stream, workspace, nbytes, check: bool):
               and workspace.get_device() == dev and workspace.is_contiguous()):
         _need(workspace, "workspace", torch.uint8)
         raise ValueError("workspace is on another device than the call's tensors")
-    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    raw = _current_stream(dev) if stream is None else stream.cuda_stream
     st = getattr(_lib or lib(), name)(*args, workspace.data_ptr(), workspace.numel(), raw)
     if st != 0:
         raise CpaError(name, st)

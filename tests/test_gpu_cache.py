@@ -195,6 +195,34 @@ def test_compact(P, H_kv, dtype, in_place):
     assert torch.equal(k, want[0]) and torch.equal(v, want[1])
 
 
+def test_compact_of_many_tokens_and_its_report():
+    """Past the size at which one block looks the call over: every warp reports for itself."""
+    g = ref.gen(9)
+    B, span, P = 9, 600, 16
+    keep = [500 - 7 * b for b in range(B)]
+    table, pool = ref.table_of([span] * B + keep, P, g)
+    k, v = ref.pool_of(pool, P, 2, g), ref.pool_of(pool, P, 2, g)
+    src, dst = table[:B].contiguous(), table[B:, :32].contiguous()
+    pos = torch.stack([torch.randperm(span, generator=g, device="cuda")[:500] for _ in range(B)])
+    want = []
+    for x in (k, v):
+        y = x.clone().view(-1, 2, 128)
+        for b in range(B):
+            a, z = pos[b, :keep[b]], torch.arange(keep[b], device="cuda")
+            y[dst[b].long()[z // P] * P + z % P] = x.view(-1, 2, 128)[src[b].long()[a // P] * P + a % P]
+        want.append(y.view_as(x))
+    pos = pos.to(torch.int32).contiguous()
+    cpa.cpa_cache_compact(k, v, src, pos, i32(keep), dst, i32([0] * B), check=True)
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    bad_pos, bad_src = pos.clone(), src.clone()
+    bad_pos[8, 3] = span + 40
+    bad_src[8] = pool
+    for s, p, status in ((src, bad_pos, 8), (bad_src, pos, 5)):
+        with pytest.raises(cpa.CpaError) as e:
+            cpa.cpa_cache_compact(k, v, s, p, i32(keep), dst, i32([0] * B), check=True)
+        assert e.value.status == status
+
+
 def test_compact_reports_bad_calls():
     k = torch.zeros(8, 8, 1, 128, dtype=torch.bfloat16, device="cuda")
     v = torch.zeros_like(k)
