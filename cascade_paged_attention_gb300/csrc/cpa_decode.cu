@@ -19,7 +19,7 @@
 // 128-row tile of tcgen05 would have to be fed through shared memory or TMEM.
 // Whole calls: 64 requests of 2000 tokens (32/8 heads, 525 MB) 83.7 us, 0.92 of the
 // measured copy rate; 16 of 1024 to 32768 (64/8 heads, 1.2 GB) 184 us, 0.97; FP8
-// pages, 64 of 512 to 8192 (572 MB) 104 us, 0.81.
+// pages, 64 of 512 to 8192 (572 MB) 102 us, 0.83.
 //
 // Split.  The tiles (64 or 128 keys) of all units (request, KV head, up to 8 or
 // 16 of its query heads) are laid end to end and cut into equal ranges, one per
@@ -45,6 +45,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// Fewest tiles of a block.  One request of 777 tokens, 8 KV heads (104 tiles): 9.5 us with 1,
+// 8.9 with 2 (half the parts to join), 9.2 with 3, 9.8 with 4; a call with two tiles or more
+// for every block does not come to it.
+constexpr int kMinTiles = 2;
 constexpr float kRescale = 8.0f;  // O is rescaled when a maximum grew by more than 2^8
 
 struct DecodeParams {
@@ -64,8 +68,7 @@ struct DecodeParams {
     float* part_o;    // [2 n_cta][heads of a unit][128]
     int stride, B, H_q, H_kv, G, chunks, lp, num_pages, max_len, window, sinks, n_cta;
     int per_channel;
-    int wh;         // KV heads of a unit (the first kernel's WH)
-    int min_tiles;  // fewest tiles of a block
+    int wh;  // KV heads of a unit (the first kernel's WH)
     float scale_log2;
 };
 
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
         }
     long long before = block_scan(mine, scan, total);
     long long per = (total + p.n_cta - 1) / p.n_cta;
-    if (per < p.min_tiles) per = p.min_tiles;
+    if (per < kMinTiles) per = kMinTiles;
     const long long t0 = per * blockIdx.x;
     long long left = t0 < total ? min(per, total - t0) : 0;
     int2 desc = make_int2(-1, 0);
@@ -323,13 +326,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
             for (int it = 0; it < n_it; ++it) {
                 const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
                 const bool whole = there == (C::kKeys == 32 ? 0xffffffffu : 0xffffu);
-                // S^T = K Q^T: keys are the rows, heads the columns
-                float s[KB][NG][4];
+                // S^T = K Q^T: keys are the rows, heads the columns (FP8: the second
+                // terms of Q in sums of their own, because products into one sum wait for
+                // one another: 104 -> 102 us)
+                float s[KB][NG][4], s_low[KB][NG][4];
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
                     for (int n = 0; n < NG; ++n)
-                        s[kb][n][0] = s[kb][n][1] = s[kb][n][2] = s[kb][n][3] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[kb][n][i] = s_low[kb][n][i] = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         uint32_t a0, a1, a2, a3;
@@ -350,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
                             if (FP8) {
                                 const uint2 ql = reinterpret_cast<const uint2*>(
                                     q_low + (n * 4 + ks / 2) * 32)[ks & 1];
-                                mma<FP8>(s[kb][n], a0, a1, a2, a3, ql.x, ql.y);
+                                mma<FP8>(s_low[kb][n], a0, a1, a2, a3, ql.x, ql.y);
                             }
                         }
                     }
@@ -367,7 +373,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
                     for (int n = 0; n < NG; ++n)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float x = s[kb][n][i] * p.scale_log2;
+                            float x = s[kb][n][i];
+                            if (FP8) x += s_low[kb][n][i];
+                            x *= p.scale_log2;
                             if (!whole && !(there >> (kb * 16 + g + (i >> 1) * 8) & 1u)) x = ninf_f();
                             s[kb][n][i] = x;
                             grow |= x > m[n][i & 1] + kRescale;
@@ -731,7 +739,6 @@ cpa_status decode_common(const void* q, const void* k_pages, const void* v_pages
     p.max_len = max_seq_len;
     p.window = window;
     p.sinks = sinks;
-    p.min_tiles = 1;
     p.scale_log2 = sm_scale * kLog2e;
     const bool one = groups_of(G) == 1;
     cudaError_t e;
