@@ -28,11 +28,11 @@
 // pair); the chain softmax -> PV -> S -> softmax of one query tile when the
 // softmax takes longer than the other tile's products.
 //
-// 2 x 8192 tokens, 32/8 heads: 666 us causal, 1650 TFLOP/s of visible pairs, 0.87 of
-// the measured bf16 rate; 364 us with a window of 2048, 1330 TFLOP/s, where units are
-// 17 tiles long and their ends weigh more.  Of a tile's 2630 cycles the products are
-// 2048 at the nominal rate and about 2500 as measured without a softmax: S reads Q
-// and K from shared memory at all that it gives.
+// 2 x 8192 tokens, 32/8 heads: 651 us causal, 1690 TFLOP/s of visible pairs, 0.89 of
+// the measured bf16 rate; 350 us with a window of 2048, 1380 TFLOP/s, where units are
+// 17 tiles long and their ends weigh more (20 us of the 350 are the output's stores).
+// Of a tile's 2630 cycles the products are 2048 at the nominal rate and about 2500 as
+// measured without a softmax: S reads Q and K from shared memory at all that it gives.
 //
 // Split.  As in decode the key tiles of all units lie end to end and every block
 // takes a range of equal cost, so unequal requests, causal triangles and short
@@ -923,11 +923,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const float lse2 = l == 0.f ? ninf_f() : m_used + lg2(l);
                 const int row = (x.t0 + (active ? tok : 0)) * p.H_q + x.hk * p.G + (active ? gq : 0);
+                // rows of the lane pair, -1 where there is none
+                const int row_x = __shfl_xor_sync(0xffffffffu, active ? row : -1, 1);
+                const int row_e = lane & 1 ? row_x : (active ? row : -1);
+                const int row_o = lane & 1 ? (active ? row : -1) : row_x;
                 float check = lse2 == ninf_f() ? 0.f : lse2;
                 float4* po = p.part_o + slot * 32 * kRows + R;
-                // (a lane writes its own row, 32 bytes at a time: whole sectors.  Through shared
-                // memory 8 lanes would write 128 bytes of a row together, at the same speed
-                // and for 32 KB that the third K stage needs more)
+                // (Two lanes exchange halves, so that they write 64 bytes of a row together:
+                // 355 -> 350 us against 32 bytes of a row by each; 128 or 256 bytes together
+                // would give 1 us more before the cost of the exchange.  Through shared memory
+                // the whole lines cost as much, and the 32 KB that the third K stage needs.)
 #pragma unroll 1
                 for (int c0 = 0; c0 < 128; c0 += 32) {
                     uint32_t v[32];
@@ -940,22 +945,32 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                         z[i & 3] = fmaf(f[i], 0.f, z[i & 3]);  // NaN once any is not finite
                     }
                     check += (z[0] + z[1]) + (z[2] + z[3]);
-                    if (!active) continue;
                     if (split) {
+                        if (active) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            po[(size_t)(c0 / 4 + i) * kRows] =
-                                make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                            for (int i = 0; i < 8; ++i)
+                                po[(size_t)(c0 / 4 + i) * kRows] =
+                                    make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                        }
                     } else {
-                        uint32_t* out = reinterpret_cast<uint32_t*>(p.o + (size_t)row * 128 + c0);
+                        uint32_t w[2][8], x[8];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t w[8];
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                w[e] = pack_bf16x2(f[16 * i + 2 * e], f[16 * i + 2 * e + 1]);
-                            store32(out + 8 * i, w);
+                                w[i][e] = pack_bf16x2(f[16 * i + 2 * e], f[16 * i + 2 * e + 1]);
+                        const bool odd = lane & 1;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            x[e] = __shfl_xor_sync(0xffffffffu, odd ? w[0][e] : w[1][e], 1);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            w[0][e] = odd ? x[e] : w[0][e];
+                            w[1][e] = odd ? w[1][e] : x[e];
                         }
+                        uint32_t* out = reinterpret_cast<uint32_t*>(p.o) + c0 / 2 + (odd ? 8 : 0);
+                        if (row_e >= 0) store32(out + (size_t)row_e * 64, w[0]);
+                        if (row_o >= 0) store32(out + (size_t)row_o * 64, w[1]);
                     }
                 }
                 if (active) {
