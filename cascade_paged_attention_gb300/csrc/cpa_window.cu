@@ -573,7 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             uint64_t* const empty = is_k ? ctrl->k_empty : ctrl->v_empty;
             const int n_stages = is_k ? kKStages : kVStages;
             uint8_t* const ring = smem + (is_k ? kOffK : kOffV);
-            const uint64_t pol = l2_policy_evict_normal();
+            // Q is read once: its lines leave L2 first (349 -> 347 us).  K and V asked to stay
+            // gave 4 us more here, which the kernels after it lost again.
+            const uint64_t pol = l2_policy_evict_normal(), pol_q = l2_policy_evict_first();
             const int NB = 128 / p.boxr;
             const uint32_t q_bytes = (uint32_t)(p.G * p.TSB) * 2u * 128u;  // of one query tile
             uint32_t q_loads[2] = {0u, 0u};
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                             mbar_arrive_expect_tx(&ctrl->q_full[mt], q_bytes);
                             for (int h = 0; h < 2; ++h)
                                 tma_load_3d(smem + kOffQ + mt * kTileBytes + h * kHalf, &p.qmap, h * 64,
-                                            x.hk * p.G, x.t0 + mt * p.TSB, &ctrl->q_full[mt], pol);
+                                            x.hk * p.G, x.t0 + mt * p.TSB, &ctrl->q_full[mt], pol_q);
                         }
                         __syncwarp();
                         ++q_loads[mt];
