@@ -484,7 +484,8 @@ cpa_status cpa_window_prefill(const void* q, const void* k_pages, const void* v_
  *   parents, children  int32 [n] on the device.  A parent may have many
  *                      children; a child may not be named twice, nor be a
  *                      parent in the same call (CPA_DEV_BAD_ROW: such children
- *                      are left as they were, their pairs -1).
+ *                      are left as they were, their pairs -1, and the page that
+ *                      such an i would have got stays free and goes to no other).
  *   copy_src, copy_dst int32 [n] on the device, output.
  * With too few free pages (CPA_DEV_NO_PAGE) the children that got none have -1
  * as their last page and their pair; all else is as described, so freeing the
