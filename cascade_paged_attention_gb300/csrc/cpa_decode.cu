@@ -567,18 +567,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
 // Joins the unit that starts in block c's range and goes on past its end: its
 // parts are block c's second slot and the first slots of the blocks after it.
 // grid (blocks, heads of a unit / 8), a warp per head, a lane per 4 dimensions.
-// Block (0, 0) also gathers what the first kernel's blocks found wrong into the
-// status word, which therefore needs no clearing.
+// The last block, whose range nothing follows, gathers what the first kernel's
+// blocks found wrong into the status word, which therefore needs no clearing.
 template <int NG>
 __global__ void __launch_bounds__(256) join_kernel(DecodeParams p) {
     constexpr int NH = 8 * NG;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y > 0) return;
         uint32_t bad = 0;
         for (int i = threadIdx.x; i < p.n_cta; i += 256) bad |= __ldcg(p.bad + i);
         uint32_t all = __syncthreads_or((int)(bad & CPA_DEV_BAD_PAGE)) ? CPA_DEV_BAD_PAGE : 0u;
         if (__syncthreads_or((int)(bad & CPA_DEV_BAD_LENGTH))) all |= CPA_DEV_BAD_LENGTH;
         if (threadIdx.x == 0) *p.status = all;
+        return;
     }
     const int2 desc = __ldcg(p.desc + blockIdx.x);
     if (desc.x < 0) return;

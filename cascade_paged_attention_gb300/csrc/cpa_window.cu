@@ -73,7 +73,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // What a unit costs besides its tiles, in tiles: its first scores, masked edge
 // tiles and output.  Ranges are cut by this cost (equal numbers of tiles alone left
-// the median block waiting 10 % of the time for those with many short units).
+// the median block waiting 10 % of the time for those with many short units).  Where
+// there are no more tiles than blocks a unit costs nothing and every block takes one
+// tile: such a call lasts as long as its longest chain of tiles.
 constexpr int kUnitCost = 3;
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
 // A wait that lasts this long means a broken pipeline.  (Longer than elsewhere:
@@ -93,8 +95,8 @@ struct WindowParams {
     float* lse;
     uint32_t* status;
     uint32_t* bad;    // [n_cta] what each block found wrong
-    int4* desc;       // [n_cta] (request, KV head, query tile, parts) of the unit that starts
-                      // in the block's range and goes on past it; request -1: none
+    int4* desc;       // [n_cta] (first token, tokens, KV head, parts) of the unit that starts
+                      // in the block's range and goes on past it; first token -1: none
     float* part_lse;  // [2 n_cta][kRows], log2 units
     float4* part_o;   // [2 n_cta][32 groups of 4 columns][kRows]
     int stride, B, T, H_q, H_kv, G, TSB, lp, boxr, num_pages, max_new, max_len, window, sinks;
@@ -182,37 +184,39 @@ struct Ctrl {
     uint32_t tmem_base;
     uint32_t abort_flag;
     uint32_t bad;
-    long long scan[kWarps];
+    int unit_cost;            // kUnitCost, or 0 where every block takes one tile
     long long t0, left, per;  // this block's range, in tiles of cost
     int b, hk, qt, off;       // where it begins: a unit, and how far into its cost
 };
-constexpr uint32_t kOffWalk = 384;  // the softmax warps' walkers
+constexpr uint32_t kOffWalk = 384;  // the softmax warps' walkers (before them: sums by warp)
 static_assert(sizeof(Ctrl) <= kOffWalk, "control block");
 
 // Cost of one KV head of a request, by a whole warp (r the same in every lane).
-__device__ __forceinline__ long long head_cost(const WindowParams& p, const Request& r) {
+__device__ __forceinline__ long long head_cost(const WindowParams& p, const Request& r,
+                                               int unit_cost) {
     const int TS = 2 * p.TSB, lane = threadIdx.x & 31;
     const int nq = (r.m + TS - 1) / TS;
     long long sum = 0;
     for (int qt = lane; qt < nq; qt += 32) {
         Unit x;
         unit_tiles(p, r, qt, x);
-        sum += x.n_tiles + kUnitCost;
+        sum += x.n_tiles + unit_cost;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
 }
 
-// The same for a request per lane: short ones by their lane, long ones by the warp.
-__device__ __forceinline__ long long lane_cost(const WindowParams& p, const Request& r) {
+// The tiles of one KV head for a request per lane: short ones by their lane, long ones
+// by the warp.
+__device__ __forceinline__ long long lane_tiles(const WindowParams& p, const Request& r) {
     const int TS = 2 * p.TSB, lane = threadIdx.x & 31;
     const int nq = (r.m + TS - 1) / TS;
     long long sum = 0;
     for (int qt = 0; qt < nq && nq <= 8; ++qt) {
         Unit x;
         unit_tiles(p, r, qt, x);
-        sum += x.n_tiles + kUnitCost;
+        sum += x.n_tiles;
     }
     __syncwarp();
     for (uint32_t many = __ballot_sync(0xffffffffu, nq > 8); many != 0u; many &= many - 1u) {
@@ -221,7 +225,7 @@ __device__ __forceinline__ long long lane_cost(const WindowParams& p, const Requ
         q.t0 = 0;
         q.m = __shfl_sync(0xffffffffu, r.m, src);
         q.L = __shfl_sync(0xffffffffu, r.L, src);
-        const long long c = head_cost(p, q);
+        const long long c = head_cost(p, q, 0);
         if (lane == src) sum = c;
     }
     return sum;
@@ -229,36 +233,54 @@ __device__ __forceinline__ long long lane_cost(const WindowParams& p, const Requ
 
 // Every thread: the problem's cost, this block's range, and the unit where it
 // begins.  Each thread sums a run of requests; one scan over the block follows.
-__device__ void schedule(const WindowParams& p, Ctrl* c) {
+__device__ void schedule(const WindowParams& p, Ctrl* c, long long* sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int per_thread = (p.B + kThreads - 1) / kThreads, b0 = (int)threadIdx.x * per_thread;
     uint32_t bad = 0;
-    long long mine = 0;
+    long long mine = 0, units = 0;
     for (int i = 0; i < per_thread; ++i) {
         Request r = {0, 0, 0};
         if (b0 + i < p.B) r = request_of(p, b0 + i, bad);
-        mine += lane_cost(p, r) * p.H_kv;
+        mine += lane_tiles(p, r) * p.H_kv;
+        units += (long long)((r.m + 2 * p.TSB - 1) / (2 * p.TSB)) * p.H_kv;
     }
     if (bad) atomicOr(&c->bad, bad);
-    long long incl = mine;
+    long long incl = mine, incl_units = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const long long z = __shfl_up_sync(0xffffffffu, incl_units, o);
+        if (lane >= o) {
+            incl += y;
+            incl_units += z;
+        }
     }
-    if (lane == 31) c->scan[warp] = incl;
+    if (lane == 31) {
+        sums[warp] = incl;
+        sums[kWarps + warp] = incl_units;
+    }
     __syncthreads();
-    long long total = 0, before = incl - mine;
+    long long total = 0, before = incl - mine, total_units = 0, units_before = incl_units - units;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += c->scan[w];
-        total += c->scan[w];
+        if (w < warp) {
+            before += sums[w];
+            units_before += sums[kWarps + w];
+        }
+        total += sums[w];
+        total_units += sums[kWarps + w];
     }
+    const int unit_cost = total <= p.n_cta ? 0 : kUnitCost;
+    total += unit_cost * total_units;
+    before += unit_cost * units_before;
+    mine += unit_cost * units;
     long long per = (total + p.n_cta - 1) / p.n_cta;
-    if (per < p.min_tiles + kUnitCost) per = p.min_tiles + kUnitCost;
+    if (unit_cost) per = max(per, (long long)(p.min_tiles + kUnitCost));
+    else per = 1;
     const long long t0 = per * blockIdx.x;
     if (threadIdx.x == 0) {
         c->per = per;
+        c->unit_cost = unit_cost;
         c->t0 = t0;
         c->left = t0 < total ? min(per, total - t0) : 0;
     }
@@ -269,7 +291,7 @@ __device__ void schedule(const WindowParams& p, Ctrl* c) {
         long long run = __shfl_sync(0xffffffffu, before, src);
         for (int b = __shfl_sync(0xffffffffu, b0, src);; ++b) {
             const Request r = request_of(p, b, bad);
-            const long long per_head = head_cost(p, r);
+            const long long per_head = head_cost(p, r, unit_cost);
             if (t0 >= run + per_head * p.H_kv) {
                 run += per_head * p.H_kv;
                 continue;
@@ -285,7 +307,7 @@ __device__ void schedule(const WindowParams& p, Ctrl* c) {
                 if (q0 + lane < nq) {
                     Unit x;
                     unit_tiles(p, r, q0 + lane, x);
-                    cost = x.n_tiles + kUnitCost;
+                    cost = x.n_tiles + unit_cost;
                 }
                 long long in = cost;
 #pragma unroll
@@ -313,17 +335,19 @@ __device__ void schedule(const WindowParams& p, Ctrl* c) {
 struct Walker {
     Unit x;
     Request r;       // x's request
+    int unit_cost;
     long long left;  // cost of the range after this piece
     int j0, j1;
     __device__ __forceinline__ void cut(int off) {
-        const int take = (int)min((long long)x.n_tiles + kUnitCost - off, left);
+        const int take = (int)min((long long)x.n_tiles + unit_cost - off, left);
         left -= take;
-        j0 = max(0, off - kUnitCost);
-        j1 = max(0, off + take - kUnitCost);  // (0: the range ends before the first tile)
+        j0 = max(0, off - unit_cost);
+        j1 = max(0, off + take - unit_cost);  // (0: the range ends before the first tile)
     }
     __device__ __forceinline__ bool more() const { return j0 < j1; }
     __device__ __forceinline__ void init(const WindowParams& p, const Ctrl* c) {
         left = c->left;
+        unit_cost = c->unit_cost;
         uint32_t bad = 0;
         r = request_of(p, c->b, bad);
         x = unit_of(p, r, c->b, c->hk, c->qt);
@@ -560,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    schedule(p, ctrl);
+    schedule(p, ctrl, reinterpret_cast<long long*>(smem + kOffWalk));
     const uint32_t tmem = ctrl->tmem_base;
     int4 desc = make_int4(-1, 0, 0, 0);
 
@@ -608,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     if (w.j0 == 0 && w.j1 < x.n_tiles) {
                         // (it ends with this piece, which ends with the range)
                         const long long last = ctrl->t0 + ctrl->left + x.n_tiles - w.j1 - 1;
-                        desc = make_int4(x.b, x.hk, x.qt, (int)(last / ctrl->per - blockIdx.x) + 1);
+                        desc = make_int4(x.t0, x.ntok, x.hk,
+                                         (int)(last / ctrl->per - blockIdx.x) + 1);
                     }
                 } else {
                     const int nq = w.tiles_q(p);
@@ -1020,10 +1045,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 // Joins the unit that starts in block c's range and goes on past its end: its
 // parts are block c's second slot and the first slots of the blocks after it, in
 // that order.  A block does 32 rows (grid.y), a thread 4 columns of a row at a
-// time.  Block (0, 0) gathers the status word.
+// time.  The last block, whose range nothing follows, gathers the status word.
 __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WindowParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y > 0) return;
         __shared__ uint32_t all;
         if (threadIdx.x == 0) all = 0;
         __syncthreads();
@@ -1032,38 +1058,58 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
         if (bad) atomicOr(&all, bad);
         __syncthreads();
         if (threadIdx.x == 0) *p.status = all;
+        return;
     }
     const int4 d = __ldcg(p.desc + blockIdx.x);
     if (d.x < 0) return;
-    uint32_t bad = 0;
-    const Unit x = unit_of(p, request_of(p, d.x, bad), d.x, d.y, d.z);
     const int np = d.w;
     const int R = blockIdx.y * 32 + (threadIdx.x & 31), r = R & 127;
     const int it = r / p.G, gq = r - it * p.G;
     const int tok = (R >> 7) * p.TSB + it;
-    if (it >= p.TSB || tok >= x.ntok) return;
-    const size_t row = (size_t)(x.t0 + tok) * p.H_q + x.hk * p.G + gq;
+    if (it >= p.TSB || tok >= d.y) return;
+    const size_t row = (size_t)(d.x + tok) * p.H_q + d.z * p.G + gq;
     auto slot = [&](int i) -> size_t { return 2 * ((size_t)blockIdx.x + i) + (i == 0 ? 1 : 0); };
-    float mx = ninf_f();
-    for (int i = 0; i < np; ++i) mx = fmaxf(mx, __ldcg(p.part_lse + slot(i) * kRows + R));
-    const float ref = mx == ninf_f() ? 0.f : mx;
-    float sum = 0.f;
+    float m = ninf_f(), sum = 0.f;
     float4 acc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     const int g0 = threadIdx.x >> 5;  // column groups g0, g0 + 8, g0 + 16, g0 + 24
-#pragma unroll 2
-    for (int i = 0; i < np; ++i) {
-        const float f = ex2(__ldcg(p.part_lse + slot(i) * kRows + R) - ref);
-        sum += f;
+    for (int i0 = 0; i0 < np; i0 += 4) {  // four parts' loads in flight at a time
+        float4 y[4][4];
+        float z[4], mx = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t at = slot(min(i0 + i, np - 1));
+            z[i] = __ldcg(p.part_lse + at * kRows + R);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[i][k] = __ldcg(p.part_o + (at * 32 + g0 + 8 * k) * kRows + R);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i0 + i < np) mx = fmaxf(mx, z[i]);
+        const float ref = mx == ninf_f() ? 0.f : mx, f = ex2(m - ref);
+        sum *= f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float4 v = __ldcg(p.part_o + (slot(i) * 32 + g0 + 8 * k) * kRows + R);
-            acc[k].x += f * v.x;
-            acc[k].y += f * v.y;
-            acc[k].z += f * v.z;
-            acc[k].w += f * v.w;
+            acc[k].x *= f;
+            acc[k].y *= f;
+            acc[k].z *= f;
+            acc[k].w *= f;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i0 + i >= np) break;
+            const float w = ex2(z[i] - ref);
+            sum += w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[k].x += w * y[i][k].x;
+                acc[k].y += w * y[i][k].y;
+                acc[k].z += w * y[i][k].z;
+                acc[k].w += w * y[i][k].w;
+            }
+        }
+        m = mx;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
@@ -1071,7 +1117,8 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
         reinterpret_cast<uint2*>(p.o + row * 128)[g0 + 8 * k] =
             make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
                        pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
-    if (g0 == 0) p.lse[row] = sum == 0.f ? ninf_f() : (ref + lg2(sum)) * kLn2;
+    if (g0 == 0)
+        p.lse[row] = sum == 0.f ? ninf_f() : ((m == ninf_f() ? 0.f : m) + lg2(sum)) * kLn2;
 }
 
 struct WindowWs {
