@@ -246,3 +246,13 @@ def test_many_requests_and_a_stream_of_ones_own():
     tol = 2.0 ** -8 * wo.abs() + 2.0 ** -14 * torch.einsum("bhgj,bjhd->bhgd", w, V.abs())
     assert bool(((o.double().view_as(wo) - wo).abs() <= tol).all())
     assert float((lse.double().view_as(want) - want)[~none].abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("spare", [-1, 0, 1])
+def test_tiles_around_the_blocks(spare, fp8):
+    """Around two tiles for every block, the fewest that a block takes; odd tiles last."""
+    blocks = 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    for tiles in (2 * blocks + spare, 2 * (blocks // 4) + spare):
+        check([64 * tiles], 4, 1, 64, seed=tiles, fp8=fp8, hide=False)
+        check([64 * (tiles - 3) - 1, 65, 64], 8, 1, 16, seed=tiles + 1, fp8=fp8, hide=False)

@@ -259,3 +259,13 @@ def test_against_the_oracle(M):
         # the 170 keys and more that a row sees
         assert np.all(np.abs(o - ref_o) <= 2.0 ** -8 * (np.abs(ref_o) + 1.0) + 1e-4)
         assert float(np.abs(lse.double().cpu().numpy().reshape(ref_lse.shape) - ref_lse).max()) <= 1e-4
+
+
+@pytest.mark.parametrize("spare", [-1, 0, 1])
+@pytest.mark.parametrize("news", [[1], [30, 1]])
+def test_as_many_tiles_as_blocks(news, spare):
+    """Calls of about one key tile a block: below and above where the split changes."""
+    tiles = torch.cuda.get_device_properties(0).multi_processor_count + spare
+    lens = [128 * (tiles - 3 * (len(news) - 1))] + [300] * (len(news) - 1)
+    check(news, lens, 4, 1, 16, seed=spare + 5, hide=False)
+    check(news, [128 * (tiles // 2)] + [129] * (len(news) - 1), 8, 2, 64, seed=spare + 6, hide=False)
