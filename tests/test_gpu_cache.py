@@ -361,3 +361,39 @@ def test_fork_free_copy_in_a_graph():
             assert L == [50, 70][r]
             assert torch.equal(ref.dense(k, rows[2 + i], L, 16), ref.dense(k, rows[r], L, 16))
             assert torch.equal(ref.dense(v, rows[2 + i], L, 16), ref.dense(v, rows[r], L, 16))
+
+
+@pytest.mark.parametrize("op", ["free", "compact", "compact_many", "compact_in_place"])
+def test_status_of_replayed_calls(op):
+    """Every replay writes the status of its own inputs, whatever the word held before."""
+    n = 600 if op == "compact_many" else 12
+    B = 8
+    per = (n + 15) // 16
+    pool = 2 * B * per
+    ids = torch.arange(pool, dtype=torch.int32, device="cuda").view(2 * B, per)
+    k = torch.randn(pool, 16, 1, 128, device="cuda").to(torch.bfloat16)
+    v = torch.randn(pool, 16, 1, 128, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").repeat(B, 1)
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    table, refs = ids.clone(), torch.ones(pool, dtype=torch.int32, device="cuda")
+    rows, zero, last, keep = (i32(x) for x in (list(range(B)), [0] * B, [per] * B, [n] * B))
+
+    def call():
+        if op == "free":
+            table.copy_(ids)
+            refs.fill_(1)
+            cpa.cpa_cache_free(table, rows, zero, last, refs, workspace=ws)
+        else:
+            dst = None if op == "compact_in_place" else table[B:]
+            cpa.cpa_cache_compact(k, v, table[:B], pos, keep, dst, zero, src_rows=rows, workspace=ws)
+
+    call()
+    assert cpa.cpa_get_device_status(ws)[0] == 0
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        call()
+    for bad, status in ((B - 1, 0), (2 * B + 1, 10), (B - 1, 0), (-1, 10), (B - 1, 0)):
+        rows[B - 1] = bad
+        for _ in range(2):
+            gr.replay()
+        assert cpa.cpa_get_device_status(ws)[0] == status
