@@ -74,8 +74,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // What a unit costs besides its tiles, in tiles: its first scores, masked edge
 // tiles and output.  Ranges are cut by this cost (equal numbers of tiles alone left
 // the median block waiting 10 % of the time for those with many short units).  Where
-// there are no more tiles than blocks a unit costs nothing and every block takes one
-// tile: such a call lasts as long as its longest chain of tiles.
+// there are no more than two tiles a block a unit costs nothing and no block takes more
+// than two: such a call lasts as long as its longest chain of tiles (88 tiles 19.3 ->
+// 16.7 us, 160 tiles 21.3 -> 19.4, 296 tiles in 64 units 20.1 -> 17.5, 256 in 8 units
+// 23.1 -> 23.3; the same rule up to three tiles: 432 tiles 19.5 -> 21.4).
 constexpr int kUnitCost = 3;
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
 // A wait that lasts this long means a broken pipeline.  (Longer than elsewhere:
@@ -184,7 +186,7 @@ struct Ctrl {
     uint32_t tmem_base;
     uint32_t abort_flag;
     uint32_t bad;
-    int unit_cost;            // kUnitCost, or 0 where every block takes one tile
+    int unit_cost;            // kUnitCost, or 0 where no block takes more than two tiles
     long long t0, left, per;  // this block's range, in tiles of cost
     int b, hk, qt, off;       // where it begins: a unit, and how far into its cost
 };
@@ -270,13 +272,12 @@ __device__ void schedule(const WindowParams& p, Ctrl* c, long long* sums) {
         total += sums[w];
         total_units += sums[kWarps + w];
     }
-    const int unit_cost = total <= p.n_cta ? 0 : kUnitCost;
+    const int unit_cost = total <= 2 * p.n_cta ? 0 : kUnitCost;
     total += unit_cost * total_units;
     before += unit_cost * units_before;
     mine += unit_cost * units;
     long long per = (total + p.n_cta - 1) / p.n_cta;
     if (unit_cost) per = max(per, (long long)(p.min_tiles + kUnitCost));
-    else per = 1;
     const long long t0 = per * blockIdx.x;
     if (threadIdx.x == 0) {
         c->per = per;

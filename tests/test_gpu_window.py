@@ -269,3 +269,12 @@ def test_as_many_tiles_as_blocks(news, spare):
     lens = [128 * (tiles - 3 * (len(news) - 1))] + [300] * (len(news) - 1)
     check(news, lens, 4, 1, 16, seed=spare + 5, hide=False)
     check(news, [128 * (tiles // 2)] + [129] * (len(news) - 1), 8, 2, 64, seed=spare + 6, hide=False)
+
+
+@pytest.mark.parametrize("spare", [-1, 0, 1])
+def test_as_many_tiles_as_twice_the_blocks(spare):
+    """Two tiles a block: the most that are shared out without regard to units."""
+    tiles = 2 * torch.cuda.get_device_properties(0).multi_processor_count + spare
+    check([3], [128 * tiles], 2, 1, 16, seed=spare + 7, hide=False)
+    check([20] * 6, [128 * (tiles // 12)] * 5 + [128 * (tiles - 11 * (tiles // 12))], 8, 2, 64,
+          seed=spare + 8, hide=False)
