@@ -28,9 +28,9 @@
 // pair); the chain softmax -> PV -> S -> softmax of one query tile when the
 // softmax takes longer than the other tile's products.
 //
-// 2 x 8192 tokens, 32/8 heads: 651 us causal, 1690 TFLOP/s of visible pairs, 0.89 of
-// the measured bf16 rate; 350 us with a window of 2048, 1380 TFLOP/s, where units are
-// 17 tiles long and their ends weigh more (20 us of the 350 are the output's stores).
+// 2 x 8192 tokens, 32/8 heads: 652 us causal, 1690 TFLOP/s of visible pairs, 0.89 of
+// the measured bf16 rate; 346 us with a window of 2048, 1400 TFLOP/s, where units are
+// 17 tiles long and their ends weigh more (the output's stores alone take 15 us of it).
 // Of a tile's 2630 cycles the products are 2048 at the nominal rate and about 2500 as
 // measured without a softmax: S reads Q and K from shared memory at all that it gives.
 //
