@@ -260,6 +260,28 @@ __global__ void __launch_bounds__(256)
     if (bad) flag(status, bad);
 }
 
+// The same for a small call by one block, an entry a thread, which writes the status
+// word as well.
+constexpr int kFreeThreads = 1024;
+__global__ void __launch_bounds__(kFreeThreads)
+    free_small_kernel(int32_t* table, int stride, int n_rows, const int32_t* __restrict__ rows,
+                      const int32_t* __restrict__ first, const int32_t* __restrict__ last, int n,
+                      int32_t* refcounts, int num_pages, uint32_t* status) {
+    __shared__ uint32_t all;
+    if (threadIdx.x == 0) all = 0u;
+    __syncthreads();
+    const int i = threadIdx.x / stride, k = threadIdx.x - i * stride;
+    if (i < n) {
+        const int r = __ldg(rows + i), a = __ldg(first + i), b = __ldg(last + i);
+        uint32_t bad = range_bits(r, a, b, stride, n_rows);
+        if (!bad && k >= a && k < b)
+            bad = give_back(table + (size_t)r * stride + k, refcounts, num_pages);
+        if (bad) atomicOr(&all, bad);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) *status = all;
+}
+
 // ---------------------------------------------------------------- copies
 constexpr int kUnroll = 8;  // 16-byte loads that a lane has in flight
 
@@ -581,6 +603,14 @@ cpa_status cpa_cache_free(int32_t* page_table, int pt_stride, int n_rows, const 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (n == 0) return clear_status(workspace, s);
     uint32_t* const status = static_cast<uint32_t*>(workspace);
+    // One launch in place of two, which is what a small call waits for: 4 sequences of 49
+    // pages 8.9 -> 7.2 us called from Python (on the device 2.1 -> 2.2; 1024 entries 2.1 -> 2.7).
+    if ((long long)n * pt_stride <= kFreeThreads) {
+        const int threads = (n * pt_stride + 31) / 32 * 32;
+        free_small_kernel<<<1, threads, 0, s>>>(page_table, pt_stride, n_rows, rows, first, last,
+                                                n, refcounts, num_pages, status);
+        return launched();
+    }
     return launch_cleared(free_kernel, dim3((unsigned)n), 256, s, status, page_table, pt_stride,
                           n_rows, rows, first, last, refcounts, num_pages, status);
 }

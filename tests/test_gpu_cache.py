@@ -397,3 +397,27 @@ def test_status_of_replayed_calls(op):
         for _ in range(2):
             gr.replay()
         assert cpa.cpa_get_device_status(ws)[0] == status
+
+
+@pytest.mark.parametrize("n,stride", [(1, 1024), (16, 64), (17, 64), (1025, 1), (40, 300), (3, 341)])
+def test_free_around_one_block(n, stride):
+    """Up to 1024 entries by one block, more by a block per range; ranges of unequal length."""
+    g = ref.gen(n + stride)
+    table = torch.randperm(n * stride, generator=g, device="cuda").to(torch.int32).view(n, stride)
+    table[n // 2] = table[0] if n > 1 else table[0].clone()  # shared by two rows
+    refs = counts_of(table, n * stride)
+    first = torch.randint(0, stride + 1, (n,), generator=g, device="cuda").to(torch.int32)
+    last = torch.randint(0, stride + 1, (n,), generator=g, device="cuda").to(torch.int32)
+    rows = torch.randperm(n, generator=g, device="cuda").to(torch.int32)
+    k = torch.arange(stride, device="cuda")
+    want = table.clone()
+    want[rows.long()] = torch.where((k >= first[:, None]) & (k < last[:, None]), -1,
+                                    table[rows.long()])
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    cpa.cpa_cache_free(table, rows, first, last, refs, workspace=ws)
+    assert cpa.cpa_get_device_status(ws)[0] == 0
+    assert torch.equal(table, want) and torch.equal(refs, counts_of(table, n * stride))
+    first[0], last[0] = 0, stride + 1
+    cpa.cpa_cache_free(table, rows, first, last, refs, workspace=ws)
+    assert cpa.cpa_get_device_status(ws)[0] == 8
+    assert torch.equal(table, want) and torch.equal(refs, counts_of(table, n * stride))
