@@ -338,7 +338,7 @@ struct CompactParams {
     uint32_t* status;
     int src_stride, n_src_rows, dst_stride, max_keep, B, lp, num_pages;
     int token16;  // 16-byte units of a token's K (or V)
-    int checker;  // the last block looks over the whole call and writes the status word
+    int status_block;  // the last block looks over the whole call and writes the status word
 };
 
 // The source row of request b and its count; false where they are out of range.
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(256, 4) compact_kernel(CompactParams p) {
     const int lane = threadIdx.x & 31;
     const long long n_items = (long long)p.B * p.max_keep;
     uint32_t bad = 0;
-    if (p.checker && blockIdx.x == gridDim.x - 1) {
+    if (p.status_block && blockIdx.x == gridDim.x - 1) {
         __shared__ uint32_t all;
         if (threadIdx.x == 0) all = 0u;
         __syncthreads();
@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(256, 4) compact_kernel(CompactParams p) {
         if (threadIdx.x == 0) *p.status = all;
         return;
     }
-    if (!p.checker) wait_for_clear();
-    const long long step = (long long)(gridDim.x - p.checker) * 8;
+    if (!p.status_block) wait_for_clear();
+    const long long step = (long long)(gridDim.x - p.status_block) * 8;
     for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < n_items; it += step) {
         long long s, d;
         const int b = (int)(it / p.max_keep);
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(256, 4) compact_kernel(CompactParams p) {
                 }
         }
     }
-    if (bad && !p.checker && lane == 0) flag(p.status, bad);
+    if (bad && !p.status_block && lane == 0) flag(p.status, bad);
 }
 
 // Within one row: positions only move down (dst_start + i <= src_pos[i], both
@@ -664,7 +664,7 @@ cpa_status cpa_cache_compact(void* k_pages, void* v_pages, const int32_t* src_ta
     // to 6 tokens: 3.6 -> 3.0 us against clear_kernel); a large one has each warp
     // report into a cleared word, because one block would be looking long after the
     // others are done.
-    p.checker = dst_table && (long long)B * max_keep <= 4096 ? 1 : 0;
+    p.status_block = dst_table && (long long)B * max_keep <= 4096 ? 1 : 0;
     p.k_pages = static_cast<uint8_t*>(k_pages);
     p.v_pages = static_cast<uint8_t*>(v_pages);
     p.src_table = src_table;
@@ -691,8 +691,8 @@ cpa_status cpa_cache_compact(void* k_pages, void* v_pages, const int32_t* src_ta
     // and written)
     long long blocks = ((long long)B * max_keep + 7) / 8;
     if (blocks > (long long)n_sm * 64) blocks = (long long)n_sm * 64;
-    const dim3 grid((unsigned)blocks + p.checker);
-    if (!p.checker) return launch_cleared(compact_kernel, grid, 256, s, p.status, p);
+    const dim3 grid((unsigned)blocks + p.status_block);
+    if (!p.status_block) return launch_cleared(compact_kernel, grid, 256, s, p.status, p);
     compact_kernel<<<grid, 256, 0, s>>>(p);
     return launched();
 }
