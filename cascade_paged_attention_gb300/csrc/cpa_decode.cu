@@ -161,7 +161,7 @@ template <bool FP8, int NG, int WH>
 __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(DecodeParams p) {
     using C = Cfg<FP8, NG>;
     constexpr int KB = C::kBlocks, KW = C::kKWords, VW = C::kVWords;
-    __shared__ float sm_o[kWarps][C::kHeads][132];
+    __shared__ __align__(16) float sm_o[kWarps][C::kHeads][132];  // (read as float4 and uint4)
     __shared__ float sm_m[kWarps][C::kHeads], sm_l[kWarps][C::kHeads];
     __shared__ long long scan[kWarps];
     __shared__ long long s_off;
