@@ -80,9 +80,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 23.1 -> 23.3; the same rule up to three tiles: 432 tiles 19.5 -> 21.4).
 constexpr int kUnitCost = 3;
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
-// A wait that lasts this long means a broken pipeline.  (Longer than elsewhere:
-// rows that are not finite are done again key by key while the other warps wait.)
-constexpr uint64_t kLimitNs = 4ull * 1000 * 1000 * 1000;
 static_assert(kSmem <= 232448, "shared memory of one block");
 
 struct WindowParams {
@@ -105,17 +102,6 @@ struct WindowParams {
     int n_cta, min_tiles;
     float scale_log2;
 };
-
-__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                        uint32_t* bad) {
-    return mbar_wait(bar, parity, abort_flag, bad, kLimitNs);
-}
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity,
-                                          volatile uint32_t* abort_flag, uint32_t* bad) {
-    // (the first look by itself: most waits find the phase complete)
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xffffffffu, wait_on(bar, parity, abort_flag, bad));
-}
 
 __device__ __forceinline__ float ninf_f() { return __int_as_float(0xff800000); }
 
@@ -183,13 +169,39 @@ struct Ctrl {
     uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: weights of keys 0..63, 64..127
     uint64_t turn[2];   // the issuing warps' turns
     uint64_t mma_done;
+    volatile uint64_t redo_ns;  // when a row that is done again last began a key tile
     uint32_t tmem_base;
-    uint32_t abort_flag;
+    volatile uint32_t abort_flag;
     uint32_t bad;
     int unit_cost;            // kUnitCost, or 0 where no block takes more than two tiles
     long long t0, left, per;  // this block's range, in tiles of cost
     int b, hk, qt, off;       // where it begins: a unit, and how far into its cost
 };
+// mbar_wait() of cpa_device.cuh, with a limit that a redo puts off: the rows that are not
+// finite are done again key by key while the other warps wait, for as long as their caches
+// are, and tell the time with every key tile.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Ctrl* c) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (n & 63u) continue;
+        if (c->abort_flag) return false;
+        const uint64_t since = max(t0, (uint64_t)c->redo_ns);
+        if ((int64_t)(globaltimer_ns() - since) > (int64_t)kWaitLimitNs) {
+            atomicOr(&c->bad, CPA_DEV_TIMEOUT);
+            c->abort_flag = 1u;
+            __threadfence_block();
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctrl* c) {
+    // (the first look by itself: most waits find the phase complete)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_on(bar, parity, c));
+}
+
 constexpr uint32_t kOffWalk = 384;  // the softmax warps' walkers (before them: sums by warp)
 static_assert(sizeof(Ctrl) <= kOffWalk, "control block");
 
@@ -470,8 +482,8 @@ __device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int c0, int 
 // One row over tiles [j0, j1) of its unit, by a whole warp, key by key: what the
 // row does not see is not touched.  Lane l ends up with dimensions 4 l .. 4 l + 3
 // of o (normalised); returns the log-sum-exp in log2 units.
-__device__ __forceinline__ float slow_row(const WindowParams& p, const Unit& x, int j0, int j1,
-                                       size_t qrow, int pos, float (&o)[4]) {
+__device__ __forceinline__ float slow_row(const WindowParams& p, Ctrl* c, const Unit& x, int j0,
+                                       int j1, size_t qrow, int pos, float (&o)[4]) {
     const int lane = threadIdx.x & 31;
     const uint2 qr = __ldg(reinterpret_cast<const uint2*>(p.q + qrow * 128) + lane);
     const float q0 = __uint_as_float(qr.x << 16), q1 = __uint_as_float(qr.x & 0xFFFF0000u);
@@ -482,6 +494,7 @@ __device__ __forceinline__ float slow_row(const WindowParams& p, const Unit& x, 
     // four keys at a time, so that their loads and sums overlap
     for (int j = j0; j < j1; ++j) {
         const int key0 = key0_of(x, j), stop = min(key0 + 128, pos + 1);
+        if (lane == 0) c->redo_ns = globaltimer_ns();
         for (int k4 = key0; k4 < stop; k4 += 4) {
             float s[4], v[4][4];
             bool on[4];
@@ -544,7 +557,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem);
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile uint32_t* abort_flag = &ctrl->abort_flag;
     uint32_t* const bad_word = &ctrl->bad;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -567,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             mbar_init(&ctrl->turn[i], 1);
         }
         mbar_init(&ctrl->mma_done, 2);
+        ctrl->redo_ns = 0;
         ctrl->abort_flag = 0;
         ctrl->bad = 0;
         fence_barrier_init();
@@ -640,8 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     const int nq = w.tiles_q(p);
                     for (int mt = 0; mt < nq && ok; ++mt) {
                         if (q_loads[mt] > 0)
-                            ok = wait_warp(&ctrl->q_empty[mt], (q_loads[mt] - 1) & 1u, abort_flag,
-                                           bad_word);
+                            ok = wait_warp(&ctrl->q_empty[mt], (q_loads[mt] - 1) & 1u, ctrl);
                         if (!ok) break;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&ctrl->q_full[mt], q_bytes);
@@ -657,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 for (int j = w.j0; j < w.j1; ++j, ++g) {
                     const int next_page = page_of(j + 1);
                     if (g >= n_stages) {
-                        ok = wait_warp(&empty[st], par, abort_flag, bad_word);
+                        ok = wait_warp(&empty[st], par, ctrl);
                         if (!ok) break;
                     }
                     const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
@@ -692,12 +704,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             }
             for (int mt = 0; mt < 2; ++mt)
                 if (q_loads[mt] > 0)
-                    wait_on(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u, abort_flag, bad_word);
+                    wait_on(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u, ctrl);
             // no copy may be in flight when the block leaves
             for (int s = 0; s < n_stages; ++s)
                 if (s < g) {
                     const long long last = s + (g - 1 - s) / n_stages * n_stages;
-                    wait_on(&full[s], (uint32_t)((last / n_stages) & 1), abort_flag, bad_word);
+                    wait_on(&full[s], (uint32_t)((last / n_stages) & 1), ctrl);
                 }
             __syncwarp();
         } else if (warp >= 10) {
@@ -717,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             uint32_t kpar = 0, vpar = 0, qpar = 0, ppar = 0, tpar = mt == 0 ? 1u : 0u;
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t par) {
-                ok = ok && wait_warp(bar, par, abort_flag, bad_word);
+                ok = ok && wait_warp(bar, par, ctrl);
                 return ok;
             };
             // half of PV: 64 keys
@@ -794,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     round(w.tiles_q(p), j == w.j0, j == w.j1 - 1);
             if (ok) round(0, false, false);
             commit(lead, &ctrl->mma_done);
-            wait_warp(&ctrl->mma_done, 0, abort_flag, bad_word);
+            wait_warp(&ctrl->mma_done, 0, ctrl);
         } else if (warp < 8) {
             // ============================== softmax and output
             const int mt = warp >> 2;
@@ -834,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     const int key0 = (j < n_sink ? j : j + skip) << 7;
                     const bool whole =
                         key0 + 127 <= p_min && (key0 > hidden || key0 + 128 <= p.sinks);
-                    ok = wait_warp(&ctrl->s_full[mt], spar, abort_flag, bad_word);
+                    ok = wait_warp(&ctrl->s_full[mt], spar, ctrl);
                     if (!ok) break;
                     spar ^= 1u;
                     tc_fence_after_sync();
@@ -895,8 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     // cleared (by both query tiles, each before its own products)
                     if (j == tail) {
                         const int st = (int)(g % kVStages);
-                        ok = wait_warp(&ctrl->v_full[st], (uint32_t)((g / kVStages) & 1),
-                                            abort_flag, bad_word);
+                        ok = wait_warp(&ctrl->v_full[st], (uint32_t)((g / kVStages) & 1), ctrl);
                         if (!ok) break;
                         const int first = xs.L - key0;
                         const int stop = min(128, (first + p.boxr - 1) & ~(p.boxr - 1));
@@ -942,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 const Unit x = w.x;
                 const int j0 = w.j0, j1 = w.j1;
                 advance(w, p);
-                ok = wait_warp(&ctrl->o_full[mt], opar, abort_flag, bad_word);
+                ok = wait_warp(&ctrl->o_full[mt], opar, ctrl);
                 if (!ok) break;
                 opar ^= 1u;
                 tc_fence_after_sync();
@@ -1017,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     const int pos_a = __shfl_sync(0xffffffffu, pos, src);
                     const int R_a = __shfl_sync(0xffffffffu, R, src);
                     float f[4];
-                    const float z = slow_row(p, x, j0, j1, row_a, pos_a, f);
+                    const float z = slow_row(p, ctrl, x, j0, j1, row_a, pos_a, f);
                     if (split) {
                         p.part_o[(slot * 32 + lane) * kRows + R_a] = make_float4(f[0], f[1], f[2], f[3]);
                         if (lane == 0) p.part_lse[slot * kRows + R_a] = z;

@@ -278,3 +278,34 @@ def test_as_many_tiles_as_twice_the_blocks(spare):
     check([3], [128 * tiles], 2, 1, 16, seed=spare + 7, hide=False)
     check([20] * 6, [128 * (tiles // 12)] * 5 + [128 * (tiles - 11 * (tiles // 12))], 8, 2, 64,
           seed=spare + 8, hide=False)
+
+
+def test_rows_done_again_for_longer_than_a_wait_may_last():
+    """A unit of 450000 keys, every row of which is done again key by key (some seconds), and one
+    of 8 keys after it in every block: no wait of the second gives up meanwhile."""
+    n_sm = torch.cuda.get_device_properties(0).multi_processor_count
+    g = ref.gen(31)
+    L, m, P = 450_000, 8, 256
+    table, pool = ref.table_of([L, m], P, g)
+    k, v = ref.pool_of(pool, P, 1, g), ref.pool_of(pool, P, 1, g)
+    v[table[0, 0].long(), 0, 0, 5] = float("nan")
+    q = torch.randn(2 * m, 32, 128, generator=g, device="cuda").to(torch.bfloat16)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    start = torch.arange(2 * n_sm + 1, dtype=torch.int32, device="cuda") * m
+    o, lse = cpa.cpa_window_prefill(q.repeat(n_sm, 1, 1), k, v, table.repeat(n_sm, 1), start,
+                                    i32([L, m] * n_sm), check=True)
+    o, lse = o.view(n_sm, 2 * m, 32, 128), lse.view(n_sm, 2 * m, 32)
+    assert torch.equal(lse, lse[:1].expand_as(lse))
+    assert bool(torch.isnan(o[:, :m, :, 5]).all())
+    o[:, :m, :, 5] = 0
+    assert torch.equal(o, o[:1].expand_as(o))
+    v[table[0, 0].long(), 0, 0, 5] = 0
+    for a, n, row in ((0, L, table[0]), (m, m, table[1])):
+        K, V = ref.dense(k, row, n, P), ref.dense(v, row, n, P)
+        for i in range(m):
+            want = ref.attend(q[a + i:a + i + 1].view(32, 1, 128), K, V,
+                              ref.seen([n - m + i] * 32, n, 0, 0, "cuda"), 128 ** -0.5, ref.E_P_BF16)
+            if a == 0:
+                want[0][..., 5] = 0
+                want[2][..., 5] = 0
+            ref.close(o[0, a + i].view(32, 1, 128), lse[0, a + i].view(32, 1), want)
