@@ -49,7 +49,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 8.9 with 2 (half the parts to join), 9.2 with 3, 9.8 with 4; a call with two tiles or more
 // for every block does not come to it.
 constexpr int kMinTiles = 2;
-constexpr float kRescale = 8.0f;  // O is rescaled when a maximum grew by more than 2^8
+// O is rescaled when a maximum grew by more than 2^8 (FP8: 2^7, which with the lift leaves f16
+// a factor of 4 for maxima so large that subtracting the lift rounds).
+constexpr float kRescale = 8.0f, kRescaleFp8 = 7.0f;
+// FP8: weights meet V in f16, so they are taken 2^7 times as large: f16 then holds a weight to
+// 2^-11 of itself down to 2^-21 of the largest, and to 2^-32 of that below (2^-14 and 2^-25
+// without: behind one strong key the flat rest of a long row lost of its share).
+constexpr float kLiftFp8 = 7.0f;
 
 struct DecodeParams {
     const __nv_bfloat16* q;
@@ -81,6 +87,8 @@ struct Cfg {
     static constexpr int kKWords = kRowBytes / 16;   // 32-bit words of a K row in one lane
     static constexpr int kVWords = kRowBytes / 32;   // of a V row
     static constexpr int kPerSm = NG == 1 ? 3 : 2;   // resident blocks (by registers)
+    static constexpr float kLift = FP8 ? kLiftFp8 : 0.f;
+    static constexpr float kGrow = FP8 ? kRescaleFp8 : kRescale;
 };
 
 // What a request's token sees: keys [0, n_sink) and [n_sink + shift, L).
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
                             x *= p.scale_log2;
                             if (!whole && !(there >> (kb * 16 + g + (i >> 1) * 8) & 1u)) x = ninf_f();
                             s[kb][n][i] = x;
-                            grow |= x > m[n][i & 1] + kRescale;
+                            grow |= x > m[n][i & 1] + C::kGrow;
                         }
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -409,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
                 for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int n = 0; n < NG; ++n) {
-                        const float r0 = m[n][0] == ninf_f() ? 0.f : m[n][0];
-                        const float r1 = m[n][1] == ninf_f() ? 0.f : m[n][1];
+                        const float r0 = m[n][0] == ninf_f() ? 0.f : m[n][0] - C::kLift;
+                        const float r1 = m[n][1] == ninf_f() ? 0.f : m[n][1] - C::kLift;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float w0 = ex2(s[kb][n][2 * i] - r0);
@@ -482,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
                     for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
                     const int head = n * 8 + 2 * c + h;
                     if (g == 0) {
-                        sm_m[warp][head] = m[n][h];
+                        sm_m[warp][head] = m[n][h] - C::kLift;  // what O and the sum refer to
                         sm_l[warp][head] = x;
                     }
 #pragma unroll

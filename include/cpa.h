@@ -420,7 +420,8 @@ cpa_status cpa_decode(const void* q, const void* k_pages, const void* v_pages,
  * Decode over FP8 E4M3 pages: cpa_decode with the pools and scales of
  * cpa_cascade_verify_fp8.  Codes are widened exactly to f16 (a NaN code that a
  * row sees gives NaN); q x k_scale is held as two f16 terms, so it must stay
- * below 65504 in magnitude; P is f16; sums are fp32.
+ * below 65504 in magnitude; a weight is f16, to 2^-11 of itself down to 2^-21 of
+ * the row's largest and to 2^-32 of that below; sums are fp32.
  */
 cpa_status cpa_decode_fp8(const void* q, const void* k_pages, const void* v_pages,
                           const float* k_scale, const float* v_scale, int scale_per_channel,

@@ -1,5 +1,7 @@
 """Decode over the paged cache against a 64-bit reference: lengths from none to
 long, odd groups, windows and sinks, FP8 pages, splits, refusals by the device."""
+import math
+
 import pytest
 import torch
 
@@ -256,3 +258,55 @@ def test_tiles_around_the_blocks(spare, fp8):
     for tiles in (2 * blocks + spare, 2 * (blocks // 4) + spare):
         check([64 * tiles], 4, 1, 64, seed=tiles, fp8=fp8, hide=False)
         check([64 * (tiles - 3) - 1, 65, 64], 8, 1, 16, seed=tiles + 1, fp8=fp8, hide=False)
+
+
+@pytest.mark.parametrize("H_kv", [1, 2])
+@pytest.mark.parametrize("bits", [12.4, 20.5])
+@pytest.mark.parametrize("many,L", [(False, 300), (True, 20000)])
+def test_fp8_weights_far_below_the_largest(many, L, bits, H_kv):
+    """One key `bits` powers of two above all others, whose own value is 0: the output is made
+    of the small weights alone.  Many requests over the same pages, so that one block walks a
+    whole one.  f16 holds a lifted weight to 2^-11 of itself down to 2^-21 of the largest."""
+    B = 3 * torch.cuda.get_device_properties(0).multi_processor_count // H_kv if many else 1
+    g = ref.gen(L)
+    table, pool = ref.table_of([L], 16, g)
+    k = torch.zeros(pool, 16, H_kv, 128, dtype=torch.uint8, device="cuda")
+    v = torch.randn(pool, 16, H_kv, 128, generator=g, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    k[table[0, 0].long(), 0] = 0x38  # 1.0
+    v[table[0, 0].long(), 0] = 0
+    ks, vs = torch.ones(1, device="cuda"), torch.full((1,), 0.75, device="cuda")
+    q = torch.ones(B, 4 * H_kv, 128, dtype=torch.bfloat16, device="cuda")
+    scale = bits * math.log(2) / 128  # (the strong key's score is 128 * scale, the others' 0)
+    o, lse = cpa.cpa_decode_fp8(q, k, v, ks, vs, table.expand(B, -1).contiguous(),
+                                torch.full((B,), L, dtype=torch.int32, device="cuda"),
+                                sm_scale=scale, check=True)
+    want = ref.attend(q[:1], ref.dense(k, table[0], L, 16, ks), ref.dense(v, table[0], L, 16, vs),
+                      ref.seen([L - 1], L, 0, 0, "cuda"), scale, ref.E_F16, ref.E_Q_SPLIT)
+    for b in range(0, B, 37):
+        ref.close(o[b:b + 1], lse[b:b + 1], want)
+
+
+@pytest.mark.parametrize("step", [0.9, 6.9, 7.1, 40.0])
+def test_fp8_scores_that_grow_and_shrink(step):
+    """FP8 scores that climb by `step` powers of two a key, then fall: the running maximum lags
+    by up to 2^7, and the lifted weights stay within f16."""
+    L = 400
+    g = ref.gen(int(step * 10))
+    table, pool = ref.table_of([L, L], 16, g)
+    v = torch.randn(pool, 16, 1, 128, generator=g, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    k = torch.zeros(pool, 16, 1, 128, device="cuda")
+    level = (8 - (torch.arange(L, device="cuda") % 33 - 16).abs() / 2)  # 0 .. 8 and back
+    pos = torch.arange(L, device="cuda")
+    for b in range(2):
+        k[table[b].long()[pos // 16], pos % 16] = level[:, None, None].expand(L, 1, 128)
+    k = k.to(torch.float8_e4m3fn).view(torch.uint8)
+    ks, vs = torch.ones(1, device="cuda"), torch.ones(1, device="cuda")
+    q = torch.ones(2, 6, 128, dtype=torch.bfloat16, device="cuda")
+    scale = 2 * step * math.log(2) / 128
+    o, lse = cpa.cpa_decode_fp8(q, k, v, ks, vs, table,
+                                torch.full((2,), L, dtype=torch.int32, device="cuda"),
+                                sm_scale=scale, check=True)
+    for b in range(2):
+        ref.close(o[b:b + 1], lse[b:b + 1], ref.attend(
+            q[b:b + 1], ref.dense(k, table[b], L, 16, ks), ref.dense(v, table[b], L, 16, vs),
+            ref.seen([L - 1], L, 0, 0, "cuda"), scale, ref.E_F16, ref.E_Q_SPLIT))
