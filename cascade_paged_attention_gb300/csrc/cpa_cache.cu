@@ -240,7 +240,7 @@ __device__ __forceinline__ uint32_t give_back(int32_t* entry, int32_t* refcounts
 
 __device__ __forceinline__ uint32_t range_bits(int r, int a, int b, int stride, int n_rows) {
     if (r < 0 || r >= n_rows) return CPA_DEV_BAD_ROW;
-    return a < 0 || b > stride ? CPA_DEV_BAD_LENGTH : 0u;
+    return a < 0 || a > stride || b < 0 || b > stride ? CPA_DEV_BAD_LENGTH : 0u;
 }
 
 // One block per named range.

@@ -507,9 +507,10 @@ cpa_status cpa_cache_fork(int32_t* page_table, int pt_stride, int n_rows, int32_
  * gives it back once.  0 .. pt_stride frees a whole sequence; a window of W
  * tokens with S sinks over L tokens has left the pages ceil(S / page_size) ..
  * max(L - W, 0) / page_size behind (seq_lens does not change).  A count that is
- * 0 already stays 0 and sets CPA_DEV_BAD_COUNT; bounds outside [0, pt_stride]
- * set CPA_DEV_BAD_LENGTH, a row outside [0, n_rows) CPA_DEV_BAD_ROW, and
- * nothing of that i is given back.  Workspace: cpa_status_workspace_size().
+ * 0 already stays 0 and sets CPA_DEV_BAD_COUNT; a bound outside [0, pt_stride]
+ * sets CPA_DEV_BAD_LENGTH, a row outside [0, n_rows) CPA_DEV_BAD_ROW, and
+ * nothing of that i is given back (first[i] >= last[i]: an empty range).
+ * Workspace: cpa_status_workspace_size().
  */
 cpa_status cpa_cache_free(int32_t* page_table, int pt_stride, int n_rows, const int32_t* rows,
                           const int32_t* first, const int32_t* last, int n, int32_t* refcounts,

@@ -421,3 +421,21 @@ def test_free_around_one_block(n, stride):
     cpa.cpa_cache_free(table, rows, first, last, refs, workspace=ws)
     assert cpa.cpa_get_device_status(ws)[0] == 8
     assert torch.equal(table, want) and torch.equal(refs, counts_of(table, n * stride))
+
+
+@pytest.mark.parametrize("stride", [16, 600])
+@pytest.mark.parametrize("first,last,status", [("past", 3, 8), (0, -1, 8), (-5, -1, 8), ("past", 0, 8),
+                                               (-1, 3, 8), (5, "past", 8), ("past", "past", 8),
+                                               ("end", "end", 0), ("end", 0, 0), (7, 2, 0)])
+def test_free_looks_at_both_bounds(first, last, status, stride):
+    """Each bound by itself, also where the range would be empty; by one block and by one a range."""
+    at = {"past": stride + 1, "end": stride}
+    table = torch.arange(2 * stride, dtype=torch.int32, device="cuda").view(2, stride)
+    refs = torch.ones(2 * stride, dtype=torch.int32, device="cuda")
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    cpa.cpa_cache_free(table, i32([0, 1]), i32([2, at.get(first, first)]), i32([5, at.get(last, last)]),
+                       refs, workspace=ws)
+    assert cpa.cpa_get_device_status(ws)[0] == status
+    want = torch.arange(2 * stride, dtype=torch.int32, device="cuda").view(2, stride)
+    want[0, 2:5] = -1
+    assert torch.equal(table, want) and torch.equal(refs, counts_of(table, 2 * stride))
