@@ -196,10 +196,10 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p) {
         int e = -1;
         if (k < whole) {
             e = from[k];
-            if (e < 0 || e >= p.num_pages) {
+            if (e < -1 || e >= p.num_pages) {
                 bad = true;
                 e = -1;
-            } else {
+            } else if (e >= 0) {  // (-1: a page that the parent gave back)
                 atomicAdd(p.refcounts + e, 1);
             }
         } else if (k == whole && tail) {

@@ -475,22 +475,26 @@ cpa_status cpa_window_prefill(const void* q, const void* k_pages, const void* v_
  *
  * cpa_cache_fork: sequence children[i] becomes a copy of sequence parents[i]
  * (rows of one page_table [n_rows, pt_stride] and of seq_lens [n_rows]).  The
- * parent's whole pages are shared, their counts raised by one each.  A last,
- * partly filled page is not shared: the child gets the lowest free page that no
- * earlier i got, with count 1, and (copy_src[i], copy_dst[i]) names the two
- * pages, for cpa_cache_copy_pages to copy in every layer.  Where there is
- * nothing to copy both are -1.  Entries past the child's last page become -1.
- * The entries that row children[i] held before are not given back: free them
- * first.
+ * parent's whole pages are shared, their counts raised by one each; entries of
+ * -1 among them (pages that a window has left and that were given back) are -1
+ * in the child's row too.  A last, partly filled page is not shared: the child
+ * gets the lowest free page that no earlier i got, with count 1, and
+ * (copy_src[i], copy_dst[i]) names the two pages, for cpa_cache_copy_pages to
+ * copy in every layer.  Where there is nothing to copy both are -1.  Entries
+ * past the child's last page become -1.  The entries that row children[i] held
+ * before are not given back: free them first.
  *   parents, children  int32 [n] on the device.  A parent may have many
  *                      children; a child may not be named twice, nor be a
  *                      parent in the same call (CPA_DEV_BAD_ROW: such children
  *                      are left as they were, their pairs -1, and the page that
  *                      such an i would have got stays free and goes to no other).
+ *                      So it is with a parent whose length is outside
+ *                      [0, pt_stride * page_size] (CPA_DEV_BAD_LENGTH).
  *   copy_src, copy_dst int32 [n] on the device, output.
  * With too few free pages (CPA_DEV_NO_PAGE) the children that got none have -1
  * as their last page and their pair; all else is as described, so freeing the
- * row undoes the fork.  n may be 0.
+ * row undoes the fork.  An entry of the parent that is no page id and not -1, or
+ * a last, partly filled page that is -1, sets CPA_DEV_BAD_PAGE.  n may be 0.
  */
 size_t cpa_cache_fork_workspace_size(int num_pages);
 

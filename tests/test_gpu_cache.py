@@ -439,3 +439,33 @@ def test_free_looks_at_both_bounds(first, last, status, stride):
     want = torch.arange(2 * stride, dtype=torch.int32, device="cuda").view(2, stride)
     want[0, 2:5] = -1
     assert torch.equal(table, want) and torch.equal(refs, counts_of(table, 2 * stride))
+
+
+def test_fork_of_a_sequence_whose_window_has_moved_on():
+    """Pages that a window has left are given back; a fork of what is left passes over them,
+    and decode of the child sees what decode of the parent sees."""
+    P, L, W, S = 16, 200, 64, 4
+    g = ref.gen(9)
+    table, pool = ref.table_of([L, L], P, g, 6)
+    k, v = ref.pool_of(pool, P, 2, g), ref.pool_of(pool, P, 2, g)
+    rows = torch.cat([table, torch.full((2, table.shape[1]), -1, dtype=torch.int32, device="cuda")])
+    refs, dl = counts_of(table, pool), i32([L, L, 0, 0])
+    cpa.cpa_cache_free(rows, i32([0]), i32([1]), i32([(L - W) // P]), refs, check=True)
+    before = refs.clone()
+    src, dst = cpa.cpa_cache_fork(rows, dl, i32([0, 1]), i32([2, 3]), refs, P, check=True)
+    cpa.cpa_cache_copy_pages(k, v, src, dst, check=True)
+    assert rows[2, :12].tolist() == rows[0, :12].tolist() and rows[3, :12].tolist() == table[1, :12].tolist()
+    assert bool((rows[2, 1:8] == -1).all()) and dl.tolist() == [L] * 4
+    assert torch.equal(refs, counts_of(rows, pool))
+    q = torch.randn(2, 8, 128, generator=g, device="cuda").to(torch.bfloat16)[[0, 1, 0, 1]].contiguous()
+    o, lse = cpa.cpa_decode(q, k, v, rows, dl, window=W, sinks=S, check=True)
+    assert torch.equal(o[:2], o[2:]) and torch.equal(lse[:2], lse[2:])
+    cpa.cpa_cache_free(rows, i32([2, 3]), i32([0, 0]), i32([rows.shape[1]] * 2), refs, check=True)
+    assert torch.equal(refs, before)
+    for entry, bad in ((3, -2), (3, pool), (12, -1), (12, -2)):  # (entry 12 is the last, partly filled)
+        was = rows[1, entry].clone()
+        rows[1, entry] = bad
+        with pytest.raises(cpa.CpaError) as e:
+            cpa.cpa_cache_fork(rows, dl, i32([1]), i32([3]), refs.clone(), P, check=True)
+        assert e.value.status == 5
+        rows[1, entry] = was
