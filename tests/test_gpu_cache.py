@@ -469,3 +469,24 @@ def test_fork_of_a_sequence_whose_window_has_moved_on():
             cpa.cpa_cache_fork(rows, dl, i32([1]), i32([3]), refs.clone(), P, check=True)
         assert e.value.status == 5
         rows[1, entry] = was
+
+
+def test_fork_in_a_pool_of_many_chunks():
+    """Free pages far apart, around and past the 256 chunks of 1024 that a block looks over at
+    a time; one child more than there are pages."""
+    pool = 700_001
+    refs = torch.ones(pool, dtype=torch.int32, device="cuda")
+    for lo, hi in ((1023, 1025), (262_140, 262_150), (263_000, 263_001), (524_280, 524_300),
+                   (pool - 1, pool)):
+        refs[lo:hi] = 0
+    free = torch.nonzero(refs == 0).view(-1).to(torch.int32)
+    n = free.numel() + 1
+    rows = torch.full((n + 1, 2), -1, dtype=torch.int32, device="cuda")
+    rows[0, 0] = 7
+    dl = torch.full((n + 1,), 5, dtype=torch.int32, device="cuda")
+    ws = torch.empty(cpa.cpa_cache_fork_workspace_size(pool), dtype=torch.uint8, device="cuda")
+    src, dst = cpa.cpa_cache_fork(rows, dl, i32([0] * n), i32(list(range(1, n + 1))), refs, 16,
+                                  workspace=ws)
+    assert cpa.cpa_get_device_status(ws)[0] == 11
+    assert torch.equal(dst[:-1], free) and int(dst[-1]) == -1
+    assert src.tolist() == [7] * (n - 1) + [-1] and bool((refs == 1).all())

@@ -144,3 +144,10 @@ def test_binding_refuses_host_tensors_and_types():
         cpa.cpa_decode(q.half(), kv, kv, i2, i1)
     with pytest.raises(TypeError, match="torch.Tensor"):
         cpa.cpa_cache_copy_pages([0], kv, i1, i1)
+
+
+def test_fork_workspace_holds_a_count_for_each_1024_pages(L):
+    """The status word, a count of 4 bytes for each 1024 pages, a bit a page."""
+    for chunks in (1, 200, 684):
+        for pages in (1024 * chunks, 1024 * chunks - 1023):
+            assert cpa.cpa_cache_fork_workspace_size(pages) >= 256 + chunks * (4 + 128)
