@@ -56,6 +56,7 @@ constexpr float kRescale = 8.0f, kRescaleFp8 = 7.0f;
 // 2^-11 of itself down to 2^-21 of the largest, and to 2^-32 of that below (2^-14 and 2^-25
 // without: behind one strong key the flat rest of a long row lost of its share).
 constexpr float kLiftFp8 = 7.0f;
+constexpr float kLeast = 1.17549435e-38f;  // 2^-126, the least normal bf16
 
 struct DecodeParams {
     const __nv_bfloat16* q;
@@ -428,14 +429,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, NG>::kPerSm) decode_kernel(
                             if (FP8) {
                                 ph[kb][n][i] = transpose8(pack_f16x2(w0, w1));
                             } else {
-                                // a weight as two bf16 terms (16 bits): a second pass of
+                                // a weight as two bf16 terms (15 bits): a second pass of
                                 // the tensor cores, which have the time, in place of
-                                // 2^-9 of every weight
-                                const uint32_t hi = pack_bf16x2(w0, w1);
-                                ph[kb][n][i] = transpose8(hi);
-                                pl[kb][n][i] = transpose8(
-                                    pack_bf16x2(w0 - __uint_as_float(hi << 16),
-                                                w1 - __uint_as_float(hi & 0xFFFF0000u)));
+                                // 2^-8 of every weight.  The first is cut off, not rounded,
+                                // and the second is never 0: both then have the weight's
+                                // sign, and an infinity in V stays one
+                                const uint32_t x0 = __float_as_uint(w0), x1 = __float_as_uint(w1);
+                                ph[kb][n][i] = transpose8(__byte_perm(x0, x1, 0x7632u));
+                                pl[kb][n][i] = transpose8(pack_bf16x2(
+                                    fmaxf(w0 - __uint_as_float(x0 & 0xFFFF0000u), kLeast),
+                                    fmaxf(w1 - __uint_as_float(x1 & 0xFFFF0000u), kLeast)));
                             }
                         }
                     }

@@ -402,6 +402,8 @@ cpa_status cpa_tree_pass_b(const void* q, const void* k_pages, const void* v_pag
  *   seq_lens    int32 [B] on the device, 0 <= seq_lens[b] <= max_seq_len; a
  *               request of length 0 gets o = 0, lse = -inf
  *   o, lse      bf16 [B, H_q, head_dim], fp32 [B, H_q]
+ * A NaN or an infinity in V reaches the requests that see it and no others; an
+ * infinity stays one unless another of unlike sign meets it.
  * The work is split over the visible length and joined, in a fixed order: the
  * result of a call depends on its inputs and the device's SM count alone.
  * Supported: head_dim 128; page_size in {8,16,32,64,128,256}; any H_q that is a

@@ -310,3 +310,26 @@ def test_fp8_scores_that_grow_and_shrink(step):
         ref.close(o[b:b + 1], lse[b:b + 1], ref.attend(
             q[b:b + 1], ref.dense(k, table[b], L, 16, ks), ref.dense(v, table[b], L, 16, vs),
             ref.seen([L - 1], L, 0, 0, "cuda"), scale, ref.E_F16, ref.E_Q_SPLIT))
+
+
+@pytest.mark.parametrize("H_q,H_kv", [(8, 2), (12, 1)])
+def test_infinities_in_v(H_q, H_kv):
+    """An infinity in V that a row sees is one in its output (two of unlike sign: a NaN), also
+    where weights are 1 or any other value that bf16 holds; nothing else changes."""
+    lens = [1, 2, 200, 9000]
+    q, k, v, _, _, table, dl = make(lens, H_q, H_kv, 16, 51)
+    inf = float("inf")
+    for b, at, c, x in ((0, 0, 3, inf), (0, 0, 4, -inf), (1, 0, 9, -inf), (1, 1, 10, inf), (2, 3, 17, inf),
+                        (2, 77, 40, -inf), (2, 5, 41, inf), (2, 199, 41, -inf), (3, 4000, 5, inf),
+                        (3, 20, 99, -inf), (3, 8999, 98, inf), (3, 0, 97, inf), (3, 8000, 97, inf)):
+        v[table[b, at // 16].long(), at % 16, H_kv - 1, c] = x
+    o, lse = cpa.cpa_decode(q, k, v, table, dl, check=True)
+    for b, L in enumerate(lens):
+        want = ref.attend(q[b:b + 1], ref.dense(k, table[b], L, 16), ref.dense(v, table[b], L, 16),
+                          ref.seen([L - 1], L, 0, 0, "cuda"), 128 ** -0.5)
+        got, w = o[b:b + 1].double(), want[0]
+        odd = ~torch.isfinite(w)
+        assert torch.equal(got[odd].nan_to_num(nan=7.0), w[odd].nan_to_num(nan=7.0))
+        assert int(odd.sum()) == H_q // H_kv * {0: 2, 1: 2, 2: 3, 3: 4}[b]
+        ref.close(torch.where(odd, 0.0, got), lse[b:b + 1],
+                  [torch.where(odd, 0.0, w), want[1], torch.where(odd, 0.0, want[2]), want[3]])
