@@ -696,6 +696,21 @@ def _shape(t: torch.Tensor, name: str, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _int(x, name: str) -> int:
+    """A whole number for the C entry points, whose ints have 32 bits (ctypes would cut it)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} does not fit 32 bits: {x}")
+    return x
+
+
+def _max_len(max_seq_len, columns: int, page_size: int) -> int:
+    """max_seq_len, by default all that a table of so many columns holds."""
+    if max_seq_len is None:
+        return min(columns * page_size, 1 << 30)  # (the longest sequence that the calls take)
+    return _int(max_seq_len, "max_seq_len")
+
+
 def _new(shape, dtype, dev: int, stream):
     """An output that the caller did not give, from PyTorch's allocator on the call's stream."""
     if stream is None:
@@ -769,7 +784,7 @@ def _decode(name, q, k_pages, v_pages, scales, page_table, seq_lens, max_seq_len
     _shape(lse, "lse", (B, H_q))
     args = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), *sc, page_table.data_ptr(),
             stride, seq_lens.data_ptr(), B, H_q, H_kv, d, P, num_pages,
-            stride * P if max_seq_len is None else int(max_seq_len), int(window), int(sinks),
+            _max_len(max_seq_len, stride, P), _int(window, "window"), _int(sinks, "sinks"),
             d ** -0.5 if sm_scale is None else float(sm_scale), o.data_ptr(), lse.data_ptr())
     _launch(name, args, dev, stream, workspace,
             lambda: cpa_decode_workspace_size(B, H_q, H_kv, d, P), check)
@@ -828,7 +843,7 @@ def cpa_window_prefill(q, k_pages, v_pages, page_table, q_start, seq_lens,
     rows, stride = page_table.shape
     if dq != d or q_start.shape[0] != B + 1 or rows != B:
         raise ValueError("inconsistent prefill shapes")
-    max_new = T if max_new is None else int(max_new)
+    max_new = T if max_new is None else _int(max_new, "max_new")
     if o is None:
         o = _new(q.shape, torch.bfloat16, dev, stream)
     if lse is None:
@@ -839,7 +854,7 @@ def cpa_window_prefill(q, k_pages, v_pages, page_table, q_start, seq_lens,
     _shape(lse, "lse", (T, H_q))
     args = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), stride,
             q_start.data_ptr(), seq_lens.data_ptr(), B, T, H_q, H_kv, d, P, num_pages, max_new,
-            stride * P if max_seq_len is None else int(max_seq_len), int(window), int(sinks),
+            _max_len(max_seq_len, stride, P), _int(window, "window"), _int(sinks, "sinks"),
             d ** -0.5 if sm_scale is None else float(sm_scale), o.data_ptr(), lse.data_ptr())
     _launch("cpa_window_prefill", args, dev, stream, workspace,
             lambda: cpa_window_prefill_workspace_size(B, T, H_q, H_kv, d, P, max_new), check)
@@ -878,7 +893,7 @@ def cpa_cache_fork(page_table, seq_lens, parents, children, refcounts, page_size
     _shape(copy_src, "copy_src", (n,))
     _shape(copy_dst, "copy_dst", (n,))
     args = (page_table.data_ptr(), stride, n_rows, seq_lens.data_ptr(), parents.data_ptr(),
-            children.data_ptr(), n, refcounts.data_ptr(), int(page_size), num_pages,
+            children.data_ptr(), n, refcounts.data_ptr(), _int(page_size, "page_size"), num_pages,
             copy_src.data_ptr(), copy_dst.data_ptr())
     _launch("cpa_cache_fork", args, dev, stream, workspace,
             lambda: cpa_cache_fork_workspace_size(num_pages), check)

@@ -333,3 +333,42 @@ def test_infinities_in_v(H_q, H_kv):
         assert int(odd.sum()) == H_q // H_kv * {0: 2, 1: 2, 2: 3, 3: 4}[b]
         ref.close(torch.where(odd, 0.0, got), lse[b:b + 1],
                   [torch.where(odd, 0.0, w), want[1], torch.where(odd, 0.0, want[2]), want[3]])
+
+
+def test_numbers_past_32_bits_are_refused():
+    """The C entry points take 32 bits: a larger number is not cut to them."""
+    q, k, v, _, _, table, dl = make([200], 8, 2, 16, 61)
+    qs = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    for name in ("window", "sinks", "max_seq_len", "max_new"):
+        for x in (2 ** 31, 2 ** 32, 2 ** 32 + 200, -2 ** 31 - 1):
+            if name != "max_new":
+                with pytest.raises(ValueError, match=name):
+                    cpa.cpa_decode(q, k, v, table, dl, **{name: x})
+            with pytest.raises(ValueError, match=name):
+                cpa.cpa_window_prefill(q, k, v, table, qs, dl, **{name: x})
+    with pytest.raises(ValueError, match="page_size"):
+        cpa.cpa_cache_fork(table, dl, dl, dl, dl, 2 ** 32 + 16)
+    # the largest number is as good as none
+    o, lse = cpa.cpa_decode(q, k, v, table, dl, check=True)
+    for kw in (dict(window=2 ** 31 - 1), dict(window=3, sinks=2 ** 31 - 1),
+               dict(window=2 ** 31 - 1, sinks=2 ** 31 - 1)):
+        o2, lse2 = cpa.cpa_decode(q, k, v, table, dl, check=True, **kw)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    o, lse = cpa.cpa_window_prefill(q, k, v, table, qs, dl, check=True)
+    for kw in (dict(window=2 ** 31 - 1), dict(window=3, sinks=2 ** 31 - 1),
+               dict(window=2 ** 31 - 1, sinks=2 ** 31 - 1), dict(max_new=2 ** 31 - 1)):
+        o2, lse2 = cpa.cpa_window_prefill(q, k, v, table, qs, dl, check=True, **kw)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_a_table_wider_than_any_sequence():
+    """2^23 + 1 columns of pages of 256: more than 2^31 tokens, of which a sequence may have 2^30."""
+    q, k, v, _, _, table, dl = make([300], 8, 2, 256, 62)
+    wide = torch.full((1, 2 ** 23 + 1), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    qs = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    for a, b in ((cpa.cpa_decode(q, k, v, table, dl, check=True),
+                  cpa.cpa_decode(q, k, v, wide, dl, check=True)),
+                 (cpa.cpa_window_prefill(q, k, v, table, qs, dl, check=True),
+                  cpa.cpa_window_prefill(q, k, v, wide, qs, dl, check=True))):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
