@@ -43,21 +43,24 @@
  *     Calls are asynchronous on `stream` (NULL = legacy default stream) and
  *     launch nothing when they return an error, except the calls that launch
  *     two kernels (cpa_cascade_verify_shared when its shared prefix ends inside
- *     a page, the cpa_decode calls, cpa_window_prefill, cpa_cache_fork): they
- *     check every argument before the first, so only CPA_ERR_LAUNCH or
- *     CPA_ERR_CUDA from the second launch can follow a launch already made.
+ *     a page, the cpa_decode calls, cpa_window_prefill, cpa_cache_fork,
+ *     cpa_cache_free where n * pt_stride is above 1024, cpa_cache_compact in
+ *     place or where B * max_keep is above 4096): they check every argument
+ *     before the first, so only CPA_ERR_LAUNCH or CPA_ERR_CUDA from the second
+ *     launch can follow a launch already made.
  *   - Errors: arguments that can be checked on the host return a status
  *     before any launch.  Problems only the GPU can see (a page id outside
  *     [0, num_pages), a prefix length outside [0, max_prefix_len], a pipeline
  *     wait that exceeded its time limit) set bits in a status word at the
  *     start of the workspace, which cpa_get_device_status reads.  Each
  *     workspace-taking call clears that word and the merge counters it uses
- *     (an asynchronous memset on `stream`) or has its kernels write the word
- *     whole.  Nothing crosses the ABI as an
- *     exception, and no kernel traps, asserts or prints.
+ *     (an asynchronous memset or kernel on `stream`) or has its kernels write
+ *     the word whole.  Nothing crosses the ABI as an exception, and no kernel
+ *     traps, asserts or prints.
  *   - When the device status word has any bit set after a call, that call's
  *     outputs are undefined (they may be partial, stale or computed from a
- *     truncated mask); only the status word is meaningful.
+ *     truncated mask) unless the call says what they are; only the status word
+ *     is meaningful.
  *   - A workspace must not be used by two calls that can run at the same time.
  */
 #ifndef CPA_H_
@@ -401,7 +404,7 @@ cpa_status cpa_tree_pass_b(const void* q, const void* k_pages, const void* v_pag
  *   page_table  int32 [B, pt_stride], pt_stride >= ceil(max_seq_len / page_size)
  *   seq_lens    int32 [B] on the device, 0 <= seq_lens[b] <= max_seq_len; a
  *               request of length 0 gets o = 0, lse = -inf
- *   o, lse      bf16 [B, H_q, head_dim], fp32 [B, H_q]
+ *   o, lse      bf16 [B, H_q, head_dim], fp32 [B, H_q]; not over any input
  * A NaN or an infinity in V reaches the requests that see it and no others; an
  * infinity stays one unless another of unlike sign meets it.
  * The work is split over the visible length and joined, in a fixed order: the
@@ -448,7 +451,7 @@ cpa_status cpa_decode_fp8(const void* q, const void* k_pages, const void* v_page
  *               past q_start[B] are left as they were
  *   seq_lens    int32 [B] on the device, m_b <= seq_lens[b] <= max_seq_len
  *   max_new     host-side upper bound of every m_b
- *   o, lse      bf16 [T, H_q, head_dim], fp32 [T, H_q]
+ *   o, lse      bf16 [T, H_q, head_dim], fp32 [T, H_q]; not over any input
  * A q_start that is not ascending or leaves [0, T], an m_b above max_new or
  * above seq_lens[b], or a length above max_seq_len sets CPA_DEV_BAD_LENGTH.
  * A NaN or an infinity in V reaches the rows that see it and no others; a call
