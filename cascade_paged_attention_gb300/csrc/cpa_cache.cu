@@ -496,8 +496,7 @@ ForkWs fork_ws(int num_pages) {
     return w;
 }
 
-// The status word's memset: what a call does before its kernel, and all that a
-// call with nothing to do does.
+// All that a call with nothing to do does.
 cpa_status clear_status(void* workspace, cudaStream_t s) {
     return cudaMemsetAsync(workspace, 0, 4, s) == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
 }

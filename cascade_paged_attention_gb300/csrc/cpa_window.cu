@@ -79,6 +79,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 16.7 us, 160 tiles 21.3 -> 19.4, 296 tiles in 64 units 20.1 -> 17.5, 256 in 8 units
 // 23.1 -> 23.3; the same rule up to three tiles: 432 tiles 19.5 -> 21.4).
 constexpr int kUnitCost = 3;
+constexpr int kMinTiles = 2;  // fewest tiles of a block where units have a cost
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
 static_assert(kSmem <= 232448, "shared memory of one block");
 
@@ -99,7 +100,7 @@ struct WindowParams {
     float* part_lse;  // [2 n_cta][kRows], log2 units
     float4* part_o;   // [2 n_cta][32 groups of 4 columns][kRows]
     int stride, B, T, H_q, H_kv, G, TSB, lp, boxr, num_pages, max_new, max_len, window, sinks;
-    int n_cta, min_tiles;
+    int n_cta;
     float scale_log2;
 };
 
@@ -289,7 +290,7 @@ __device__ void schedule(const WindowParams& p, Ctrl* c, long long* sums) {
     before += unit_cost * units_before;
     mine += unit_cost * units;
     long long per = (total + p.n_cta - 1) / p.n_cta;
-    if (unit_cost) per = max(per, (long long)(p.min_tiles + kUnitCost));
+    if (unit_cost) per = max(per, (long long)(kMinTiles + kUnitCost));
     const long long t0 = per * blockIdx.x;
     if (threadIdx.x == 0) {
         c->per = per;
@@ -1233,7 +1234,6 @@ cpa_status cpa_window_prefill(const void* q, const void* k_pages, const void* v_
     p.window = window;
     p.sinks = sinks;
     p.n_cta = n_sm;
-    p.min_tiles = 2;
     p.scale_log2 = sm_scale * kLog2e;
     const uint64_t slots = (uint64_t)num_pages * page_size;
     if (!make_map(&p.qmap, q, H_q, (uint64_t)T, p.G, p.TSB) ||
