@@ -17,9 +17,9 @@
 // mma.sync and not tcgen05: with 8 heads as N = 8 and 16 keys as M = 16 nothing
 // is padded for G = 8 and the operands are the loaded registers themselves; the
 // 128-row tile of tcgen05 would have to be fed through shared memory or TMEM.
-// Whole calls: 64 requests of 2000 tokens (32/8 heads, 525 MB) 83.7 us, 0.92 of the
-// measured copy rate; 16 of 1024 to 32768 (64/8 heads, 1.2 GB) 184 us, 0.97; FP8
-// pages, 64 of 512 to 8192 (572 MB) 102 us, 0.83.
+// Whole calls: 64 requests of 2000 tokens (32/8 heads, 525 MB) 85.2 us, 0.91 of the
+// measured copy rate; 16 of 1024 to 32768 (64/8 heads, 1.2 GB) 186 us, 0.96; FP8
+// pages, 64 of 512 to 8192 (572 MB) 103 us, 0.82.
 //
 // Split.  The tiles (64 or 128 keys) of all units (request, KV head, up to 8 or
 // 16 of its query heads) are laid end to end and cut into equal ranges, one per
@@ -54,7 +54,7 @@ constexpr int kMinTiles = 2;
 constexpr float kRescale = 8.0f, kRescaleFp8 = 7.0f;
 // FP8: weights meet V in f16, so they are taken 2^7 times as large: f16 then holds a weight to
 // 2^-11 of itself down to 2^-21 of the largest, and to 2^-32 of that below (2^-14 and 2^-25
-// without: behind one strong key the flat rest of a long row lost of its share).
+// without: behind one strong key the flat rest of a long row lost part of its share).
 constexpr float kLiftFp8 = 7.0f;
 constexpr float kLeast = 1.17549435e-38f;  // 2^-126, the least normal bf16
 

@@ -28,8 +28,8 @@
 // pair); the chain softmax -> PV -> S -> softmax of one query tile when the
 // softmax takes longer than the other tile's products.
 //
-// 2 x 8192 tokens, 32/8 heads: 652 us causal, 1690 TFLOP/s of visible pairs, 0.89 of
-// the measured bf16 rate; 346 us with a window of 2048, 1400 TFLOP/s, where units are
+// 2 x 8192 tokens, 32/8 heads: 650 us causal, 1690 TFLOP/s of visible pairs, 0.89 of
+// the measured bf16 rate; 349 us with a window of 2048, 1390 TFLOP/s, where units are
 // 17 tiles long and their ends weigh more (the output's stores alone take 15 us of it).
 // Of a tile's 2630 cycles the products are 2048 at the nominal rate and about 2500 as
 // measured without a softmax: S reads Q and K from shared memory at all that it gives.
@@ -42,9 +42,9 @@
 // Values that are not numbers.  A masked key has weight 0, but 0 times a NaN in V
 // is a NaN in a matrix product.  A row whose weights are finite and whose result is
 // not is therefore done again, key by key over what it sees, by its warp: exact,
-// slow (hundreds of times when every row of a call is), and never taken by finite
-// caches.  (Slots past a sequence's end may hold anything: their V rows are cleared
-// in shared memory.)
+// slow (hundreds of times when every row of a call is: the waits of the other warps
+// know of it), and never taken by finite caches.  (Slots past a sequence's end may hold
+// anything: their V rows are cleared in shared memory.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
