@@ -55,6 +55,16 @@ __all__ = [
     "cpa_cache_free",
     "cpa_cache_copy_pages",
     "cpa_cache_compact",
+    "cpa_cache_append",
+    "cpa_cache_append_fp8",
+    "cpa_cache_gather",
+    "cpa_cache_gather_fp8",
+    "cpa_latent_append",
+    "cpa_latent_gather",
+    "cpa_latent_decode_workspace_size",
+    "cpa_latent_decode",
+    "cpa_latent_prefill_workspace_size",
+    "cpa_latent_prefill",
     "cpa_get_device_status",
     "cpa_noalloc_device_status",
     "cpa_debug_wait_timeout",
@@ -144,6 +154,19 @@ def lib() -> ctypes.CDLL:
         "cpa_cache_free": (I, [P, I, I, P, P, P, I, P, I, P, SZ, P]),
         "cpa_cache_copy_pages": (I, [P, P, P, P, I, I, SZ, P, SZ, P]),
         "cpa_cache_compact": (I, [P, P, P, I, I, P, P, I, P, P, I, P, I, I, I, SZ, P, SZ, P]),
+        "cpa_cache_append": (I, [P, P, SZ, SZ, P, P, P, I, P, P, I, I, I, I, SZ, P, SZ, P]),
+        "cpa_cache_append_fp8": (I, [P, P, SZ, SZ, P, P, P, P, I, P, I, P, P, I, I, I, I, I, P, SZ,
+                                     P]),
+        "cpa_cache_gather": (I, [P, P, P, I, P, P, I, I, I, I, SZ, P, P, P, SZ, P]),
+        "cpa_cache_gather_fp8": (I, [P, P, P, P, I, P, I, P, P, I, I, I, I, I, P, P, P, SZ, P]),
+        "cpa_latent_append": (I, [P, P, SZ, SZ, P, P, I, P, P, I, I, I, I, I, I, P, SZ, P]),
+        "cpa_latent_gather": (I, [P, P, I, P, P, I, I, I, I, I, I, P, P, P, SZ, P]),
+        "cpa_latent_decode_workspace_size": (SZ, [I, I, I, I, I, I]),
+        "cpa_latent_decode": (I, [P, I64, I64, P, I64, I64, P, P, I, P, I, I, I, I, I, I, I, I, F, P,
+                                  P, P, SZ, P]),
+        "cpa_latent_prefill_workspace_size": (SZ, [I, I, I, I, I, I, I]),
+        "cpa_latent_prefill": (I, [P, P, I64, I64, P, I64, P, I64, I64, P, P, I, I, I, I, I, I, I, F,
+                                   P, P, P, SZ, P]),
         "cpa_get_device_status": (I, [P, ctypes.POINTER(ctypes.c_uint32), P]),
         "cpa_noalloc_device_status": (I, [ctypes.POINTER(ctypes.c_uint32), P]),
         "cpa_debug_wait_timeout": (I, [P, SZ, I, P]),
@@ -972,6 +995,301 @@ def cpa_cache_compact(k_pages, v_pages, src_page_table, src_pos, n_keep, dst_pag
             None if src_rows is None else src_rows.data_ptr(), src_pos.data_ptr(), max_keep,
             n_keep.data_ptr(), dst, dst_stride, dst_start.data_ptr(), B, P, num_pages, token)
     _launch("cpa_cache_compact", args, dev, stream, workspace, lambda: _STATUS_BYTES, check)
+
+
+# ---------------------------------------------------------------- rows written and read back
+def _rows_of(t, name: str, dtype, shape, dev: int) -> int:
+    """Rows that may lie inside wider ones: `shape` with contiguous rows.  Returns the elements
+    from one row to the next."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}: the call's tensors must be on one device"
+                         if t.is_cuda else f"{name} must be on a CUDA device")
+    _shape(t, name, shape)
+    inner = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != inner:
+            raise ValueError(f"{name}: the values of a token must be contiguous")
+        inner *= n
+    return t.stride(0) if t.shape[0] > 1 else inner
+
+
+def _request_args(page_table, start, lens, lens_name: str, dev: int):
+    """Checks a table with the starts (and lengths or first positions) of its requests; returns
+    (B, columns)."""
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    B, stride = page_table.shape
+    _want(start, "new_start" if lens_name == "seq_lens" else "out_start", torch.int32, 1, dev)
+    if lens is not None:
+        _want(lens, lens_name, torch.int32, 1, dev)
+    if start.shape[0] != B + 1 or (lens is not None and lens.shape[0] != B):
+        raise ValueError("page_table must have a row for each request")
+    return B, stride
+
+
+def _kv_scales(k_scale, v_scale, channels: int, dev: int):
+    """(pointers, per channel) of scales that hold one value or `channels`."""
+    n = k_scale.numel() if isinstance(k_scale, torch.Tensor) else 0
+    for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _want(t, nm, torch.float32, t.dim() if isinstance(t, torch.Tensor) else 1, dev)
+        if t.numel() != n or n not in (1, channels):
+            raise ValueError("k_scale / v_scale must hold 1 or H_kv * head_dim values each")
+    return k_scale.data_ptr(), v_scale.data_ptr(), int(n > 1)
+
+
+def _append(name, k_new, v_new, k_pages, v_pages, scales, page_table, new_start, seq_lens,
+            workspace, stream, check):
+    dev, num_pages, P, token = _any_pools(k_pages, v_pages)
+    H_kv, d = k_pages.shape[2:]
+    if scales:
+        _want(k_pages, "k_pages", torch.uint8, 4, dev)
+    dtype = torch.bfloat16 if scales else k_pages.dtype
+    T = k_new.shape[0] if isinstance(k_new, torch.Tensor) and k_new.dim() == 3 else 0
+    ks = _rows_of(k_new, "k_new", dtype, (T, H_kv, d), dev)
+    vs = _rows_of(v_new, "v_new", dtype, (T, H_kv, d), dev)
+    B, stride = _request_args(page_table, new_start, seq_lens, "seq_lens", dev)
+    es = k_new.element_size()
+    args = (k_new.data_ptr(), v_new.data_ptr(), ks * es, vs * es, k_pages.data_ptr(),
+            v_pages.data_ptr())
+    if scales:
+        args += _kv_scales(*scales, H_kv * d, dev)
+    args += (page_table.data_ptr(), stride, new_start.data_ptr(), seq_lens.data_ptr(), B, T)
+    args += (H_kv * d, P, num_pages) if scales else (P, num_pages, token)
+    _launch(name, args, dev, stream, workspace, lambda: _STATUS_BYTES, check)
+
+
+def cpa_cache_append(k_new, v_new, k_pages, v_pages, page_table, new_start, seq_lens,
+                     workspace=None, stream=None, check: bool = False) -> None:
+    """Write K and V of new tokens to their slots: rows ``new_start[b] .. new_start[b+1]-1`` of
+    ``k_new`` and ``v_new`` [T, H_kv, head_dim] are the last tokens of request b's
+    ``seq_lens[b]``.  The rows may be slices of wider ones (a fused projection's)."""
+    _append("cpa_cache_append", k_new, v_new, k_pages, v_pages, None, page_table, new_start,
+            seq_lens, workspace, stream, check)
+
+
+def cpa_cache_append_fp8(k_new, v_new, k_pages, v_pages, k_scale, v_scale, page_table, new_start,
+                         seq_lens, workspace=None, stream=None, check: bool = False) -> None:
+    """cpa_cache_append of bf16 rows into FP8 E4M3 pages: codes of x / scale, rounded to the
+    nearest and cut at +-448 (pools and scales as for cpa_cascade_verify_fp8)."""
+    _append("cpa_cache_append_fp8", k_new, v_new, k_pages, v_pages, (k_scale, v_scale), page_table,
+            new_start, seq_lens, workspace, stream, check)
+
+
+def _out_rows(T, given) -> int:
+    """Rows of a gather: T, or those of the outputs that the caller gave."""
+    for t in given:
+        if isinstance(t, torch.Tensor) and t.dim() > 0:
+            if T is not None and T != t.shape[0]:
+                raise ValueError(f"T is {T}, the output has {t.shape[0]} rows")
+            return t.shape[0]
+    if T is None:
+        raise ValueError("T, the number of output rows, is needed where no output is given")
+    T = _int(T, "T")
+    if T < 0:
+        raise ValueError("T must not be negative")
+    return T
+
+
+def _gather(name, k_pages, v_pages, scales, page_table, out_start, T, first, k_out, v_out,
+            workspace, stream, check):
+    dev, num_pages, P, token = _any_pools(k_pages, v_pages)
+    H_kv, d = k_pages.shape[2:]
+    if scales:
+        _want(k_pages, "k_pages", torch.uint8, 4, dev)
+    dtype = torch.bfloat16 if scales else k_pages.dtype
+    B, stride = _request_args(page_table, out_start, first, "first", dev)
+    shape = (_out_rows(T, (k_out, v_out)), H_kv, d)
+    if k_out is None:
+        k_out = _new(shape, dtype, dev, stream)
+    if v_out is None:
+        v_out = _new(shape, dtype, dev, stream)
+    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
+        _want(t, nm, dtype, 3, dev)
+        _shape(t, nm, shape)
+    args = (k_pages.data_ptr(), v_pages.data_ptr())
+    if scales:
+        args += _kv_scales(*scales, H_kv * d, dev)
+    args += (page_table.data_ptr(), stride, out_start.data_ptr(),
+             None if first is None else first.data_ptr(), B, shape[0])
+    args += (H_kv * d, P, num_pages) if scales else (P, num_pages, token)
+    _launch(name, args + (k_out.data_ptr(), v_out.data_ptr()), dev, stream, workspace,
+            lambda: _STATUS_BYTES, check)
+    return k_out, v_out
+
+
+def cpa_cache_gather(k_pages, v_pages, page_table, out_start, T: Optional[int] = None, first=None,
+                     k_out=None, v_out=None, workspace=None, stream=None, check: bool = False):
+    """Read rows of the cache back: positions ``first[b]`` (default 0) and on of request b go to
+    rows ``out_start[b] .. out_start[b+1]-1``.  Returns (k_out, v_out), [T, H_kv, head_dim]; rows
+    of no request are not written."""
+    return _gather("cpa_cache_gather", k_pages, v_pages, None, page_table, out_start, T, first,
+                   k_out, v_out, workspace, stream, check)
+
+
+def cpa_cache_gather_fp8(k_pages, v_pages, k_scale, v_scale, page_table, out_start,
+                         T: Optional[int] = None, first=None, k_out=None, v_out=None,
+                         workspace=None, stream=None, check: bool = False):
+    """cpa_cache_gather from FP8 E4M3 pages to bf16 rows (code x scale, rounded once)."""
+    return _gather("cpa_cache_gather_fp8", k_pages, v_pages, (k_scale, v_scale), page_table,
+                   out_start, T, first, k_out, v_out, workspace, stream, check)
+
+
+# ---------------------------------------------------------------- latent attention
+LATENT_DIM, ROPE_DIM, NOPE_DIM = 512, 64, 128
+
+
+def _latent_pool(pages):
+    """(device, pages, page size) of a pool of latents."""
+    dev = _device(pages, "pages", torch.bfloat16)
+    _want(pages, "pages", torch.bfloat16, 3, dev)
+    num_pages, P, width = pages.shape
+    if width != LATENT_DIM + ROPE_DIM:
+        raise ValueError(f"pages must be [num_pages, page_size, {LATENT_DIM + ROPE_DIM}], got "
+                         f"{tuple(pages.shape)}")
+    return dev, num_pages, P
+
+
+def cpa_latent_append(c_new, r_new, pages, page_table, new_start, seq_lens, workspace=None,
+                      stream=None, check: bool = False) -> None:
+    """cpa_cache_append for a pool of latents [num_pages, page_size, 576]: ``c_new`` [T, 512] and
+    ``r_new`` [T, 64], the compressed part and the one that carries the position."""
+    dev, num_pages, P = _latent_pool(pages)
+    T = c_new.shape[0] if isinstance(c_new, torch.Tensor) and c_new.dim() == 2 else 0
+    cs = _rows_of(c_new, "c_new", torch.bfloat16, (T, LATENT_DIM), dev)
+    rs = _rows_of(r_new, "r_new", torch.bfloat16, (T, ROPE_DIM), dev)
+    B, stride = _request_args(page_table, new_start, seq_lens, "seq_lens", dev)
+    args = (c_new.data_ptr(), r_new.data_ptr(), 2 * cs, 2 * rs, pages.data_ptr(),
+            page_table.data_ptr(), stride, new_start.data_ptr(), seq_lens.data_ptr(), B, T,
+            LATENT_DIM, ROPE_DIM, P, num_pages)
+    _launch("cpa_latent_append", args, dev, stream, workspace, lambda: _STATUS_BYTES, check)
+
+
+def cpa_latent_gather(pages, page_table, out_start, T: Optional[int] = None, first=None,
+                      c_out=None, r_out=None, workspace=None, stream=None, check: bool = False):
+    """cpa_cache_gather for a pool of latents.  Returns (c_out [T, 512], r_out [T, 64])."""
+    dev, num_pages, P = _latent_pool(pages)
+    B, stride = _request_args(page_table, out_start, first, "first", dev)
+    T = _out_rows(T, (c_out, r_out))
+    if c_out is None:
+        c_out = _new((T, LATENT_DIM), torch.bfloat16, dev, stream)
+    if r_out is None:
+        r_out = _new((T, ROPE_DIM), torch.bfloat16, dev, stream)
+    for t, nm, width in ((c_out, "c_out", LATENT_DIM), (r_out, "r_out", ROPE_DIM)):
+        _want(t, nm, torch.bfloat16, 2, dev)
+        _shape(t, nm, (T, width))
+    args = (pages.data_ptr(), page_table.data_ptr(), stride, out_start.data_ptr(),
+            None if first is None else first.data_ptr(), B, T, LATENT_DIM, ROPE_DIM, P, num_pages,
+            c_out.data_ptr(), r_out.data_ptr())
+    _launch("cpa_latent_gather", args, dev, stream, workspace, lambda: _STATUS_BYTES, check)
+    return c_out, r_out
+
+
+def _heads_of(t, name: str, shape, dev: int):
+    """Checks [tokens, heads, width] bf16 whose last dimension is contiguous; returns the strides
+    of a token and a head in elements (the least that says nothing where there is one)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}: the call's tensors must be on one device"
+                         if t.is_cuda else f"{name} must be on a CUDA device")
+    _shape(t, name, shape)
+    n, H, w = shape
+    if t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    return (t.stride(0) if n > 1 else H * w), (t.stride(1) if H > 1 else w)
+
+
+def cpa_latent_decode_workspace_size(B, S, H, latent_dim=LATENT_DIM, rope_dim=ROPE_DIM,
+                                     page_size=16) -> int:
+    return lib().cpa_latent_decode_workspace_size(B, S, H, latent_dim, rope_dim, page_size)
+
+
+def cpa_latent_decode(q_c, q_r, pages, page_table, seq_lens, S: int = 1,
+                      max_seq_len: Optional[int] = None, sm_scale: Optional[float] = None, o=None,
+                      lse=None, workspace=None, stream=None, check: bool = False):
+    """Latent attention in its absorbed form.  Returns (o bf16 [B*S, H, 512], lse fp32).
+
+    ``q_c`` [B*S, H, 512] and ``q_r`` [B*S, H, 64] are the queries against the two parts of a
+    latent, ``pages`` [num_pages, page_size, 576] the cache.  Token s of request b is at position
+    ``seq_lens[b] - S + s`` and sees the keys up to its own.  ``sm_scale`` defaults to
+    (128 + 64) ** -0.5, that of the expanded head.
+    """
+    dev, num_pages, P = _latent_pool(pages)
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    _want(seq_lens, "seq_lens", torch.int32, 1, dev)
+    B, S = seq_lens.shape[0], _int(S, "S")
+    if not isinstance(q_c, torch.Tensor):
+        raise TypeError("q_c must be a torch.Tensor")
+    if S < 1 or q_c.dim() != 3 or q_c.shape[0] != B * S or page_table.shape[0] != B:
+        raise ValueError("inconsistent latent decode shapes")
+    n, H = q_c.shape[:2]
+    qc = _heads_of(q_c, "q_c", (n, H, LATENT_DIM), dev)
+    qr = _heads_of(q_r, "q_r", (n, H, ROPE_DIM), dev)
+    stride = page_table.shape[1]
+    if o is None:
+        o = _new((n, H, LATENT_DIM), torch.bfloat16, dev, stream)
+    if lse is None:
+        lse = _new((n, H), torch.float32, dev, stream)
+    _want(o, "o", torch.bfloat16, 3, dev)
+    _want(lse, "lse", torch.float32, 2, dev)
+    _shape(o, "o", (n, H, LATENT_DIM))
+    _shape(lse, "lse", (n, H))
+    args = (q_c.data_ptr(), *qc, q_r.data_ptr(), *qr, pages.data_ptr(), page_table.data_ptr(),
+            stride, seq_lens.data_ptr(), B, S, H, LATENT_DIM, ROPE_DIM, P, num_pages,
+            _max_len(max_seq_len, stride, P),
+            (NOPE_DIM + ROPE_DIM) ** -0.5 if sm_scale is None else float(sm_scale), o.data_ptr(),
+            lse.data_ptr())
+    _launch("cpa_latent_decode", args, dev, stream, workspace,
+            lambda: cpa_latent_decode_workspace_size(B, S, H, LATENT_DIM, ROPE_DIM, P), check)
+    return o, lse
+
+
+def cpa_latent_prefill_workspace_size(B, T, T_k, H, nope_dim=NOPE_DIM, rope_dim=ROPE_DIM,
+                                      v_dim=NOPE_DIM) -> int:
+    return lib().cpa_latent_prefill_workspace_size(B, T, T_k, H, nope_dim, rope_dim, v_dim)
+
+
+def cpa_latent_prefill(q, k_nope, k_rope, v, q_start, k_start, sm_scale: Optional[float] = None,
+                       o=None, lse=None, workspace=None, stream=None, check: bool = False):
+    """Latent attention in its expanded form: causal prefill of ragged prompt chunks.  Returns
+    (o bf16 [T, H, 128], lse fp32); rows that belong to no request are not written.
+
+    Request b has the new tokens ``q_start[b] .. q_start[b+1]-1`` of ``q`` [T, H, 192] and the
+    keys and values ``k_start[b] .. k_start[b+1]-1`` of ``k_nope`` and ``v`` [T_k, H, 128] (which
+    may be slices of one product) and ``k_rope`` [T_k, 64], the new tokens' last.
+    """
+    dev = _device(q, "q", torch.bfloat16)
+    _want(q, "q", torch.bfloat16, 3, dev)
+    _want(q_start, "q_start", torch.int32, 1, dev)
+    _want(k_start, "k_start", torch.int32, 1, dev)
+    T, H, width = q.shape
+    B = q_start.shape[0] - 1
+    if width != NOPE_DIM + ROPE_DIM or k_start.shape[0] != B + 1:
+        raise ValueError("inconsistent latent prefill shapes")
+    T_k = k_nope.shape[0] if isinstance(k_nope, torch.Tensor) and k_nope.dim() == 3 else 0
+    ks = _heads_of(k_nope, "k_nope", (T_k, H, NOPE_DIM), dev)
+    vs = _heads_of(v, "v", (T_k, H, NOPE_DIM), dev)
+    rs = _rows_of(k_rope, "k_rope", torch.bfloat16, (T_k, ROPE_DIM), dev)
+    if o is None:
+        o = _new((T, H, NOPE_DIM), torch.bfloat16, dev, stream)
+    if lse is None:
+        lse = _new((T, H), torch.float32, dev, stream)
+    _want(o, "o", torch.bfloat16, 3, dev)
+    _want(lse, "lse", torch.float32, 2, dev)
+    _shape(o, "o", (T, H, NOPE_DIM))
+    _shape(lse, "lse", (T, H))
+    args = (q.data_ptr(), k_nope.data_ptr(), *ks, k_rope.data_ptr(), rs, v.data_ptr(), *vs,
+            q_start.data_ptr(), k_start.data_ptr(), B, T, T_k, H, NOPE_DIM, ROPE_DIM, NOPE_DIM,
+            (NOPE_DIM + ROPE_DIM) ** -0.5 if sm_scale is None else float(sm_scale), o.data_ptr(),
+            lse.data_ptr())
+    _launch("cpa_latent_prefill", args, dev, stream, workspace,
+            lambda: cpa_latent_prefill_workspace_size(B, T, T_k, H), check)
+    return o, lse
 
 
 def cpa_get_device_status(workspace: torch.Tensor, stream=None) -> tuple[int, int]:

@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libcpa.so")
 # Diagnostic variant with the kernels' trace hooks compiled in (-DCPA_TRACE);
 # never loaded unless CPA_LIBRARY names it.
 TRACE_LIB = os.path.join(HERE, "libcpa_trace.so")
-SOURCES = ["cpa_api.cu", "cpa_small.cu", "cpa_decode.cu", "cpa_window.cu", "cpa_cache.cu"]
+SOURCES = ["cpa_api.cu", "cpa_small.cu", "cpa_decode.cu", "cpa_window.cu", "cpa_cache.cu",
+           "cpa_rows.cu", "cpa_latent.cu", "cpa_latent_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,413 @@
+// cpa_rows.cu -- rows of new tokens written to the pages of a cache, and rows of a
+// cache read back: bf16 as it is, FP8 E4M3 quantised on the way in and widened on
+// the way out, latents (two rows of unequal width that share a slot).
+//
+// A code is e4m3(x / scale), the quotient in 32 bits, rounded to the nearest with
+// ties to even, cut at +-448; what is read back is bf16(code * scale), the product
+// in 32 bits.
+//
+// What bounds it: HBM for prompts (a row is read once and written once), latency for
+// the tokens of a decode step.
+//
+// A warp takes up to 32 tokens and a segment of 32 pieces (a piece is 8 elements: 16
+// bytes of a row in bf16, 8 codes in an FP8 page).  Its lanes first look up the slots
+// of the tokens, one each, all at once; then lane l moves piece l of one token after
+// the other, kUnroll tokens' loads in flight.  So the scales of its 8 channels stay in
+// registers, and a row narrower than a segment (the 64 columns of a latent that
+// carry the position: 8 pieces) shares the warp with the next tokens' rows.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cpa.h"
+#include "cpa_checks.h"
+#include "cpa_device.cuh"
+#include "cpa_launch.cuh"
+
+namespace cpa {
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kUnroll = 8;
+constexpr int kLatentC = 512, kLatentR = 64;  // elements of a latent's two parts
+
+struct RowParams {
+    uint8_t* rows[2];       // ragged rows (of new tokens, or the output)
+    uint8_t* pages[2];      // the pool, from the first byte that the part has of a slot
+    size_t row_bytes[2];    // from one row to the next
+    size_t slot_bytes[2];   // from one slot of the pool to the next
+    const float* scale[2];
+    int pieces[2];          // of a row
+    int log_lanes[2];       // lanes that a row takes of a warp (8, 16 or 32)
+    int segments[2];
+    const int32_t* table;
+    const int32_t* start;
+    const int32_t* lens;    // of the sequences (append), or first positions (gather; may be null)
+    uint32_t* status;
+    int stride, B, T, lp, num_pages, per_channel;
+    int tokens;             // of a warp
+    long long max_len;      // positions that a row of the table holds
+    int status_block;       // the last block looks the call over and writes the status word
+};
+
+// What a request asks for: its rows [s0, s1) and the position of the first.
+struct RowRequest {
+    int s0, s1;
+    long long pos;
+    bool ok;
+};
+template <bool GATHER>
+__device__ __forceinline__ RowRequest row_request(const RowParams& p, int b) {
+    RowRequest r;
+    r.s0 = __ldg(p.start + b);
+    r.s1 = __ldg(p.start + b + 1);
+    const long long x = p.lens ? __ldg(p.lens + b) : 0, m = (long long)r.s1 - r.s0;
+    r.pos = GATHER ? x : x - m;
+    r.ok = r.s0 >= 0 && m >= 0 && r.s1 <= p.T && r.pos >= 0 && r.pos + m <= p.max_len;
+    return r;
+}
+
+// The slot of token t of a warp's run t0 .. t0 + n - 1 (lane i: token t0 + i), or -1
+// where there is nothing to move.  Every lane takes part.
+template <bool GATHER>
+__device__ __forceinline__ int slot_of_token(const RowParams& p, int t0, int n, uint32_t& bad) {
+    const int lane = threadIdx.x & 31;
+    // the last request that starts at or before t0: 32 probes at a time
+    int lo = 0, hi = p.B;  // it is in [lo, hi)
+    while (hi - lo > 32) {
+        const int step = (hi - lo + 31) >> 5;
+        const int b = lo + lane * step;
+        const uint32_t le = __ballot_sync(0xffffffffu, b < hi && __ldg(p.start + b) <= t0);
+        const int k = le ? 31 - __clz((int)le) : 0;
+        hi = min(hi, lo + (k + 1) * step);
+        lo += k * step;
+    }
+    // each token's request: those of the 32 starts behind lo that are at or before it
+    const int t = t0 + lane;
+    int b = lo;
+    for (int base = lo;; base += 32) {
+        const int s = base + 1 + lane < p.B ? __ldg(p.start + base + 1 + lane) : 0x7fffffff;
+        int k = 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            if (__shfl_sync(0xffffffffu, s, k + o - 1) <= t) k += o;
+        k += __shfl_sync(0xffffffffu, s, k) <= t ? 1 : 0;
+        if (b == base) b = base + k;
+        if (!__any_sync(0xffffffffu, lane < n && b == base + 32)) break;
+    }
+    if (lane >= n || b >= p.B) return -1;
+    const RowRequest r = row_request<GATHER>(p, b);
+    if (!r.ok || t < r.s0 || t >= r.s1) return -1;
+    const long long pos = r.pos + (t - r.s0);
+    const int pg = __ldg(p.table + (size_t)b * p.stride + (pos >> p.lp));
+    if (pg < 0 || pg >= p.num_pages) {
+        bad |= CPA_DEV_BAD_PAGE;
+        return -1;
+    }
+    return (int)(((uint32_t)pg << p.lp) + ((uint32_t)pos & ((1u << p.lp) - 1u)));
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <bool FP8, bool GATHER>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(RowParams p) {
+    const int lane = threadIdx.x & 31;
+    uint32_t bad = 0;
+    if (p.status_block && blockIdx.x == gridDim.x - 1) {
+        for (int b = threadIdx.x; b < p.B; b += kRowThreads)
+            if (!row_request<GATHER>(p, b).ok) bad |= CPA_DEV_BAD_LENGTH;
+        for (int t0 = (threadIdx.x >> 5) * 32; t0 < p.T; t0 += kRowThreads)
+            slot_of_token<GATHER>(p, t0, min(32, p.T - t0), bad);
+        const bool page = __syncthreads_or((int)(bad & CPA_DEV_BAD_PAGE));
+        const bool len = __syncthreads_or((int)(bad & CPA_DEV_BAD_LENGTH));
+        if (threadIdx.x == 0)
+            *p.status = (page ? CPA_DEV_BAD_PAGE : 0u) | (len ? CPA_DEV_BAD_LENGTH : 0u);
+        return;
+    }
+    if (!p.status_block) {
+        wait_for_clear();
+        if (blockIdx.x == 0)
+            for (int b = threadIdx.x; b < p.B; b += kRowThreads)
+                if (!row_request<GATHER>(p, b).ok) bad |= CPA_DEV_BAD_LENGTH;
+    }
+    const int per_group = p.segments[0] + p.segments[1];
+    const long long w = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    const long long t0 = w / per_group * p.tokens;
+    if (t0 < p.T) {
+        int seg = (int)(w % per_group);
+        const int part = seg >= p.segments[0] ? 1 : 0;
+        if (part) seg -= p.segments[0];
+        const int n = min(p.tokens, p.T - (int)t0);
+        const int slot = slot_of_token<GATHER>(p, (int)t0, n, bad);
+        const int log_lanes = p.log_lanes[part], sub = 32 >> log_lanes;
+        const int piece = seg * 32 + (lane & ((1 << log_lanes) - 1)), mine = lane >> log_lanes;
+        const bool inside = piece < p.pieces[part];
+        float scale[8];
+        if (FP8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                scale[i] = __ldg(p.scale[part] + (p.per_channel && inside ? piece * 8 + i : 0));
+        }
+        uint8_t* const rows = p.rows[part] + (size_t)piece * 16;
+        uint8_t* const pages = p.pages[part] + (size_t)piece * (FP8 ? 8 : 16);
+        const size_t row_bytes = p.row_bytes[part], slot_bytes = p.slot_bytes[part];
+        for (int i0 = 0; i0 < n; i0 += sub * kUnroll) {
+            uint4 x[kUnroll];
+            int at[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int i = i0 + u * sub + mine;
+                at[u] = __shfl_sync(0xffffffffu, slot, i & 31);
+                if (i >= n || !inside) at[u] = -1;
+                if (at[u] < 0) continue;
+                if (!GATHER) {
+                    x[u] = __ldcs(reinterpret_cast<const uint4*>(rows + (size_t)(t0 + i) * row_bytes));
+                } else if (FP8) {
+                    const uint2 c = __ldcs(reinterpret_cast<const uint2*>(pages + (size_t)at[u] * slot_bytes));
+                    x[u].x = c.x;
+                    x[u].y = c.y;
+                } else {
+                    x[u] = __ldcs(reinterpret_cast<const uint4*>(pages + (size_t)at[u] * slot_bytes));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (at[u] < 0) continue;
+                const int i = i0 + u * sub + mine;
+                if (GATHER) {
+                    if (FP8) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t h = e4m3x2_to_f16x2(k < 2 ? x[u].x : x[u].y, k & 1);
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                            o[k] = pack_bf16x2(f.x * scale[2 * k], f.y * scale[2 * k + 1]);
+                        }
+                        x[u] = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    *reinterpret_cast<uint4*>(rows + (size_t)(t0 + i) * row_bytes) = x[u];
+                } else if (FP8) {
+                    float f[8];
+                    bf16x8_to_f32(x[u], f);
+                    uint32_t c[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        c[k] = e4m3x2(f[2 * k] / scale[2 * k], f[2 * k + 1] / scale[2 * k + 1]);
+                    *reinterpret_cast<uint2*>(pages + (size_t)at[u] * slot_bytes) =
+                        make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+                } else {
+                    *reinterpret_cast<uint4*>(pages + (size_t)at[u] * slot_bytes) = x[u];
+                }
+            }
+        }
+    }
+    if (bad && !p.status_block) flag(p.status, bad);
+}
+
+// One part of a row: `bytes` of it in bf16.
+void set_part(RowParams& p, int i, const void* rows, size_t row_bytes, void* pages,
+              size_t slot_bytes, size_t bytes, const float* scale) {
+    p.rows[i] = static_cast<uint8_t*>(const_cast<void*>(rows));
+    p.pages[i] = static_cast<uint8_t*>(pages);
+    p.row_bytes[i] = row_bytes;
+    p.slot_bytes[i] = slot_bytes;
+    p.scale[i] = scale;
+    p.pieces[i] = (int)(bytes / 16);
+    p.log_lanes[i] = p.pieces[i] > 16 ? 5 : p.pieces[i] > 8 ? 4 : 3;
+    p.segments[i] = (p.pieces[i] + 31) / 32;
+}
+
+// Checks that every call shares; parts are set when it returns CPA_OK.
+cpa_status rows_ready(RowParams& p, const int32_t* table, int stride, const int32_t* start,
+                      const int32_t* lens, int B, int T, int page_size, int num_pages,
+                      void* workspace, size_t workspace_bytes) {
+    if (!table || !start || B < 1 || T < 0 || num_pages < 1 || stride < 1)
+        return CPA_ERR_INVALID_ARG;
+    if (!page_size_ok(page_size)) return CPA_ERR_UNSUPPORTED;
+    if ((long long)num_pages * page_size > (1ll << 31) || T > kMaxLength)
+        return CPA_ERR_UNSUPPORTED;
+    const cpa_status st = status_ws(workspace, workspace_bytes);
+    if (st != CPA_OK) return st;
+    p.table = table;
+    p.start = start;
+    p.lens = lens;
+    p.status = static_cast<uint32_t*>(workspace);
+    p.stride = stride;
+    p.B = B;
+    p.T = T;
+    p.lp = 31 - __builtin_clz((unsigned)page_size);
+    p.num_pages = num_pages;
+    p.max_len = (long long)stride * page_size;
+    if (p.max_len > kMaxLength) p.max_len = kMaxLength;
+    return CPA_OK;
+}
+
+template <bool FP8, bool GATHER>
+cpa_status launch_rows(RowParams& p, cudaStream_t s) {
+    if (p.T == 0) return clear_status(p.status, s);
+    const int n_sm = sm_count();
+    if (n_sm <= 0) return CPA_ERR_CUDA;
+    const long long per_group = p.segments[0] + p.segments[1];
+    // few tokens: fewer to a warp, so that all SMs take part
+    p.tokens = 32;
+    while (p.tokens > 4 && (long long)(p.T / p.tokens) * per_group < (long long)n_sm * 16)
+        p.tokens /= 2;
+    const long long warps = ((long long)p.T + p.tokens - 1) / p.tokens * per_group;
+    // a block more looks a small call over and writes the status word
+    p.status_block = p.T <= 4096 && p.B <= 4096 ? 1 : 0;
+    const dim3 grid((unsigned)((warps + kRowWarps - 1) / kRowWarps + p.status_block));
+    if (!p.status_block)
+        return launch_cleared(rows_kernel<FP8, GATHER>, grid, kRowThreads, s, p.status, p);
+    rows_kernel<FP8, GATHER><<<grid, kRowThreads, 0, s>>>(p);
+    return launched();
+}
+
+bool stride_ok(size_t stride, int T) { return T <= 1 || stride % 16 == 0; }
+
+}  // namespace
+}  // namespace cpa
+
+using namespace cpa;
+
+extern "C" {
+
+cpa_status cpa_cache_append(const void* k_new, const void* v_new, size_t k_stride_bytes,
+                            size_t v_stride_bytes, void* k_pages, void* v_pages,
+                            const int32_t* page_table, int pt_stride, const int32_t* new_start,
+                            const int32_t* seq_lens, int B, int T, int page_size, int num_pages,
+                            size_t token_bytes, void* workspace, size_t workspace_bytes,
+                            cpa_stream_t stream) {
+    if (!k_pages || !v_pages || !seq_lens || token_bytes < 16 || token_bytes % 16)
+        return CPA_ERR_INVALID_ARG;
+    if (T > 0 && (!k_new || !v_new)) return CPA_ERR_INVALID_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_new) || !aligned16(v_new) ||
+        !stride_ok(k_stride_bytes, T) || !stride_ok(v_stride_bytes, T))
+        return CPA_ERR_INVALID_ARG;
+    if (token_bytes > ((size_t)1 << 20)) return CPA_ERR_UNSUPPORTED;
+    RowParams p = {};
+    const cpa_status st = rows_ready(p, page_table, pt_stride, new_start, seq_lens, B, T, page_size,
+                                     num_pages, workspace, workspace_bytes);
+    if (st != CPA_OK) return st;
+    set_part(p, 0, k_new, k_stride_bytes, k_pages, token_bytes, token_bytes, nullptr);
+    set_part(p, 1, v_new, v_stride_bytes, v_pages, token_bytes, token_bytes, nullptr);
+    return launch_rows<false, false>(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cpa_status cpa_cache_append_fp8(const void* k_new, const void* v_new, size_t k_stride_bytes,
+                                size_t v_stride_bytes, void* k_pages, void* v_pages,
+                                const float* k_scale, const float* v_scale, int scale_per_channel,
+                                const int32_t* page_table, int pt_stride,
+                                const int32_t* new_start, const int32_t* seq_lens, int B, int T,
+                                int channels, int page_size, int num_pages, void* workspace,
+                                size_t workspace_bytes, cpa_stream_t stream) {
+    if (!k_pages || !v_pages || !k_scale || !v_scale || !seq_lens || channels < 16 || channels % 16)
+        return CPA_ERR_INVALID_ARG;
+    if (T > 0 && (!k_new || !v_new)) return CPA_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)channels * 2;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_new) || !aligned16(v_new) ||
+        !stride_ok(k_stride_bytes, T) || !stride_ok(v_stride_bytes, T))
+        return CPA_ERR_INVALID_ARG;
+    if (channels > (1 << 19)) return CPA_ERR_UNSUPPORTED;
+    RowParams p = {};
+    const cpa_status st = rows_ready(p, page_table, pt_stride, new_start, seq_lens, B, T, page_size,
+                                     num_pages, workspace, workspace_bytes);
+    if (st != CPA_OK) return st;
+    p.per_channel = scale_per_channel ? 1 : 0;
+    set_part(p, 0, k_new, k_stride_bytes, k_pages, (size_t)channels, bytes, k_scale);
+    set_part(p, 1, v_new, v_stride_bytes, v_pages, (size_t)channels, bytes, v_scale);
+    return launch_rows<true, false>(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cpa_status cpa_latent_append(const void* c_new, const void* r_new, size_t c_stride_bytes,
+                             size_t r_stride_bytes, void* pages, const int32_t* page_table,
+                             int pt_stride, const int32_t* new_start, const int32_t* seq_lens,
+                             int B, int T, int latent_dim, int rope_dim, int page_size,
+                             int num_pages, void* workspace, size_t workspace_bytes,
+                             cpa_stream_t stream) {
+    if (!pages || !seq_lens) return CPA_ERR_INVALID_ARG;
+    if (T > 0 && (!c_new || !r_new)) return CPA_ERR_INVALID_ARG;
+    if (latent_dim != kLatentC || rope_dim != kLatentR) return CPA_ERR_UNSUPPORTED;
+    if (!aligned16(pages) || !aligned16(c_new) || !aligned16(r_new) ||
+        !stride_ok(c_stride_bytes, T) || !stride_ok(r_stride_bytes, T))
+        return CPA_ERR_INVALID_ARG;
+    RowParams p = {};
+    const cpa_status st = rows_ready(p, page_table, pt_stride, new_start, seq_lens, B, T, page_size,
+                                     num_pages, workspace, workspace_bytes);
+    if (st != CPA_OK) return st;
+    const size_t slot = (kLatentC + kLatentR) * 2;
+    set_part(p, 0, c_new, c_stride_bytes, pages, slot, kLatentC * 2, nullptr);
+    set_part(p, 1, r_new, r_stride_bytes, static_cast<uint8_t*>(pages) + kLatentC * 2, slot,
+             kLatentR * 2, nullptr);
+    return launch_rows<false, false>(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cpa_status cpa_cache_gather(const void* k_pages, const void* v_pages, const int32_t* page_table,
+                            int pt_stride, const int32_t* out_start, const int32_t* first, int B,
+                            int T, int page_size, int num_pages, size_t token_bytes, void* k_out,
+                            void* v_out, void* workspace, size_t workspace_bytes,
+                            cpa_stream_t stream) {
+    if (!k_pages || !v_pages || token_bytes < 16 || token_bytes % 16) return CPA_ERR_INVALID_ARG;
+    if (T > 0 && (!k_out || !v_out)) return CPA_ERR_INVALID_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_out) || !aligned16(v_out))
+        return CPA_ERR_INVALID_ARG;
+    if (token_bytes > ((size_t)1 << 20)) return CPA_ERR_UNSUPPORTED;
+    RowParams p = {};
+    const cpa_status st = rows_ready(p, page_table, pt_stride, out_start, first, B, T, page_size,
+                                     num_pages, workspace, workspace_bytes);
+    if (st != CPA_OK) return st;
+    set_part(p, 0, k_out, token_bytes, const_cast<void*>(k_pages), token_bytes, token_bytes, nullptr);
+    set_part(p, 1, v_out, token_bytes, const_cast<void*>(v_pages), token_bytes, token_bytes, nullptr);
+    return launch_rows<false, true>(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cpa_status cpa_cache_gather_fp8(const void* k_pages, const void* v_pages, const float* k_scale,
+                                const float* v_scale, int scale_per_channel,
+                                const int32_t* page_table, int pt_stride,
+                                const int32_t* out_start, const int32_t* first, int B, int T,
+                                int channels, int page_size, int num_pages, void* k_out,
+                                void* v_out, void* workspace, size_t workspace_bytes,
+                                cpa_stream_t stream) {
+    if (!k_pages || !v_pages || !k_scale || !v_scale || channels < 16 || channels % 16)
+        return CPA_ERR_INVALID_ARG;
+    if (T > 0 && (!k_out || !v_out)) return CPA_ERR_INVALID_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_out) || !aligned16(v_out))
+        return CPA_ERR_INVALID_ARG;
+    if (channels > (1 << 19)) return CPA_ERR_UNSUPPORTED;
+    RowParams p = {};
+    const cpa_status st = rows_ready(p, page_table, pt_stride, out_start, first, B, T, page_size,
+                                     num_pages, workspace, workspace_bytes);
+    if (st != CPA_OK) return st;
+    p.per_channel = scale_per_channel ? 1 : 0;
+    const size_t bytes = (size_t)channels * 2;
+    set_part(p, 0, k_out, bytes, const_cast<void*>(k_pages), (size_t)channels, bytes, k_scale);
+    set_part(p, 1, v_out, bytes, const_cast<void*>(v_pages), (size_t)channels, bytes, v_scale);
+    return launch_rows<true, true>(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cpa_status cpa_latent_gather(const void* pages, const int32_t* page_table, int pt_stride,
+                             const int32_t* out_start, const int32_t* first, int B, int T,
+                             int latent_dim, int rope_dim, int page_size, int num_pages,
+                             void* c_out, void* r_out, void* workspace, size_t workspace_bytes,
+                             cpa_stream_t stream) {
+    if (!pages) return CPA_ERR_INVALID_ARG;
+    if (T > 0 && (!c_out || !r_out)) return CPA_ERR_INVALID_ARG;
+    if (latent_dim != kLatentC || rope_dim != kLatentR) return CPA_ERR_UNSUPPORTED;
+    if (!aligned16(pages) || !aligned16(c_out) || !aligned16(r_out)) return CPA_ERR_INVALID_ARG;
+    RowParams p = {};
+    const cpa_status st = rows_ready(p, page_table, pt_stride, out_start, first, B, T, page_size,
+                                     num_pages, workspace, workspace_bytes);
+    if (st != CPA_OK) return st;
+    const size_t slot = (kLatentC + kLatentR) * 2;
+    uint8_t* const base = static_cast<uint8_t*>(const_cast<void*>(pages));
+    set_part(p, 0, c_out, kLatentC * 2, base, slot, kLatentC * 2, nullptr);
+    set_part(p, 1, r_out, kLatentR * 2, base + kLatentC * 2, slot, kLatentR * 2, nullptr);
+    return launch_rows<false, true>(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

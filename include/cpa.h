@@ -569,6 +569,170 @@ cpa_status cpa_cache_compact(void* k_pages, void* v_pages, const int32_t* src_ta
                              void* workspace, size_t workspace_bytes, cpa_stream_t stream);
 
 /*
+ * Rows of new tokens written to the pages, and rows read back.
+ *
+ * cpa_cache_append: K and V of the new tokens of each request go to their slots.
+ * Request b has the rows new_start[b] .. new_start[b+1]-1 of k_new and v_new, m_b
+ * of them; they are the last m_b tokens of its sequence of seq_lens[b] tokens
+ * (the new ones among them, as cpa_window_prefill takes it): row new_start[b] + i
+ * goes to position seq_lens[b] - m_b + i.  Every other slot is left as it was.
+ *   k_new, v_new  T rows of token_bytes, 16-byte aligned, k_stride_bytes and
+ *                 v_stride_bytes apart (multiples of 16: rows may lie inside
+ *                 wider ones, as those of a fused projection do)
+ *   page_table    int32 [B, pt_stride]
+ *   new_start     int32 [B + 1] on the device, ascending, 0 <= new_start[0] and
+ *                 new_start[B] <= T; rows outside belong to no request
+ *   seq_lens      int32 [B] on the device, m_b <= seq_lens[b] <= pt_stride * page_size
+ *                 (and 2^30)
+ *   token_bytes   K (or V) of one token: H_kv x head_dim x element size, a
+ *                 multiple of 16 up to 2^20
+ * No slot may be written twice by a call: a page that two sequences share takes new
+ * tokens of one of them at most (cpa_cache_fork shares whole pages only).
+ * A new_start that is not ascending or leaves [0, T] or a length out of range sets
+ * CPA_DEV_BAD_LENGTH, a page id outside [0, num_pages) CPA_DEV_BAD_PAGE; such a
+ * request's, or such a page's, tokens are not written, all others are.
+ * T up to 2^30.  Workspace: cpa_status_workspace_size().
+ */
+cpa_status cpa_cache_append(const void* k_new, const void* v_new, size_t k_stride_bytes,
+                            size_t v_stride_bytes, void* k_pages, void* v_pages,
+                            const int32_t* page_table, int pt_stride, const int32_t* new_start,
+                            const int32_t* seq_lens, int B, int T, int page_size, int num_pages,
+                            size_t token_bytes, void* workspace, size_t workspace_bytes,
+                            cpa_stream_t stream);
+
+/*
+ * cpa_cache_append_fp8: bf16 rows of `channels` (H_kv x head_dim, a multiple of 16
+ * up to 2^19) quantised into FP8 E4M3 pages, with the scales that
+ * cpa_cascade_verify_fp8 and cpa_decode_fp8 read (fp32, one value or one per
+ * channel): the code of x is x / scale in 32 bits, rounded to the nearest E4M3
+ * value, ties to even, and cut at +-448 (infinities too); a NaN stays one.
+ */
+cpa_status cpa_cache_append_fp8(const void* k_new, const void* v_new, size_t k_stride_bytes,
+                                size_t v_stride_bytes, void* k_pages, void* v_pages,
+                                const float* k_scale, const float* v_scale, int scale_per_channel,
+                                const int32_t* page_table, int pt_stride,
+                                const int32_t* new_start, const int32_t* seq_lens, int B, int T,
+                                int channels, int page_size, int num_pages, void* workspace,
+                                size_t workspace_bytes, cpa_stream_t stream);
+
+/*
+ * cpa_cache_gather: rows of the cache as one contiguous array.  Request b's tokens
+ * at positions first[b] .. first[b] + n_b - 1 go to rows out_start[b] ..
+ * out_start[b+1]-1, n_b of them, of k_out and v_out (T rows of token_bytes each,
+ * 16-byte aligned, not over any input).  first NULL: position 0.  Rows of no
+ * request, and those whose request or page sets a bit of the status word (as for
+ * cpa_cache_append, with first[b] + n_b in the place of the length), are left as
+ * they were.  Workspace: cpa_status_workspace_size().
+ */
+cpa_status cpa_cache_gather(const void* k_pages, const void* v_pages, const int32_t* page_table,
+                            int pt_stride, const int32_t* out_start, const int32_t* first, int B,
+                            int T, int page_size, int num_pages, size_t token_bytes, void* k_out,
+                            void* v_out, void* workspace, size_t workspace_bytes,
+                            cpa_stream_t stream);
+
+/* cpa_cache_gather_fp8: the same from FP8 E4M3 pages to bf16 rows: code x scale in 32
+ * bits, rounded once (a NaN code gives NaN). */
+cpa_status cpa_cache_gather_fp8(const void* k_pages, const void* v_pages, const float* k_scale,
+                                const float* v_scale, int scale_per_channel,
+                                const int32_t* page_table, int pt_stride,
+                                const int32_t* out_start, const int32_t* first, int B, int T,
+                                int channels, int page_size, int num_pages, void* k_out,
+                                void* v_out, void* workspace, size_t workspace_bytes,
+                                cpa_stream_t stream);
+
+/*
+ * Latent attention.  The keys and values of all heads come from one vector a token:
+ * latent_dim elements c that every head's products expand, and rope_dim elements r
+ * that carry the position and are part of every head's key as they are.  Head h has
+ * the key [W_k,h c; r] and the value W_v,h c.  Two forms give the same attention:
+ * absorbed (cpa_latent_decode: the queries go through W_k,h first and the outputs
+ * through W_v,h afterwards, and attention is over the latents themselves) and
+ * expanded (cpa_latent_prefill, over the products).  sm_scale is that of the expanded
+ * head in both, (nope_dim + rope_dim)^-1/2 by custom.
+ *
+ * The cache of latents is one pool, bf16 [num_pages, page_size, latent_dim +
+ * rope_dim], c first; the page operations take it as a pool of tokens of
+ * 2 x (latent_dim + rope_dim) bytes.
+ *
+ * cpa_latent_append and cpa_latent_gather are cpa_cache_append and cpa_cache_gather
+ * for that pool: the two parts come from, and go to, arrays of their own.
+ */
+cpa_status cpa_latent_append(const void* c_new, const void* r_new, size_t c_stride_bytes,
+                             size_t r_stride_bytes, void* pages, const int32_t* page_table,
+                             int pt_stride, const int32_t* new_start, const int32_t* seq_lens,
+                             int B, int T, int latent_dim, int rope_dim, int page_size,
+                             int num_pages, void* workspace, size_t workspace_bytes,
+                             cpa_stream_t stream);
+
+cpa_status cpa_latent_gather(const void* pages, const int32_t* page_table, int pt_stride,
+                             const int32_t* out_start, const int32_t* first, int B, int T,
+                             int latent_dim, int rope_dim, int page_size, int num_pages,
+                             void* c_out, void* r_out, void* workspace, size_t workspace_bytes,
+                             cpa_stream_t stream);
+
+/*
+ * cpa_latent_decode: S query tokens of each request against its paged latents.
+ * Token s of request b is at position p = seq_lens[b] - S + s (S = 1: the newest
+ * token; S > 1: a token and the drafts after it, whose latents are in the cache) and
+ * sees the keys j <= p; with p < 0 it sees none.  Head h of it has the scores
+ *     x_j = sm_scale (q_c . c_j + q_r . r_j)
+ * and the output sum_j softmax(x)_j c_j, of latent_dim elements.
+ *   q_c, q_r    bf16, element (t, h, i) at t * token_stride + h * head_stride + i
+ *               for token t = b*S + s: latent_dim and rope_dim elements, strides in
+ *               elements, multiples of 8 and positive (where there is more than one
+ *               token, or head)
+ *   page_table  int32 [B, pt_stride], pt_stride >= ceil(max_seq_len / page_size)
+ *   seq_lens    int32 [B] on the device, 0 <= seq_lens[b] <= max_seq_len
+ *   o, lse      bf16 [B*S, H, latent_dim] (32-byte aligned), fp32 [B*S, H]; not over
+ *               any input
+ * A NaN or an infinity in a latent reaches the rows that see it and no others.
+ * The work is split over the visible length and joined, in a fixed order: the
+ * result of a call depends on its inputs and the device's SM count alone.
+ * Supported: latent_dim 512, rope_dim 64; page_size in {8,16,32,64,128,256};
+ * B*S*H up to 2^22; max_seq_len up to 2^30.
+ */
+size_t cpa_latent_decode_workspace_size(int B, int S, int H, int latent_dim, int rope_dim,
+                                        int page_size);
+
+cpa_status cpa_latent_decode(const void* q_c, int64_t qc_token_stride, int64_t qc_head_stride,
+                             const void* q_r, int64_t qr_token_stride, int64_t qr_head_stride,
+                             const void* pages, const int32_t* page_table, int pt_stride,
+                             const int32_t* seq_lens, int B, int S, int H, int latent_dim,
+                             int rope_dim, int page_size, int num_pages, int max_seq_len,
+                             float sm_scale, void* o, float* lse, void* workspace,
+                             size_t workspace_bytes, cpa_stream_t stream);
+
+/*
+ * cpa_latent_prefill: causal prefill of ragged prompt chunks over expanded latents,
+ * which lie one after the other without pages.  Request b has the new tokens
+ * q_start[b] .. q_start[b+1]-1 of q, m_b of them, and the keys and values
+ * k_start[b] .. k_start[b+1]-1 of k_nope, k_rope and v, n_b >= m_b of them, the new
+ * tokens' last; new token i sees the first n_b - m_b + i + 1 of them.
+ *   q              bf16 [T, H, nope_dim + rope_dim], contiguous
+ *   k_nope, v      bf16, element (j, h, i) at j * token_stride + h * head_stride + i,
+ *                  strides in elements, multiples of 8 and positive: both may be slices
+ *                  of one product [T_k, H, nope_dim + v_dim]
+ *   k_rope         bf16 [T_k, rope_dim], rows rope_token_stride elements apart
+ *   q_start, k_start  int32 [B + 1] on the device, ascending, within [0, T] and
+ *                  [0, T_k]; rows of o and lse of no request are left as they were
+ *   o, lse         bf16 [T, H, v_dim] (32-byte aligned), fp32 [T, H]; not over any input
+ * A start that is not ascending or out of range, or an m_b above n_b, sets
+ * CPA_DEV_BAD_LENGTH.  A NaN or an infinity in v reaches the rows that see it and no
+ * others; a call with many rows beside such values is exact, and slow.
+ * Supported: nope_dim 128, rope_dim 64, v_dim 128; T * H up to 2^24; T_k up to 2^30.
+ */
+size_t cpa_latent_prefill_workspace_size(int B, int T, int T_k, int H, int nope_dim, int rope_dim,
+                                         int v_dim);
+
+cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token_stride,
+                              int64_t k_head_stride, const void* k_rope, int64_t rope_token_stride,
+                              const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                              const int32_t* q_start, const int32_t* k_start, int B, int T, int T_k,
+                              int H, int nope_dim, int rope_dim, int v_dim, float sm_scale, void* o,
+                              float* lse, void* workspace, size_t workspace_bytes,
+                              cpa_stream_t stream);
+
+/*
  * Read the device status word of `workspace` (written by the last call that
  * used it) into *status_out (host).  SYNCHRONISES `stream`.  Returns CPA_OK
  * when the word is 0, otherwise the status matching its most serious bit

@@ -1,0 +1,290 @@
+"""Rows written to the pages of a cache and read back, against indexing in PyTorch.  What is
+copied is equal bit for bit; FP8 codes equal those of the quotient in 32 bits rounded by PyTorch,
+and what is read back equals the product in 32 bits rounded once."""
+import pytest
+import torch
+
+import cascade_paged_attention_gb300 as cpa
+from tests import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def starts(n, lead=0):
+    out = [lead]
+    for m in n:
+        out.append(out[-1] + m)
+    return out
+
+
+def slots(table, firsts, news, P):
+    """Slot of every token, request by request."""
+    out = []
+    for b, (f, m) in enumerate(zip(firsts, news)):
+        pos = torch.arange(f, f + m, device="cuda")
+        out.append(table[b].long()[pos // P] * P + pos % P)
+    return torch.cat(out)
+
+
+def random_bits(shape, dtype, g):
+    """Any bit pattern: what is copied is not looked at."""
+    n = torch.empty(shape, dtype=dtype).element_size()
+    x = torch.randint(0, 256, (*shape[:-1], shape[-1] * n), generator=g, device="cuda", dtype=torch.uint8)
+    return x.view(dtype)
+
+
+def bits(x):
+    return x.contiguous().view(torch.uint8)
+
+
+CASES = [([1], [1]), ([1, 1, 1], [1, 17, 300]), ([0, 5, 0, 33, 1], [0, 5, 9, 40, 64]),
+         ([64, 65, 31, 32], [64, 100, 31, 1000]), ([700, 3], [700, 1000]), ([1] * 40, range(1, 41)),
+         ([0] * 70 + [9] + [0] * 3, [5] * 70 + [20] + [0] * 3)]
+
+
+def quantised(x, scale):
+    return (x.float() / scale).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def same_codes(got, want):
+    nan = (want & 0x7F) == 0x7F
+    assert torch.equal((got & 0x7F) == 0x7F, nan) and torch.equal(got[~nan], want[~nan])
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+@pytest.mark.parametrize("H,d,P,dtype", [(8, 128, 16, torch.bfloat16), (1, 128, 8, torch.bfloat16),
+                                         (3, 128, 256, torch.float16), (2, 8, 64, torch.uint8),
+                                         (1, 8, 32, torch.bfloat16), (5, 24, 16, torch.float32)])
+def test_copies(case, H, d, P, dtype):
+    news, lens = (list(x) for x in CASES[case])
+    g = ref.gen(case)
+    table, pool = ref.table_of(lens, P, g)
+    st = starts(news, lead=2)
+    T = st[-1] + 3
+    k, v = (random_bits((pool, P, H, d), dtype, g) for _ in "kv")
+    wide = random_bits((T, 2 * H + 3, d * 16), dtype, g)  # (whole pieces of 16 bytes before it)
+    kn = wide.view(T, -1)[:, 16 * d:16 * d + H * d].view(T, H, d)
+    vn = random_bits((T, H, d), dtype, g)
+    want = [x.clone() for x in (k, v)]
+    at = slots(table, [L - m for L, m in zip(lens, news)], news, P)
+    for x, n in zip(want, (kn, vn)):
+        bits(x.view(-1, H * d))  # (contiguous)
+        x.view(-1, H, d).view(torch.uint8)[at] = n[2:st[-1]].contiguous().view(torch.uint8)
+    cpa.cpa_cache_append(kn, vn, k, v, table, i32(st), i32(lens), check=True)
+    for x, w in zip((k, v), want):
+        assert torch.equal(bits(x), bits(w))
+    # read back: the same rows, and rows of no request as they were
+    first = [L - m for L, m in zip(lens, news)]
+    out = [torch.zeros((T, H, d), dtype=dtype, device="cuda") for _ in "kv"]
+    for o in out:
+        o.view(torch.uint8).fill_(0x5A)
+    cpa.cpa_cache_gather(k, v, table, i32(st), first=i32(first), k_out=out[0], v_out=out[1], check=True)
+    for o, n in zip(out, (kn, vn)):
+        assert torch.equal(bits(o[2:st[-1]]), bits(n[2:st[-1]]))
+        assert bool((o[:2].view(torch.uint8) == 0x5A).all()) and bool((o[st[-1]:].view(torch.uint8) == 0x5A).all())
+
+
+@pytest.mark.parametrize("H,P", [(8, 16), (1, 8), (5, 128)])
+@pytest.mark.parametrize("per_channel", [False, True])
+def test_fp8(H, P, per_channel):
+    news, lens = [0, 5, 33, 1, 200], [7, 5, 100, 64, 333]
+    g = ref.gen(H + P)
+    table, pool = ref.table_of(lens, P, g)
+    st = starts(news)
+    n = (H, 128) if per_channel else (1,)
+    scale = [torch.rand(n, generator=g, device="cuda") * 0.02 + 0.001 for _ in "kv"]
+    if per_channel:
+        scale[0][0, :4] = torch.tensor([2.0 ** -7, 0.03125, 1.0, 3.0], device="cuda")  # exact ties
+    new = [torch.randn(st[-1], H, 128, generator=g, device="cuda").to(torch.bfloat16) for _ in "kv"]
+    new[0][::7, :, 5] = 1e30
+    new[0][::5, :, 6] = float("inf")
+    new[0][::3, :, 7] = float("-inf")
+    new[1][::4, :, 8] = float("nan")
+    new[1][:, :, 9] = 0.0
+    new[1][:, :, 10] = 1e-30
+    pages = [torch.randint(0, 256, (pool, P, H, 128), generator=g, device="cuda", dtype=torch.uint8) for _ in "kv"]
+    want = [x.clone() for x in pages]
+    at = slots(table, [L - m for L, m in zip(lens, news)], news, P)
+    for w, x, s in zip(want, new, scale):
+        w.view(-1, H, 128)[at] = quantised(x, s)
+    cpa.cpa_cache_append_fp8(*new, *pages, *scale, table, i32(st), i32(lens), check=True)
+    for x, w in zip(pages, want):
+        same_codes(x, w)
+    # from the first position on
+    full = starts(lens)
+    got = cpa.cpa_cache_gather_fp8(*pages, *scale, table, i32(full), T=full[-1], check=True)
+    at = slots(table, [0] * len(lens), lens, P)
+    for o, x, s in zip(got, pages, scale):
+        x = x.view(-1, H, 128)[at].view(torch.float8_e4m3fn).float() * s
+        w = x.to(torch.bfloat16)
+        assert torch.equal(torch.isnan(o), torch.isnan(w)) and torch.equal(o.nan_to_num(7), w.nan_to_num(7))
+
+
+@pytest.mark.parametrize("P", [8, 64, 256])
+def test_latents(P):
+    news, lens = [3, 0, 40, 513], [3, 2, 100, 700]
+    g = ref.gen(P)
+    table, pool = ref.table_of(lens, P, g)
+    st = starts(news, lead=1)
+    pages = random_bits((pool, P, 576), torch.bfloat16, g)
+    wide = random_bits((st[-1], 640), torch.bfloat16, g)
+    c, r = random_bits((st[-1], 512), torch.bfloat16, g), wide[:, 64:128]
+    want = pages.clone()
+    first = [L - m for L, m in zip(lens, news)]
+    at = slots(table, first, news, P)
+    want.view(-1, 576).view(torch.int16)[at] = torch.cat([c, r], 1)[1:].view(torch.int16)
+    cpa.cpa_latent_append(c, r, pages, table, i32(st), i32(lens), check=True)
+    assert torch.equal(bits(pages), bits(want))
+    got = cpa.cpa_latent_gather(pages, table, i32(st), T=st[-1], first=i32(first), check=True)
+    assert torch.equal(bits(got[0][1:]), bits(c[1:])) and torch.equal(bits(got[1][1:]), bits(r[1:].contiguous()))
+
+
+@pytest.mark.parametrize("big", [False, True])
+def test_what_is_wrong_is_reported_and_left_out(big):
+    """(big: the form whose blocks report by themselves.)"""
+    P, H = 16, 2
+    news, lens = [10, 5000 if big else 20, 7], [50, 5000 if big else 30, 9]
+    g = ref.gen(3)
+    table, pool = ref.table_of(lens, P, g)
+    st = starts(news)
+    new = random_bits((st[-1], H, 128), torch.bfloat16, g)
+    ws = torch.full((256,), 0xA5, dtype=torch.uint8, device="cuda")
+
+    def go(t, s, n, status):
+        pages = torch.zeros(pool, P, H, 128, dtype=torch.bfloat16, device="cuda")
+        cpa.cpa_cache_append(new, new, pages, pages.clone(), t, s, n, workspace=ws)
+        assert cpa.cpa_get_device_status(ws)[0] == status
+        out = torch.zeros_like(new)
+        cpa.cpa_cache_gather(pages, pages, t, s, first=n - (s[1:] - s[:-1]), k_out=out,
+                             v_out=torch.zeros_like(new), workspace=ws)
+        assert cpa.cpa_get_device_status(ws)[0] == status
+        return pages, bits(out) == bits(new)
+    pages, same = go(table, i32(st), i32(lens), 0)
+    assert bool(same.all())
+    for bad in (pool, -1, 2 ** 31 - 1, -2 ** 31):
+        t = table.clone()
+        t[1, 1] = bad  # positions 16 .. 31 of the second request
+        pages, same = go(t, i32(st), i32(lens), 5)
+        lo, hi = max(16, lens[1] - news[1]), min(32, lens[1])
+        hit = torch.zeros(st[-1], dtype=torch.bool, device="cuda")
+        a = st[1] - (lens[1] - news[1])
+        hit[a + lo:a + hi] = True
+        assert bool(same[~hit].all()) and bool((pages.view(-1, H, 128)[slots(table, [lo], [hi - lo], P)] == 0).all())
+    for lengths in ([50, 4, 9], [50, 5000 * 16, 9], [50, -1, 9], [50, 2 ** 31 - 1, 9]):
+        pages, same = go(table, i32(st), i32(lengths), 8)
+        assert bool(same[:st[1]].all()) and bool(same[st[2]:].all())
+    for s in ([0, 10, 5, st[-1]], [0, 10, st[2], st[-1] + 1], [-1, 10, st[2], st[-1]]):
+        go(table, i32(s), i32(lens), 8)
+
+
+def test_many_requests_and_empty_ones():
+    g = ref.gen(9)
+    B, P = 5000, 8
+    news = torch.randint(0, 3, (B,), generator=g, device="cuda")
+    news[100:400] = 0
+    lens = (news + torch.randint(0, 5, (B,), generator=g, device="cuda")).tolist()
+    news = news.tolist()
+    table, pool = ref.table_of(lens, P, g)
+    st = starts(news)
+    new = random_bits((st[-1], 1, 128), torch.bfloat16, g)
+    k, v = torch.zeros(pool, P, 1, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(pool, P, 1, 128, dtype=torch.bfloat16, device="cuda")
+    cpa.cpa_cache_append(new, new, k, v, table, i32(st), i32(lens), check=True)
+    rows = torch.repeat_interleave(torch.arange(B, device="cuda"), torch.tensor(news, device="cuda"))
+    pos = torch.arange(st[-1], device="cuda") - i32(st)[rows].long() + (i32(lens) - i32(news))[rows].long()
+    at = table[rows, pos // P].long() * P + pos % P
+    for x in (k, v):
+        assert torch.equal(bits(x.view(-1, 1, 128)[at]), bits(new))
+        left = torch.ones(pool * P, dtype=torch.bool, device="cuda")
+        left[at] = False
+        assert bool((x.view(-1, 128)[left] == 0).all())
+
+
+def test_nothing_to_do():
+    k = torch.full((2, 16, 1, 128), 3.0, device="cuda").to(torch.bfloat16)
+    ws = torch.full((256,), 0xFF, dtype=torch.uint8, device="cuda")
+    none = torch.empty(0, 1, 128, dtype=torch.bfloat16, device="cuda")
+    cpa.cpa_cache_append(none, none, k, k, i32([[0]]), i32([0, 0]), i32([0]), workspace=ws, check=True)
+    assert bool((k == 3).all())
+    ws.fill_(0xFF)
+    out = cpa.cpa_cache_gather(k, k, i32([[0]]), i32([0, 0]), T=0, workspace=ws, check=True)
+    assert out[0].shape == (0, 1, 128)
+
+
+def test_offsets_past_32_bits():
+    """Slots past 2^31 elements and 2^32 bytes of the pools."""
+    P, H = 256, 8
+    pool = 2 ** 32 // (P * H * 128) + 2
+    k, v = (torch.zeros(pool, P, H, 128, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    g = ref.gen(1)
+    new = random_bits((300, H, 128), torch.bfloat16, g)
+    table = i32([[pool - 1, pool - 2]])
+    cpa.cpa_cache_append(new, new, k, v, table, i32([0, 300]), i32([300]), check=True)
+    got = cpa.cpa_cache_gather(k, v, table, i32([0, 300]), T=300, check=True)
+    for o, x in zip(got, (k, v)):
+        assert torch.equal(bits(o), bits(new))
+        assert torch.equal(bits(x[-1]), bits(new[:256])) and torch.equal(bits(x[-2, :44]), bits(new[256:]))
+        assert int(x.view(torch.int16)[:-2].count_nonzero()) == 0
+
+
+def test_streams_and_graphs():
+    """A captured decode step's append, replayed with other rows and lengths, on its own stream."""
+    g = ref.gen(4)
+    B, P, H = 9, 16, 4
+    lens = list(range(30, 30 + B))
+    table, pool = ref.table_of([64] * B, P, g)
+    new = [torch.randn(B, H, 128, generator=g, device="cuda").to(torch.bfloat16) for _ in "kv"]
+    scale = [torch.rand(1, generator=g, device="cuda") * 0.01 + 0.01 for _ in "kv"]
+    pages = [torch.zeros(pool, P, H, 128, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    st, n = i32(list(range(B + 1))), i32(lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    cpa.cpa_cache_append_fp8(*new, *pages, *scale, table, st, n, stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cpa.cpa_cache_append_fp8(*new, *pages, *scale, table, st, n)
+        out = cpa.cpa_cache_gather_fp8(*pages, *scale, table, st, T=B, first=n - 1)
+    for step in range(3):
+        for x in new:
+            x.copy_(torch.randn(B, H, 128, generator=g, device="cuda"))
+        n.add_(1)
+        graph.replay()
+        at = table[torch.arange(B), ((n - 1) // P).long()].long() * P + ((n - 1) % P).long()
+        for x, p, s, o in zip(new, pages, scale, out):
+            want = quantised(x, s)
+            assert torch.equal(p.view(-1, H, 128)[at], want)
+            assert torch.equal(o, (want.view(torch.float8_e4m3fn).float() * s).to(torch.bfloat16))
+
+
+def test_binding_refuses():
+    k = torch.zeros(4, 16, 2, 128, dtype=torch.bfloat16, device="cuda")
+    new = torch.zeros(3, 2, 128, dtype=torch.bfloat16, device="cuda")
+    t, s, n = i32([[0], [1]]), i32([0, 1, 3]), i32([1, 2])
+    for bad in (new.transpose(0, 1).contiguous().transpose(0, 1), new[..., ::2], new[:, :1], new[0]):
+        with pytest.raises(ValueError):
+            cpa.cpa_cache_append(bad, new, k, k, t, s, n)
+    with pytest.raises(TypeError):
+        cpa.cpa_cache_append(new.half(), new, k, k, t, s, n)
+    with pytest.raises(ValueError, match="row for each request"):
+        cpa.cpa_cache_append(new, new, k, k, t, s[:2], n)
+    with pytest.raises(ValueError, match="row for each request"):
+        cpa.cpa_cache_append(new, new, k, k, t, s, n[:1])
+    with pytest.raises(ValueError, match="T, the number"):
+        cpa.cpa_cache_gather(k, k, t, s)
+    with pytest.raises(ValueError, match="the output has"):
+        cpa.cpa_cache_gather(k, k, t, s, T=4, k_out=new)
+    with pytest.raises(ValueError, match="shape"):
+        cpa.cpa_cache_gather(k, k, t, s, k_out=new, v_out=new[:2].clone())
+    with pytest.raises(TypeError):
+        cpa.cpa_cache_append_fp8(new, new, k, k, torch.ones(1, device="cuda"), torch.ones(1, device="cuda"), t, s, n)
+    with pytest.raises(ValueError, match="1 or H_kv"):
+        cpa.cpa_cache_gather_fp8(k.byte(), k.byte(), torch.ones(2, device="cuda"), torch.ones(2, device="cuda"), t, s, T=3)
+    odd = torch.zeros(3, 257, dtype=torch.bfloat16, device="cuda")[:, :256].view(3, 2, 128)
+    with pytest.raises(cpa.CpaError, match="INVALID_ARG"):
+        cpa.cpa_cache_append(odd, new, k, k, t, s, n)
+    with pytest.raises(ValueError, match="576"):
+        cpa.cpa_latent_gather(k.view(4, 16, 256), t, s, T=3)
