@@ -1,6 +1,34 @@
 // cpa_latent.cu -- decode over a paged cache of latents, in the absorbed form: every
 // head's keys and values come from one vector of 512 + 64 elements a token, all of
 // it the key, the first 512 the value.
+//
+// Unit: up to 64 rows of one request (a row is a (token, head) pair; whole tokens, or
+// a part of one token's heads) against its key tiles of 64 tokens.  A tile is loaded
+// once and read twice, as K (nine chunks of 64 columns) and as V (eight of them):
+//     S[64 rows x 64 keys]    = Q K^T              M = 64, N = 64, 36 products
+//     O^T[512 x rows]        += V^T P^T            M = 128 (four blocks), N = rows
+// O^T and not O: its four blocks of 128 columns lie in the 128 lanes of TMEM, a column
+// per row, so 64 rows need 256 of the 512 columns (as O[64 x 512] they would need all),
+// and V^T comes straight from the tile, whose rows are keys.  P is the only operand that
+// goes through shared memory.
+//
+// The order of the products is S(i) PV(i-1): while one tile's scores go through the
+// softmax, the next tile's are made.
+//
+// Warps (6): 0-3 softmax and output, 4 loads, 5 issues the products.  Scores lie 16 rows
+// to a warp; a thread holds 16 scores of two rows, a row's maximum is exchanged between
+// four lanes.  A rescale of O (a row's maximum grew by more than 2^8) is of columns, and
+// so for all four warps: they agree on it with one barrier a tile.
+//
+// Values that are not numbers.  A masked key has weight 0, but 0 times a NaN in V is a
+// NaN in a matrix product.  Slots past a sequence's end are cleared in shared memory.  Of
+// keys that some rows of the request see and others do not (the last S - 1 at most)
+// elements that are not finite are cleared too, and added to the rows that see them when
+// the output is written.
+//
+// Split.  As in cpa_decode the key tiles of all units lie end to end, every block takes a
+// range of equal cost, and a unit cut by a range's end is joined by a second kernel in the
+// order of its parts.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -10,109 +38,743 @@
 #include "cpa.h"
 #include "cpa_checks.h"
 #include "cpa_device.cuh"
-#include "cpa_launch.cuh"
+#include "cpa_host.h"
+#include "cpa_mma.cuh"
 
 namespace cpa {
 namespace {
 
 constexpr int kC = 512, kR = 64, kSlot = kC + kR;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kThreads = 192;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 64;   // rows of a unit
+constexpr int kKeys = 64;   // tokens of a tile
+constexpr int kMaxTokens = 64;  // S: the mask of a request's last tokens is one word
+constexpr int kStages = 2;
+constexpr int kParts = 5;   // of a tile: 64 columns of position, then four blocks of 128
+constexpr uint32_t kChunk = 64u * 128u;          // 64 rows of 64 columns: 8 KB
+constexpr uint32_t kTileBytes = 9 * kChunk;
+constexpr uint32_t kOffQ = 1024;
+constexpr uint32_t kOffK = kOffQ + kTileBytes;
+constexpr uint32_t kOffP = kOffK + kStages * kTileBytes;
+constexpr uint32_t kSmem = kOffP + kChunk + 1024;  // (aligned up inside)
+constexpr uint32_t kColS = 256;  // TMEM: O^T in columns 0 .. 255, the scores of two tiles
+// What a unit costs besides its tiles, in tiles.
+constexpr int kUnitCost = 2;
+constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
+static_assert(kSmem <= 232448, "shared memory of one block");
 
 struct LatentParams {
-    const __nv_bfloat16* q_c;
-    const __nv_bfloat16* q_r;
+    CUtensorMap cmap, rmap, kmap;
     const __nv_bfloat16* pages;
     const int32_t* table;
     const int32_t* lens;
     __nv_bfloat16* o;
     float* lse;
     uint32_t* status;
-    size_t qc_token, qc_head, qr_token, qr_head;  // strides in elements
-    int stride, B, S, H, lp, num_pages, max_len;
+    uint32_t* bad;    // [n_cta] what each block found wrong
+    int4* desc;       // [n_grp] (request, pair, parts, 0) of the unit that starts in the
+                      // group's range and goes on past it; request -1: none
+    float* part_lse;  // [2 n_cta][kRows], log2 units
+    float* part_o;    // [2 n_cta][kRows][kC]
+    int stride, B, S, H, lp, boxr, num_pages, max_len;
+    int heads, n_ht;    // heads of a unit, and units of a token
+    int toks, n_rt;     // tokens of a unit, and units of a request
+    int cl, n_pairs;    // blocks of a group (they share key ranges), groups of units of a request
+    int n_cta, n_grp;
     float scale_log2;
 };
 
-__device__ __forceinline__ float ninf_f() { return __int_as_float(0xff800000); }
+// The length of a request; 0 where it is out of range.
+__device__ __forceinline__ int length_of(const LatentParams& p, int b, uint32_t& bad) {
+    const int L = __ldg(p.lens + b);
+    if (L >= 0 && L <= p.max_len) return L;
+    bad |= CPA_DEV_BAD_LENGTH;
+    return 0;
+}
+// (a request without keys has one tile, all of it masked, so that its rows are written)
+__device__ __forceinline__ int tiles_of(int L) { return L > 0 ? (L + kKeys - 1) / kKeys : 1; }
 
-// One row against keys [k0, k1) of its request, by a whole warp, key by key: lane l
-// holds elements 64 i + 2 l, 64 i + 2 l + 1 of every 64 columns i.  Returns the
-// log-sum-exp in log2 units.
-__device__ __forceinline__ float latent_row(const LatentParams& p, int b, int s, int h, int k0,
-                                           int k1, float (&o)[16], uint32_t& bad) {
-    const int lane = threadIdx.x & 31;
-    float q[18];
-#pragma unroll
-    for (int i = 0; i < 9; ++i) {
-        const size_t t = (size_t)b * p.S + s;
-        const __nv_bfloat16* src = i < 8 ? p.q_c + t * p.qc_token + h * p.qc_head + 64 * i
-                                         : p.q_r + t * p.qr_token + h * p.qr_head;
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src) + lane);
-        q[2 * i] = __uint_as_float(w << 16);
-        q[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
-    }
-    float m = ninf_f(), l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = 0.f;
-    for (int key = k0; key < k1; ++key) {
-        const int pg = __ldg(p.table + (size_t)b * p.stride + (key >> p.lp));
-        if (pg < 0 || pg >= p.num_pages) {
-            bad |= CPA_DEV_BAD_PAGE;
-            continue;
-        }
-        const size_t slot = ((size_t)pg << p.lp) + (key & ((1 << p.lp) - 1));
-        float x[18], d = 0.f;
-#pragma unroll
-        for (int i = 0; i < 9; ++i) {
-            const uint32_t w =
-                __ldg(reinterpret_cast<const uint32_t*>(p.pages + slot * kSlot) + 32 * i + lane);
-            x[2 * i] = __uint_as_float(w << 16);
-            x[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
-            d += q[2 * i] * x[2 * i] + q[2 * i + 1] * x[2 * i + 1];
-        }
-#pragma unroll
-        for (int e = 16; e > 0; e >>= 1) d += __shfl_xor_sync(0xffffffffu, d, e);
-        d *= p.scale_log2;
-        const float mn = fmaxf(m, d), r = mn == ninf_f() ? 0.f : mn;
-        const float f = ex2(m - r), e = ex2(d - r);
-        l = l * f + e;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = o[i] * f + e * x[i];
-        m = mn;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] *= inv;
-    return l == 0.f ? ninf_f() : m + lg2(l);
+struct Ctrl {
+    uint64_t q_full, q_empty;
+    uint64_t k_full[kStages][kParts], k_empty[kStages][kParts];
+    uint64_t s_full[2], p_full, pv_done, o_full, o_empty, mma_done;
+    unsigned long long odd;  // keys L - S + 1 + i of the unit with values that are not finite
+    uint32_t tmem_base;
+    volatile uint32_t abort_flag;
+    uint32_t bad;
+    int unit_cost;            // kUnitCost, or 0 where no block takes more than two tiles
+    long long left, t0, per;  // this group's range, in tiles of cost
+    int b, pair, off;         // where it begins: a unit, and how far into its cost
+    float row[kRows];         // factors of the rows for a rescale, or for the output
+};
+static_assert(sizeof(Ctrl) + 2 * kWarps * 8 <= kOffQ, "control block");
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctrl* c) {
+    // (the first look by itself: most waits find the phase complete)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return mbar_wait_warp(bar, parity, &c->abort_flag, &c->bad);
 }
 
-__global__ void __launch_bounds__(256) latent_rows_kernel(const __grid_constant__ LatentParams p) {
-    wait_for_clear();
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (long long)p.B * p.S * p.H) return;
-    const int h = (int)(row % p.H), t = (int)(row / p.H), b = t / p.S, s = t % p.S;
-    int L = __ldg(p.lens + b);
+// Every thread: the problem's cost, this group's range, and the unit where it begins.
+// Each thread sums a run of requests; one scan over the block follows.
+__device__ void schedule(const LatentParams& p, Ctrl* c, long long* sums, int grp) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per_thread = (p.B + kThreads - 1) / kThreads, b0 = (int)threadIdx.x * per_thread;
     uint32_t bad = 0;
-    if (L < 0 || L > p.max_len) {
-        bad |= CPA_DEV_BAD_LENGTH;
-        L = 0;
-    }
-    float o[16];
-    const float z = latent_row(p, b, s, h, 0, L - p.S + 1 + s, o, bad);
+    long long mine = 0;
+    int n = 0;
+    for (int i = 0; i < per_thread && b0 + i < p.B; ++i, ++n)
+        mine += tiles_of(length_of(p, b0 + i, bad));
+    mine *= p.n_pairs;
+    if (bad) atomicOr(&c->bad, bad);
+    long long incl = mine;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint32_t*>(p.o + (size_t)row * kC)[32 * i + lane] =
-            pack_bf16x2(o[2 * i], o[2 * i + 1]);
-    if (lane == 0) {
-        p.lse[row] = z == ninf_f() ? z : z * kLn2;
-        if (bad) flag(p.status, bad);
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    long long total = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    const int uc = total <= 2 * p.n_grp ? 0 : kUnitCost;
+    total += (long long)uc * p.B * p.n_pairs;
+    before += (long long)uc * min(b0, p.B) * p.n_pairs;
+    mine += (long long)uc * n * p.n_pairs;
+    const long long per = (total + p.n_grp - 1) / p.n_grp;
+    const long long t0 = per * grp;
+    if (threadIdx.x == 0) {
+        c->per = per;
+        c->t0 = t0;
+        c->unit_cost = uc;
+        c->left = t0 < total ? min(per, total - t0) : 0;
+    }
+    if (before <= t0 && t0 < before + mine) {
+        long long at = before;
+        for (int b = b0;; ++b) {
+            const int cost = tiles_of(length_of(p, b, bad)) + uc;
+            const long long all = (long long)cost * p.n_pairs;
+            if (t0 < at + all) {
+                c->b = b;
+                c->pair = (int)((t0 - at) / cost);
+                c->off = (int)((t0 - at) % cost);
+                break;
+            }
+            at += all;
+        }
+    }
+    __syncthreads();
+}
+
+// Walks the pieces (unit, tiles [j0, j1)) of this group's range; j0 == j1 past the
+// last.  A unit's own cost counts as lying before its first tile.
+struct Walker {
+    int b, pair, L, nt, j0, j1, unit_cost;
+    long long left;
+    __device__ __forceinline__ void cut(int off) {
+        const int take = (int)min((long long)nt + unit_cost - off, left);
+        left -= take;
+        j0 = max(0, off - unit_cost);
+        j1 = max(0, off + take - unit_cost);  // (0: the range ends before the first tile)
+    }
+    __device__ __forceinline__ bool more() const { return j0 < j1; }
+    __device__ __forceinline__ void at(const LatentParams& p, int off) {
+        uint32_t bad = 0;
+        L = length_of(p, b, bad);
+        nt = tiles_of(L);
+        cut(off);
+    }
+    __device__ __forceinline__ void init(const LatentParams& p, const Ctrl* c) {
+        left = c->left;
+        unit_cost = c->unit_cost;
+        b = c->b;
+        pair = c->pair;
+        at(p, c->off);
+    }
+    __device__ __forceinline__ void next(const LatentParams& p) {
+        if (left == 0) {
+            j0 = j1;
+            return;
+        }
+        if (++pair == p.n_pairs) {
+            pair = 0;
+            ++b;
+        }
+        at(p, 0);
+    }
+};
+
+// The rows of a unit: heads h0 .. h0 + nh - 1 of tokens s0 .. s0 + ns - 1.
+struct Rows {
+    int s0, ns, h0, nh;
+    __device__ __forceinline__ Rows(const LatentParams& p, int rt) {
+        s0 = rt / p.n_ht * p.toks;
+        h0 = rt % p.n_ht * p.heads;
+        ns = min(p.toks, p.S - s0);
+        nh = min(p.heads, p.H - h0);
+        if (rt >= p.n_rt) ns = nh = 0;
+    }
+};
+
+__global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_constant__ LatentParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int grp = blockIdx.x / p.cl, rank = blockIdx.x % p.cl;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (threadIdx.x == 0) {
+        mbar_init(&ctrl->q_full, 1);
+        mbar_init(&ctrl->q_empty, 1);
+        for (int i = 0; i < kStages; ++i)
+            for (int k = 0; k < kParts; ++k) {
+                mbar_init(&ctrl->k_full[i][k], 1);
+                mbar_init(&ctrl->k_empty[i][k], 1);
+            }
+        mbar_init(&ctrl->s_full[0], 1);
+        mbar_init(&ctrl->s_full[1], 1);
+        mbar_init(&ctrl->p_full, 4);  // one arrival per softmax warp
+        mbar_init(&ctrl->pv_done, 1);
+        mbar_init(&ctrl->o_full, 1);
+        mbar_init(&ctrl->o_empty, 4);
+        mbar_init(&ctrl->mma_done, 1);
+        ctrl->odd = 0;
+        ctrl->abort_flag = 0;
+        ctrl->bad = 0;
+        fence_barrier_init();
+        prefetch_tmap(&p.cmap);
+        prefetch_tmap(&p.rmap);
+        prefetch_tmap(&p.kmap);
+    }
+    if (warp == 5) {
+        tmem_alloc(&ctrl->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    schedule(p, ctrl, reinterpret_cast<long long*>(smem + sizeof(Ctrl)), grp);
+    const uint32_t tmem = ctrl->tmem_base;
+    int4 desc = make_int4(-1, 0, 0, 0);
+    const int rows_n = (p.heads * p.toks + 15) & ~15;  // columns of O^T: N of its products
+
+    if (ctrl->left > 0) {
+        if (warp == 4) {
+            // ============================== loads
+            const uint64_t pol = p.n_pairs * p.cl > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+            const uint64_t pol_q = l2_policy_evict_first();
+            const int NB = kKeys / p.boxr;
+            const uint32_t q_bytes = (uint32_t)(p.heads * p.toks) * 9u * 128u;
+            uint32_t g = 0, q_loads = 0;
+            bool ok = true;
+            Walker w;
+            w.init(p, ctrl);
+            for (; w.more() && ok; w.next(p)) {
+                const Rows r(p, w.pair * p.cl + rank);
+                if (w.j0 == 0 && w.j1 < w.nt) {
+                    // the unit that this group leaves unfinished, for the join (it ends with
+                    // this piece, which ends with the range)
+                    const long long last = ctrl->t0 + ctrl->left + w.nt - w.j1 - 1;
+                    desc = make_int4(w.b, w.pair, (int)(last / ctrl->per - grp) + 1, 0);
+                }
+                if (r.ns == 0) continue;
+                const int32_t* trow = p.table + (size_t)w.b * p.stride;
+                // lane bi: the page of box bi of a tile, or -1
+                auto page_of = [&](int j) -> int {
+                    const int pos = j * kKeys + lane * p.boxr;
+                    if (lane >= NB || j >= w.j1 || pos >= w.L) return -1;
+                    const int pg = __ldg(trow + (pos >> p.lp));
+                    if (pg < 0 || pg >= p.num_pages) {
+                        atomicOr(&ctrl->bad, CPA_DEV_BAD_PAGE);
+                        return -1;
+                    }
+                    return pg;
+                };
+                int page = page_of(w.j0);
+                if (q_loads > 0) ok = wait_warp(&ctrl->q_empty, (q_loads - 1) & 1u, ctrl);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&ctrl->q_full, q_bytes);
+                __syncwarp();
+                if (lane < 9)
+                    tma_load_3d(smem + kOffQ + lane * kChunk, lane < 8 ? &p.cmap : &p.rmap,
+                                lane < 8 ? lane * 64 : 0, r.h0, w.b * p.S + r.s0, &ctrl->q_full, pol_q);
+                __syncwarp();
+                ++q_loads;
+                for (int j = w.j0; j < w.j1 && ok; ++j, ++g) {
+                    const int next_page = page_of(j + 1);
+                    const int st = g % kStages;
+                    uint8_t* dst = smem + kOffK + st * kTileBytes;
+                    const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
+                    const int row0 = (j * kKeys) & ((1 << p.lp) - 1);
+                    for (int part = 0; part < kParts && ok; ++part) {
+                        // part 0: chunk 8; part k: chunks 2 k - 2, 2 k - 1
+                        const int nch = part ? 2 : 1, c0 = part ? 2 * part - 2 : 8;
+                        if (g >= kStages)
+                            ok = wait_warp(&ctrl->k_empty[st][part], (g / kStages - 1) & 1u, ctrl);
+                        if (!ok) break;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&ctrl->k_full[st][part],
+                                                  (uint32_t)(__popc(mask) * nch * p.boxr) * 128u);
+                        __syncwarp();
+                        const int bi = lane & (NB - 1), ch = lane / NB;
+                        const int pg = __shfl_sync(0xffffffffu, page, bi);
+                        if (ch < nch && pg >= 0)
+                            tma_load_2d(dst + (c0 + ch) * kChunk + bi * p.boxr * 128, &p.kmap,
+                                        (c0 + ch) * 64,
+                                        (int)(((uint32_t)pg << p.lp) +
+                                              (uint32_t)((row0 + bi * p.boxr) & ((1 << p.lp) - 1))),
+                                        &ctrl->k_full[st][part], pol);
+                    }
+                    page = next_page;
+                }
+            }
+            // no copy may be in flight when the block leaves
+            if (q_loads > 0)
+                mbar_wait(&ctrl->q_full, (q_loads - 1) & 1u, &ctrl->abort_flag, &ctrl->bad);
+            for (uint32_t s = 0; s < kStages; ++s)
+                if (s < g) {
+                    const uint32_t n = (g - 1 - s) / kStages;
+                    for (int k = 0; k < kParts; ++k)
+                        mbar_wait(&ctrl->k_full[s][k], n & 1u, &ctrl->abort_flag, &ctrl->bad);
+                }
+            __syncwarp();
+        } else if (warp == 5) {
+            // ============================== products
+            // All lanes run the loop, so that addresses and descriptors stay uniform across
+            // the warp; one elected lane's predicate issues.
+            const uint32_t lead = elect_one();
+            const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, false);
+            const uint32_t idesc_o = idesc_bf16_f32(128, rows_n, false) | (1u << 15);  // A: keys are rows
+            const uint64_t q_desc = sdesc_sw128(sbase + kOffQ, 16, 1024);
+            const uint64_t k_desc = sdesc_sw128(sbase + kOffK, 16, 1024);
+            const uint64_t v_desc = sdesc_sw128(sbase + kOffK, kChunk, 1024);
+            const uint64_t p_desc = sdesc_sw128(sbase + kOffP, 16, 1024);
+            uint32_t g = 0, done = 0, pieces = 0;  // tiles whose scores, whose PV was issued
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t par) {
+                ok = ok && wait_warp(bar, par, ctrl);
+                return ok;
+            };
+            auto scores = [&](bool last) {
+                const uint32_t st = g % kStages;
+                for (int part = 0; part < kParts; ++part) {
+                    if (!wait(&ctrl->k_full[st][part], (g / kStages) & 1u)) return;
+                    tc_fence_after_sync();
+                    const int nch = part ? 2 : 1, c0 = part ? 2 * part - 2 : 8;
+                    for (int ch = c0; ch < c0 + nch; ++ch) {
+                        const uint64_t b = k_desc + ((st * kTileBytes + ch * kChunk) >> 4);
+                        const uint64_t a = q_desc + ((ch * kChunk) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ss(lead, tmem + kColS + (g & 1u) * kKeys, a + kk * 2, b + kk * 2,
+                                   idesc_s, part + kk > 0 ? 1u : 0u);
+                    }
+                }
+                commit(lead, &ctrl->s_full[g & 1u]);
+                commit(lead, &ctrl->k_empty[st][0]);
+                if (last) commit(lead, &ctrl->q_empty);
+                ++g;
+            };
+            auto values = [&](bool first, bool last) {
+                const uint32_t st = done % kStages;
+                if (!wait(&ctrl->p_full, done & 1u)) return;
+                if (first && pieces > 0 && !wait(&ctrl->o_empty, (pieces - 1) & 1u)) return;
+                tc_fence_after_sync();
+                for (int blk = 0; blk < 4; ++blk) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss(lead, tmem + blk * kRows,
+                               v_desc + ((st * kTileBytes + blk * 2 * kChunk + kk * 2048) >> 4),
+                               p_desc + kk * 2, idesc_o, first && kk == 0 ? 0u : 1u);
+                    commit(lead, &ctrl->k_empty[st][blk + 1]);
+                }
+                commit(lead, &ctrl->pv_done);
+                if (last) commit(lead, &ctrl->o_full);
+                ++done;
+            };
+            Walker w;
+            w.init(p, ctrl);
+            for (; w.more() && ok; w.next(p)) {
+                if (w.pair * p.cl + rank >= p.n_rt) continue;
+                if (!wait(&ctrl->q_full, pieces & 1u)) break;
+                for (int j = w.j0; j < w.j1 && ok; ++j) {
+                    scores(j == w.j1 - 1);
+                    if (ok && j > w.j0) values(j - 1 == w.j0, false);
+                }
+                if (ok) values(w.j1 - 1 == w.j0, true);
+                ++pieces;
+            }
+            commit(lead, &ctrl->mma_done);
+            wait_warp(&ctrl->mma_done, 0, ctrl);
+        } else {
+            // ============================== softmax and output
+            // Scores: rows 16 warp + lane / 4 (a) and 8 more (b), columns 8 i + 2 (lane % 4) and
+            // the next.  Outputs: columns 128 blk + 32 warp + lane, a row per TMEM column.
+            const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+            const int ra = warp * 16 + (lane >> 2), rb = ra + 8;
+            uint32_t g = 0, pieces = 0;
+            bool ok = true;
+            Walker w;
+            w.init(p, ctrl);
+            for (; w.more(); w.next(p)) {
+                const Rows r(p, w.pair * p.cl + rank);
+                if (r.ns == 0) continue;
+                // the last key that a row sees; -1 for one that sees none, or is none
+                const int sa = ra / p.heads, sb = rb / p.heads;
+                const bool act_a = sa < r.ns && ra - sa * p.heads < r.nh;
+                const bool act_b = sb < r.ns && rb - sb * p.heads < r.nh;
+                const int p_first = w.L - p.S + r.s0;
+                const int pos_a = act_a ? max(p_first + sa, -1) : -1;
+                const int pos_b = act_b ? max(p_first + sb, -1) : -1;
+                float ma = ninf_f(), mb = ninf_f(), la = 0.f, lb = 0.f;  // (l: this lane's columns)
+                // (the unit before has been read, and the first tile's barrier comes before what is
+                // marked here)
+                if (threadIdx.x == 0) ctrl->odd = 0;
+                for (int j = w.j0; j < w.j1; ++j, ++g) {
+                    const int key0 = j * kKeys;
+                    ok = ok && wait_warp(&ctrl->s_full[g & 1u], (g >> 1) & 1u, ctrl);
+                    uint32_t s[32];
+                    float ta = ninf_f(), tb = ninf_f();
+                    bool need_a = false, need_b = false;
+                    if (ok) {
+                        tc_fence_after_sync();
+                        tmem_ld_16x256_x8(tmem + lanes + kColS + (g & 1u) * kKeys, s);
+                        if (key0 + kKeys - 1 > p_first) {
+                            const int c = key0 + 2 * (lane & 3);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    if (c + 8 * i + e > pos_a) s[4 * i + e] = 0xff800000u;
+                                    if (c + 8 * i + e > pos_b) s[4 * i + 2 + e] = 0xff800000u;
+                                }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            ta = fmax3(ta, __uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
+                            tb = fmax3(tb, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
+                        }
+#pragma unroll
+                        for (int o = 1; o < 4; o <<= 1) {
+                            ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
+                            tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
+                        }
+                        ta *= p.scale_log2;
+                        tb *= p.scale_log2;
+                        need_a = act_a && ma != ninf_f() && ta > ma + kRescale;
+                        need_b = act_b && mb != ninf_f() && tb > mb + kRescale;
+                    }
+                    if (!bar_and(1, 128, ok && !need_a && !need_b)) {
+                        // O holds the tiles before this one when PV of the last is done
+                        ok = ok && wait_warp(&ctrl->pv_done, (g - 1) & 1u, ctrl);
+                        const float fa = need_a ? ex2(ma - ta) : 1.f, fb = need_b ? ex2(mb - tb) : 1.f;
+                        if ((lane & 3) == 0) {
+                            ctrl->row[ra] = fa;
+                            ctrl->row[rb] = fb;
+                        }
+                        la *= fa;
+                        lb *= fb;
+                        if (need_a) ma = ta;
+                        if (need_b) mb = tb;
+                        ok = bar_and(1, 128, ok);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 4 * kRows; c0 += 8) {
+                            if ((c0 & (kRows - 1)) >= rows_n) continue;
+                            uint32_t v[8];
+                            tmem_ld_x8(tmem + lanes + c0, v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                v[i] = __float_as_uint(__uint_as_float(v[i]) *
+                                                       ctrl->row[(c0 & (kRows - 1)) + i]);
+                            tmem_st_x8_nowait(tmem + lanes + c0, v);
+                        }
+                        tmem_wait_st();
+                        tc_fence_before_sync();
+                        bar_and(1, 128, true);  // (the factors may be written again)
+                    }
+                    if (ma == ninf_f()) ma = ta;
+                    if (mb == ninf_f()) mb = tb;
+                    const float xa = ma == ninf_f() ? 0.f : ma, xb = mb == ninf_f() ? 0.f : mb;
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float e0 = ex2(fmaf(__uint_as_float(s[4 * i]), p.scale_log2, -xa));
+                        const float e1 = ex2(fmaf(__uint_as_float(s[4 * i + 1]), p.scale_log2, -xa));
+                        const float e2 = ex2(fmaf(__uint_as_float(s[4 * i + 2]), p.scale_log2, -xb));
+                        const float e3 = ex2(fmaf(__uint_as_float(s[4 * i + 3]), p.scale_log2, -xb));
+                        la += e0 + e1;
+                        lb += e2 + e3;
+                        // (a weight's rounding of 2^-9 is of the size of the output's own; the
+                        // sum is of the unrounded weights in 32 bits)
+                        pk[2 * i] = pack_bf16x2(e0, e1);
+                        pk[2 * i + 1] = pack_bf16x2(e2, e3);
+                    }
+                    // the weights' buffer is free, and so is what the products of this tile's
+                    // scores read, when PV of the tile before is done
+                    if (g > 0) ok = ok && wait_warp(&ctrl->pv_done, (g - 1) & 1u, ctrl);
+                    uint8_t* const v = smem + kOffK + (g % kStages) * kTileBytes;
+                    if (key0 + kKeys > w.L) {
+                        // slots past the sequence's end
+                        const int first = max(w.L - key0, 0), n = (kKeys - first) * 8;
+                        for (int i = threadIdx.x; i < 8 * n; i += 128)
+                            *reinterpret_cast<uint4*>(v + i / n * kChunk + first * 128 + i % n * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    if (p.S > 1 && key0 + kKeys - 1 > p_first) {
+                        // keys that not every row sees: a warp each
+                        for (int k = max(key0, p_first + 1) + warp; k < min(key0 + kKeys, w.L); k += 4) {
+                            bool odd = false;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint4* at = reinterpret_cast<uint4*>(
+                                    v + (lane >> 3) * kChunk + i * 4 * kChunk + (k - key0) * 128 + (lane & 7) * 16);
+                                uint32_t x[4] = {at->x, at->y, at->z, at->w};
+                                bool here = false;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((x[e] & 0x7F80u) == 0x7F80u) x[e] &= 0xFFFF0000u, here = true;
+                                    if ((x[e] & 0x7F800000u) == 0x7F800000u) x[e] &= 0xFFFFu, here = true;
+                                }
+                                if (here) *at = make_uint4(x[0], x[1], x[2], x[3]);
+                                odd |= here;
+                            }
+                            if (__any_sync(0xffffffffu, odd) && lane == 0)
+                                atomicOr(&ctrl->odd, 1ull << (k - (w.L - p.S + 1)));
+                        }
+                    }
+                    uint8_t* const dst = smem + kOffP + (lane & 3) * 4;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        *reinterpret_cast<uint32_t*>(dst + ra * 128 + ((i ^ (ra & 7)) << 4)) = pk[2 * i];
+                        *reinterpret_cast<uint32_t*>(dst + rb * 128 + ((i ^ (rb & 7)) << 4)) = pk[2 * i + 1];
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctrl->p_full);
+                }
+
+                // ---- output: the rows, or their part of a unit cut by the range
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    la += __shfl_xor_sync(0xffffffffu, la, o);
+                    lb += __shfl_xor_sync(0xffffffffu, lb, o);
+                }
+                const bool split = w.j0 > 0 || w.j1 < w.nt;
+                const size_t slot = 2 * (size_t)blockIdx.x + (w.j0 > 0 ? 0 : 1);
+                // row of the output that row x of the unit is
+                auto out_row = [&](int x) -> size_t {
+                    const int s = x / p.heads;
+                    return ((size_t)w.b * p.S + r.s0 + s) * p.H + r.h0 + (x - s * p.heads);
+                };
+                if ((lane & 3) == 0) {
+                    ctrl->row[ra] = la == 0.f ? 0.f : 1.f / la;
+                    ctrl->row[rb] = lb == 0.f ? 0.f : 1.f / lb;
+                    const float za = la == 0.f ? ninf_f() : ma + lg2(la);
+                    const float zb = lb == 0.f ? ninf_f() : mb + lg2(lb);
+                    if (act_a && ok) (split ? p.part_lse + slot * kRows + ra : p.lse + out_row(ra))[0] = split || la == 0.f ? za : za * kLn2;
+                    if (act_b && ok) (split ? p.part_lse + slot * kRows + rb : p.lse + out_row(rb))[0] = split || lb == 0.f ? zb : zb * kLn2;
+                }
+                ok = ok && wait_warp(&ctrl->o_full, pieces & 1u, ctrl);
+                ++pieces;
+                ok = bar_and(1, 128, ok);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const unsigned long long odd = ctrl->odd;
+                const int n_act = (r.ns - 1) * p.heads + r.nh;
+#pragma unroll 1
+                for (int x0 = 0; x0 < n_act; x0 += 8) {
+                    uint32_t v[4][8];
+#pragma unroll
+                    for (int blk = 0; blk < 4; ++blk) tmem_ld_x8(tmem + lanes + blk * kRows + x0, v[blk]);
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const int x = x0 + i;
+                        const float f0 = ctrl->row[x], f1 = ctrl->row[x + 1];
+                        const int s0 = x / p.heads, s1 = (x + 1) / p.heads;
+                        const bool on0 = s0 < r.ns && x - s0 * p.heads < r.nh;
+                        const bool on1 = s1 < r.ns && x + 1 - s1 * p.heads < r.nh;
+#pragma unroll
+                        for (int blk = 0; blk < 4; ++blk) {
+                            const float y0 = __uint_as_float(v[blk][i]) * f0;
+                            const float y1 = __uint_as_float(v[blk][i + 1]) * f1;
+                            const int col = blk * 128 + warp * 32;
+                            if (split) {
+                                float* out = p.part_o + (slot * kRows + x) * kC + col + lane;
+                                if (on0) out[0] = y0;
+                                if (on1) out[kC] = y1;
+                            } else {
+                                // two lanes exchange: an even lane writes two columns of row x,
+                                // an odd one of row x + 1
+                                const bool up = lane & 1;
+                                const float z = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 1);
+                                const uint32_t two = up ? pack_bf16x2(z, y1) : pack_bf16x2(y0, z);
+                                if (up ? on1 : on0)
+                                    reinterpret_cast<uint32_t*>(p.o + out_row(x + (up ? 1 : 0)) * kC + col)[lane >> 1] = two;
+                            }
+                        }
+                    }
+                }
+                if (odd) {
+                    // values that are not finite, to the rows that see them: a warp's own columns
+                    // (the rows' values above are this warp's, but not all of them this lane's)
+                    __threadfence_block();
+                    __syncwarp();
+                    for (unsigned long long m = odd; m; m &= m - 1) {
+                        const int i = __ffsll((long long)m) - 1, k = w.L - p.S + 1 + i;
+                        if (k < w.j0 * kKeys || k >= w.j1 * kKeys) continue;
+                        const int pg = __ldg(p.table + (size_t)w.b * p.stride + (k >> p.lp));
+                        if (pg < 0 || pg >= p.num_pages) continue;
+                        const size_t at = (((size_t)pg << p.lp) + (k & ((1 << p.lp) - 1))) * kSlot;
+                        for (int blk = 0; blk < 4; ++blk) {
+                            const int col = blk * 128 + warp * 32 + lane;
+                            const float y = __bfloat162float(p.pages[at + col]);
+                            if (isfinite(y)) continue;
+                            // token i + 1 of the request is at position k
+                            for (int x = max(0, (i + 1 - r.s0) * p.heads); x < n_act; ++x) {
+                                if (x % p.heads >= r.nh) continue;
+                                if (split) {
+                                    p.part_o[(slot * kRows + x) * kC + col] += y;
+                                } else {
+                                    __nv_bfloat16* out = p.o + out_row(x) * kC + col;
+                                    *out = __float2bfloat16(__bfloat162float(*out) + y);
+                                }
+                            }
+                        }
+                    }
+                }
+                tc_fence_before_sync();  // O may be written again
+                bar_and(1, 128, true);   // (and so may the factors and the mask)
+                if (lane == 0) mbar_arrive(&ctrl->o_empty);
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+    if (warp == 4 && lane == 0) {
+        if (rank == 0) p.desc[grp] = desc;
+        p.bad[blockIdx.x] = ctrl->bad;
     }
 }
 
-bool strides_ok(int64_t token, int64_t head, int tokens, int heads) {
-    return (tokens <= 1 || (token > 0 && token % 8 == 0)) &&
-           (heads <= 1 || (head > 0 && head % 8 == 0));
+// Joins the unit that starts in a group's range and goes on past its end: its parts are
+// the group's second slots and the first slots of the groups after it, in that order.
+// Block (x, y) of the grid: unit of block x, eight rows of it, a warp each.  The last
+// group's range is followed by nothing; its blocks gather the status word.
+__global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ LatentParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int grp = blockIdx.x / p.cl, rank = blockIdx.x % p.cl;
+    if (grp == p.n_grp - 1) {
+        if (blockIdx.y > 0 || rank > 0) return;
+        __shared__ uint32_t all;
+        if (threadIdx.x == 0) all = 0;
+        __syncthreads();
+        uint32_t bad = 0;
+        for (int i = threadIdx.x; i < p.n_cta; i += 256) bad |= __ldcg(p.bad + i);
+        if (bad) atomicOr(&all, bad);
+        __syncthreads();
+        if (threadIdx.x == 0) *p.status = all;
+        return;
+    }
+    const int4 d = __ldcg(p.desc + grp);
+    if (d.x < 0) return;
+    const Rows r(p, d.y * p.cl + rank);
+    const int lane = threadIdx.x & 31, x = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int s = x / p.heads, h = x - s * p.heads, np = d.z;
+    if (s >= r.ns || h >= r.nh) return;
+    auto row_of = [&](int i) -> size_t {
+        return (2 * ((size_t)blockIdx.x + (size_t)i * p.cl) + (i == 0 ? 1 : 0)) * kRows + x;
+    };
+    float m = ninf_f(), sum = 0.f;
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < np; i0 += 4) {  // four parts' loads in flight at a time
+        float4 y[4][4];
+        float z[4], mx = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t at = row_of(min(i0 + i, np - 1));
+            z[i] = __ldcg(p.part_lse + at);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                y[i][k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kC) + 32 * k + lane);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i0 + i < np) mx = fmaxf(mx, z[i]);
+        const float ref = mx == ninf_f() ? 0.f : mx, f = ex2(m - ref);
+        sum *= f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            acc[k].x *= f;
+            acc[k].y *= f;
+            acc[k].z *= f;
+            acc[k].w *= f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i0 + i >= np) break;
+            const float w = ex2(z[i] - ref);
+            sum += w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[k].x += w * y[i][k].x;
+                acc[k].y += w * y[i][k].y;
+                acc[k].z += w * y[i][k].z;
+                acc[k].w += w * y[i][k].w;
+            }
+        }
+        m = mx;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t row = ((size_t)d.x * p.S + r.s0 + s) * p.H + r.h0 + h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        reinterpret_cast<uint2*>(p.o + row * kC)[32 * k + lane] =
+            make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
+                       pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    if (lane == 0)
+        p.lse[row] = sum == 0.f ? ninf_f() : ((m == ninf_f() ? 0.f : m) + lg2(sum)) * kLn2;
+}
+
+struct LatentWs {
+    size_t bad, desc, part_lse, part_o, total;
+};
+LatentWs latent_ws(int n_cta) {
+    LatentWs w;
+    w.bad = kStatusBytes;
+    w.desc = align_up(w.bad + (size_t)n_cta * 4, 256);
+    w.part_lse = align_up(w.desc + (size_t)n_cta * 16, 256);
+    w.part_o = align_up(w.part_lse + (size_t)2 * n_cta * kRows * 4, 256);
+    w.total = align_up(w.part_o + (size_t)2 * n_cta * kRows * kC * 4, 256);
+    return w;
+}
+
+cudaError_t raise_smem_once() {
+    static PerDevice<int> state;
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return (cudaError_t)state.run(dev, (int)cudaErrorInvalidDevice, [](int&) {
+        return (int)cudaFuncSetAttribute(latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmem);
+    });
 }
 
 }  // namespace
@@ -124,9 +786,11 @@ extern "C" {
 
 size_t cpa_latent_decode_workspace_size(int B, int S, int H, int latent_dim, int rope_dim,
                                         int page_size) {
-    if (B < 1 || S < 1 || H < 1 || latent_dim != kC || rope_dim != kR || !page_size_ok(page_size))
+    if (B < 1 || S < 1 || S > kMaxTokens || H < 1 || latent_dim != kC || rope_dim != kR ||
+        !page_size_ok(page_size))
         return 0;
-    return kStatusBytes;
+    const int n_sm = sm_count();
+    return n_sm <= 0 ? 0 : latent_ws(n_sm).total;
 }
 
 cpa_status cpa_latent_decode(const void* q_c, int64_t qc_token_stride, int64_t qc_head_stride,
@@ -141,7 +805,8 @@ cpa_status cpa_latent_decode(const void* q_c, int64_t qc_token_stride, int64_t q
     if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return CPA_ERR_INVALID_ARG;
     if (!aligned16(q_c) || !aligned16(q_r) || !aligned16(pages) || !aligned32(o))
         return CPA_ERR_INVALID_ARG;
-    if (latent_dim != kC || rope_dim != kR || !page_size_ok(page_size)) return CPA_ERR_UNSUPPORTED;
+    if (latent_dim != kC || rope_dim != kR || !page_size_ok(page_size) || S > kMaxTokens)
+        return CPA_ERR_UNSUPPORTED;
     if (pt_stride < 1 || pt_stride < ((long long)max_seq_len + page_size - 1) / page_size)
         return CPA_ERR_INVALID_ARG;
     if ((long long)num_pages * page_size > (1ll << 31) || max_seq_len > kMaxLength)
@@ -153,30 +818,60 @@ cpa_status cpa_latent_decode(const void* q_c, int64_t qc_token_stride, int64_t q
         return CPA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < kStatusBytes) return CPA_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return CPA_ERR_INVALID_ARG;
+    const int n_sm = sm_count();
+    if (n_sm <= 0) return CPA_ERR_CUDA;
+    const LatentWs w = latent_ws(n_sm);
+    if (workspace_bytes < w.total) return CPA_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     LatentParams p = {};
-    p.q_c = static_cast<const __nv_bfloat16*>(q_c);
-    p.q_r = static_cast<const __nv_bfloat16*>(q_r);
     p.pages = static_cast<const __nv_bfloat16*>(pages);
     p.table = page_table;
     p.lens = seq_lens;
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
-    p.status = static_cast<uint32_t*>(workspace);
-    p.qc_token = (size_t)qc_token_stride;
-    p.qc_head = (size_t)qc_head_stride;
-    p.qr_token = (size_t)qr_token_stride;
-    p.qr_head = (size_t)qr_head_stride;
+    p.status = reinterpret_cast<uint32_t*>(ws);
+    p.bad = reinterpret_cast<uint32_t*>(ws + w.bad);
+    p.desc = reinterpret_cast<int4*>(ws + w.desc);
+    p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+    p.part_o = reinterpret_cast<float*>(ws + w.part_o);
     p.stride = pt_stride;
     p.B = B;
     p.S = S;
     p.H = H;
     p.lp = 31 - __builtin_clz((unsigned)page_size);
+    p.boxr = page_size < kKeys ? page_size : kKeys;
     p.num_pages = num_pages;
     p.max_len = max_seq_len;
+    p.n_ht = (H + kRows - 1) / kRows;
+    p.heads = (H + p.n_ht - 1) / p.n_ht;
+    p.toks = p.n_ht > 1 ? 1 : kRows / H;
+    if (p.toks > S) p.toks = S;
+    p.n_rt = (S + p.toks - 1) / p.toks * p.n_ht;
+    p.cl = p.n_rt % 2 == 0 && n_sm % 2 == 0 ? 2 : 1;
+    p.n_pairs = p.n_rt / p.cl;
+    p.n_cta = n_sm;
+    p.n_grp = n_sm / p.cl;
     p.scale_log2 = sm_scale * kLog2e;
-    const long long rows = (long long)B * S * H;
-    return launch_cleared(latent_rows_kernel, dim3((unsigned)((rows + 7) / 8)), 256,
-                          reinterpret_cast<cudaStream_t>(stream), p.status, p);
+    if (!make_heads_map(&p.cmap, q_c, kC, H, (uint64_t)B * S, qc_head_stride, qc_token_stride, p.heads,
+                        p.toks) ||
+        !make_heads_map(&p.rmap, q_r, kR, H, (uint64_t)B * S, qr_head_stride, qr_token_stride, p.heads,
+                        p.toks) ||
+        !make_rows_map(&p.kmap, pages, kSlot, (uint64_t)num_pages * page_size, kSlot, p.boxr))
+        return CPA_ERR_CUDA;
+    if (raise_smem_once() != cudaSuccess) return CPA_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    latent_kernel<<<p.n_cta, kThreads, kSmem, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return CPA_ERR_LAUNCH;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.n_cta, kRows / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_join_kernel, p) == cudaSuccess ? CPA_OK : CPA_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -11,13 +11,12 @@
 #include "cpa_checks.h"
 #include "cpa_device.cuh"
 #include "cpa_launch.cuh"
+#include "cpa_mma.cuh"
 
 namespace cpa {
 namespace {
 
 constexpr int kNope = 128, kRope = 64, kQk = kNope + kRope, kV = 128;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct ExpandedParams {
     const __nv_bfloat16* q;
@@ -33,8 +32,6 @@ struct ExpandedParams {
     int B, T, T_k, H;
     float scale_log2;
 };
-
-__device__ __forceinline__ float ninf_f() { return __int_as_float(0xff800000); }
 
 // One request: its new tokens and its keys; m = 0 where nothing is to be done.
 struct Request {
@@ -119,11 +116,6 @@ __global__ void __launch_bounds__(256) expanded_rows_kernel(const __grid_constan
         }
     }
     if (bad) flag(p.status, bad);
-}
-
-bool strides_ok(int64_t token, int64_t head, int tokens, int heads) {
-    return (tokens <= 1 || (token > 0 && token % 8 == 0)) &&
-           (heads <= 1 || (head > 0 && head % 8 == 0));
 }
 
 }  // namespace

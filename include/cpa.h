@@ -689,7 +689,7 @@ cpa_status cpa_latent_gather(const void* pages, const int32_t* page_table, int p
  * The work is split over the visible length and joined, in a fixed order: the
  * result of a call depends on its inputs and the device's SM count alone.
  * Supported: latent_dim 512, rope_dim 64; page_size in {8,16,32,64,128,256};
- * B*S*H up to 2^22; max_seq_len up to 2^30.
+ * S up to 64; B*S*H up to 2^22; max_seq_len up to 2^30.
  */
 size_t cpa_latent_decode_workspace_size(int B, int S, int H, int latent_dim, int rope_dim,
                                         int page_size);

@@ -72,7 +72,7 @@ def test_heads_of_many_tiles(H):
 
 
 @pytest.mark.parametrize("S,H", [(2, 1), (2, 16), (3, 20), (5, 32), (7, 9), (4, 64), (3, 65),
-                                 (2, 128), (6, 5), (33, 2), (70, 1), (140, 3)])
+                                 (2, 128), (6, 5), (33, 2), (64, 1), (50, 3)])
 def test_tokens_causal_among_themselves(S, H):
     check(LENS, S, H, 16, seed=S + H)
 

@@ -92,13 +92,14 @@ def test_row_limits(L, p):
     assert call(L, p, "latent_prefill", T=1 << 22) == 2
     assert call(L, p, "latent_prefill", T_k=(1 << 30) + 1) == 2
     assert call(L, p, "latent_decode", B=1 << 20) == 2
-    assert call(L, p, "latent_decode", S=1 << 20) == 2
+    assert call(L, p, "latent_decode", S=65) == 2
     assert call(L, p, "latent_decode", max_len=(1 << 30) + 1, stride=1 << 27) == 2
 
 
 def test_workspace_sizes(L):
     for bad in ((0, 1, 8, 512, 64, 16), (1, 0, 8, 512, 64, 16), (1, 1, 0, 512, 64, 16),
-                (1, 1, 8, 256, 64, 16), (1, 1, 8, 512, 32, 16), (1, 1, 8, 512, 64, 7)):
+                (1, 1, 8, 256, 64, 16), (1, 1, 8, 512, 32, 16), (1, 1, 8, 512, 64, 7),
+                (1, 65, 8, 512, 64, 16)):
         assert L.cpa_latent_decode_workspace_size(*bad) == 0
     for bad in ((0, 1, 1, 8, 128, 64, 128), (1, -1, 1, 8, 128, 64, 128), (1, 1, -1, 8, 128, 64, 128),
                 (1, 1, 1, 0, 128, 64, 128), (1, 1, 1, 8, 64, 64, 128), (1, 1, 1, 8, 128, 32, 128),
