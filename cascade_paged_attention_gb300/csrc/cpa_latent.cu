@@ -50,19 +50,27 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 64;   // rows of a unit
 constexpr int kKeys = 64;   // tokens of a tile
 constexpr int kMaxTokens = 64;  // S: the mask of a request's last tokens is one word
-constexpr int kStages = 2;
-constexpr int kParts = 5;   // of a tile: 64 columns of position, then four blocks of 128
-constexpr uint32_t kChunk = 64u * 128u;          // 64 rows of 64 columns: 8 KB
-constexpr uint32_t kTileBytes = 9 * kChunk;
+// Eight tokens are one box of a load, 9 KB that lie together in a page: in shared memory
+// nine chunks of 64 columns, eight rows of 128 bytes each.  Four of them, half a tile, are a
+// slot of the ring.
+constexpr uint32_t kBox = 9u * 1024u;
+constexpr uint32_t kSlotBytes = 4 * kBox;
+constexpr int kMaxSlots = 5;
 constexpr uint32_t kOffQ = 1024;
-constexpr uint32_t kOffK = kOffQ + kTileBytes;
-constexpr uint32_t kOffP = kOffK + kStages * kTileBytes;
-constexpr uint32_t kSmem = kOffP + kChunk + 1024;  // (aligned up inside)
+constexpr uint32_t kMaxSmem = 232448;
 constexpr uint32_t kColS = 256;  // TMEM: O^T in columns 0 .. 255, the scores of two tiles
 // What a unit costs besides its tiles, in tiles.
 constexpr int kUnitCost = 2;
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
-static_assert(kSmem <= 232448, "shared memory of one block");
+
+// Shared memory by rows of a unit: Q, P, then the ring.  Five slots up to 32 rows, four for 64.
+CPA_HD uint32_t q_chunk(int rows) { return (uint32_t)((rows + 7) & ~7) * 128u; }
+CPA_HD uint32_t off_p(int rows) { return kOffQ + 9u * q_chunk(rows); }
+CPA_HD uint32_t off_k(int rows) { return off_p(rows) + (uint32_t)((rows + 15) & ~15) * 128u; }
+CPA_HD int slots_of(int rows) {
+    const int n = (int)((kMaxSmem - 1024u - off_k(rows)) / kSlotBytes);  // (aligned up inside)
+    return n < kMaxSlots ? n : kMaxSlots;
+}
 
 struct LatentParams {
     CUtensorMap cmap, rmap, kmap;
@@ -77,11 +85,12 @@ struct LatentParams {
                       // group's range and goes on past it; request -1: none
     float* part_lse;  // [2 n_cta][kRows], log2 units
     float* part_o;    // [2 n_cta][kRows][kC]
-    int stride, B, S, H, lp, boxr, num_pages, max_len;
+    int stride, B, S, H, lp, num_pages, max_len;
     int heads, n_ht;    // heads of a unit, and units of a token
     int toks, n_rt;     // tokens of a unit, and units of a request
     int cl, n_pairs;    // blocks of a group (they share key ranges), groups of units of a request
     int n_cta, n_grp;
+    int n_slots;
     float scale_log2;
 };
 
@@ -97,7 +106,7 @@ __device__ __forceinline__ int tiles_of(int L) { return L > 0 ? (L + kKeys - 1) 
 
 struct Ctrl {
     uint64_t q_full, q_empty;
-    uint64_t k_full[kStages][kParts], k_empty[kStages][kParts];
+    uint64_t k_full[kMaxSlots], k_empty[kMaxSlots];
     uint64_t s_full[2], p_full, pv_done, o_full, o_empty, mma_done;
     unsigned long long odd;  // keys L - S + 1 + i of the unit with values that are not finite
     uint32_t tmem_base;
@@ -209,15 +218,17 @@ struct Walker {
     }
 };
 
-// The rows of a unit: heads h0 .. h0 + nh - 1 of tokens s0 .. s0 + ns - 1.
+// The rows of a unit: heads h0 .. h0 + nh - 1 of tokens s0 .. s0 + ns - 1, n of them.  (Whole
+// tokens or one of them: row x of the unit is row `first` + x of the request.)
 struct Rows {
-    int s0, ns, h0, nh;
+    int s0, ns, h0, nh, n, first;
     __device__ __forceinline__ Rows(const LatentParams& p, int rt) {
         s0 = rt / p.n_ht * p.toks;
         h0 = rt % p.n_ht * p.heads;
         ns = min(p.toks, p.S - s0);
         nh = min(p.heads, p.H - h0);
-        if (rt >= p.n_rt) ns = nh = 0;
+        n = ns * nh;
+        first = s0 * p.H + h0;
     }
 };
 
@@ -234,11 +245,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         mbar_init(&ctrl->q_full, 1);
         mbar_init(&ctrl->q_empty, 1);
-        for (int i = 0; i < kStages; ++i)
-            for (int k = 0; k < kParts; ++k) {
-                mbar_init(&ctrl->k_full[i][k], 1);
-                mbar_init(&ctrl->k_empty[i][k], 1);
-            }
+        for (int i = 0; i < kMaxSlots; ++i) {
+            mbar_init(&ctrl->k_full[i], 1);
+            mbar_init(&ctrl->k_empty[i], 1);
+        }
         mbar_init(&ctrl->s_full[0], 1);
         mbar_init(&ctrl->s_full[1], 1);
         mbar_init(&ctrl->p_full, 4);  // one arrival per softmax warp
@@ -264,16 +274,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     schedule(p, ctrl, reinterpret_cast<long long*>(smem + sizeof(Ctrl)), grp);
     const uint32_t tmem = ctrl->tmem_base;
     int4 desc = make_int4(-1, 0, 0, 0);
-    const int rows_n = (p.heads * p.toks + 15) & ~15;  // columns of O^T: N of its products
+    const int rows = p.heads * p.toks, rows_n = (rows + 15) & ~15;  // N of the products of O^T
+    const uint32_t o_p = off_p(rows), o_k = off_k(rows);
+    const int n_slots = p.n_slots;
 
     if (ctrl->left > 0) {
         if (warp == 4) {
             // ============================== loads
             const uint64_t pol = p.n_pairs * p.cl > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
             const uint64_t pol_q = l2_policy_evict_first();
-            const int NB = kKeys / p.boxr;
-            const uint32_t q_bytes = (uint32_t)(p.heads * p.toks) * 9u * 128u;
-            uint32_t g = 0, q_loads = 0;
+            const uint32_t chunk = q_chunk(rows), q_bytes = (uint32_t)rows * 9u * 128u;
+            uint32_t q_loads = 0, h = 0;  // halves of tiles so far
+            int slot = 0;
+            uint32_t par = 1;  // parity of the ring's previous round
             bool ok = true;
             Walker w;
             w.init(p, ctrl);
@@ -285,66 +298,56 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     const long long last = ctrl->t0 + ctrl->left + w.nt - w.j1 - 1;
                     desc = make_int4(w.b, w.pair, (int)(last / ctrl->per - grp) + 1, 0);
                 }
-                if (r.ns == 0) continue;
                 const int32_t* trow = p.table + (size_t)w.b * p.stride;
-                // lane bi: the page of box bi of a tile, or -1
-                auto page_of = [&](int j) -> int {
-                    const int pos = j * kKeys + lane * p.boxr;
-                    if (lane >= NB || j >= w.j1 || pos >= w.L) return -1;
+                // lane bi: the slot of the pool that box bi of a half begins with, or -1
+                auto box_of = [&](int half) -> int {
+                    const int pos = half * 32 + lane * 8;
+                    if (lane >= 4 || half >= 2 * w.j1 || pos >= w.L) return -1;
                     const int pg = __ldg(trow + (pos >> p.lp));
                     if (pg < 0 || pg >= p.num_pages) {
                         atomicOr(&ctrl->bad, CPA_DEV_BAD_PAGE);
                         return -1;
                     }
-                    return pg;
+                    return (int)(((uint32_t)pg << p.lp) + (uint32_t)(pos & ((1 << p.lp) - 1)));
                 };
-                int page = page_of(w.j0);
+                int box = box_of(2 * w.j0);
                 if (q_loads > 0) ok = wait_warp(&ctrl->q_empty, (q_loads - 1) & 1u, ctrl);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&ctrl->q_full, q_bytes);
                 __syncwarp();
                 if (lane < 9)
-                    tma_load_3d(smem + kOffQ + lane * kChunk, lane < 8 ? &p.cmap : &p.rmap,
+                    tma_load_3d(smem + kOffQ + lane * chunk, lane < 8 ? &p.cmap : &p.rmap,
                                 lane < 8 ? lane * 64 : 0, r.h0, w.b * p.S + r.s0, &ctrl->q_full, pol_q);
                 __syncwarp();
                 ++q_loads;
-                for (int j = w.j0; j < w.j1 && ok; ++j, ++g) {
-                    const int next_page = page_of(j + 1);
-                    const int st = g % kStages;
-                    uint8_t* dst = smem + kOffK + st * kTileBytes;
-                    const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
-                    const int row0 = (j * kKeys) & ((1 << p.lp) - 1);
-                    for (int part = 0; part < kParts && ok; ++part) {
-                        // part 0: chunk 8; part k: chunks 2 k - 2, 2 k - 1
-                        const int nch = part ? 2 : 1, c0 = part ? 2 * part - 2 : 8;
-                        if (g >= kStages)
-                            ok = wait_warp(&ctrl->k_empty[st][part], (g / kStages - 1) & 1u, ctrl);
+                for (int half = 2 * w.j0; half < 2 * w.j1; ++half, ++h) {
+                    const int next = box_of(half + 1);
+                    if (h >= (uint32_t)n_slots) {
+                        ok = wait_warp(&ctrl->k_empty[slot], par, ctrl);
                         if (!ok) break;
-                        if (lane == 0)
-                            mbar_arrive_expect_tx(&ctrl->k_full[st][part],
-                                                  (uint32_t)(__popc(mask) * nch * p.boxr) * 128u);
-                        __syncwarp();
-                        const int bi = lane & (NB - 1), ch = lane / NB;
-                        const int pg = __shfl_sync(0xffffffffu, page, bi);
-                        if (ch < nch && pg >= 0)
-                            tma_load_2d(dst + (c0 + ch) * kChunk + bi * p.boxr * 128, &p.kmap,
-                                        (c0 + ch) * 64,
-                                        (int)(((uint32_t)pg << p.lp) +
-                                              (uint32_t)((row0 + bi * p.boxr) & ((1 << p.lp) - 1))),
-                                        &ctrl->k_full[st][part], pol);
                     }
-                    page = next_page;
+                    const uint32_t mask = __ballot_sync(0xffffffffu, box >= 0);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&ctrl->k_full[slot], (uint32_t)__popc(mask) * kBox);
+                    __syncwarp();
+                    if (box >= 0)
+                        tma_load_3d(smem + o_k + slot * kSlotBytes + lane * kBox, &p.kmap, 0, box, 0,
+                                    &ctrl->k_full[slot], pol);
+                    __syncwarp();
+                    box = next;
+                    if (++slot == n_slots) {
+                        slot = 0;
+                        par ^= 1u;
+                    }
                 }
             }
             // no copy may be in flight when the block leaves
             if (q_loads > 0)
                 mbar_wait(&ctrl->q_full, (q_loads - 1) & 1u, &ctrl->abort_flag, &ctrl->bad);
-            for (uint32_t s = 0; s < kStages; ++s)
-                if (s < g) {
-                    const uint32_t n = (g - 1 - s) / kStages;
-                    for (int k = 0; k < kParts; ++k)
-                        mbar_wait(&ctrl->k_full[s][k], n & 1u, &ctrl->abort_flag, &ctrl->bad);
-                }
+            for (uint32_t i = 0; i < (uint32_t)n_slots; ++i)
+                if (i < h)
+                    mbar_wait(&ctrl->k_full[i], ((h - 1 - i) / n_slots) & 1u, &ctrl->abort_flag,
+                              &ctrl->bad);
             __syncwarp();
         } else if (warp == 5) {
             // ============================== products
@@ -352,65 +355,108 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             // the warp; one elected lane's predicate issues.
             const uint32_t lead = elect_one();
             const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, false);
+            const uint32_t idesc_h = idesc_bf16_f32(kRows, kKeys / 2, false);
             const uint32_t idesc_o = idesc_bf16_f32(128, rows_n, false) | (1u << 15);  // A: keys are rows
+            const uint32_t chunk = q_chunk(rows) >> 4;
             const uint64_t q_desc = sdesc_sw128(sbase + kOffQ, 16, 1024);
-            const uint64_t k_desc = sdesc_sw128(sbase + kOffK, 16, 1024);
-            const uint64_t v_desc = sdesc_sw128(sbase + kOffK, kChunk, 1024);
-            const uint64_t p_desc = sdesc_sw128(sbase + kOffP, 16, 1024);
-            uint32_t g = 0, done = 0, pieces = 0;  // tiles whose scores, whose PV was issued
-            bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t par) {
-                ok = ok && wait_warp(bar, par, ctrl);
-                return ok;
-            };
-            auto scores = [&](bool last) {
-                const uint32_t st = g % kStages;
-                for (int part = 0; part < kParts; ++part) {
-                    if (!wait(&ctrl->k_full[st][part], (g / kStages) & 1u)) return;
-                    tc_fence_after_sync();
-                    const int nch = part ? 2 : 1, c0 = part ? 2 * part - 2 : 8;
-                    for (int ch = c0; ch < c0 + nch; ++ch) {
-                        const uint64_t b = k_desc + ((st * kTileBytes + ch * kChunk) >> 4);
-                        const uint64_t a = q_desc + ((ch * kChunk) >> 4);
+            const uint64_t k_desc = sdesc_sw128(sbase + o_k, 16, kBox);
+            const uint64_t v_desc = sdesc_sw128(sbase + o_k, 1024, kBox);  // chunk after chunk, keys as rows
+            const uint64_t p_desc = sdesc_sw128(sbase + o_p, 16, 1024);
+            // Two walks over the same tiles: scores g, and the values of tile d behind it.  What is
+            // ready goes first; the scores where both are (the softmax then has work while the
+            // values' products run).
+            uint32_t g = 0, d = 0, d_pieces = 0;
+            int ks = 0, vs = 0;  // slots of their first halves
+            uint32_t kpar = 0, qpar = 0;
+            Walker wk, wv;
+            wk.init(p, ctrl);
+            wv = wk;
+            int jk = wk.j0, jv = wv.j0;
+            uint64_t since = 0;
+            uint32_t n_idle = 0;
+            while (wv.more()) {
+                bool did = false;
+                if (wk.more() && g - d < 2) {
+                    const int ks2 = ks + 1 == n_slots ? 0 : ks + 1;
+                    const uint32_t kpar2 = ks2 == 0 ? kpar ^ 1u : kpar;
+                    if (__all_sync(0xffffffffu, mbar_test(&ctrl->k_full[ks2], kpar2) &&
+                                                    mbar_test(&ctrl->k_full[ks], kpar) &&
+                                                    (jk > wk.j0 || mbar_test(&ctrl->q_full, qpar)))) {
+                        tc_fence_after_sync();
+                        const uint32_t s_col = tmem + kColS + (g & 1u) * kKeys;
+                        const uint64_t b = k_desc + ((ks * kSlotBytes) >> 4);
+                        if (ks2 > 0) {
+                            for (int ch = 0; ch < 9; ++ch)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(lead, tmem + kColS + (g & 1u) * kKeys, a + kk * 2, b + kk * 2,
-                                   idesc_s, part + kk > 0 ? 1u : 0u);
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_ss(lead, s_col, q_desc + ch * chunk + kk * 2, b + ch * 64 + kk * 2,
+                                           idesc_s, ch + kk > 0 ? 1u : 0u);
+                        } else {  // the tile's halves are the ring's last slot and its first
+                            for (int ch = 0; ch < 9; ++ch)
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) {
+                                    mma_ss(lead, s_col, q_desc + ch * chunk + kk * 2, b + ch * 64 + kk * 2,
+                                           idesc_h, ch + kk > 0 ? 1u : 0u);
+                                    mma_ss(lead, s_col + 32, q_desc + ch * chunk + kk * 2,
+                                           k_desc + ch * 64 + kk * 2, idesc_h, ch + kk > 0 ? 1u : 0u);
+                                }
+                        }
+                        commit(lead, &ctrl->s_full[g & 1u]);
+                        ++g;
+                        ks = ks2 + 1 == n_slots ? 0 : ks2 + 1;
+                        if (ks < 2) kpar ^= 1u;
+                        if (++jk == wk.j1) {
+                            commit(lead, &ctrl->q_empty);
+                            qpar ^= 1u;
+                            wk.next(p);
+                            jk = wk.j0;
+                        }
+                        did = true;
                     }
                 }
-                commit(lead, &ctrl->s_full[g & 1u]);
-                commit(lead, &ctrl->k_empty[st][0]);
-                if (last) commit(lead, &ctrl->q_empty);
-                ++g;
-            };
-            auto values = [&](bool first, bool last) {
-                const uint32_t st = done % kStages;
-                if (!wait(&ctrl->p_full, done & 1u)) return;
-                if (first && pieces > 0 && !wait(&ctrl->o_empty, (pieces - 1) & 1u)) return;
-                tc_fence_after_sync();
-                for (int blk = 0; blk < 4; ++blk) {
+                if (!did && d < g &&
+                    __all_sync(0xffffffffu, mbar_test(&ctrl->p_full, d & 1u) &&
+                                                (jv > wv.j0 || d_pieces == 0 ||
+                                                 mbar_test(&ctrl->o_empty, (d_pieces - 1) & 1u)))) {
+                    tc_fence_after_sync();
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(lead, tmem + blk * kRows,
-                               v_desc + ((st * kTileBytes + blk * 2 * kChunk + kk * 2048) >> 4),
-                               p_desc + kk * 2, idesc_o, first && kk == 0 ? 0u : 1u);
-                    commit(lead, &ctrl->k_empty[st][blk + 1]);
+                    for (int half = 0; half < 2; ++half) {
+                        const uint64_t a = v_desc + ((vs * kSlotBytes) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                            for (int blk = 0; blk < 4; ++blk)
+                                mma_ss(lead, tmem + blk * kRows, a + ((kk * 2 * kBox + blk * 2048) >> 4),
+                                       p_desc + (half * 2 + kk) * 2, idesc_o,
+                                       jv == wv.j0 && half + kk == 0 ? 0u : 1u);
+                        commit(lead, &ctrl->k_empty[vs]);
+                        if (++vs == n_slots) vs = 0;
+                    }
+                    commit(lead, &ctrl->pv_done);
+                    ++d;
+                    if (++jv == wv.j1) {
+                        commit(lead, &ctrl->o_full);
+                        ++d_pieces;
+                        wv.next(p);
+                        jv = wv.j0;
+                    }
+                    did = true;
                 }
-                commit(lead, &ctrl->pv_done);
-                if (last) commit(lead, &ctrl->o_full);
-                ++done;
-            };
-            Walker w;
-            w.init(p, ctrl);
-            for (; w.more() && ok; w.next(p)) {
-                if (w.pair * p.cl + rank >= p.n_rt) continue;
-                if (!wait(&ctrl->q_full, pieces & 1u)) break;
-                for (int j = w.j0; j < w.j1 && ok; ++j) {
-                    scores(j == w.j1 - 1);
-                    if (ok && j > w.j0) values(j - 1 == w.j0, false);
+                if (did) {
+                    n_idle = 0;
+                    continue;
                 }
-                if (ok) values(w.j1 - 1 == w.j0, true);
-                ++pieces;
+                // nothing is ready: wait, with the limit of every wait
+                if (n_idle++ == 0) since = globaltimer_ns();
+                if ((n_idle & 63u) == 0) {
+                    const bool late = globaltimer_ns() - since > kWaitLimitNs;
+                    if (late) {
+                        atomicOr(&ctrl->bad, CPA_DEV_TIMEOUT);
+                        ctrl->abort_flag = 1u;
+                        __threadfence_block();
+                    }
+                    if (__any_sync(0xffffffffu, late || ctrl->abort_flag)) break;
+                }
             }
             commit(lead, &ctrl->mma_done);
             wait_warp(&ctrl->mma_done, 0, ctrl);
@@ -421,19 +467,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             const uint32_t lanes = (uint32_t)(warp * 32) << 16;
             const int ra = warp * 16 + (lane >> 2), rb = ra + 8;
             uint32_t g = 0, pieces = 0;
+            int vs = 0;  // slot of the tile's first half
             bool ok = true;
             Walker w;
             w.init(p, ctrl);
             for (; w.more(); w.next(p)) {
                 const Rows r(p, w.pair * p.cl + rank);
-                if (r.ns == 0) continue;
                 // the last key that a row sees; -1 for one that sees none, or is none
-                const int sa = ra / p.heads, sb = rb / p.heads;
-                const bool act_a = sa < r.ns && ra - sa * p.heads < r.nh;
-                const bool act_b = sb < r.ns && rb - sb * p.heads < r.nh;
+                const bool act_a = ra < r.n, act_b = rb < r.n;
                 const int p_first = w.L - p.S + r.s0;
-                const int pos_a = act_a ? max(p_first + sa, -1) : -1;
-                const int pos_b = act_b ? max(p_first + sb, -1) : -1;
+                const int pos_a = act_a ? max(p_first + ra / p.heads, -1) : -1;
+                const int pos_b = act_b ? max(p_first + rb / p.heads, -1) : -1;
                 float ma = ninf_f(), mb = ninf_f(), la = 0.f, lb = 0.f;  // (l: this lane's columns)
                 // (the unit before has been read, and the first tile's barrier comes before what is
                 // marked here)
@@ -522,13 +566,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     // the weights' buffer is free, and so is what the products of this tile's
                     // scores read, when PV of the tile before is done
                     if (g > 0) ok = ok && wait_warp(&ctrl->pv_done, (g - 1) & 1u, ctrl);
-                    uint8_t* const v = smem + kOffK + (g % kStages) * kTileBytes;
+                    // box bi of the tile, in its half's slot
+                    const int vs2 = vs + 1 == n_slots ? 0 : vs + 1;
+                    auto box_at = [&](int bi) -> uint8_t* {
+                        return smem + o_k + (bi < 4 ? vs : vs2) * kSlotBytes + (bi & 3) * kBox;
+                    };
                     if (key0 + kKeys > w.L) {
-                        // slots past the sequence's end
-                        const int first = max(w.L - key0, 0), n = (kKeys - first) * 8;
-                        for (int i = threadIdx.x; i < 8 * n; i += 128)
-                            *reinterpret_cast<uint4*>(v + i / n * kChunk + first * 128 + i % n * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                        // slots past the sequence's end: a piece of 16 bytes of a row each
+                        const int first = max(w.L - key0, 0);
+                        for (int i = threadIdx.x + 64 * first; i < 64 * kKeys; i += 128) {
+                            const int k = i >> 6, c = i & 63;
+                            *reinterpret_cast<uint4*>(box_at(k >> 3) + (c >> 3) * 1024 + (k & 7) * 128 +
+                                                      (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
                     if (p.S > 1 && key0 + kKeys - 1 > p_first) {
                         // keys that not every row sees: a warp each
@@ -537,7 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 uint4* at = reinterpret_cast<uint4*>(
-                                    v + (lane >> 3) * kChunk + i * 4 * kChunk + (k - key0) * 128 + (lane & 7) * 16);
+                                    box_at((k - key0) >> 3) + ((lane >> 3) + 4 * i) * 1024 +
+                                    ((k - key0) & 7) * 128 + (lane & 7) * 16);
                                 uint32_t x[4] = {at->x, at->y, at->z, at->w};
                                 bool here = false;
 #pragma unroll
@@ -552,12 +603,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                                 atomicOr(&ctrl->odd, 1ull << (k - (w.L - p.S + 1)));
                         }
                     }
-                    uint8_t* const dst = smem + kOffP + (lane & 3) * 4;
+                    if (warp * 16 < rows_n) {
+                        uint8_t* const dst = smem + o_p + (lane & 3) * 4;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        *reinterpret_cast<uint32_t*>(dst + ra * 128 + ((i ^ (ra & 7)) << 4)) = pk[2 * i];
-                        *reinterpret_cast<uint32_t*>(dst + rb * 128 + ((i ^ (rb & 7)) << 4)) = pk[2 * i + 1];
+                        for (int i = 0; i < 8; ++i) {
+                            *reinterpret_cast<uint32_t*>(dst + ra * 128 + ((i ^ (ra & 7)) << 4)) = pk[2 * i];
+                            *reinterpret_cast<uint32_t*>(dst + rb * 128 + ((i ^ (rb & 7)) << 4)) = pk[2 * i + 1];
+                        }
                     }
+                    vs = vs2 + 1 == n_slots ? 0 : vs2 + 1;
                     fence_proxy_async_smem();
                     tc_fence_before_sync();
                     __syncwarp();
@@ -572,18 +626,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 }
                 const bool split = w.j0 > 0 || w.j1 < w.nt;
                 const size_t slot = 2 * (size_t)blockIdx.x + (w.j0 > 0 ? 0 : 1);
-                // row of the output that row x of the unit is
-                auto out_row = [&](int x) -> size_t {
-                    const int s = x / p.heads;
-                    return ((size_t)w.b * p.S + r.s0 + s) * p.H + r.h0 + (x - s * p.heads);
-                };
+                const size_t row0 = (size_t)w.b * p.S * p.H + r.first;  // of the output
+                float* const part_l = p.part_lse + slot * kRows;
                 if ((lane & 3) == 0) {
                     ctrl->row[ra] = la == 0.f ? 0.f : 1.f / la;
                     ctrl->row[rb] = lb == 0.f ? 0.f : 1.f / lb;
                     const float za = la == 0.f ? ninf_f() : ma + lg2(la);
                     const float zb = lb == 0.f ? ninf_f() : mb + lg2(lb);
-                    if (act_a && ok) (split ? p.part_lse + slot * kRows + ra : p.lse + out_row(ra))[0] = split || la == 0.f ? za : za * kLn2;
-                    if (act_b && ok) (split ? p.part_lse + slot * kRows + rb : p.lse + out_row(rb))[0] = split || lb == 0.f ? zb : zb * kLn2;
+                    if (act_a && ok) (split ? part_l : p.lse + row0)[ra] = split || la == 0.f ? za : za * kLn2;
+                    if (act_b && ok) (split ? part_l : p.lse + row0)[rb] = split || lb == 0.f ? zb : zb * kLn2;
                 }
                 ok = ok && wait_warp(&ctrl->o_full, pieces & 1u, ctrl);
                 ++pieces;
@@ -591,38 +642,39 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 if (!ok) break;
                 tc_fence_after_sync();
                 const unsigned long long odd = ctrl->odd;
-                const int n_act = (r.ns - 1) * p.heads + r.nh;
+                const int col0 = warp * 32 + lane;
 #pragma unroll 1
-                for (int x0 = 0; x0 < n_act; x0 += 8) {
+                for (int x0 = 0; x0 < r.n; x0 += 8) {
                     uint32_t v[4][8];
+                    tmem_ld_4x8(tmem + lanes + x0, kRows, v);
+                    float f[8];
 #pragma unroll
-                    for (int blk = 0; blk < 4; ++blk) tmem_ld_x8(tmem + lanes + blk * kRows + x0, v[blk]);
+                    for (int i = 0; i < 8; ++i) f[i] = ctrl->row[x0 + i];
+                    if (split) {
+                        float* out = p.part_o + (slot * kRows + x0) * kC + col0;
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const int x = x0 + i;
-                        const float f0 = ctrl->row[x], f1 = ctrl->row[x + 1];
-                        const int s0 = x / p.heads, s1 = (x + 1) / p.heads;
-                        const bool on0 = s0 < r.ns && x - s0 * p.heads < r.nh;
-                        const bool on1 = s1 < r.ns && x + 1 - s1 * p.heads < r.nh;
+                        for (int i = 0; i < 8; ++i)
+                            if (x0 + i < r.n)
 #pragma unroll
-                        for (int blk = 0; blk < 4; ++blk) {
-                            const float y0 = __uint_as_float(v[blk][i]) * f0;
-                            const float y1 = __uint_as_float(v[blk][i + 1]) * f1;
-                            const int col = blk * 128 + warp * 32;
-                            if (split) {
-                                float* out = p.part_o + (slot * kRows + x) * kC + col + lane;
-                                if (on0) out[0] = y0;
-                                if (on1) out[kC] = y1;
-                            } else {
-                                // two lanes exchange: an even lane writes two columns of row x,
-                                // an odd one of row x + 1
-                                const bool up = lane & 1;
+                                for (int blk = 0; blk < 4; ++blk)
+                                    out[i * kC + blk * 128] = __uint_as_float(v[blk][i]) * f[i];
+                    } else {
+                        // two lanes exchange: an even one writes two columns of row x, an odd one
+                        // of row x + 1
+                        const bool up = lane & 1;
+                        uint32_t* out = reinterpret_cast<uint32_t*>(p.o + (row0 + x0 + (up ? 1 : 0)) * kC) +
+                                        (col0 >> 1);
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2)
+#pragma unroll
+                            for (int blk = 0; blk < 4; ++blk) {
+                                const float y0 = __uint_as_float(v[blk][i]) * f[i];
+                                const float y1 = __uint_as_float(v[blk][i + 1]) * f[i + 1];
                                 const float z = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 1);
-                                const uint32_t two = up ? pack_bf16x2(z, y1) : pack_bf16x2(y0, z);
-                                if (up ? on1 : on0)
-                                    reinterpret_cast<uint32_t*>(p.o + out_row(x + (up ? 1 : 0)) * kC + col)[lane >> 1] = two;
+                                if (x0 + i + (up ? 1 : 0) < r.n)
+                                    out[i * (kC / 2) + blk * 64] =
+                                        up ? pack_bf16x2(z, y1) : pack_bf16x2(y0, z);
                             }
-                        }
                     }
                 }
                 if (odd) {
@@ -641,12 +693,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                             const float y = __bfloat162float(p.pages[at + col]);
                             if (isfinite(y)) continue;
                             // token i + 1 of the request is at position k
-                            for (int x = max(0, (i + 1 - r.s0) * p.heads); x < n_act; ++x) {
-                                if (x % p.heads >= r.nh) continue;
+                            for (int x = max(0, (i + 1 - r.s0) * p.heads); x < r.n; ++x) {
                                 if (split) {
                                     p.part_o[(slot * kRows + x) * kC + col] += y;
                                 } else {
-                                    __nv_bfloat16* out = p.o + out_row(x) * kC + col;
+                                    __nv_bfloat16* out = p.o + (row0 + x) * kC + col;
                                     *out = __float2bfloat16(__bfloat162float(*out) + y);
                                 }
                             }
@@ -695,8 +746,8 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     if (d.x < 0) return;
     const Rows r(p, d.y * p.cl + rank);
     const int lane = threadIdx.x & 31, x = blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int s = x / p.heads, h = x - s * p.heads, np = d.z;
-    if (s >= r.ns || h >= r.nh) return;
+    const int np = d.z;
+    if (x >= r.n) return;
     auto row_of = [&](int i) -> size_t {
         return (2 * ((size_t)blockIdx.x + (size_t)i * p.cl) + (i == 0 ? 1 : 0)) * kRows + x;
     };
@@ -743,7 +794,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
         m = mx;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const size_t row = ((size_t)d.x * p.S + r.s0 + s) * p.H + r.h0 + h;
+    const size_t row = (size_t)d.x * p.S * p.H + r.first + x;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         reinterpret_cast<uint2*>(p.o + row * kC)[32 * k + lane] =
@@ -766,6 +817,20 @@ LatentWs latent_ws(int n_cta) {
     return w;
 }
 
+// The pool seen as (64 columns, slot, chunk of 64 columns): boxes of eight slots, whole.
+bool make_boxes_map(CUtensorMap* map, const void* base, uint64_t slots) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {64, slots, kSlot / 64};
+    cuuint64_t strides[2] = {kSlot * 2, 128};
+    cuuint32_t box[3] = {64, 8, kSlot / 64};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t raise_smem_once() {
     static PerDevice<int> state;
     int dev = -1;
@@ -773,7 +838,7 @@ cudaError_t raise_smem_once() {
     if (e != cudaSuccess) return e;
     return (cudaError_t)state.run(dev, (int)cudaErrorInvalidDevice, [](int&) {
         return (int)cudaFuncSetAttribute(latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmem);
+                                         (int)kMaxSmem);
     });
 }
 
@@ -839,7 +904,6 @@ cpa_status cpa_latent_decode(const void* q_c, int64_t qc_token_stride, int64_t q
     p.S = S;
     p.H = H;
     p.lp = 31 - __builtin_clz((unsigned)page_size);
-    p.boxr = page_size < kKeys ? page_size : kKeys;
     p.num_pages = num_pages;
     p.max_len = max_seq_len;
     p.n_ht = (H + kRows - 1) / kRows;
@@ -856,11 +920,14 @@ cpa_status cpa_latent_decode(const void* q_c, int64_t qc_token_stride, int64_t q
                         p.toks) ||
         !make_heads_map(&p.rmap, q_r, kR, H, (uint64_t)B * S, qr_head_stride, qr_token_stride, p.heads,
                         p.toks) ||
-        !make_rows_map(&p.kmap, pages, kSlot, (uint64_t)num_pages * page_size, kSlot, p.boxr))
+        !make_boxes_map(&p.kmap, pages, (uint64_t)num_pages * page_size))
         return CPA_ERR_CUDA;
     if (raise_smem_once() != cudaSuccess) return CPA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    latent_kernel<<<p.n_cta, kThreads, kSmem, s>>>(p);
+    const int rows = p.heads * p.toks;
+    p.n_slots = slots_of(rows);
+    const uint32_t smem = off_k(rows) + (uint32_t)p.n_slots * kSlotBytes + 1024;
+    latent_kernel<<<p.n_cta, kThreads, smem, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return CPA_ERR_LAUNCH;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -52,6 +52,25 @@ __device__ __forceinline__ void tmem_ld_16x256_x8(uint32_t taddr, uint32_t (&r)[
         : "memory");
 }
 #undef W8
+// 8 columns at taddr and at three more places, `apart` columns after one another.
+__device__ __forceinline__ void tmem_ld_4x8(uint32_t taddr, uint32_t apart, uint32_t (&r)[4][8]) {
+#define L8(i, a)                                                                                   \
+    "tcgen05.ld.sync.aligned.32x32b.x8.b32 {" i "}, [" a "];\n\t"
+    asm volatile(L8("%0,%1,%2,%3,%4,%5,%6,%7", "%32") L8("%8,%9,%10,%11,%12,%13,%14,%15", "%33")
+                     L8("%16,%17,%18,%19,%20,%21,%22,%23", "%34")
+                         L8("%24,%25,%26,%27,%28,%29,%30,%31", "%35")
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[0][4]),
+                   "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]), "=r"(r[1][0]), "=r"(r[1][1]),
+                   "=r"(r[1][2]), "=r"(r[1][3]), "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]),
+                   "=r"(r[1][7]), "=r"(r[2][0]), "=r"(r[2][1]), "=r"(r[2][2]), "=r"(r[2][3]),
+                   "=r"(r[2][4]), "=r"(r[2][5]), "=r"(r[2][6]), "=r"(r[2][7]), "=r"(r[3][0]),
+                   "=r"(r[3][1]), "=r"(r[3][2]), "=r"(r[3][3]), "=r"(r[3][4]), "=r"(r[3][5]),
+                   "=r"(r[3][6]), "=r"(r[3][7])
+                 : "r"(taddr), "r"(taddr + apart), "r"(taddr + 2 * apart), "r"(taddr + 3 * apart)
+                 : "memory");
+#undef L8
+}
 __device__ __forceinline__ void tmem_st_x8_nowait(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
