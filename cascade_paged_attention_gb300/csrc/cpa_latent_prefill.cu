@@ -1,6 +1,23 @@
 // cpa_latent_prefill.cu -- causal prefill of ragged prompt chunks over expanded
-// latents: a head's key is its own 128 elements and 64 that all heads share, its
-// value 128.
+// latents, on the tensor cores (tcgen05): a head's key is its own 128 elements and 64
+// that all heads share, its value 128.
+//
+// The plan is that of cpa_window.cu: a unit is two tiles of 128 query tokens of one request
+// and head against the key tiles (128 keys) up to its last token; both query tiles meet each
+// K/V tile while it is in shared memory and take turns on the tensor cores, in the order
+//     PV0(i-1) S0(i) PV1(i-1) S1(i)   for key tile i;
+// P overwrites the scores that it came from, so S0, S1, O0 and O1 fill the 512 columns of
+// TMEM; an issuing warp for each query tile; the order goes on from a unit into the next.
+//
+// What differs: keys of 192 columns make S 1.5 times as long as PV, so that the softmax of one
+// query tile (about 1150 cycles) hides behind the other's products (1280 at the nominal rate);
+// and Q takes 96 KB of shared memory, which leaves 128 KB.  K and V therefore share one ring
+// of eight slots of 16 KB, 128 rows of 64 columns each: a key tile is three slots of K (the
+// third the shared part) and two of V, and what is loaded ahead is three slots at any time,
+// in the order of need.  V's two slots are one operand unless they are the ring's last and
+// its first; then each is an operand of its own.
+//
+// Split, join and values that are not numbers: as in cpa_window.cu.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -10,15 +27,31 @@
 #include "cpa.h"
 #include "cpa_checks.h"
 #include "cpa_device.cuh"
-#include "cpa_launch.cuh"
+#include "cpa_host.h"
 #include "cpa_mma.cuh"
 
 namespace cpa {
 namespace {
 
 constexpr int kNope = 128, kRope = 64, kQk = kNope + kRope, kV = 128;
+constexpr int kThreads = 384;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 256;  // query tokens of a unit
+constexpr int kTile = 128;  // keys of a tile, query tokens of a query tile
+constexpr int kSlots = 8;
+constexpr uint32_t kSlotBytes = 128u * 128u;  // 64 columns of 128 rows
+constexpr uint32_t kQBytes = 3 * kSlotBytes;
+constexpr uint32_t kOffQ = 1024;
+constexpr uint32_t kOffRing = kOffQ + 2 * kQBytes;
+constexpr uint32_t kSmem = kOffRing + kSlots * kSlotBytes + 1024;  // (aligned up inside)
+// What a unit costs besides its tiles, in tiles (see cpa_window.cu).
+constexpr int kUnitCost = 3;
+constexpr int kMinTiles = 2;  // fewest tiles of a block where units have a cost
+constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
+static_assert(kSmem <= 232448, "shared memory of one block");
 
 struct ExpandedParams {
+    CUtensorMap qmap, kmap, rmap, vmap;
     const __nv_bfloat16* q;
     const __nv_bfloat16* k_nope;
     const __nv_bfloat16* k_rope;
@@ -28,8 +61,13 @@ struct ExpandedParams {
     __nv_bfloat16* o;
     float* lse;
     uint32_t* status;
+    uint32_t* bad;    // [n_cta] what each block found wrong
+    int4* desc;       // [n_cta] (first token, tokens, head, parts) of the unit that starts in
+                      // the block's range and goes on past it; first token -1: none
+    float* part_lse;  // [2 n_cta][kRows], log2 units
+    float4* part_o;   // [2 n_cta][32 groups of 4 columns][kRows]
     size_t k_token, k_head, r_token, v_token, v_head;  // strides in elements
-    int B, T, T_k, H;
+    int B, T, T_k, H, n_cta;
     float scale_log2;
 };
 
@@ -49,42 +87,278 @@ __device__ __forceinline__ Request request_of(const ExpandedParams& p, int b, ui
     }
     return r;
 }
+__device__ __forceinline__ int units_of(const Request& r) { return (r.m + kRows - 1) / kRows; }
+// Tiles of a request's query tokens qt * kRows and on.
+__device__ __forceinline__ int tiles_of(const Request& r, int qt) {
+    return (r.L - r.m + min(r.m, (qt + 1) * kRows) + kTile - 1) / kTile;
+}
 
-// One row against keys [k0, k1) (rows of k and v), by a whole warp, key by key: lane l
-// holds elements 2 l, 2 l + 1 of every 64 columns.  Returns the log-sum-exp in log2 units.
-__device__ __forceinline__ float expanded_row(const ExpandedParams& p, size_t row, int h, int k0,
-                                             int k1, float (&o)[4]) {
-    const int lane = threadIdx.x & 31;
-    float q[6];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p.q + row * kQk) + 32 * i + lane);
-        q[2 * i] = __uint_as_float(w << 16);
-        q[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+struct Ctrl {
+    uint64_t q_full[2], q_empty[2];
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: weights of keys 0..63, 64..127
+    uint64_t turn[2];   // the issuing warps' turns
+    uint64_t mma_done;
+    volatile uint64_t redo_ns;  // when a row that is done again last began a run of keys
+    uint32_t tmem_base;
+    volatile uint32_t abort_flag;
+    uint32_t bad;
+    int unit_cost;            // kUnitCost, or 0 where no block takes more than two tiles
+    long long t0, left, per;  // this block's range, in tiles of cost
+    int b, h, qt, off;        // where it begins: a unit, and how far into its cost
+};
+// mbar_wait() of cpa_device.cuh, with a limit that a redo puts off: the rows that are not
+// finite are done again key by key while the other warps wait, for as long as their caches
+// are, and tell the time with every key tile.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Ctrl* c) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (n & 63u) continue;
+        if (c->abort_flag) return false;
+        const uint64_t since = max(t0, (uint64_t)c->redo_ns);
+        if ((int64_t)(globaltimer_ns() - since) > (int64_t)kWaitLimitNs) {
+            atomicOr(&c->bad, CPA_DEV_TIMEOUT);
+            c->abort_flag = 1u;
+            __threadfence_block();
+            return false;
+        }
     }
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctrl* c) {
+    // (the first look by itself: most waits find the phase complete)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_on(bar, parity, c));
+}
+
+constexpr uint32_t kOffWalk = 384;  // the softmax warps' walkers (before them: sums by warp)
+static_assert(sizeof(Ctrl) <= kOffWalk, "control block");
+
+// Cost of one head of a request, by a whole warp (r the same in every lane).
+__device__ __forceinline__ long long head_cost(const Request& r, int unit_cost) {
+    const int lane = threadIdx.x & 31, nq = units_of(r);
+    long long sum = 0;
+    for (int qt = lane; qt < nq; qt += 32) sum += tiles_of(r, qt) + unit_cost;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+// The tiles of one head for a request per lane: short ones by their lane, long ones by the
+// warp.
+__device__ __forceinline__ long long lane_tiles(const Request& r) {
+    const int lane = threadIdx.x & 31, nq = units_of(r);
+    long long sum = 0;
+    for (int qt = 0; qt < nq && nq <= 8; ++qt) sum += tiles_of(r, qt);
+    __syncwarp();
+    for (uint32_t many = __ballot_sync(0xffffffffu, nq > 8); many != 0u; many &= many - 1u) {
+        const int src = __ffs((int)many) - 1;
+        Request q = {0, 0, 0, 0};
+        q.m = __shfl_sync(0xffffffffu, r.m, src);
+        q.L = __shfl_sync(0xffffffffu, r.L, src);
+        const long long c = head_cost(q, 0);
+        if (lane == src) sum = c;
+    }
+    return sum;
+}
+
+// Every thread: the problem's cost, this block's range, and the unit where it begins.  Each
+// thread sums a run of requests; one scan over the block follows.
+__device__ void schedule(const ExpandedParams& p, Ctrl* c, long long* sums) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per_thread = (p.B + kThreads - 1) / kThreads, b0 = (int)threadIdx.x * per_thread;
+    uint32_t bad = 0;
+    long long mine = 0, units = 0;
+    for (int i = 0; i < per_thread; ++i) {
+        Request r = {0, 0, 0, 0};
+        if (b0 + i < p.B) r = request_of(p, b0 + i, bad);
+        mine += lane_tiles(r) * p.H;
+        units += (long long)units_of(r) * p.H;
+    }
+    if (bad) atomicOr(&c->bad, bad);
+    long long incl = mine, incl_units = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        const long long z = __shfl_up_sync(0xffffffffu, incl_units, o);
+        if (lane >= o) {
+            incl += y;
+            incl_units += z;
+        }
+    }
+    if (lane == 31) {
+        sums[warp] = incl;
+        sums[kWarps + warp] = incl_units;
+    }
+    __syncthreads();
+    long long total = 0, before = incl - mine, total_units = 0, units_before = incl_units - units;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) {
+            before += sums[w];
+            units_before += sums[kWarps + w];
+        }
+        total += sums[w];
+        total_units += sums[kWarps + w];
+    }
+    const int unit_cost = total <= 2 * p.n_cta ? 0 : kUnitCost;
+    total += unit_cost * total_units;
+    before += unit_cost * units_before;
+    mine += unit_cost * units;
+    long long per = (total + p.n_cta - 1) / p.n_cta;
+    if (unit_cost) per = max(per, (long long)(kMinTiles + kUnitCost));
+    const long long t0 = per * blockIdx.x;
+    if (threadIdx.x == 0) {
+        c->per = per;
+        c->unit_cost = unit_cost;
+        c->t0 = t0;
+        c->left = t0 < total ? min(per, total - t0) : 0;
+    }
+    // the warp whose requests hold position t0 looks through them
+    const uint32_t here = __ballot_sync(0xffffffffu, before <= t0 && t0 < before + mine);
+    if (here) {
+        const int src = __ffs((int)here) - 1;
+        long long run = __shfl_sync(0xffffffffu, before, src);
+        for (int b = __shfl_sync(0xffffffffu, b0, src);; ++b) {
+            const Request r = request_of(p, b, bad);
+            const long long per_head = head_cost(r, unit_cost);
+            if (t0 >= run + per_head * p.H) {
+                run += per_head * p.H;
+                continue;
+            }
+            // the head, then the query tokens
+            long long off = t0 - run;
+            const int h = (int)(off / per_head);
+            off -= h * per_head;
+            const int nq = units_of(r);
+            long long at = 0;
+            for (int q0 = 0; q0 < nq && at <= off; q0 += 32) {
+                const int cost = q0 + lane < nq ? tiles_of(r, q0 + lane) + unit_cost : 0;
+                long long in = cost;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, in, o);
+                    if (lane >= o) in += y;
+                }
+                const long long ex = at + in - cost;
+                if (ex <= off && off < ex + cost) {
+                    c->b = b;
+                    c->h = h;
+                    c->qt = q0 + lane;
+                    c->off = (int)(off - ex);
+                }
+                at += __shfl_sync(0xffffffffu, in, 31);
+            }
+            break;
+        }
+    }
+    __syncthreads();
+}
+
+// Walks the pieces (unit, tiles [j0, j1)) of this block's range; j0 == j1 past the last.  A
+// unit's own cost counts as lying before its first tile.
+struct Walker {
+    Request r;
+    int b, h, qt, nt, j0, j1, unit_cost;
+    long long left;  // cost of the range after this piece
+    __device__ __forceinline__ void cut(int off) {
+        nt = tiles_of(r, qt);
+        const int take = (int)min((long long)nt + unit_cost - off, left);
+        left -= take;
+        j0 = max(0, off - unit_cost);
+        j1 = max(0, off + take - unit_cost);  // (0: the range ends before the first tile)
+    }
+    __device__ __forceinline__ bool more() const { return j0 < j1; }
+    __device__ __forceinline__ void init(const ExpandedParams& p, const Ctrl* c) {
+        left = c->left;
+        unit_cost = c->unit_cost;
+        b = c->b;
+        h = c->h;
+        qt = c->qt;
+        uint32_t bad = 0;
+        r = request_of(p, b, bad);
+        cut(c->off);
+    }
+    __device__ __forceinline__ void next(const ExpandedParams& p) {
+        if (left == 0) {
+            j0 = j1;
+            return;
+        }
+        if ((++qt) * kRows >= r.m) {
+            qt = 0;
+            if (++h == p.H) {
+                h = 0;
+                uint32_t bad = 0;
+                do r = request_of(p, ++b, bad);
+                while (r.m == 0);  // (cost is left, so a request with tokens is)
+            }
+        }
+        cut(0);
+    }
+    __device__ __forceinline__ int t0() const { return r.t0 + qt * kRows; }        // row of q
+    __device__ __forceinline__ int ntok() const { return min(kRows, r.m - qt * kRows); }
+    __device__ __forceinline__ int p0() const { return r.L - r.m + qt * kRows; }  // its position
+    __device__ __forceinline__ int tiles_q() const { return ntok() > kTile ? 2 : 1; }
+};
+static_assert(kOffWalk + 8 * sizeof(Walker) <= kOffQ, "control block");
+
+// The next piece of a walker in shared memory: one lane walks.
+__device__ __forceinline__ void advance(Walker& w, const ExpandedParams& p) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) w.next(p);
+    __syncwarp();
+}
+
+// One row against keys [k0, k1) (rows of k and v) of head h, by a whole warp: what the row does
+// not see is not touched.  Lane l ends up with columns 4 l .. 4 l + 3 of o (normalised); returns
+// the log-sum-exp in log2 units.
+__device__ __forceinline__ float slow_row(const ExpandedParams& p, Ctrl* c, size_t qrow, int h,
+                                       int k0, int k1, float (&o)[4]) {
+    const int lane = threadIdx.x & 31;
+    const uint2 qn = __ldg(reinterpret_cast<const uint2*>(p.q + qrow * kQk) + lane);
+    const uint32_t qr = __ldg(reinterpret_cast<const uint32_t*>(p.q + qrow * kQk + kNope) + lane);
+    auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+    auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
     float m = ninf_f(), l = 0.f;
     o[0] = o[1] = o[2] = o[3] = 0.f;
-    for (int key = k0; key < k1; ++key) {
-        const uint32_t* kn = reinterpret_cast<const uint32_t*>(p.k_nope + key * p.k_token + h * p.k_head);
-        const uint32_t* kr = reinterpret_cast<const uint32_t*>(p.k_rope + key * p.r_token);
-        const uint32_t* vr = reinterpret_cast<const uint32_t*>(p.v + key * p.v_token + h * p.v_head);
-        float d = 0.f;
+    // four keys at a time, so that their loads and sums overlap
+    for (int k4 = k0; k4 < k1; k4 += 4) {
+        if (lane == 0 && ((k4 - k0) & 127) == 0) c->redo_ns = globaltimer_ns();
+        float s[4];
+        uint2 v[4];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const uint32_t w = __ldg((i < 2 ? kn + 32 * i : kr) + lane);
-            d += q[2 * i] * __uint_as_float(w << 16) + q[2 * i + 1] * __uint_as_float(w & 0xFFFF0000u);
+        for (int u = 0; u < 4; ++u) {
+            const size_t key = min(k4 + u, k1 - 1);
+            const uint2 kn = __ldg(reinterpret_cast<const uint2*>(p.k_nope + key * p.k_token + h * p.k_head) + lane);
+            const uint32_t kr = __ldg(reinterpret_cast<const uint32_t*>(p.k_rope + key * p.r_token) + lane);
+            v[u] = __ldg(reinterpret_cast<const uint2*>(p.v + key * p.v_token + h * p.v_head) + lane);
+            s[u] = lo(qn.x) * lo(kn.x) + hi(qn.x) * hi(kn.x) + lo(qn.y) * lo(kn.y) +
+                   hi(qn.y) * hi(kn.y) + lo(qr) * lo(kr) + hi(qr) * hi(kr);
         }
 #pragma unroll
-        for (int e = 16; e > 0; e >>= 1) d += __shfl_xor_sync(0xffffffffu, d, e);
-        d *= p.scale_log2;
-        const float mn = fmaxf(m, d), r = mn == ninf_f() ? 0.f : mn;
-        const float f = ex2(m - r), e = ex2(d - r);
-        l = l * f + e;
+        for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t w = __ldg(vr + 32 * i + lane);
-            o[2 * i] = o[2 * i] * f + e * __uint_as_float(w << 16);
-            o[2 * i + 1] = o[2 * i + 1] * f + e * __uint_as_float(w & 0xFFFF0000u);
+            for (int u = 0; u < 4; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], d);
+        float mn = m;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            s[u] = k4 + u < k1 ? s[u] * p.scale_log2 : ninf_f();
+            mn = fmaxf(mn, s[u]);
+        }
+        const float r = mn == ninf_f() ? 0.f : mn, f = ex2(m - r);
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] *= f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (k4 + u >= k1) continue;
+            const float e = ex2(s[u] - r);
+            l += e;
+            o[0] += e * lo(v[u].x);
+            o[1] += e * hi(v[u].x);
+            o[2] += e * lo(v[u].y);
+            o[3] += e * hi(v[u].y);
         }
         m = mn;
     }
@@ -94,28 +368,552 @@ __device__ __forceinline__ float expanded_row(const ExpandedParams& p, size_t ro
     return l == 0.f ? ninf_f() : m + lg2(l);
 }
 
-__global__ void __launch_bounds__(256) expanded_rows_kernel(const __grid_constant__ ExpandedParams p) {
-    wait_for_clear();
-    const int lane = threadIdx.x & 31;
-    uint32_t bad = 0;
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < p.B; b += 256) request_of(p, b, bad);
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (w < (long long)p.T * p.H) {
-        const int t = (int)(w / p.H), h = (int)(w % p.H);
-        for (int b = 0; b < p.B; ++b) {
-            uint32_t none = 0;
-            const Request r = request_of(p, b, none);
-            if (t < r.t0 || t >= r.t0 + r.m) continue;
-            float o[4];
-            const float z = expanded_row(p, (size_t)w, h, r.k0, r.k0 + r.L - r.m + (t - r.t0) + 1, o);
-            uint32_t* out = reinterpret_cast<uint32_t*>(p.o + (size_t)w * kV);
-            out[lane] = pack_bf16x2(o[0], o[1]);
-            out[32 + lane] = pack_bf16x2(o[2], o[3]);
-            if (lane == 0) p.lse[w] = z == ninf_f() ? z : z * kLn2;
+__global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_constant__ ExpandedParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&ctrl->full[i], 1);
+            mbar_init(&ctrl->empty[i], 2);  // the two issuing warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctrl->q_full[i], 1);
+            mbar_init(&ctrl->q_empty[i], 1);
+            mbar_init(&ctrl->s_full[i], 1);
+            mbar_init(&ctrl->p_full[i][0], 4);  // one arrival per softmax warp
+            mbar_init(&ctrl->p_full[i][1], 4);
+            mbar_init(&ctrl->o_full[i], 1);
+            mbar_init(&ctrl->turn[i], 1);
+        }
+        mbar_init(&ctrl->mma_done, 2);
+        ctrl->redo_ns = 0;
+        ctrl->abort_flag = 0;
+        ctrl->bad = 0;
+        fence_barrier_init();
+        prefetch_tmap(&p.qmap);
+        prefetch_tmap(&p.kmap);
+        prefetch_tmap(&p.rmap);
+        prefetch_tmap(&p.vmap);
+    }
+    if (warp == 11) {
+        tmem_alloc(&ctrl->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    schedule(p, ctrl, reinterpret_cast<long long*>(smem + kOffWalk));
+    const uint32_t tmem = ctrl->tmem_base;
+    int4 desc = make_int4(-1, 0, 0, 0);
+
+    if (ctrl->left > 0) {
+        if (warp == 8) {
+            // ============================== loads of K and V
+            const uint64_t pol = l2_policy_evict_normal();
+            uint32_t g = 0;  // slots so far
+            bool ok = true;
+            Walker w;
+            w.init(p, ctrl);
+            for (; w.more() && ok; w.next(p)) {
+                if (w.j0 == 0 && w.j1 < w.nt) {
+                    // the unit that this block leaves unfinished, for the join (it ends with
+                    // this piece, which ends with the range)
+                    const long long last = ctrl->t0 + ctrl->left + w.nt - w.j1 - 1;
+                    desc = make_int4(w.t0(), w.ntok(), w.h, (int)(last / ctrl->per - blockIdx.x) + 1);
+                }
+                for (int j = w.j0; j < w.j1 && ok; ++j)
+                    for (int i = 0; i < 5; ++i, ++g) {
+                        const uint32_t st = g % kSlots;
+                        if (g >= kSlots) {
+                            ok = wait_warp(&ctrl->empty[st], (g / kSlots - 1) & 1u, ctrl);
+                            if (!ok) break;
+                        }
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&ctrl->full[st], kSlotBytes);
+                            uint8_t* dst = smem + kOffRing + st * kSlotBytes;
+                            const int key = w.r.k0 + j * kTile;
+                            if (i == 2)
+                                tma_load_2d(dst, &p.rmap, 0, key, &ctrl->full[st], pol);
+                            else
+                                tma_load_3d(dst, i < 2 ? &p.kmap : &p.vmap, i < 2 ? i * 64 : (i - 3) * 64,
+                                            w.h, key, &ctrl->full[st], pol);
+                        }
+                        __syncwarp();
+                    }
+            }
+            // no copy may be in flight when the block leaves
+            for (uint32_t s = 0; s < kSlots; ++s)
+                if (s < g) wait_on(&ctrl->full[s], ((g - 1 - s) / kSlots) & 1u, ctrl);
+            __syncwarp();
+        } else if (warp == 9) {
+            // ============================== loads of Q
+            const uint64_t pol_q = l2_policy_evict_first();
+            uint32_t q_loads[2] = {0u, 0u};
+            bool ok = true;
+            Walker w;
+            w.init(p, ctrl);
+            for (; w.more() && ok; w.next(p)) {
+                const int nq = w.tiles_q();
+                for (int mt = 0; mt < nq && ok; ++mt) {
+                    if (q_loads[mt] > 0)
+                        ok = wait_warp(&ctrl->q_empty[mt], (q_loads[mt] - 1) & 1u, ctrl);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&ctrl->q_full[mt], kQBytes);
+                        for (int c = 0; c < 3; ++c)
+                            tma_load_3d(smem + kOffQ + mt * kQBytes + c * kSlotBytes, &p.qmap, c * 64, w.h,
+                                        w.t0() + mt * kTile, &ctrl->q_full[mt], pol_q);
+                    }
+                    __syncwarp();
+                    ++q_loads[mt];
+                }
+                // the next unit's Q into L2: its load is then short
+                Walker y = w;
+                y.next(p);
+                if (ok && y.more() && lane < 3 * y.tiles_q())
+                    prefetch_3d(&p.qmap, lane % 3 * 64, y.h, y.t0() + lane / 3 * kTile);
+            }
+            for (int mt = 0; mt < 2; ++mt)
+                if (q_loads[mt] > 0) wait_on(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u, ctrl);
+            __syncwarp();
+        } else if (warp >= 10) {
+            // ============================== products of query tile mt
+            // All lanes run the loop, so that addresses and descriptors stay uniform
+            // across the warp; one elected lane's predicate issues.
+            const int mt = warp - 10;
+            const uint32_t lead = elect_one();
+            const uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
+            const uint32_t idesc_o = idesc_bf16_f32(128, 128, true);
+            const uint32_t idesc_w = idesc_bf16_f32(128, 64, true);
+            const uint64_t q_desc = sdesc_sw128(sbase + kOffQ + mt * kQBytes, 16, 1024);
+            const uint64_t k_desc = sdesc_sw128(sbase + kOffRing, 16, 1024);
+            const uint64_t v_desc = sdesc_sw128(sbase + kOffRing, kSlotBytes, 1024);
+            constexpr uint32_t kStep = kSlotBytes >> 4;
+            const uint32_t s_col = tmem + mt * 128u, o_col = tmem + 256u + mt * 128u;
+            uint32_t kg = 0, vg = 3;  // ring positions of the tile whose scores / values are next
+            uint32_t qpar = 0, ppar = 0, tpar = mt == 0 ? 1u : 0u;
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t par) {
+                ok = ok && wait_warp(bar, par, ctrl);
+                return ok;
+            };
+            auto wait_slot = [&](uint32_t at) {
+                return wait(&ctrl->full[at % kSlots], (at / kSlots) & 1u);
+            };
+            // half of PV: 64 keys
+            auto issue_pv = [&](int half, bool first) {
+                const uint32_t st = vg % kSlots;
+#pragma unroll
+                for (int k4 = 0; k4 < 4; ++k4) {
+                    const int kk = half * 4 + k4;
+                    const uint32_t row = (kk * 16 * 128) >> 4, acc = first && kk == 0 ? 0u : 1u;
+                    if (st + 1 < kSlots) {
+                        mma_ts(lead, o_col, s_col + kk * 8u, v_desc + st * kStep + row, idesc_o, acc);
+                    } else {
+                        mma_ts(lead, o_col, s_col + kk * 8u, v_desc + st * kStep + row, idesc_w, acc);
+                        mma_ts(lead, o_col + 64, s_col + kk * 8u, v_desc + row, idesc_w, acc);
+                    }
+                }
+            };
+            // what the tile before the current one was
+            int nq_prev = 0;
+            bool first_prev = false, last_prev = false;
+            // A round: PV of the tile before, S of this one (after the last tile there is
+            // one more round).  The weights are waited for last, as what comes last; the
+            // turn is handed on when all is issued.
+            auto round = [&](int nq, bool first, bool last) {
+                const bool pv = mt < nq_prev, sc = mt < nq;
+                if (pv && !(wait_slot(vg) && wait_slot(vg + 1))) return;
+                if (sc && first) {
+                    if (!wait(&ctrl->q_full[mt], qpar)) return;
+                    qpar ^= 1u;
+                }
+                if (!wait(&ctrl->turn[mt], tpar)) return;
+                tpar ^= 1u;
+                if (pv) {
+                    if (!wait(&ctrl->p_full[mt][0], ppar)) return;
+                    tc_fence_after_sync();
+                    issue_pv(0, first_prev);
+                    if (!wait(&ctrl->p_full[mt][1], ppar)) return;
+                    ppar ^= 1u;
+                    tc_fence_after_sync();
+                    issue_pv(1, false);
+                    if (last_prev) commit(lead, &ctrl->o_full[mt]);
+                    commit(lead, &ctrl->empty[vg % kSlots]);
+                    commit(lead, &ctrl->empty[(vg + 1) % kSlots]);
+                } else if (nq_prev && lead) {
+                    mbar_arrive(&ctrl->empty[vg % kSlots]);
+                    mbar_arrive(&ctrl->empty[(vg + 1) % kSlots]);
+                }
+                if (sc) {
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        if (!wait_slot(kg + c)) return;
+                        const uint64_t b = k_desc + (kg + c) % kSlots * kStep;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ss(lead, s_col, q_desc + c * kStep + kk * 2, b + kk * 2, idesc_s,
+                                   c + kk > 0 ? 1u : 0u);
+                    }
+                    commit(lead, &ctrl->s_full[mt]);
+                    if (last) commit(lead, &ctrl->q_empty[mt]);
+                    for (int c = 0; c < 3; ++c) commit(lead, &ctrl->empty[(kg + c) % kSlots]);
+                } else if (nq && lead) {
+                    for (int c = 0; c < 3; ++c) mbar_arrive(&ctrl->empty[(kg + c) % kSlots]);
+                }
+                if (lead) mbar_arrive(&ctrl->turn[mt ^ 1]);
+                __syncwarp();
+                if (nq_prev) vg += 5;
+                if (nq) kg += 5;
+                nq_prev = nq;
+                first_prev = first;
+                last_prev = last;
+            };
+            Walker w;
+            w.init(p, ctrl);
+            for (; w.more() && ok; w.next(p))
+                for (int j = w.j0; j < w.j1 && ok; ++j)
+                    round(w.tiles_q(), j == w.j0, j == w.j1 - 1);
+            if (ok) round(0, false, false);
+            commit(lead, &ctrl->mma_done);
+            wait_warp(&ctrl->mma_done, 0, ctrl);
+        } else {
+            // ============================== softmax and output
+            const int mt = warp >> 2;
+            const int r = (warp & 3) * 32 + lane, R = mt * 128 + r;
+            const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t s_addr = tmem + lane_addr + mt * 128u;
+            const uint32_t o_addr = tmem + lane_addr + 256u + mt * 128u;
+            uint32_t spar = 0, opar = 0;
+            uint32_t g = 0;  // key tiles of this block so far (the ring's position)
+            bool ok = true;
+            // the walk of this warp, in shared memory: registers are for the scores
+            Walker& w = reinterpret_cast<Walker*>(smem + kOffWalk)[warp];
+            if (lane == 0) w.init(p, ctrl);
+            __syncwarp();
+            while (w.more() && ok) {
+                if (mt >= w.tiles_q()) {
+                    g += w.j1 - w.j0;
+                    advance(w, p);
+                    continue;
+                }
+                const bool active = R < w.ntok();
+                const int pos = w.p0() + R, jend = w.j1;
+                const int p_min = w.p0() + mt * 128;  // position of this query tile's first token
+                const int L = w.r.L;
+                float m_used = ninf_f(), l = 0.f;
+                for (int j = w.j0; j < jend; ++j, ++g) {
+                    const int key0 = j << 7;
+                    ok = wait_warp(&ctrl->s_full[mt], spar, ctrl);
+                    if (!ok) break;
+                    spar ^= 1u;
+                    tc_fence_after_sync();
+                    uint32_t s[128];
+                    tmem_ld_x128(s_addr, s);
+                    if (key0 + 127 > p_min) {
+                        const int z = pos + 1 - key0;  // columns below z
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4) {
+                            const uint32_t bits = bits_below(z - 32 * q4);
+                            // (most groups of an edge tile are whole for the whole warp)
+                            if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(bits >> c & 1u)) s[32 * q4 + c] = 0xff800000u;
+                        }
+                    }
+                    float m4[4] = {ninf_f(), ninf_f(), ninf_f(), ninf_f()};
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        m4[c & 3] = fmax3(m4[c & 3],
+                                          fmax3(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1]),
+                                                __uint_as_float(s[4 * c + 2])),
+                                          __uint_as_float(s[4 * c + 3]));
+                    const float tmax =
+                        fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+                    // O holds every earlier tile of this unit: PV(j - 1) was issued before
+                    // S(j), whose completion s_full told
+                    const bool need = active && m_used != ninf_f() && tmax > m_used + kRescale;
+                    if (__any_sync(0xffffffffu, need)) {
+                        const float f = need ? ex2(m_used - tmax) : 1.f;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 128; c0 += 8) {
+                            uint32_t v[8];
+                            tmem_ld_x8(o_addr + c0, v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                            asm volatile(
+                                "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], "
+                                "{%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(o_addr + c0),
+                                "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+                                "r"(v[6]), "r"(v[7])
+                                : "memory");
+                        }
+                        if (need) {
+                            l *= f;
+                            m_used = tmax;
+                        }
+                    }
+                    if (m_used == ninf_f()) m_used = tmax;
+                    const float mref = m_used == ninf_f() ? 0.f : m_used;
+                    // keys past the sequence's end (the next request's, or none): their V rows are
+                    // cleared (by both query tiles, each before its own products)
+                    if (key0 + 128 > L) {
+                        const uint32_t at = 5 * g + 3;
+                        ok = wait_warp(&ctrl->full[at % kSlots], (at / kSlots) & 1u, ctrl) &&
+                             wait_warp(&ctrl->full[(at + 1) % kSlots], ((at + 1) / kSlots) & 1u, ctrl);
+                        if (!ok) break;
+                        const int first = L - key0;
+                        for (int i = r; i < 16 * (128 - first); i += 128)
+                            *reinterpret_cast<uint4*>(smem + kOffRing + (at + (i & 1)) % kSlots * kSlotBytes +
+                                                      first * 128 + (i >> 1) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                    }
+                    // P = 2^(s * scale - m) in bf16 over the first 64 columns of the scores
+                    // (a weight's rounding of 2^-9 is of the size of the output's own; the
+                    // sum is of the unrounded weights in 32 bits)
+                    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+                    const float2 nm2 = make_float2(-mref, -mref);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float2 t = __ffma2_rn(
+                                make_float2(__uint_as_float(s[32 * q4 + 2 * c]),
+                                            __uint_as_float(s[32 * q4 + 2 * c + 1])),
+                                sc2, nm2);
+                            const float ea = ex2(t.x), eb = ex2(t.y);
+                            sum[c & 1] = __fadd2_rn(sum[c & 1], make_float2(ea, eb));
+                            pk[c] = pack_bf16x2(ea, eb);
+                        }
+                        tmem_st_x16_nowait(s_addr + 16u * q4, pk);
+                        if (q4 & 1) {  // 64 keys: their products may begin
+                            tmem_wait_st();
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&ctrl->p_full[mt][q4 >> 1]);
+                        }
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                }
+                if (!ok) break;
+
+                // ---- output: the row, or its part of a unit cut by the block's range.  The
+                // walk goes on first, while the last products run.
+                const int j0 = w.j0, j1 = w.j1, h = w.h, k0 = w.r.k0;
+                const bool split = j0 > 0 || j1 < w.nt;
+                const int row = (w.t0() + (active ? R : 0)) * p.H + h;
+                advance(w, p);
+                ok = wait_warp(&ctrl->o_full[mt], opar, ctrl);
+                if (!ok) break;
+                opar ^= 1u;
+                tc_fence_after_sync();
+                const size_t slot = 2 * (size_t)blockIdx.x + (j0 > 0 ? 0 : 1);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float lse2 = l == 0.f ? ninf_f() : m_used + lg2(l);
+                // rows of the lane pair, -1 where there is none
+                const int row_x = __shfl_xor_sync(0xffffffffu, active ? row : -1, 1);
+                const int row_e = lane & 1 ? row_x : (active ? row : -1);
+                const int row_o = lane & 1 ? (active ? row : -1) : row_x;
+                float check = lse2 == ninf_f() ? 0.f : lse2;
+                float4* po = p.part_o + slot * 32 * kRows + R;
+                // (Two lanes exchange halves, so that they write 64 bytes of a row together:
+                // 355 -> 350 us against 32 bytes of a row by each; 128 or 256 bytes together
+                // would give 1 us more before the cost of the exchange.  Through shared memory
+                // the whole lines cost as much, and the 32 KB that the third K stage needs.)
+#pragma unroll 1
+                for (int c0 = 0; c0 < 128; c0 += 32) {
+                    uint32_t v[32];
+                    tmem_ld_x32(o_addr + c0, v);
+                    float f[32];
+                    float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        f[i] = __uint_as_float(v[i]) * inv;
+                        z[i & 3] = fmaf(f[i], 0.f, z[i & 3]);  // NaN once any is not finite
+                    }
+                    check += (z[0] + z[1]) + (z[2] + z[3]);
+                    if (split) {
+                        if (active) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                po[(size_t)(c0 / 4 + i) * kRows] =
+                                    make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                        }
+                    } else {
+                        uint32_t w[2][8], x[8];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                w[i][e] = pack_bf16x2(f[16 * i + 2 * e], f[16 * i + 2 * e + 1]);
+                        const bool odd = lane & 1;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            x[e] = __shfl_xor_sync(0xffffffffu, odd ? w[0][e] : w[1][e], 1);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            w[0][e] = odd ? x[e] : w[0][e];
+                            w[1][e] = odd ? w[1][e] : x[e];
+                        }
+                        uint32_t* out = reinterpret_cast<uint32_t*>(p.o) + c0 / 2 + (odd ? 8 : 0);
+                        if (row_e >= 0) store32(out + (size_t)row_e * 64, w[0]);
+                        if (row_o >= 0) store32(out + (size_t)row_o * 64, w[1]);
+                    }
+                }
+                if (active) {
+                    if (split) p.part_lse[slot * kRows + R] = lse2;
+                    else p.lse[row] = lse2 == ninf_f() ? lse2 : lse2 * kLn2;
+                }
+                tc_fence_before_sync();  // O may be written again after this warp's next P
+                __syncwarp();
+                // (a sum that is not a number comes from a seen score: the row's result is
+                // that, in every column)
+                uint32_t again =
+                    __ballot_sync(0xffffffffu, active && isfinite(l) && !isfinite(check));
+                for (; again != 0u; again &= again - 1u) {
+                    const int src = __ffs((int)again) - 1;
+                    const size_t row_a = (size_t)__shfl_sync(0xffffffffu, row, src);
+                    const int pos_a = __shfl_sync(0xffffffffu, pos, src);
+                    const int R_a = __shfl_sync(0xffffffffu, R, src);
+                    float f[4];
+                    const float z = slow_row(p, ctrl, row_a, h, k0 + j0 * 128,
+                                             k0 + min(j1 * 128, pos_a + 1), f);
+                    if (split) {
+                        p.part_o[(slot * 32 + lane) * kRows + R_a] = make_float4(f[0], f[1], f[2], f[3]);
+                        if (lane == 0) p.part_lse[slot * kRows + R_a] = z;
+                    } else {
+                        reinterpret_cast<uint2*>(p.o + row_a * kV)[lane] =
+                            make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+                        if (lane == 0) p.lse[row_a] = z == ninf_f() ? z : z * kLn2;
+                    }
+                }
+            }
         }
     }
-    if (bad) flag(p.status, bad);
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 11) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+    if (warp == 8 && lane == 0) {
+        p.desc[blockIdx.x] = desc;
+        p.bad[blockIdx.x] = ctrl->bad;
+    }
+}
+
+// Joins the unit that starts in block c's range and goes on past its end: its
+// parts are block c's second slot and the first slots of the blocks after it, in
+// that order.  A block does 32 rows (grid.y), a thread 4 columns of a row at a
+// time.  The last block, whose range nothing follows, gathers the status word.
+__global__ void __launch_bounds__(256) expanded_join_kernel(const __grid_constant__ ExpandedParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y > 0) return;
+        __shared__ uint32_t all;
+        if (threadIdx.x == 0) all = 0;
+        __syncthreads();
+        uint32_t bad = 0;
+        for (int i = threadIdx.x; i < p.n_cta; i += 256) bad |= __ldcg(p.bad + i);
+        if (bad) atomicOr(&all, bad);
+        __syncthreads();
+        if (threadIdx.x == 0) *p.status = all;
+        return;
+    }
+    const int4 d = __ldcg(p.desc + blockIdx.x);
+    if (d.x < 0) return;
+    const int np = d.w;
+    const int R = blockIdx.y * 32 + (threadIdx.x & 31);
+    if (R >= d.y) return;
+    const size_t row = (size_t)(d.x + R) * p.H + d.z;
+    auto slot = [&](int i) -> size_t { return 2 * ((size_t)blockIdx.x + i) + (i == 0 ? 1 : 0); };
+    float m = ninf_f(), sum = 0.f;
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int g0 = threadIdx.x >> 5;  // column groups g0, g0 + 8, g0 + 16, g0 + 24
+    for (int i0 = 0; i0 < np; i0 += 4) {  // four parts' loads in flight at a time
+        float4 y[4][4];
+        float z[4], mx = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t at = slot(min(i0 + i, np - 1));
+            z[i] = __ldcg(p.part_lse + at * kRows + R);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[i][k] = __ldcg(p.part_o + (at * 32 + g0 + 8 * k) * kRows + R);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i0 + i < np) mx = fmaxf(mx, z[i]);
+        const float ref = mx == ninf_f() ? 0.f : mx, f = ex2(m - ref);
+        sum *= f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            acc[k].x *= f;
+            acc[k].y *= f;
+            acc[k].z *= f;
+            acc[k].w *= f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i0 + i >= np) break;
+            const float w = ex2(z[i] - ref);
+            sum += w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[k].x += w * y[i][k].x;
+                acc[k].y += w * y[i][k].y;
+                acc[k].z += w * y[i][k].z;
+                acc[k].w += w * y[i][k].w;
+            }
+        }
+        m = mx;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        reinterpret_cast<uint2*>(p.o + row * 128)[g0 + 8 * k] =
+            make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
+                       pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    if (g0 == 0)
+        p.lse[row] = sum == 0.f ? ninf_f() : ((m == ninf_f() ? 0.f : m) + lg2(sum)) * kLn2;
+}
+
+struct ExpandedWs {
+    size_t bad, desc, part_lse, part_o, total;
+};
+ExpandedWs expanded_ws(int n_cta) {
+    ExpandedWs w;
+    w.bad = kStatusBytes;
+    w.desc = align_up(w.bad + (size_t)n_cta * 4, 256);
+    w.part_lse = align_up(w.desc + (size_t)n_cta * 16, 256);
+    w.part_o = align_up(w.part_lse + (size_t)2 * n_cta * kRows * 4, 256);
+    w.total = align_up(w.part_o + (size_t)2 * n_cta * kRows * 128 * 4, 256);
+    return w;
+}
+
+cudaError_t raise_smem_once() {
+    static PerDevice<int> state;
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return (cudaError_t)state.run(dev, (int)cudaErrorInvalidDevice, [](int&) {
+        return (int)cudaFuncSetAttribute(expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmem);
+    });
 }
 
 }  // namespace
@@ -129,7 +927,8 @@ size_t cpa_latent_prefill_workspace_size(int B, int T, int T_k, int H, int nope_
                                          int v_dim) {
     if (B < 1 || T < 0 || T_k < 0 || H < 1 || nope_dim != kNope || rope_dim != kRope || v_dim != kV)
         return 0;
-    return kStatusBytes;
+    const int n_sm = sm_count();
+    return n_sm <= 0 ? 0 : expanded_ws(n_sm).total;
 }
 
 cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token_stride,
@@ -154,7 +953,12 @@ cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token
     if (!workspace || workspace_bytes < kStatusBytes) return CPA_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return CPA_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (T == 0) return clear_status(workspace, s);
+    if (T == 0) return cudaMemsetAsync(workspace, 0, 4, s) == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
+    const int n_sm = sm_count();
+    if (n_sm <= 0) return CPA_ERR_CUDA;
+    const ExpandedWs w = expanded_ws(n_sm);
+    if (workspace_bytes < w.total) return CPA_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     ExpandedParams p = {};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.k_nope = static_cast<const __nv_bfloat16*>(k_nope);
@@ -164,7 +968,11 @@ cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token
     p.k_start = k_start;
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
-    p.status = static_cast<uint32_t*>(workspace);
+    p.status = reinterpret_cast<uint32_t*>(ws);
+    p.bad = reinterpret_cast<uint32_t*>(ws + w.bad);
+    p.desc = reinterpret_cast<int4*>(ws + w.desc);
+    p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+    p.part_o = reinterpret_cast<float4*>(ws + w.part_o);
     p.k_token = (size_t)k_token_stride;
     p.k_head = (size_t)k_head_stride;
     p.r_token = (size_t)rope_token_stride;
@@ -175,8 +983,31 @@ cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token
     p.T_k = T_k;
     p.H = H;
     p.scale_log2 = sm_scale * kLog2e;
-    const long long rows = (long long)T * H;
-    return launch_cleared(expanded_rows_kernel, dim3((unsigned)((rows + 7) / 8)), 256, s, p.status, p);
+    p.n_cta = n_sm;
+    // (no keys: every request is empty, or its starts are refused on the device; the maps are
+    // not used then)
+    const void* const kn = T_k > 0 ? k_nope : q;
+    const void* const kr = T_k > 0 ? k_rope : q;
+    const void* const vv = T_k > 0 ? v : q;
+    const uint64_t keys = T_k > 0 ? (uint64_t)T_k : 1;
+    if (!make_heads_map(&p.qmap, q, kQk, H, (uint64_t)T, kQk, (int64_t)H * kQk, 1, 128) ||
+        !make_heads_map(&p.kmap, kn, kNope, H, keys, k_head_stride, k_token_stride, 1, 128) ||
+        !make_heads_map(&p.vmap, vv, kV, H, keys, v_head_stride, v_token_stride, 1, 128) ||
+        !make_rows_map(&p.rmap, kr, kRope, keys, rope_token_stride, 128))
+        return CPA_ERR_CUDA;
+    if (raise_smem_once() != cudaSuccess) return CPA_ERR_CUDA;
+    expanded_kernel<<<n_sm, kThreads, kSmem, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return CPA_ERR_LAUNCH;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)n_sm, kRows / 32);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, expanded_join_kernel, p) == cudaSuccess ? CPA_OK : CPA_ERR_LAUNCH;
 }
 
 }  // extern "C"
