@@ -12,10 +12,9 @@
 // What differs: keys of 192 columns make S 1.5 times as long as PV, so that the softmax of one
 // query tile (about 1150 cycles) hides behind the other's products (1280 at the nominal rate);
 // and Q takes 96 KB of shared memory, which leaves 128 KB.  K and V therefore share one ring
-// of eight slots of 16 KB, 128 rows of 64 columns each: a key tile is three slots of K (the
-// third the shared part) and two of V, and what is loaded ahead is three slots at any time,
-// in the order of need.  V's two slots are one operand unless they are the ring's last and
-// its first; then each is an operand of its own.
+// of eight slots of 16 KB, filled in the order of need: a key tile is three slots of K (128
+// keys of 64 columns each, the third the shared part) and two of V (64 keys of 128 columns).
+// Each is free as soon as its own products are done.
 //
 // Split, join and values that are not numbers: as in cpa_window.cu.
 #include <cuda_bf16.h>
@@ -39,7 +38,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 256;  // query tokens of a unit
 constexpr int kTile = 128;  // keys of a tile, query tokens of a query tile
 constexpr int kSlots = 8;
-constexpr uint32_t kSlotBytes = 128u * 128u;  // 64 columns of 128 rows
+constexpr uint32_t kSlotBytes = 128u * 128u;
 constexpr uint32_t kQBytes = 3 * kSlotBytes;
 constexpr uint32_t kOffQ = 1024;
 constexpr uint32_t kOffRing = kOffQ + 2 * kQBytes;
@@ -438,11 +437,14 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                             mbar_arrive_expect_tx(&ctrl->full[st], kSlotBytes);
                             uint8_t* dst = smem + kOffRing + st * kSlotBytes;
                             const int key = w.r.k0 + j * kTile;
-                            if (i == 2)
+                            if (i < 2)
+                                tma_load_3d(dst, &p.kmap, i * 64, w.h, key, &ctrl->full[st], pol);
+                            else if (i == 2)
                                 tma_load_2d(dst, &p.rmap, 0, key, &ctrl->full[st], pol);
                             else
-                                tma_load_3d(dst, i < 2 ? &p.kmap : &p.vmap, i < 2 ? i * 64 : (i - 3) * 64,
-                                            w.h, key, &ctrl->full[st], pol);
+                                for (int c = 0; c < 2; ++c)
+                                    tma_load_3d(dst + c * (kSlotBytes / 2), &p.vmap, c * 64, w.h,
+                                                key + (i - 3) * 64, &ctrl->full[st], pol);
                         }
                         __syncwarp();
                     }
@@ -490,10 +492,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             const uint32_t lead = elect_one();
             const uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
             const uint32_t idesc_o = idesc_bf16_f32(128, 128, true);
-            const uint32_t idesc_w = idesc_bf16_f32(128, 64, true);
             const uint64_t q_desc = sdesc_sw128(sbase + kOffQ + mt * kQBytes, 16, 1024);
             const uint64_t k_desc = sdesc_sw128(sbase + kOffRing, 16, 1024);
-            const uint64_t v_desc = sdesc_sw128(sbase + kOffRing, kSlotBytes, 1024);
+            const uint64_t v_desc = sdesc_sw128(sbase + kOffRing, kSlotBytes / 2, 1024);
             constexpr uint32_t kStep = kSlotBytes >> 4;
             const uint32_t s_col = tmem + mt * 128u, o_col = tmem + 256u + mt * 128u;
             uint32_t kg = 0, vg = 3;  // ring positions of the tile whose scores / values are next
@@ -508,18 +509,12 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             };
             // half of PV: 64 keys
             auto issue_pv = [&](int half, bool first) {
-                const uint32_t st = vg % kSlots;
+                const uint64_t b = v_desc + (vg + half) % kSlots * kStep;
 #pragma unroll
-                for (int k4 = 0; k4 < 4; ++k4) {
-                    const int kk = half * 4 + k4;
-                    const uint32_t row = (kk * 16 * 128) >> 4, acc = first && kk == 0 ? 0u : 1u;
-                    if (st + 1 < kSlots) {
-                        mma_ts(lead, o_col, s_col + kk * 8u, v_desc + st * kStep + row, idesc_o, acc);
-                    } else {
-                        mma_ts(lead, o_col, s_col + kk * 8u, v_desc + st * kStep + row, idesc_w, acc);
-                        mma_ts(lead, o_col + 64, s_col + kk * 8u, v_desc + row, idesc_w, acc);
-                    }
-                }
+                for (int k4 = 0; k4 < 4; ++k4)
+                    mma_ts(lead, o_col, s_col + (half * 4 + k4) * 8u, b + ((k4 * 16 * 128) >> 4), idesc_o,
+                           first && k4 == 0 ? 0u : 1u);
+                commit(lead, &ctrl->empty[(vg + half) % kSlots]);
             };
             // what the tile before the current one was
             int nq_prev = 0;
@@ -529,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             // turn is handed on when all is issued.
             auto round = [&](int nq, bool first, bool last) {
                 const bool pv = mt < nq_prev, sc = mt < nq;
-                if (pv && !(wait_slot(vg) && wait_slot(vg + 1))) return;
+                if (pv && !wait_slot(vg)) return;
                 if (sc && first) {
                     if (!wait(&ctrl->q_full[mt], qpar)) return;
                     qpar ^= 1u;
@@ -540,13 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                     if (!wait(&ctrl->p_full[mt][0], ppar)) return;
                     tc_fence_after_sync();
                     issue_pv(0, first_prev);
+                    if (!wait_slot(vg + 1)) return;
                     if (!wait(&ctrl->p_full[mt][1], ppar)) return;
                     ppar ^= 1u;
                     tc_fence_after_sync();
                     issue_pv(1, false);
                     if (last_prev) commit(lead, &ctrl->o_full[mt]);
-                    commit(lead, &ctrl->empty[vg % kSlots]);
-                    commit(lead, &ctrl->empty[(vg + 1) % kSlots]);
                 } else if (nq_prev && lead) {
                     mbar_arrive(&ctrl->empty[vg % kSlots]);
                     mbar_arrive(&ctrl->empty[(vg + 1) % kSlots]);
@@ -561,10 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                         for (int kk = 0; kk < 4; ++kk)
                             mma_ss(lead, s_col, q_desc + c * kStep + kk * 2, b + kk * 2, idesc_s,
                                    c + kk > 0 ? 1u : 0u);
+                        commit(lead, &ctrl->empty[(kg + c) % kSlots]);
                     }
                     commit(lead, &ctrl->s_full[mt]);
                     if (last) commit(lead, &ctrl->q_empty[mt]);
-                    for (int c = 0; c < 3; ++c) commit(lead, &ctrl->empty[(kg + c) % kSlots]);
                 } else if (nq && lead) {
                     for (int c = 0; c < 3; ++c) mbar_arrive(&ctrl->empty[(kg + c) % kSlots]);
                 }
@@ -672,10 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                              wait_warp(&ctrl->full[(at + 1) % kSlots], ((at + 1) / kSlots) & 1u, ctrl);
                         if (!ok) break;
                         const int first = L - key0;
-                        for (int i = r; i < 16 * (128 - first); i += 128)
-                            *reinterpret_cast<uint4*>(smem + kOffRing + (at + (i & 1)) % kSlots * kSlotBytes +
-                                                      first * 128 + (i >> 1) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                        for (int i = 16 * first + r; i < 16 * 128; i += 128) {  // 16 bytes of key i / 16
+                            const int k = i >> 4, c = i & 15;
+                            *reinterpret_cast<uint4*>(smem + kOffRing + (at + (k >> 6)) % kSlots * kSlotBytes +
+                                                      (c >> 3) * (kSlotBytes / 2) + (k & 63) * 128 +
+                                                      (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
                         fence_proxy_async_smem();
                     }
                     // P = 2^(s * scale - m) in bf16 over the first 64 columns of the scores
@@ -992,7 +988,7 @@ cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token
     const uint64_t keys = T_k > 0 ? (uint64_t)T_k : 1;
     if (!make_heads_map(&p.qmap, q, kQk, H, (uint64_t)T, kQk, (int64_t)H * kQk, 1, 128) ||
         !make_heads_map(&p.kmap, kn, kNope, H, keys, k_head_stride, k_token_stride, 1, 128) ||
-        !make_heads_map(&p.vmap, vv, kV, H, keys, v_head_stride, v_token_stride, 1, 128) ||
+        !make_heads_map(&p.vmap, vv, kV, H, keys, v_head_stride, v_token_stride, 1, 64) ||
         !make_rows_map(&p.rmap, kr, kRope, keys, rope_token_stride, 128))
         return CPA_ERR_CUDA;
     if (raise_smem_once() != cudaSuccess) return CPA_ERR_CUDA;
