@@ -16,7 +16,16 @@
 // keys of 64 columns each, the third the shared part) and two of V (64 keys of 128 columns).
 // Each is free as soon as its own products are done.
 //
-// Split, join and values that are not numbers: as in cpa_window.cu.
+// Who does what.  A call with few units a block is split as in cpa_window.cu: the key tiles of
+// all units lie end to end in the order request, head, query tokens, every block takes a range
+// of equal cost, and a second kernel joins the units that a range's end cuts.  With heads that
+// share no keys that order has every head's K and V in use at a time, more than L2 holds
+// (2 x 8192 tokens, 32 heads: 3.8 GB read from DRAM in place of 0.6).  A call with many units
+// therefore hands them out whole, a few heads at a time, the longest of these heads first, so
+// that what is left at the end is short.  Either way the warp that loads K and V finds the
+// units, and the others read them from a ring in shared memory.
+//
+// Values that are not numbers: as in cpa_window.cu.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -46,6 +55,9 @@ constexpr uint32_t kSmem = kOffRing + kSlots * kSlotBytes + 1024;  // (aligned u
 // What a unit costs besides its tiles, in tiles (see cpa_window.cu).
 constexpr int kUnitCost = 3;
 constexpr int kMinTiles = 2;  // fewest tiles of a block where units have a cost
+constexpr int kWholeUnits = 6;       // units a block from which they are handed out whole
+constexpr int kMostHeads = 8;        // that are handed out side by side,
+constexpr int kSharedKeys = 65536;   // as long as their keys are no more than these (32 MB)
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
 static_assert(kSmem <= 232448, "shared memory of one block");
 
@@ -66,7 +78,9 @@ struct ExpandedParams {
     float* part_lse;  // [2 n_cta][kRows], log2 units
     float4* part_o;   // [2 n_cta][32 groups of 4 columns][kRows]
     size_t k_token, k_head, r_token, v_token, v_head;  // strides in elements
+    uint32_t* counter;  // units handed out beyond the blocks' first ones
     int B, T, T_k, H, n_cta;
+    int whole;          // units are handed out whole
     float scale_log2;
 };
 
@@ -92,7 +106,19 @@ __device__ __forceinline__ int tiles_of(const Request& r, int qt) {
     return (r.L - r.m + min(r.m, (qt + 1) * kRows) + kTile - 1) / kTile;
 }
 
+// A unit, or the part [j0, j1) of its tiles that a block does; j0 == j1: no more.
+struct Piece {
+    int t0, ntok;  // rows of q
+    int p0;        // position of the first
+    int k0, L;     // rows of k and v
+    int h, nt, j0, j1;
+    __device__ __forceinline__ int tiles_q() const { return ntok > kTile ? 2 : 1; }
+};
+constexpr int kPieces = 4;   // of the ring: the one that is loaded and the next, two behind
+constexpr int kReaders = 11; // warps that read it
+
 struct Ctrl {
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t q_full[2], q_empty[2];
     uint64_t full[kSlots], empty[kSlots];
     uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: weights of keys 0..63, 64..127
@@ -105,6 +131,7 @@ struct Ctrl {
     int unit_cost;            // kUnitCost, or 0 where no block takes more than two tiles
     long long t0, left, per;  // this block's range, in tiles of cost
     int b, h, qt, off;        // where it begins: a unit, and how far into its cost
+    Piece piece[kPieces];
 };
 // mbar_wait() of cpa_device.cuh, with a limit that a redo puts off: the rows that are not
 // finite are done again key by key while the other warps wait, for as long as their caches
@@ -131,8 +158,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctrl* 
     return __all_sync(0xffffffffu, wait_on(bar, parity, c));
 }
 
-constexpr uint32_t kOffWalk = 384;  // the softmax warps' walkers (before them: sums by warp)
-static_assert(sizeof(Ctrl) <= kOffWalk, "control block");
+static_assert(sizeof(Ctrl) + 2 * kWarps * 8 <= kOffQ && sizeof(Ctrl) % 8 == 0, "control block");
 
 // Cost of one head of a request, by a whole warp (r the same in every lane).
 __device__ __forceinline__ long long head_cost(const Request& r, int unit_cost) {
@@ -255,59 +281,97 @@ __device__ void schedule(const ExpandedParams& p, Ctrl* c, long long* sums) {
     __syncthreads();
 }
 
-// Walks the pieces (unit, tiles [j0, j1)) of this block's range; j0 == j1 past the last.  A
-// unit's own cost counts as lying before its first tile.
-struct Walker {
+// Finds this block's pieces, by a whole warp.
+struct Finder {
     Request r;
-    int b, h, qt, nt, j0, j1, unit_cost;
+    int b, h, qt, unit_cost;
     long long left;  // cost of the range after this piece
-    __device__ __forceinline__ void cut(int off) {
-        nt = tiles_of(r, qt);
-        const int take = (int)min((long long)nt + unit_cost - off, left);
-        left -= take;
-        j0 = max(0, off - unit_cost);
-        j1 = max(0, off + take - unit_cost);  // (0: the range ends before the first tile)
+    int base;        // whole units: the first of request b
+    bool first;
+    __device__ __forceinline__ Piece piece(int j0, int j1) const {
+        const int m0 = qt * kRows;
+        return {r.t0 + m0, min(kRows, r.m - m0), r.L - r.m + m0, r.k0, r.L, h, tiles_of(r, qt), j0, j1};
     }
-    __device__ __forceinline__ bool more() const { return j0 < j1; }
+    // [off, ..) of the unit's cost, of which its own lies before its first tile
+    __device__ __forceinline__ Piece cut(int off) {
+        const int take = (int)min((long long)tiles_of(r, qt) + unit_cost - off, left);
+        left -= take;
+        // (0, 0: the range ends before the first tile)
+        return piece(max(0, off - unit_cost), max(0, off + take - unit_cost));
+    }
     __device__ __forceinline__ void init(const ExpandedParams& p, const Ctrl* c) {
+        first = true;
         left = c->left;
         unit_cost = c->unit_cost;
-        b = c->b;
-        h = c->h;
-        qt = c->qt;
         uint32_t bad = 0;
+        base = 0;
+        // (a block without a range has no place where it begins)
+        const bool range = !p.whole && left > 0;
+        b = range ? c->b : 0;
+        h = range ? c->h : 0;
+        qt = range ? c->qt : 0;
         r = request_of(p, b, bad);
-        cut(c->off);
     }
-    __device__ __forceinline__ void next(const ExpandedParams& p) {
-        if (left == 0) {
-            j0 = j1;
-            return;
+    __device__ __forceinline__ Piece next(const ExpandedParams& p, const Ctrl* c) {
+        uint32_t bad = 0;
+        const Piece none = {};
+        const bool begin = first;
+        first = false;
+        if (p.whole) {
+            int u = blockIdx.x;
+            if (!begin) {
+                if ((threadIdx.x & 31) == 0) u = p.n_cta + (int)atomicAdd(p.counter, 1u);
+                u = __shfl_sync(0xffffffffu, u, 0);
+            }
+            while (u - base >= units_of(r) * p.H) {
+                base += units_of(r) * p.H;
+                if (++b == p.B) {
+                    b = p.B - 1;  // (no unit is at or past here)
+                    r.m = 0;
+                    return none;
+                }
+                r = request_of(p, b, bad);
+            }
+            // as many heads at a time as kSharedKeys allows, the last query tokens first
+            const int nq = units_of(r);
+            const int most = min(p.H, max(1, min(kMostHeads, kSharedKeys / max(r.L, 1))));
+            const int x = u - base, h0 = x / (nq * most) * most;
+            const int heads = min(most, p.H - h0), y = x - h0 * nq;
+            qt = nq - 1 - y / heads;
+            h = h0 + y % heads;
+            return piece(0, tiles_of(r, qt));
         }
+        if (begin) return left > 0 ? cut(c->off) : none;
+        if (left == 0) return none;
         if ((++qt) * kRows >= r.m) {
             qt = 0;
             if (++h == p.H) {
                 h = 0;
-                uint32_t bad = 0;
                 do r = request_of(p, ++b, bad);
                 while (r.m == 0);  // (cost is left, so a request with tokens is)
             }
         }
-        cut(0);
+        return cut(0);
     }
-    __device__ __forceinline__ int t0() const { return r.t0 + qt * kRows; }        // row of q
-    __device__ __forceinline__ int ntok() const { return min(kRows, r.m - qt * kRows); }
-    __device__ __forceinline__ int p0() const { return r.L - r.m + qt * kRows; }  // its position
-    __device__ __forceinline__ int tiles_q() const { return ntok() > kTile ? 2 : 1; }
 };
-static_assert(kOffWalk + 8 * sizeof(Walker) <= kOffQ, "control block");
 
-// The next piece of a walker in shared memory: one lane walks.
-__device__ __forceinline__ void advance(Walker& w, const ExpandedParams& p) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) w.next(p);
-    __syncwarp();
-}
+// The pieces as the other warps read them.
+struct Reader {
+    uint32_t n;
+    Piece x;
+    // the next piece; false: no more, or a wait gave up
+    __device__ __forceinline__ bool next(Ctrl* c) {
+        if (!wait_warp(&c->piece_full[n % kPieces], (n / kPieces) & 1u, c)) return false;
+        x = c->piece[n % kPieces];
+        return x.j0 < x.j1;
+    }
+    // it is not looked at again
+    __device__ __forceinline__ void done(Ctrl* c) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&c->piece_empty[n % kPieces]);
+        ++n;
+    }
+};
 
 // One row against keys [k0, k1) (rows of k and v) of head h, by a whole warp: what the row does
 // not see is not touched.  Lane l ends up with columns 4 l .. 4 l + 3 of o (normalised); returns
@@ -377,6 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (threadIdx.x == 0) {
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&ctrl->piece_full[i], 1);
+            mbar_init(&ctrl->piece_empty[i], kReaders);
+        }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&ctrl->full[i], 1);
             mbar_init(&ctrl->empty[i], 2);  // the two issuing warps
@@ -407,26 +475,43 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    schedule(p, ctrl, reinterpret_cast<long long*>(smem + kOffWalk));
+    schedule(p, ctrl, reinterpret_cast<long long*>(smem + sizeof(Ctrl)));
     const uint32_t tmem = ctrl->tmem_base;
     int4 desc = make_int4(-1, 0, 0, 0);
 
-    if (ctrl->left > 0) {
+    {
         if (warp == 8) {
             // ============================== loads of K and V
             const uint64_t pol = l2_policy_evict_normal();
             uint32_t g = 0;  // slots so far
+            uint32_t n = 0;  // pieces shown
             bool ok = true;
-            Walker w;
-            w.init(p, ctrl);
-            for (; w.more() && ok; w.next(p)) {
-                if (w.j0 == 0 && w.j1 < w.nt) {
+            Finder find;
+            find.init(p, ctrl);
+            auto show = [&]() -> Piece {
+                const Piece x = find.next(p, ctrl);
+                if (n >= kPieces)
+                    ok = wait_warp(&ctrl->piece_empty[n % kPieces], (n / kPieces - 1) & 1u, ctrl);
+                if (lane == 0 && ok) {
+                    ctrl->piece[n % kPieces] = x;
+                    mbar_arrive(&ctrl->piece_full[n % kPieces]);
+                }
+                __syncwarp();
+                ++n;
+                return x;
+            };
+            Piece x = show();
+            while (x.j0 < x.j1 && ok) {
+                // (one piece ahead, so that its Q can be asked for)
+                const Piece next = show();
+                if (!ok) break;
+                if (x.j0 == 0 && x.j1 < x.nt) {
                     // the unit that this block leaves unfinished, for the join (it ends with
                     // this piece, which ends with the range)
-                    const long long last = ctrl->t0 + ctrl->left + w.nt - w.j1 - 1;
-                    desc = make_int4(w.t0(), w.ntok(), w.h, (int)(last / ctrl->per - blockIdx.x) + 1);
+                    const long long last = ctrl->t0 + ctrl->left + x.nt - x.j1 - 1;
+                    desc = make_int4(x.t0, x.ntok, x.h, (int)(last / ctrl->per - blockIdx.x) + 1);
                 }
-                for (int j = w.j0; j < w.j1 && ok; ++j)
+                for (int j = x.j0; j < x.j1 && ok; ++j)
                     for (int i = 0; i < 5; ++i, ++g) {
                         const uint32_t st = g % kSlots;
                         if (g >= kSlots) {
@@ -436,18 +521,19 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&ctrl->full[st], kSlotBytes);
                             uint8_t* dst = smem + kOffRing + st * kSlotBytes;
-                            const int key = w.r.k0 + j * kTile;
+                            const int key = x.k0 + j * kTile;
                             if (i < 2)
-                                tma_load_3d(dst, &p.kmap, i * 64, w.h, key, &ctrl->full[st], pol);
+                                tma_load_3d(dst, &p.kmap, i * 64, x.h, key, &ctrl->full[st], pol);
                             else if (i == 2)
                                 tma_load_2d(dst, &p.rmap, 0, key, &ctrl->full[st], pol);
                             else
                                 for (int c = 0; c < 2; ++c)
-                                    tma_load_3d(dst + c * (kSlotBytes / 2), &p.vmap, c * 64, w.h,
+                                    tma_load_3d(dst + c * (kSlotBytes / 2), &p.vmap, c * 64, x.h,
                                                 key + (i - 3) * 64, &ctrl->full[st], pol);
                         }
                         __syncwarp();
                     }
+                x = next;
             }
             // no copy may be in flight when the block leaves
             for (uint32_t s = 0; s < kSlots; ++s)
@@ -458,10 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             const uint64_t pol_q = l2_policy_evict_first();
             uint32_t q_loads[2] = {0u, 0u};
             bool ok = true;
-            Walker w;
-            w.init(p, ctrl);
-            for (; w.more() && ok; w.next(p)) {
-                const int nq = w.tiles_q();
+            Reader w = {};
+            bool more = w.next(ctrl);
+            while (more && ok) {
+                const Piece x = w.x;
+                const int nq = x.tiles_q();
+                w.done(ctrl);
+                more = w.next(ctrl);
                 for (int mt = 0; mt < nq && ok; ++mt) {
                     if (q_loads[mt] > 0)
                         ok = wait_warp(&ctrl->q_empty[mt], (q_loads[mt] - 1) & 1u, ctrl);
@@ -469,17 +558,15 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&ctrl->q_full[mt], kQBytes);
                         for (int c = 0; c < 3; ++c)
-                            tma_load_3d(smem + kOffQ + mt * kQBytes + c * kSlotBytes, &p.qmap, c * 64, w.h,
-                                        w.t0() + mt * kTile, &ctrl->q_full[mt], pol_q);
+                            tma_load_3d(smem + kOffQ + mt * kQBytes + c * kSlotBytes, &p.qmap, c * 64, x.h,
+                                        x.t0 + mt * kTile, &ctrl->q_full[mt], pol_q);
                     }
                     __syncwarp();
                     ++q_loads[mt];
                 }
                 // the next unit's Q into L2: its load is then short
-                Walker y = w;
-                y.next(p);
-                if (ok && y.more() && lane < 3 * y.tiles_q())
-                    prefetch_3d(&p.qmap, lane % 3 * 64, y.h, y.t0() + lane / 3 * kTile);
+                if (more && lane < 3 * w.x.tiles_q())
+                    prefetch_3d(&p.qmap, lane % 3 * 64, w.x.h, w.x.t0 + lane / 3 * kTile);
             }
             for (int mt = 0; mt < 2; ++mt)
                 if (q_loads[mt] > 0) wait_on(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u, ctrl);
@@ -570,12 +657,13 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                 first_prev = first;
                 last_prev = last;
             };
-            Walker w;
-            w.init(p, ctrl);
-            for (; w.more() && ok; w.next(p))
-                for (int j = w.j0; j < w.j1 && ok; ++j)
-                    round(w.tiles_q(), j == w.j0, j == w.j1 - 1);
-            if (ok) round(0, false, false);
+            Reader w = {};
+            while (ok && w.next(ctrl)) {
+                const int nq = w.x.tiles_q(), n_tiles = w.x.j1 - w.x.j0;
+                w.done(ctrl);
+                for (int j = 0; j < n_tiles && ok; ++j) round(nq, j == 0, j == n_tiles - 1);
+            }
+            if (ok && kg > 0) round(0, false, false);
             commit(lead, &ctrl->mma_done);
             wait_warp(&ctrl->mma_done, 0, ctrl);
         } else {
@@ -588,22 +676,21 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             uint32_t spar = 0, opar = 0;
             uint32_t g = 0;  // key tiles of this block so far (the ring's position)
             bool ok = true;
-            // the walk of this warp, in shared memory: registers are for the scores
-            Walker& w = reinterpret_cast<Walker*>(smem + kOffWalk)[warp];
-            if (lane == 0) w.init(p, ctrl);
-            __syncwarp();
-            while (w.more() && ok) {
-                if (mt >= w.tiles_q()) {
-                    g += w.j1 - w.j0;
-                    advance(w, p);
+            Reader w = {};
+            while (ok && w.next(ctrl)) {
+                const Piece x = w.x;
+                w.done(ctrl);
+                const int j0 = x.j0, j1 = x.j1, h = x.h, k0 = x.k0, L = x.L;
+                if (mt >= x.tiles_q()) {
+                    g += j1 - j0;
                     continue;
                 }
-                const bool active = R < w.ntok();
-                const int pos = w.p0() + R, jend = w.j1;
-                const int p_min = w.p0() + mt * 128;  // position of this query tile's first token
-                const int L = w.r.L;
+                const bool active = R < x.ntok, split = j0 > 0 || j1 < x.nt;
+                const int pos = x.p0 + R;
+                const int p_min = x.p0 + mt * 128;  // position of this query tile's first token
+                const int row = (x.t0 + (active ? R : 0)) * p.H + h;
                 float m_used = ninf_f(), l = 0.f;
-                for (int j = w.j0; j < jend; ++j, ++g) {
+                for (int j = j0; j < j1; ++j, ++g) {
                     const int key0 = j << 7;
                     ok = wait_warp(&ctrl->s_full[mt], spar, ctrl);
                     if (!ok) break;
@@ -705,12 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                 }
                 if (!ok) break;
 
-                // ---- output: the row, or its part of a unit cut by the block's range.  The
-                // walk goes on first, while the last products run.
-                const int j0 = w.j0, j1 = w.j1, h = w.h, k0 = w.r.k0;
-                const bool split = j0 > 0 || j1 < w.nt;
-                const int row = (w.t0() + (active ? R : 0)) * p.H + h;
-                advance(w, p);
+                // ---- output: the row, or its part of a unit cut by the block's range
                 ok = wait_warp(&ctrl->o_full[mt], opar, ctrl);
                 if (!ok) break;
                 opar ^= 1u;
@@ -889,10 +971,11 @@ __global__ void __launch_bounds__(256) expanded_join_kernel(const __grid_constan
 }
 
 struct ExpandedWs {
-    size_t bad, desc, part_lse, part_o, total;
+    size_t counter, bad, desc, part_lse, part_o, total;
 };
 ExpandedWs expanded_ws(int n_cta) {
     ExpandedWs w;
+    w.counter = 128;  // (beside the status word)
     w.bad = kStatusBytes;
     w.desc = align_up(w.bad + (size_t)n_cta * 4, 256);
     w.part_lse = align_up(w.desc + (size_t)n_cta * 16, 256);
@@ -965,6 +1048,7 @@ cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
     p.status = reinterpret_cast<uint32_t*>(ws);
+    p.counter = reinterpret_cast<uint32_t*>(ws + w.counter);
     p.bad = reinterpret_cast<uint32_t*>(ws + w.bad);
     p.desc = reinterpret_cast<int4*>(ws + w.desc);
     p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
@@ -992,6 +1076,8 @@ cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token
         !make_rows_map(&p.rmap, kr, kRope, keys, rope_token_stride, 128))
         return CPA_ERR_CUDA;
     if (raise_smem_once() != cudaSuccess) return CPA_ERR_CUDA;
+    p.whole = (long long)T * H >= (long long)kWholeUnits * n_sm * kRows;
+    if (p.whole && cudaMemsetAsync(p.counter, 0, 4, s) != cudaSuccess) return CPA_ERR_CUDA;
     expanded_kernel<<<n_sm, kThreads, kSmem, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return CPA_ERR_LAUNCH;
     cudaLaunchAttribute at[1];
