@@ -9,12 +9,13 @@
 // What bounds it: HBM for prompts (a row is read once and written once), latency for
 // the tokens of a decode step.
 //
-// A warp takes up to 32 tokens and a segment of 32 pieces (a piece is 8 elements: 16
-// bytes of a row in bf16, 8 codes in an FP8 page).  Its lanes first look up the slots
-// of the tokens, one each, all at once; then lane l moves piece l of one token after
-// the other, kUnroll tokens' loads in flight.  So the scales of its 8 channels stay in
-// registers, and a row narrower than a segment (the 64 columns of a latent that
-// carry the position: 8 pieces) shares the warp with the next tokens' rows.
+// A warp takes up to 32 tokens and a segment of a row, up to 32 pieces (a piece is eight
+// elements: 16 bytes of a row in bf16, 8 codes in an FP8 page).  Its lanes first look up the slots of the
+// tokens, one each, all at once; then each moves its piece of one token after the other, several
+// of them in flight, so that the scales of its channels stay in registers.  A segment narrower
+// than a warp (128 bytes in a latent's row, whose nine are then alike) shares it with the next
+// tokens.  There are more blocks than run at a time: the lookups of those that begin hide behind
+// the rows of the others.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,7 +31,14 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kUnroll = 8;
+// Tokens in flight a lane, blocks an SM (their registers), tokens of a warp in a call with many.
+// (Prompts of 41k tokens to FP8 pages: 4, 3, 32 58.8 us; 4, 3, 24 60.2; 4, 4, 32 66.8; 8, 3, 32
+// 66.9.  74k tokens of FP8 pages to rows: 8, 3, 32 82.9 us; 6, 4, 24 81.9; 4, 3, 32 93.0.
+// Copies: 4, 3, 16 as 6, 3, 24, 2 % before 4, 4, 32.  A loop over runs in as many blocks as run
+// at a time: 1.2 to 1.5 times as long.)
+constexpr int unroll_of(bool fp8, bool gather) { return fp8 && gather ? 8 : 4; }
+constexpr int tokens_of(bool fp8) { return fp8 ? 32 : 16; }
+constexpr int kMinBlocks = 3;
 constexpr int kLatentC = 512, kLatentR = 64;  // elements of a latent's two parts
 
 struct RowParams {
@@ -49,7 +57,7 @@ struct RowParams {
     int stride, B, T, lp, num_pages, per_channel;
     int tokens;             // of a warp
     long long max_len;      // positions that a row of the table holds
-    int status_block;       // the last block looks the call over and writes the status word
+    int status_block;       // 1: the first block looks the call over and writes the status word
 };
 
 // What a request asks for: its rows [s0, s1) and the position of the first.
@@ -115,48 +123,107 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-template <bool FP8, bool GATHER>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(RowParams p) {
+// A value is quantised by its channel's reciprocal.  The quotient in 32 bits, and x * (1 / scale)
+// with its own two roundings, are both within 3 * 2^-24 of x / scale: where the product less and
+// more 2^-21 of itself round to one code, that is the quotient's too.  Elsewhere (one value in
+// 10^5, and ties of scales of few bits) it is divided.  Scales that are powers of two have exact
+// reciprocals and need no margin; one far from 1 is always divided by.  (Every value divided:
+// 106 us in place of 79 for 41k tokens.)
+struct Reciprocals {
+    float inv[8], more;  // the reciprocals less the margin, and the factor to the other side
+    bool divide;
+    template <class F>
+    __device__ __forceinline__ Reciprocals(F scale_of) {
+        bool exact = true;
+        divide = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float s = scale_of(i);
+            inv[i] = 1.f / s;
+            divide |= !(fabsf(s) > 0x1p-100f && fabsf(s) < 0x1p100f);
+            exact = exact && fmaf(inv[i], s, -1.f) == 0.f;
+        }
+        more = exact ? 1.f : 1.f + 0x1p-20f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) inv[i] *= exact ? 1.f : 1.f - 0x1p-21f;
+    }
+};
+
+// What is wrong with a call, by one block: every request, and every page that it names.
+template <bool GATHER>
+__device__ void look_over(const RowParams& p) {
     const int lane = threadIdx.x & 31;
     uint32_t bad = 0;
-    if (p.status_block && blockIdx.x == gridDim.x - 1) {
-        for (int b = threadIdx.x; b < p.B; b += kRowThreads)
-            if (!row_request<GATHER>(p, b).ok) bad |= CPA_DEV_BAD_LENGTH;
-        for (int t0 = (threadIdx.x >> 5) * 32; t0 < p.T; t0 += kRowThreads)
-            slot_of_token<GATHER>(p, t0, min(32, p.T - t0), bad);
-        const bool page = __syncthreads_or((int)(bad & CPA_DEV_BAD_PAGE));
-        const bool len = __syncthreads_or((int)(bad & CPA_DEV_BAD_LENGTH));
-        if (threadIdx.x == 0)
-            *p.status = (page ? CPA_DEV_BAD_PAGE : 0u) | (len ? CPA_DEV_BAD_LENGTH : 0u);
+    // up to 32 requests to a warp at a time, fewer so that all warps have some: a request for
+    // each lane, then the pages of each by the warp
+    const int chunk = min(32, (p.B + kRowWarps - 1) / kRowWarps);
+    for (int b0 = (threadIdx.x >> 5) * chunk; b0 < p.B; b0 += kRowWarps * chunk) {
+        int first = 0, n = 0;
+        if (lane < chunk && b0 + lane < p.B) {
+            const RowRequest r = row_request<GATHER>(p, b0 + lane);
+            if (!r.ok) {
+                bad |= CPA_DEV_BAD_LENGTH;
+            } else if (r.s1 > r.s0) {
+                first = (int)(r.pos >> p.lp);
+                n = (int)((r.pos + (r.s1 - r.s0) - 1) >> p.lp) - first + 1;
+            }
+        }
+        auto look = [&](int b, int entry) {
+            const int pg = __ldg(p.table + (size_t)b * p.stride + entry);
+            if (pg < 0 || pg >= p.num_pages) bad |= CPA_DEV_BAD_PAGE;
+        };
+        if (n > 0) look(b0 + lane, first);
+        __syncwarp();
+        for (uint32_t m = __ballot_sync(0xffffffffu, n > 1); m; m &= m - 1) {
+            const int src = __ffs((int)m) - 1;
+            const int f = __shfl_sync(0xffffffffu, first, src), k = __shfl_sync(0xffffffffu, n, src);
+#pragma unroll 4
+            for (int e = 1 + lane; e < k; e += 32) look(b0 + src, f + e);
+        }
+    }
+    const bool page = __syncthreads_or((int)(bad & CPA_DEV_BAD_PAGE));
+    const bool len = __syncthreads_or((int)(bad & CPA_DEV_BAD_LENGTH));
+    if (threadIdx.x == 0)
+        *p.status = (page ? CPA_DEV_BAD_PAGE : 0u) | (len ? CPA_DEV_BAD_LENGTH : 0u);
+}
+
+template <bool FP8, bool GATHER>
+__global__ void __launch_bounds__(kRowThreads, kMinBlocks) rows_kernel(const __grid_constant__ RowParams p) {
+    constexpr int kUnroll = unroll_of(FP8, GATHER);
+    const int lane = threadIdx.x & 31;
+    uint32_t bad = 0;
+    if (p.status_block && blockIdx.x == 0) {
+        look_over<GATHER>(p);
         return;
     }
+    const int block = (int)blockIdx.x - p.status_block;
+    const int per_group = p.segments[0] + p.segments[1];
+    const long long w = (long long)block * kRowWarps + (threadIdx.x >> 5);
+    int seg = (int)(w % per_group);
+    const int part = seg >= p.segments[0] ? 1 : 0;
+    if (part) seg -= p.segments[0];
+    const long long t0 = w / per_group * p.tokens;
     if (!p.status_block) {
         wait_for_clear();
-        if (blockIdx.x == 0)
+        if (block == 0)
             for (int b = threadIdx.x; b < p.B; b += kRowThreads)
                 if (!row_request<GATHER>(p, b).ok) bad |= CPA_DEV_BAD_LENGTH;
     }
-    const int per_group = p.segments[0] + p.segments[1];
-    const long long w = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-    const long long t0 = w / per_group * p.tokens;
     if (t0 < p.T) {
-        int seg = (int)(w % per_group);
-        const int part = seg >= p.segments[0] ? 1 : 0;
-        if (part) seg -= p.segments[0];
-        const int n = min(p.tokens, p.T - (int)t0);
-        const int slot = slot_of_token<GATHER>(p, (int)t0, n, bad);
         const int log_lanes = p.log_lanes[part], sub = 32 >> log_lanes;
-        const int piece = seg * 32 + (lane & ((1 << log_lanes) - 1)), mine = lane >> log_lanes;
+        const int piece = (seg << log_lanes) + (lane & ((1 << log_lanes) - 1)), mine = lane >> log_lanes;
         const bool inside = piece < p.pieces[part];
+        const float* const scales = FP8 ? p.scale[part] + (p.per_channel && inside ? piece * 8 : 0) : nullptr;
+        auto scale_of = [&](int i) { return FP8 ? __ldg(scales + (p.per_channel ? i : 0)) : 1.f; };
+        const Reciprocals r(scale_of);  // (in the kernels that quantise; the others use none of it)
         float scale[8];
-        if (FP8) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                scale[i] = __ldg(p.scale[part] + (p.per_channel && inside ? piece * 8 + i : 0));
-        }
+        for (int i = 0; i < 8; ++i) scale[i] = scale_of(i);
         uint8_t* const rows = p.rows[part] + (size_t)piece * 16;
         uint8_t* const pages = p.pages[part] + (size_t)piece * (FP8 ? 8 : 16);
         const size_t row_bytes = p.row_bytes[part], slot_bytes = p.slot_bytes[part];
+        const int n = min(p.tokens, p.T - (int)t0);
+        const int slot = slot_of_token<GATHER>(p, (int)t0, n, bad);
         for (int i0 = 0; i0 < n; i0 += sub * kUnroll) {
             uint4 x[kUnroll];
             int at[kUnroll];
@@ -166,43 +233,49 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(RowParams p) {
                 at[u] = __shfl_sync(0xffffffffu, slot, i & 31);
                 if (i >= n || !inside) at[u] = -1;
                 if (at[u] < 0) continue;
-                if (!GATHER) {
-                    x[u] = __ldcs(reinterpret_cast<const uint4*>(rows + (size_t)(t0 + i) * row_bytes));
-                } else if (FP8) {
-                    const uint2 c = __ldcs(reinterpret_cast<const uint2*>(pages + (size_t)at[u] * slot_bytes));
+                const uint8_t* const from =
+                    GATHER ? pages + (size_t)at[u] * slot_bytes : rows + (size_t)(t0 + i) * row_bytes;
+                if (GATHER && FP8) {
+                    const uint2 c = __ldcs(reinterpret_cast<const uint2*>(from));
                     x[u].x = c.x;
                     x[u].y = c.y;
                 } else {
-                    x[u] = __ldcs(reinterpret_cast<const uint4*>(pages + (size_t)at[u] * slot_bytes));
+                    x[u] = __ldcs(reinterpret_cast<const uint4*>(from));
                 }
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 if (at[u] < 0) continue;
-                const int i = i0 + u * sub + mine;
-                if (GATHER) {
-                    if (FP8) {
-                        uint32_t o[4];
+                uint4* const row = reinterpret_cast<uint4*>(rows + (size_t)(t0 + i0 + u * sub + mine) * row_bytes);
+                uint8_t* const page = pages + (size_t)at[u] * slot_bytes;
+                if (GATHER && FP8) {
+                    uint32_t o[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t h = e4m3x2_to_f16x2(k < 2 ? x[u].x : x[u].y, k & 1);
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                            o[k] = pack_bf16x2(f.x * scale[2 * k], f.y * scale[2 * k + 1]);
-                        }
-                        x[u] = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t h = e4m3x2_to_f16x2(k < 2 ? x[u].x : x[u].y, k & 1);
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                        o[k] = pack_bf16x2(f.x * scale[2 * k], f.y * scale[2 * k + 1]);
                     }
-                    *reinterpret_cast<uint4*>(rows + (size_t)(t0 + i) * row_bytes) = x[u];
+                    *row = make_uint4(o[0], o[1], o[2], o[3]);
+                } else if (GATHER) {
+                    *row = x[u];
                 } else if (FP8) {
                     float f[8];
                     bf16x8_to_f32(x[u], f);
-                    uint32_t c[4];
+                    uint32_t c[4], differ = 0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        c[k] = e4m3x2(f[2 * k] / scale[2 * k], f[2 * k + 1] / scale[2 * k + 1]);
-                    *reinterpret_cast<uint2*>(pages + (size_t)at[u] * slot_bytes) =
-                        make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+                    for (int k = 0; k < 4; ++k) {
+                        const float y0 = f[2 * k] * r.inv[2 * k], y1 = f[2 * k + 1] * r.inv[2 * k + 1];
+                        c[k] = e4m3x2(y0, y1);
+                        differ |= c[k] ^ e4m3x2(y0 * r.more, y1 * r.more);
+                    }
+                    if (differ || r.divide)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            c[k] = e4m3x2(f[2 * k] / scale_of(2 * k), f[2 * k + 1] / scale_of(2 * k + 1));
+                    *reinterpret_cast<uint2*>(page) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
                 } else {
-                    *reinterpret_cast<uint4*>(pages + (size_t)at[u] * slot_bytes) = x[u];
+                    *reinterpret_cast<uint4*>(page) = x[u];
                 }
             }
         }
@@ -221,6 +294,14 @@ void set_part(RowParams& p, int i, const void* rows, size_t row_bytes, void* pag
     p.pieces[i] = (int)(bytes / 16);
     p.log_lanes[i] = p.pieces[i] > 16 ? 5 : p.pieces[i] > 8 ? 4 : 3;
     p.segments[i] = (p.pieces[i] + 31) / 32;
+}
+// A latent's row: segments of eight pieces in both parts.
+void set_latent(RowParams& p, const void* c, size_t c_bytes, const void* r, size_t r_bytes, void* pages) {
+    constexpr size_t slot = (kLatentC + kLatentR) * 2;
+    set_part(p, 0, c, c_bytes, pages, slot, kLatentC * 2, nullptr);
+    set_part(p, 1, r, r_bytes, static_cast<uint8_t*>(pages) + kLatentC * 2, slot, kLatentR * 2, nullptr);
+    p.log_lanes[0] = 3;
+    p.segments[0] = p.pieces[0] / 8;
 }
 
 // Checks that every call shares; parts are set when it returns CPA_OK.
@@ -255,13 +336,14 @@ cpa_status launch_rows(RowParams& p, cudaStream_t s) {
     if (n_sm <= 0) return CPA_ERR_CUDA;
     const long long per_group = p.segments[0] + p.segments[1];
     // few tokens: fewer to a warp, so that all SMs take part
-    p.tokens = 32;
-    while (p.tokens > 4 && (long long)(p.T / p.tokens) * per_group < (long long)n_sm * 16)
-        p.tokens /= 2;
+    p.tokens = tokens_of(FP8);
+    while (p.tokens > 4 && p.T / p.tokens * per_group < (long long)n_sm * 16) p.tokens /= 2;
     const long long warps = ((long long)p.T + p.tokens - 1) / p.tokens * per_group;
-    // a block more looks a small call over and writes the status word
-    p.status_block = p.T <= 4096 && p.B <= 4096 ? 1 : 0;
-    const dim3 grid((unsigned)((warps + kRowWarps - 1) / kRowWarps + p.status_block));
+    const long long blocks = (warps + kRowWarps - 1) / kRowWarps;
+    // One block more looks a call over while the others move rows; where it would take longer
+    // than they do, every warp reports into a cleared word.
+    p.status_block = p.B <= 8192 && (p.T >> p.lp) <= 16384 ? 1 : 0;
+    const dim3 grid((unsigned)(blocks + p.status_block));
     if (!p.status_block)
         return launch_cleared(rows_kernel<FP8, GATHER>, grid, kRowThreads, s, p.status, p);
     rows_kernel<FP8, GATHER><<<grid, kRowThreads, 0, s>>>(p);
@@ -340,10 +422,7 @@ cpa_status cpa_latent_append(const void* c_new, const void* r_new, size_t c_stri
     const cpa_status st = rows_ready(p, page_table, pt_stride, new_start, seq_lens, B, T, page_size,
                                      num_pages, workspace, workspace_bytes);
     if (st != CPA_OK) return st;
-    const size_t slot = (kLatentC + kLatentR) * 2;
-    set_part(p, 0, c_new, c_stride_bytes, pages, slot, kLatentC * 2, nullptr);
-    set_part(p, 1, r_new, r_stride_bytes, static_cast<uint8_t*>(pages) + kLatentC * 2, slot,
-             kLatentR * 2, nullptr);
+    set_latent(p, c_new, c_stride_bytes, r_new, r_stride_bytes, pages);
     return launch_rows<false, false>(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -403,10 +482,7 @@ cpa_status cpa_latent_gather(const void* pages, const int32_t* page_table, int p
     const cpa_status st = rows_ready(p, page_table, pt_stride, out_start, first, B, T, page_size,
                                      num_pages, workspace, workspace_bytes);
     if (st != CPA_OK) return st;
-    const size_t slot = (kLatentC + kLatentR) * 2;
-    uint8_t* const base = static_cast<uint8_t*>(const_cast<void*>(pages));
-    set_part(p, 0, c_out, kLatentC * 2, base, slot, kLatentC * 2, nullptr);
-    set_part(p, 1, r_out, kLatentR * 2, base + kLatentC * 2, slot, kLatentR * 2, nullptr);
+    set_latent(p, c_out, kLatentC * 2, r_out, kLatentR * 2, const_cast<void*>(pages));
     return launch_rows<false, true>(p, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -145,9 +145,9 @@ def test_latents(P):
 
 @pytest.mark.parametrize("big", [False, True])
 def test_what_is_wrong_is_reported_and_left_out(big):
-    """(big: the form whose blocks report by themselves.)"""
-    P, H = 16, 2
-    news, lens = [10, 5000 if big else 20, 7], [50, 5000 if big else 30, 9]
+    """(big: the form whose warps report by themselves.)"""
+    P, H = 8 if big else 16, 1 if big else 2
+    news, lens = [10, 140000 if big else 20, 7], [50, 140000 if big else 30, 9]
     g = ref.gen(3)
     table, pool = ref.table_of(lens, P, g)
     st = starts(news)
@@ -167,23 +167,24 @@ def test_what_is_wrong_is_reported_and_left_out(big):
     assert bool(same.all())
     for bad in (pool, -1, 2 ** 31 - 1, -2 ** 31):
         t = table.clone()
-        t[1, 1] = bad  # positions 16 .. 31 of the second request
+        t[1, 1] = bad  # positions P .. 2 P - 1 of the second request
         pages, same = go(t, i32(st), i32(lens), 5)
-        lo, hi = max(16, lens[1] - news[1]), min(32, lens[1])
+        lo, hi = max(P, lens[1] - news[1]), min(2 * P, lens[1])
         hit = torch.zeros(st[-1], dtype=torch.bool, device="cuda")
         a = st[1] - (lens[1] - news[1])
         hit[a + lo:a + hi] = True
         assert bool(same[~hit].all()) and bool((pages.view(-1, H, 128)[slots(table, [lo], [hi - lo], P)] == 0).all())
-    for lengths in ([50, 4, 9], [50, 5000 * 16, 9], [50, -1, 9], [50, 2 ** 31 - 1, 9]):
+    for lengths in ([50, 4, 9], [50, 140000 * 16, 9], [50, -1, 9], [50, 2 ** 31 - 1, 9]):
         pages, same = go(table, i32(st), i32(lengths), 8)
         assert bool(same[:st[1]].all()) and bool(same[st[2]:].all())
     for s in ([0, 10, 5, st[-1]], [0, 10, st[2], st[-1] + 1], [-1, 10, st[2], st[-1]]):
         go(table, i32(s), i32(lens), 8)
 
 
-def test_many_requests_and_empty_ones():
+@pytest.mark.parametrize("B", [5000, 9000])
+def test_many_requests_and_empty_ones(B):
     g = ref.gen(9)
-    B, P = 5000, 8
+    P = 8
     news = torch.randint(0, 3, (B,), generator=g, device="cuda")
     news[100:400] = 0
     lens = (news + torch.randint(0, 5, (B,), generator=g, device="cuda")).tolist()
