@@ -56,6 +56,10 @@ constexpr int kMaxTokens = 64;  // S: the mask of a request's last tokens is one
 constexpr uint32_t kBox = 9u * 1024u;
 constexpr uint32_t kSlotBytes = 4 * kBox;
 constexpr int kMaxSlots = 5;
+#ifndef KAHEAD
+#define KAHEAD 1
+#endif
+constexpr int kAhead = KAHEAD;  // halves that are asked into L2 ahead of their load, at most 8
 constexpr uint32_t kOffQ = 1024;
 constexpr uint32_t kMaxSmem = 232448;
 constexpr uint32_t kColS = 256;  // TMEM: O^T in columns 0 .. 255, the scores of two tiles
@@ -299,10 +303,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     desc = make_int4(w.b, w.pair, (int)(last / ctrl->per - grp) + 1, 0);
                 }
                 const int32_t* trow = p.table + (size_t)w.b * p.stride;
-                // lane bi: the slot of the pool that box bi of a half begins with, or -1
-                auto box_of = [&](int half) -> int {
-                    const int pos = half * 32 + lane * 8;
-                    if (lane >= 4 || half >= 2 * w.j1 || pos >= w.L) return -1;
+                // the slot of the pool that box `at` of the sequence begins with, or -1
+                auto box_of = [&](int at) -> int {
+                    const int pos = at * 8;
+                    if (at >= 8 * w.j1 || pos >= w.L) return -1;
                     const int pg = __ldg(trow + (pos >> p.lp));
                     if (pg < 0 || pg >= p.num_pages) {
                         atomicOr(&ctrl->bad, CPA_DEV_BAD_PAGE);
@@ -310,7 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     }
                     return (int)(((uint32_t)pg << p.lp) + (uint32_t)(pos & ((1 << p.lp) - 1)));
                 };
-                int box = box_of(2 * w.j0);
+                // 32 boxes (eight halves) are looked up at a time, a lane each, and the next 32
+                int at = 8 * w.j0;
+                int boxes = box_of(at + lane), boxes_next = box_of(at + 32 + lane);
                 if (q_loads > 0) ok = wait_warp(&ctrl->q_empty, (q_loads - 1) & 1u, ctrl);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&ctrl->q_full, q_bytes);
@@ -321,20 +327,32 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 __syncwarp();
                 ++q_loads;
                 for (int half = 2 * w.j0; half < 2 * w.j1; ++half, ++h) {
-                    const int next = box_of(half + 1);
+                    const int i4 = (4 * half - at) & 31;
+                    if (half > 2 * w.j0 && i4 == 0) {
+                        at += 32;
+                        boxes = boxes_next;
+                        boxes_next = box_of(at + 32 + lane);
+                    }
+                    const int box = __shfl_sync(0xffffffffu, boxes, i4 + (lane & 3));
+                    // what the ring has no place for yet comes into L2 meanwhile
+                    const int far = i4 + kAhead * 4 + (lane & 3);
+                    const int b0 = __shfl_sync(0xffffffffu, boxes, far & 31);
+                    const int b1 = __shfl_sync(0xffffffffu, boxes_next, far & 31);
+                    const int ahead = far < 32 ? b0 : b1;
+                    if (kAhead > 0 && h >= (uint32_t)n_slots && lane < 4 && ahead >= 0) prefetch_3d(&p.kmap, 0, ahead, 0);
+                    __syncwarp();
                     if (h >= (uint32_t)n_slots) {
                         ok = wait_warp(&ctrl->k_empty[slot], par, ctrl);
                         if (!ok) break;
                     }
-                    const uint32_t mask = __ballot_sync(0xffffffffu, box >= 0);
+                    const uint32_t mask = __ballot_sync(0xffffffffu, lane < 4 && box >= 0);
                     if (lane == 0)
                         mbar_arrive_expect_tx(&ctrl->k_full[slot], (uint32_t)__popc(mask) * kBox);
                     __syncwarp();
-                    if (box >= 0)
+                    if (lane < 4 && box >= 0)
                         tma_load_3d(smem + o_k + slot * kSlotBytes + lane * kBox, &p.kmap, 0, box, 0,
                                     &ctrl->k_full[slot], pol);
                     __syncwarp();
-                    box = next;
                     if (++slot == n_slots) {
                         slot = 0;
                         par ^= 1u;
