@@ -394,7 +394,35 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             uint32_t n_idle = 0;
             while (wv.more()) {
                 bool did = false;
-                if (wk.more() && g - d < 2) {
+                if (d < g &&
+                    __all_sync(0xffffffffu, mbar_test(&ctrl->p_full, d & 1u) &&
+                                                (jv > wv.j0 || d_pieces == 0 ||
+                                                 mbar_test(&ctrl->o_empty, (d_pieces - 1) & 1u)))) {
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint64_t a = v_desc + ((vs * kSlotBytes) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                            for (int blk = 0; blk < 4; ++blk)
+                                mma_ss(lead, tmem + blk * kRows, a + ((kk * 2 * kBox + blk * 2048) >> 4),
+                                       p_desc + (half * 2 + kk) * 2, idesc_o,
+                                       jv == wv.j0 && half + kk == 0 ? 0u : 1u);
+                        commit(lead, &ctrl->k_empty[vs]);
+                        if (++vs == n_slots) vs = 0;
+                    }
+                    commit(lead, &ctrl->pv_done);
+                    ++d;
+                    if (++jv == wv.j1) {
+                        commit(lead, &ctrl->o_full);
+                        ++d_pieces;
+                        wv.next(p);
+                        jv = wv.j0;
+                    }
+                    did = true;
+                }
+                if (!did && wk.more() && g - d < 2) {
                     const int ks2 = ks + 1 == n_slots ? 0 : ks + 1;
                     const uint32_t kpar2 = ks2 == 0 ? kpar ^ 1u : kpar;
                     if (__all_sync(0xffffffffu, mbar_test(&ctrl->k_full[ks2], kpar2) &&
@@ -431,34 +459,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                         }
                         did = true;
                     }
-                }
-                if (!did && d < g &&
-                    __all_sync(0xffffffffu, mbar_test(&ctrl->p_full, d & 1u) &&
-                                                (jv > wv.j0 || d_pieces == 0 ||
-                                                 mbar_test(&ctrl->o_empty, (d_pieces - 1) & 1u)))) {
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint64_t a = v_desc + ((vs * kSlotBytes) >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                            for (int blk = 0; blk < 4; ++blk)
-                                mma_ss(lead, tmem + blk * kRows, a + ((kk * 2 * kBox + blk * 2048) >> 4),
-                                       p_desc + (half * 2 + kk) * 2, idesc_o,
-                                       jv == wv.j0 && half + kk == 0 ? 0u : 1u);
-                        commit(lead, &ctrl->k_empty[vs]);
-                        if (++vs == n_slots) vs = 0;
-                    }
-                    commit(lead, &ctrl->pv_done);
-                    ++d;
-                    if (++jv == wv.j1) {
-                        commit(lead, &ctrl->o_full);
-                        ++d_pieces;
-                        wv.next(p);
-                        jv = wv.j0;
-                    }
-                    did = true;
                 }
                 if (did) {
                     n_idle = 0;
