@@ -1001,6 +1001,11 @@ def cpa_cache_compact(k_pages, v_pages, src_page_table, src_pos, n_keep, dst_pag
 def _rows_of(t, name: str, dtype, shape, dev: int) -> int:
     """Rows that may lie inside wider ones: `shape` with contiguous rows.  Returns the elements
     from one row to the next."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and \
+            t.shape == shape:
+        st = t.stride()
+        if st[-1] == 1 and (len(shape) == 2 or st[1] == shape[2]):
+            return st[0]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -1021,8 +1026,8 @@ def _request_args(page_table, start, lens, lens_name: str, dev: int):
     """Checks a table with the starts (and lengths or first positions) of its requests; returns
     (B, columns)."""
     _want(page_table, "page_table", torch.int32, 2, dev)
-    B, stride = page_table.shape
     _want(start, "new_start" if lens_name == "seq_lens" else "out_start", torch.int32, 1, dev)
+    B, stride = page_table.shape
     if lens is not None:
         _want(lens, lens_name, torch.int32, 1, dev)
     if start.shape[0] != B + 1 or (lens is not None and lens.shape[0] != B):
@@ -1032,6 +1037,13 @@ def _request_args(page_table, start, lens, lens_name: str, dev: int):
 
 def _kv_scales(k_scale, v_scale, channels: int, dev: int):
     """(pointers, per channel) of scales that hold one value or `channels`."""
+    if isinstance(k_scale, torch.Tensor) and isinstance(v_scale, torch.Tensor) and \
+            k_scale.dtype is v_scale.dtype is torch.float32 and \
+            k_scale.get_device() == v_scale.get_device() == dev and \
+            k_scale.is_contiguous() and v_scale.is_contiguous():
+        n = k_scale.numel()
+        if n == v_scale.numel() and n in (1, channels):
+            return k_scale.data_ptr(), v_scale.data_ptr(), int(n > 1)
     n = k_scale.numel() if isinstance(k_scale, torch.Tensor) else 0
     for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         _want(t, nm, torch.float32, t.dim() if isinstance(t, torch.Tensor) else 1, dev)
@@ -1040,24 +1052,34 @@ def _kv_scales(k_scale, v_scale, channels: int, dev: int):
     return k_scale.data_ptr(), v_scale.data_ptr(), int(n > 1)
 
 
+def _row_pools(k_pages, v_pages, fp8: bool):
+    """(device, shape, type of the rows) of K and V pools, FP8 ones where `fp8`."""
+    dev = _device(k_pages, "k_pages")
+    kind = torch.uint8 if fp8 else k_pages.dtype
+    _want(k_pages, "k_pages", kind, 4, dev)
+    _want(v_pages, "v_pages", kind, 4, dev)
+    shape = k_pages.shape
+    if shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    return dev, shape, torch.bfloat16 if fp8 else kind
+
+
 def _append(name, k_new, v_new, k_pages, v_pages, scales, page_table, new_start, seq_lens,
             workspace, stream, check):
-    dev, num_pages, P, token = _any_pools(k_pages, v_pages)
-    H_kv, d = k_pages.shape[2:]
-    if scales:
-        _want(k_pages, "k_pages", torch.uint8, 4, dev)
-    dtype = torch.bfloat16 if scales else k_pages.dtype
+    dev, (num_pages, P, H_kv, d), dtype = _row_pools(k_pages, v_pages, scales is not None)
     T = k_new.shape[0] if isinstance(k_new, torch.Tensor) and k_new.dim() == 3 else 0
-    ks = _rows_of(k_new, "k_new", dtype, (T, H_kv, d), dev)
-    vs = _rows_of(v_new, "v_new", dtype, (T, H_kv, d), dev)
+    shape = (T, H_kv, d)
+    ks = _rows_of(k_new, "k_new", dtype, shape, dev)
+    vs = _rows_of(v_new, "v_new", dtype, shape, dev)
     B, stride = _request_args(page_table, new_start, seq_lens, "seq_lens", dev)
     es = k_new.element_size()
-    args = (k_new.data_ptr(), v_new.data_ptr(), ks * es, vs * es, k_pages.data_ptr(),
+    rows = (k_new.data_ptr(), v_new.data_ptr(), ks * es, vs * es, k_pages.data_ptr(),
             v_pages.data_ptr())
-    if scales:
-        args += _kv_scales(*scales, H_kv * d, dev)
-    args += (page_table.data_ptr(), stride, new_start.data_ptr(), seq_lens.data_ptr(), B, T)
-    args += (H_kv * d, P, num_pages) if scales else (P, num_pages, token)
+    requests = (page_table.data_ptr(), stride, new_start.data_ptr(), seq_lens.data_ptr(), B, T)
+    if scales is not None:
+        args = (*rows, *_kv_scales(*scales, H_kv * d, dev), *requests, H_kv * d, P, num_pages)
+    else:
+        args = (*rows, *requests, P, num_pages, H_kv * d * es)
     _launch(name, args, dev, stream, workspace, lambda: _STATUS_BYTES, check)
 
 
@@ -1095,11 +1117,7 @@ def _out_rows(T, given) -> int:
 
 def _gather(name, k_pages, v_pages, scales, page_table, out_start, T, first, k_out, v_out,
             workspace, stream, check):
-    dev, num_pages, P, token = _any_pools(k_pages, v_pages)
-    H_kv, d = k_pages.shape[2:]
-    if scales:
-        _want(k_pages, "k_pages", torch.uint8, 4, dev)
-    dtype = torch.bfloat16 if scales else k_pages.dtype
+    dev, (num_pages, P, H_kv, d), dtype = _row_pools(k_pages, v_pages, scales is not None)
     B, stride = _request_args(page_table, out_start, first, "first", dev)
     shape = (_out_rows(T, (k_out, v_out)), H_kv, d)
     if k_out is None:
@@ -1109,14 +1127,15 @@ def _gather(name, k_pages, v_pages, scales, page_table, out_start, T, first, k_o
     for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
         _want(t, nm, dtype, 3, dev)
         _shape(t, nm, shape)
-    args = (k_pages.data_ptr(), v_pages.data_ptr())
-    if scales:
-        args += _kv_scales(*scales, H_kv * d, dev)
-    args += (page_table.data_ptr(), stride, out_start.data_ptr(),
-             None if first is None else first.data_ptr(), B, shape[0])
-    args += (H_kv * d, P, num_pages) if scales else (P, num_pages, token)
-    _launch(name, args + (k_out.data_ptr(), v_out.data_ptr()), dev, stream, workspace,
-            lambda: _STATUS_BYTES, check)
+    pools = (k_pages.data_ptr(), v_pages.data_ptr())
+    requests = (page_table.data_ptr(), stride, out_start.data_ptr(),
+                None if first is None else first.data_ptr(), B, shape[0])
+    out = (k_out.data_ptr(), v_out.data_ptr())
+    if scales is not None:
+        args = (*pools, *_kv_scales(*scales, H_kv * d, dev), *requests, H_kv * d, P, num_pages, *out)
+    else:
+        args = (*pools, *requests, P, num_pages, H_kv * d * k_out.element_size(), *out)
+    _launch(name, args, dev, stream, workspace, lambda: _STATUS_BYTES, check)
     return k_out, v_out
 
 
@@ -1190,6 +1209,11 @@ def cpa_latent_gather(pages, page_table, out_start, T: Optional[int] = None, fir
 def _heads_of(t, name: str, shape, dev: int):
     """Checks [tokens, heads, width] bf16 whose last dimension is contiguous; returns the strides
     of a token and a head in elements (the least that says nothing where there is one)."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and \
+            t.shape == shape:
+        st = t.stride()
+        if st[2] == 1 and shape[0] > 1 and shape[1] > 1:
+            return st[0], st[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
