@@ -643,13 +643,15 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                             mma_ss(lead, s_col, q_desc + c * kStep + kk * 2, b + kk * 2, idesc_s,
                                    c + kk > 0 ? 1u : 0u);
                         commit(lead, &ctrl->empty[(kg + c) % kSlots]);
+                        // (the other warp is up before these are done)
+                        if (c == 1 && lead) mbar_arrive(&ctrl->turn[mt ^ 1]);
                     }
                     commit(lead, &ctrl->s_full[mt]);
                     if (last) commit(lead, &ctrl->q_empty[mt]);
-                } else if (nq && lead) {
-                    for (int c = 0; c < 3; ++c) mbar_arrive(&ctrl->empty[(kg + c) % kSlots]);
+                } else if (lead) {
+                    for (int c = 0; c < 3 && nq; ++c) mbar_arrive(&ctrl->empty[(kg + c) % kSlots]);
+                    mbar_arrive(&ctrl->turn[mt ^ 1]);
                 }
-                if (lead) mbar_arrive(&ctrl->turn[mt ^ 1]);
                 __syncwarp();
                 if (nq_prev) vg += 5;
                 if (nq) kg += 5;
