@@ -15,7 +15,8 @@
 // The order of the products is S(i) PV(i-1): while one tile's scores go through the
 // softmax, the next tile's are made.
 //
-// Warps (6): 0-3 softmax and output, 4 loads, 5 issues the products.  Scores lie 16 rows
+// Warps (7): 0-3 softmax and output, 4 loads the tiles and 6 Q, 5 issues the products.  Every
+// warp finds the block's range by itself, before the barriers are ready.  Scores lie 16 rows
 // to a warp; a thread holds 16 scores of two rows, a row's maximum is exchanged between
 // four lanes.  A rescale of O (a row's maximum grew by more than 2^8) is of columns, and
 // so for all four warps: they agree on it with one barrier a tile.
@@ -31,6 +32,7 @@
 // order of its parts.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include <cmath>
@@ -45,8 +47,7 @@ namespace cpa {
 namespace {
 
 constexpr int kC = 512, kR = 64, kSlot = kC + kR;
-constexpr int kThreads = 192;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 224;
 constexpr int kRows = 64;   // rows of a unit
 constexpr int kKeys = 64;   // tokens of a tile
 constexpr int kMaxTokens = 64;  // S: the mask of a request's last tokens is one word
@@ -111,17 +112,15 @@ __device__ __forceinline__ int tiles_of(int L) { return L > 0 ? (L + kKeys - 1) 
 struct Ctrl {
     uint64_t q_full, q_empty;
     uint64_t k_full[kMaxSlots], k_empty[kMaxSlots];
-    uint64_t s_full[2], p_full, pv_done, o_full, o_empty, mma_done;
+    uint64_t s_full[2], p_full, pv_done, o_full, o_empty, mma_done;  // (the last of the barriers)
     unsigned long long odd;  // keys L - S + 1 + i of the unit with values that are not finite
     uint32_t tmem_base;
     volatile uint32_t abort_flag;
     uint32_t bad;
-    int unit_cost;            // kUnitCost, or 0 where no block takes more than two tiles
-    long long left, t0, per;  // this group's range, in tiles of cost
-    int b, pair, off;         // where it begins: a unit, and how far into its cost
     float row[kRows];         // factors of the rows for a rescale, or for the output
 };
-static_assert(sizeof(Ctrl) + 2 * kWarps * 8 <= kOffQ, "control block");
+constexpr int kBarriers = 2 + 2 * kMaxSlots + 7;
+static_assert(sizeof(Ctrl) <= kOffQ && offsetof(Ctrl, odd) == 8 * kBarriers, "control block");
 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctrl* c) {
     // (the first look by itself: most waits find the phase complete)
@@ -129,66 +128,13 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctrl* 
     return mbar_wait_warp(bar, parity, &c->abort_flag, &c->bad);
 }
 
-// Every thread: the problem's cost, this group's range, and the unit where it begins.
-// Each thread sums a run of requests; one scan over the block follows.
-__device__ void schedule(const LatentParams& p, Ctrl* c, long long* sums, int grp) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per_thread = (p.B + kThreads - 1) / kThreads, b0 = (int)threadIdx.x * per_thread;
-    uint32_t bad = 0;
-    long long mine = 0;
-    int n = 0;
-    for (int i = 0; i < per_thread && b0 + i < p.B; ++i, ++n)
-        mine += tiles_of(length_of(p, b0 + i, bad));
-    mine *= p.n_pairs;
-    if (bad) atomicOr(&c->bad, bad);
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    long long total = 0, before = incl - mine;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
-    }
-    const int uc = total <= 2 * p.n_grp ? 0 : kUnitCost;
-    total += (long long)uc * p.B * p.n_pairs;
-    before += (long long)uc * min(b0, p.B) * p.n_pairs;
-    mine += (long long)uc * n * p.n_pairs;
-    const long long per = (total + p.n_grp - 1) / p.n_grp;
-    const long long t0 = per * grp;
-    if (threadIdx.x == 0) {
-        c->per = per;
-        c->t0 = t0;
-        c->unit_cost = uc;
-        c->left = t0 < total ? min(per, total - t0) : 0;
-    }
-    if (before <= t0 && t0 < before + mine) {
-        long long at = before;
-        for (int b = b0;; ++b) {
-            const int cost = tiles_of(length_of(p, b, bad)) + uc;
-            const long long all = (long long)cost * p.n_pairs;
-            if (t0 < at + all) {
-                c->b = b;
-                c->pair = (int)((t0 - at) / cost);
-                c->off = (int)((t0 - at) % cost);
-                break;
-            }
-            at += all;
-        }
-    }
-    __syncthreads();
-}
-
-// Walks the pieces (unit, tiles [j0, j1)) of this group's range; j0 == j1 past the
-// last.  A unit's own cost counts as lying before its first tile.
+// Walks the pieces (unit, tiles [j0, j1)) of a group's range of cost, in tiles; j0 == j1 past
+// the last.  A unit costs its tiles and unit_cost (kUnitCost, or 0 where no group takes more than
+// two tiles), which counts as lying before its first tile.
 struct Walker {
     int b, pair, L, nt, j0, j1, unit_cost;
-    long long left;
+    long long left;     // cost of the range after this piece
+    long long end, per; // of the range; of every range
     __device__ __forceinline__ void cut(int off) {
         const int take = (int)min((long long)nt + unit_cost - off, left);
         left -= take;
@@ -202,12 +148,57 @@ struct Walker {
         nt = tiles_of(L);
         cut(off);
     }
-    __device__ __forceinline__ void init(const LatentParams& p, const Ctrl* c) {
-        left = c->left;
-        unit_cost = c->unit_cost;
-        b = c->b;
-        pair = c->pair;
-        at(p, c->off);
+    // By a whole warp: the problem's cost, the range of group grp, and the unit where it begins.
+    __device__ void init(const LatentParams& p, int grp, uint32_t& bad) {
+        const int lane = threadIdx.x & 31;
+        long long total = 0;
+        int tiles = 0;  // of this lane's request in the last 32
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            tiles = b0 + lane < p.B ? tiles_of(length_of(p, b0 + lane, bad)) : 0;
+            total += tiles;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        total *= p.n_pairs;
+        unit_cost = total <= 2 * p.n_grp ? 0 : kUnitCost;
+        total += (long long)unit_cost * p.B * p.n_pairs;
+        // (a 64-bit division is a long sequence)
+        per = total < 0x7fffffffll - p.n_grp ? (int)(total + p.n_grp - 1) / p.n_grp
+                                             : (total + p.n_grp - 1) / p.n_grp;
+        const long long t0 = per * grp;
+        left = t0 < total ? min(per, total - t0) : 0;
+        end = t0 + left;
+        b = pair = j0 = j1 = 0;
+        if (left == 0) return;
+        long long before = 0;  // cost of the requests before these 32
+        for (int b0 = 0;; b0 += 32) {
+            if (p.B > 32) {
+                uint32_t none = 0;
+                tiles = b0 + lane < p.B ? tiles_of(length_of(p, b0 + lane, none)) : 0;
+            }
+            const int cost = tiles + unit_cost;
+            const long long mine = b0 + lane < p.B ? (long long)cost * p.n_pairs : 0;
+            long long incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const long long from = before + incl - mine;
+            const uint32_t here = __ballot_sync(0xffffffffu, from <= t0 && t0 < from + mine);
+            if (here) {
+                const int src = __ffs((int)here) - 1;
+                b = b0 + src;
+                const long long in = __shfl_sync(0xffffffffu, t0 - from, src);
+                const int of = __shfl_sync(0xffffffffu, cost, src);
+                pair = in < 0x7fffffffll ? (int)in / of : (int)(in / of);
+                L = length_of(p, b, bad);
+                nt = of - unit_cost;
+                cut((int)(in - (long long)pair * of));
+                return;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
     }
     __device__ __forceinline__ void next(const LatentParams& p) {
         if (left == 0) {
@@ -246,86 +237,72 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     const int grp = blockIdx.x / p.cl, rank = blockIdx.x % p.cl;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    if (threadIdx.x < kBarriers) {
+        uint64_t* const bar = &ctrl->q_full + threadIdx.x;
+        // (one arrival per softmax warp, where they arrive)
+        mbar_init(bar, bar == &ctrl->p_full || bar == &ctrl->o_empty ? 4 : 1);
+        fence_barrier_init();
+    }
     if (threadIdx.x == 0) {
-        mbar_init(&ctrl->q_full, 1);
-        mbar_init(&ctrl->q_empty, 1);
-        for (int i = 0; i < kMaxSlots; ++i) {
-            mbar_init(&ctrl->k_full[i], 1);
-            mbar_init(&ctrl->k_empty[i], 1);
-        }
-        mbar_init(&ctrl->s_full[0], 1);
-        mbar_init(&ctrl->s_full[1], 1);
-        mbar_init(&ctrl->p_full, 4);  // one arrival per softmax warp
-        mbar_init(&ctrl->pv_done, 1);
-        mbar_init(&ctrl->o_full, 1);
-        mbar_init(&ctrl->o_empty, 4);
-        mbar_init(&ctrl->mma_done, 1);
         ctrl->odd = 0;
         ctrl->abort_flag = 0;
         ctrl->bad = 0;
-        fence_barrier_init();
-        prefetch_tmap(&p.cmap);
-        prefetch_tmap(&p.rmap);
-        prefetch_tmap(&p.kmap);
     }
     if (warp == 5) {
         tmem_alloc(&ctrl->tmem_base, 512);
         tmem_relinquish();
     }
+    uint32_t bad = 0;
+    Walker w;
+    w.init(p, grp, bad);
+    // the slot of the pool that box `at` of the walk's request begins with, or -1
+    auto box_of = [&](int at) -> int {
+        const int pos = at * 8;
+        if (at >= 8 * w.j1 || pos >= w.L) return -1;
+        const int pg = __ldg(p.table + (size_t)w.b * p.stride + (pos >> p.lp));
+        if (pg < 0 || pg >= p.num_pages) {
+            bad |= CPA_DEV_BAD_PAGE;
+            return -1;
+        }
+        return (int)(((uint32_t)pg << p.lp) + (uint32_t)(pos & ((1 << p.lp) - 1)));
+    };
+    // 32 boxes (eight halves) are looked up at a time, a lane each, and the next 32
+    int at = 8 * w.j0, boxes = -1, boxes_next = -1;
+    if (warp == 4) {
+        boxes = box_of(at + lane);
+        boxes_next = box_of(at + 32 + lane);
+        prefetch_tmap(&p.kmap);
+    }
+    if (warp == 6 && lane < 2) prefetch_tmap(lane ? &p.cmap : &p.rmap);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    schedule(p, ctrl, reinterpret_cast<long long*>(smem + sizeof(Ctrl)), grp);
     const uint32_t tmem = ctrl->tmem_base;
     int4 desc = make_int4(-1, 0, 0, 0);
     const int rows = p.heads * p.toks, rows_n = (rows + 15) & ~15;  // N of the products of O^T
     const uint32_t o_p = off_p(rows), o_k = off_k(rows);
     const int n_slots = p.n_slots;
 
-    if (ctrl->left > 0) {
+    if (w.more()) {
         if (warp == 4) {
             // ============================== loads
             const uint64_t pol = p.n_pairs * p.cl > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-            const uint64_t pol_q = l2_policy_evict_first();
-            const uint32_t chunk = q_chunk(rows), q_bytes = (uint32_t)rows * 9u * 128u;
-            uint32_t q_loads = 0, h = 0;  // halves of tiles so far
+            uint32_t h = 0;  // halves of tiles so far
             int slot = 0;
             uint32_t par = 1;  // parity of the ring's previous round
             bool ok = true;
-            Walker w;
-            w.init(p, ctrl);
             for (; w.more() && ok; w.next(p)) {
-                const Rows r(p, w.pair * p.cl + rank);
                 if (w.j0 == 0 && w.j1 < w.nt) {
                     // the unit that this group leaves unfinished, for the join (it ends with
                     // this piece, which ends with the range)
-                    const long long last = ctrl->t0 + ctrl->left + w.nt - w.j1 - 1;
-                    desc = make_int4(w.b, w.pair, (int)(last / ctrl->per - grp) + 1, 0);
+                    const long long last = w.end + w.nt - w.j1 - 1;
+                    desc = make_int4(w.b, w.pair, (int)(last / w.per - grp) + 1, 0);
                 }
-                const int32_t* trow = p.table + (size_t)w.b * p.stride;
-                // the slot of the pool that box `at` of the sequence begins with, or -1
-                auto box_of = [&](int at) -> int {
-                    const int pos = at * 8;
-                    if (at >= 8 * w.j1 || pos >= w.L) return -1;
-                    const int pg = __ldg(trow + (pos >> p.lp));
-                    if (pg < 0 || pg >= p.num_pages) {
-                        atomicOr(&ctrl->bad, CPA_DEV_BAD_PAGE);
-                        return -1;
-                    }
-                    return (int)(((uint32_t)pg << p.lp) + (uint32_t)(pos & ((1 << p.lp) - 1)));
-                };
-                // 32 boxes (eight halves) are looked up at a time, a lane each, and the next 32
-                int at = 8 * w.j0;
-                int boxes = box_of(at + lane), boxes_next = box_of(at + 32 + lane);
-                if (q_loads > 0) ok = wait_warp(&ctrl->q_empty, (q_loads - 1) & 1u, ctrl);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&ctrl->q_full, q_bytes);
-                __syncwarp();
-                if (lane < 9)
-                    tma_load_3d(smem + kOffQ + lane * chunk, lane < 8 ? &p.cmap : &p.rmap,
-                                lane < 8 ? lane * 64 : 0, r.h0, w.b * p.S + r.s0, &ctrl->q_full, pol_q);
-                __syncwarp();
-                ++q_loads;
+                if (h > 0) {
+                    at = 8 * w.j0;
+                    boxes = box_of(at + lane);
+                    boxes_next = box_of(at + 32 + lane);
+                }
                 for (int half = 2 * w.j0; half < 2 * w.j1; ++half, ++h) {
                     const int i4 = (4 * half - at) & 31;
                     if (half > 2 * w.j0 && i4 == 0) {
@@ -360,12 +337,29 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 }
             }
             // no copy may be in flight when the block leaves
-            if (q_loads > 0)
-                mbar_wait(&ctrl->q_full, (q_loads - 1) & 1u, &ctrl->abort_flag, &ctrl->bad);
             for (uint32_t i = 0; i < (uint32_t)n_slots; ++i)
                 if (i < h)
                     mbar_wait(&ctrl->k_full[i], ((h - 1 - i) / n_slots) & 1u, &ctrl->abort_flag,
                               &ctrl->bad);
+            __syncwarp();
+        } else if (warp == 6) {
+            // ============================== loads of Q
+            const uint64_t pol_q = l2_policy_evict_first();
+            const uint32_t chunk = q_chunk(rows), q_bytes = (uint32_t)rows * 9u * 128u;
+            uint32_t q_loads = 0;
+            for (; w.more(); w.next(p)) {
+                const Rows r(p, w.pair * p.cl + rank);
+                if (q_loads > 0 && !wait_warp(&ctrl->q_empty, (q_loads - 1) & 1u, ctrl)) break;
+                if (lane == 0) mbar_arrive_expect_tx(&ctrl->q_full, q_bytes);
+                __syncwarp();
+                if (lane < 9)
+                    tma_load_3d(smem + kOffQ + lane * chunk, lane < 8 ? &p.cmap : &p.rmap,
+                                lane < 8 ? lane * 64 : 0, r.h0, w.b * p.S + r.s0, &ctrl->q_full, pol_q);
+                __syncwarp();
+                ++q_loads;
+            }
+            // (no copy may be in flight when the block leaves)
+            mbar_wait(&ctrl->q_full, (q_loads - 1) & 1u, &ctrl->abort_flag, &ctrl->bad);
             __syncwarp();
         } else if (warp == 5) {
             // ============================== products
@@ -386,9 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             uint32_t g = 0, d = 0, d_pieces = 0;
             int ks = 0, vs = 0;  // slots of their first halves
             uint32_t kpar = 0, qpar = 0;
-            Walker wk, wv;
-            wk.init(p, ctrl);
-            wv = wk;
+            Walker& wk = w;
+            Walker wv = w;
             int jk = wk.j0, jv = wv.j0;
             uint64_t since = 0;
             uint32_t n_idle = 0;
@@ -487,8 +480,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             uint32_t g = 0, pieces = 0;
             int vs = 0;  // slot of the tile's first half
             bool ok = true;
-            Walker w;
-            w.init(p, ctrl);
             for (; w.more(); w.next(p)) {
                 const Rows r(p, w.pair * p.cl + rank);
                 // the last key that a row sees; -1 for one that sees none, or is none
@@ -729,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
         }
     }
 
+    if (bad) atomicOr(&ctrl->bad, bad);
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 5) {
@@ -951,7 +943,7 @@ cpa_status cpa_latent_decode(const void* q_c, int64_t qc_token_stride, int64_t q
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.n_cta, kRows / 8);
+    cfg.gridDim = dim3((unsigned)p.n_cta, (unsigned)(rows + 7) / 8);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cfg.attrs = at;

@@ -1089,7 +1089,7 @@ cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)n_sm, kRows / 32);
+    cfg.gridDim = dim3((unsigned)n_sm, (unsigned)((T < kRows ? T : kRows) + 31) / 32);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cfg.attrs = at;
