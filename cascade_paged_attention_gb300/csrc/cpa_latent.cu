@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
         tmem_alloc(&ctrl->tmem_base, 512);
         tmem_relinquish();
     }
+    wait_for_earlier();
     uint32_t bad = 0;
     Walker w;
     w.init(p, grp, bad);
@@ -738,7 +739,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
 // Block (x, y) of the grid: unit of block x, eight rows of it, a warp each.  The last
 // group's range is followed by nothing; its blocks gather the status word.
 __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ LatentParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_for_earlier();
     const int grp = blockIdx.x / p.cl, rank = blockIdx.x % p.cl;
     if (grp == p.n_grp - 1) {
         if (blockIdx.y > 0 || rank > 0) return;
@@ -937,18 +939,13 @@ cpa_status cpa_latent_decode(const void* q_c, int64_t qc_token_stride, int64_t q
     const int rows = p.heads * p.toks;
     p.n_slots = slots_of(rows);
     const uint32_t smem = off_k(rows) + (uint32_t)p.n_slots * kSlotBytes + 1024;
-    latent_kernel<<<p.n_cta, kThreads, smem, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return CPA_ERR_LAUNCH;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.n_cta, (unsigned)(rows + 7) / 8);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_join_kernel, p) == cudaSuccess ? CPA_OK : CPA_ERR_LAUNCH;
+    if (launch_overlapped(latent_kernel, dim3((unsigned)p.n_cta), kThreads, smem, s, p) !=
+        cudaSuccess)
+        return CPA_ERR_LAUNCH;
+    return launch_overlapped(latent_join_kernel, dim3((unsigned)p.n_cta, (unsigned)(rows + 7) / 8), 256, 0, s,
+                             p) == cudaSuccess
+               ? CPA_OK
+               : CPA_ERR_LAUNCH;
 }
 
 }  // extern "C"

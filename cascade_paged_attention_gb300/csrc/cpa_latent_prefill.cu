@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    wait_for_earlier();
     schedule(p, ctrl, reinterpret_cast<long long*>(smem + sizeof(Ctrl)));
     const uint32_t tmem = ctrl->tmem_base;
     int4 desc = make_int4(-1, 0, 0, 0);
@@ -903,7 +904,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
 // that order.  A block does 32 rows (grid.y), a thread 4 columns of a row at a
 // time.  The last block, whose range nothing follows, gathers the status word.
 __global__ void __launch_bounds__(256) expanded_join_kernel(const __grid_constant__ ExpandedParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_for_earlier();
     if (blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y > 0) return;
         __shared__ uint32_t all;
@@ -1083,18 +1085,13 @@ cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token
     if (raise_smem_once() != cudaSuccess) return CPA_ERR_CUDA;
     p.whole = (long long)T * H >= (long long)kWholeUnits * n_sm * kRows;
     if (p.whole && cudaMemsetAsync(p.counter, 0, 4, s) != cudaSuccess) return CPA_ERR_CUDA;
-    expanded_kernel<<<n_sm, kThreads, kSmem, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return CPA_ERR_LAUNCH;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)n_sm, (unsigned)((T < kRows ? T : kRows) + 31) / 32);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, expanded_join_kernel, p) == cudaSuccess ? CPA_OK : CPA_ERR_LAUNCH;
+    if (launch_overlapped(expanded_kernel, dim3((unsigned)n_sm), kThreads, kSmem, s, p) != cudaSuccess)
+        return CPA_ERR_LAUNCH;
+    return launch_overlapped(expanded_join_kernel,
+                             dim3((unsigned)n_sm, (unsigned)((T < kRows ? T : kRows) + 31) / 32), 256, 0, s,
+                             p) == cudaSuccess
+               ? CPA_OK
+               : CPA_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -144,6 +144,28 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// A kernel and the one before it on the stream: the later one may be launched, and make its
+// barriers and take its tensor memory, while the earlier one runs; what the earlier ones wrote
+// may be read, and what they read be written, after wait_for_earlier().
+__device__ __forceinline__ void wait_for_earlier() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <class P>
+cudaError_t launch_overlapped(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                              const P& p) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // Strides of [tokens, heads, width] in elements: rows of 16-byte pieces, apart where there
 // is more than one.
 inline bool strides_ok(int64_t token, int64_t head, int tokens, int heads) {
