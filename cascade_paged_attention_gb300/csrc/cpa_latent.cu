@@ -57,10 +57,10 @@ constexpr int kMaxTokens = 64;  // S: the mask of a request's last tokens is one
 constexpr uint32_t kBox = 9u * 1024u;
 constexpr uint32_t kSlotBytes = 4 * kBox;
 constexpr int kMaxSlots = 5;
-#ifndef KAHEAD
-#define KAHEAD 1
-#endif
-constexpr int kAhead = KAHEAD;  // halves that are asked into L2 ahead of their load, at most 8
+// Halves that are asked into L2 ahead of their load.  (None: 64 x 2000 tokens 40.5 us in place of
+// 41.1, 64 x 16000 205 in place of 198, 32 ragged requests with 128 heads 128 in place of 119;
+// two to eight: 0.5 to 4 us longer for the first, no shorter for the others.)
+constexpr int kAhead = 1;
 constexpr uint32_t kOffQ = 1024;
 constexpr uint32_t kMaxSmem = 232448;
 constexpr uint32_t kColS = 256;  // TMEM: O^T in columns 0 .. 255, the scores of two tiles
@@ -86,8 +86,9 @@ struct LatentParams {
     float* lse;
     uint32_t* status;
     uint32_t* bad;    // [n_cta] what each block found wrong
-    int4* desc;       // [n_grp] (request, pair, parts, 0) of the unit that starts in the
-                      // group's range and goes on past it; request -1: none
+    int4* desc;       // (request, pair, parts, group) of units that start in a group's range and
+                      // go on past it: [n_grp] by group (request -1: none), or, where there are no
+                      // more units than groups, by unit (parts 1: none)
     float* part_lse;  // [2 n_cta][kRows], log2 units
     float* part_o;    // [2 n_cta][kRows][kC]
     int stride, B, S, H, lp, num_pages, max_len;
@@ -95,6 +96,7 @@ struct LatentParams {
     int toks, n_rt;     // tokens of a unit, and units of a request
     int cl, n_pairs;    // blocks of a group (they share key ranges), groups of units of a request
     int n_cta, n_grp;
+    int by_unit;
     int n_slots;
     float scale_log2;
 };
@@ -293,11 +295,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             uint32_t par = 1;  // parity of the ring's previous round
             bool ok = true;
             for (; w.more() && ok; w.next(p)) {
-                if (w.j0 == 0 && w.j1 < w.nt) {
-                    // the unit that this group leaves unfinished, for the join (it ends with
-                    // this piece, which ends with the range)
-                    const long long last = w.end + w.nt - w.j1 - 1;
-                    desc = make_int4(w.b, w.pair, (int)(last / w.per - grp) + 1, 0);
+                if (w.j0 == 0) {
+                    // for the join: a unit that this group leaves unfinished ends with this piece,
+                    // which ends with the range
+                    int parts = 1;
+                    if (w.j1 < w.nt) {
+                        const long long last = w.end + w.nt - w.j1 - 1;
+                        parts = (int)(last / w.per - grp) + 1;
+                        desc = make_int4(w.b, w.pair, parts, grp);
+                    }
+                    if (p.by_unit && lane == 0 && rank == 0)
+                        p.desc[w.b * p.n_pairs + w.pair] = make_int4(w.b, w.pair, parts, grp);
                 }
                 if (h > 0) {
                     at = 8 * w.j0;
@@ -317,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     const int b0 = __shfl_sync(0xffffffffu, boxes, far & 31);
                     const int b1 = __shfl_sync(0xffffffffu, boxes_next, far & 31);
                     const int ahead = far < 32 ? b0 : b1;
-                    if (kAhead > 0 && h >= (uint32_t)n_slots && lane < 4 && ahead >= 0) prefetch_3d(&p.kmap, 0, ahead, 0);
+                    if (h >= (uint32_t)n_slots && lane < 4 && ahead >= 0) prefetch_3d(&p.kmap, 0, ahead, 0);
                     __syncwarp();
                     if (h >= (uint32_t)n_slots) {
                         ok = wait_warp(&ctrl->k_empty[slot], par, ctrl);
@@ -729,74 +737,80 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
         tmem_dealloc(tmem, 512);
     }
     if (warp == 4 && lane == 0) {
-        if (rank == 0) p.desc[grp] = desc;
+        if (rank == 0 && !p.by_unit) p.desc[grp] = desc;
         p.bad[blockIdx.x] = ctrl->bad;
     }
 }
 
-// Joins the unit that starts in a group's range and goes on past its end: its parts are
-// the group's second slots and the first slots of the groups after it, in that order.
-// Block (x, y) of the grid: unit of block x, eight rows of it, a warp each.  The last
-// group's range is followed by nothing; its blocks gather the status word.
-__global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ LatentParams p) {
+// Joins the units that ranges cut: a unit's parts are the second slots of the group where it
+// starts and the first slots of the groups after it, in that order.  Block (x, y) of the grid:
+// entry x of desc, some of its rows, a warp for F * 128 columns of a row; the last x gathers the
+// status word.  What a join takes is the latency of its loads, 16 / F parts at a time, and the
+// launch of its blocks.
+constexpr int kJoinWarps = 8;
+constexpr int join_rows(int F) { return kJoinWarps * F / 4; }
+template <int F>
+__global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const __grid_constant__ LatentParams p) {
+    constexpr int kAtATime = 16 / F;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     wait_for_earlier();
-    const int grp = blockIdx.x / p.cl, rank = blockIdx.x % p.cl;
-    if (grp == p.n_grp - 1) {
-        if (blockIdx.y > 0 || rank > 0) return;
+    if (blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y > 0) return;
         __shared__ uint32_t all;
         if (threadIdx.x == 0) all = 0;
         __syncthreads();
         uint32_t bad = 0;
-        for (int i = threadIdx.x; i < p.n_cta; i += 256) bad |= __ldcg(p.bad + i);
+        for (int i = threadIdx.x; i < p.n_cta; i += kJoinWarps * 32) bad |= __ldcg(p.bad + i);
         if (bad) atomicOr(&all, bad);
         __syncthreads();
         if (threadIdx.x == 0) *p.status = all;
         return;
     }
-    const int4 d = __ldcg(p.desc + grp);
-    if (d.x < 0) return;
+    const int rank = blockIdx.x % p.cl;
+    const int4 d = __ldcg(p.desc + blockIdx.x / p.cl);
+    if (d.x < 0 || d.z < 2) return;
     const Rows r(p, d.y * p.cl + rank);
-    const int lane = threadIdx.x & 31, x = blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int np = d.z;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, np = d.z;
+    const int x = blockIdx.y * join_rows(F) + warp * F / 4;
+    const int at4 = (warp * F & 3) * 32 + lane;  // float4 of the row
     if (x >= r.n) return;
     auto row_of = [&](int i) -> size_t {
-        return (2 * ((size_t)blockIdx.x + (size_t)i * p.cl) + (i == 0 ? 1 : 0)) * kRows + x;
+        return (2 * ((size_t)(d.w + i) * p.cl + rank) + (i == 0 ? 1 : 0)) * kRows + x;
     };
     float m = ninf_f(), sum = 0.f;
-    float4 acc[4];
+    float4 acc[F];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < np; i0 += 4) {  // four parts' loads in flight at a time
-        float4 y[4][4];
-        float z[4], mx = m;
+    for (int k = 0; k < F; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < np; i0 += kAtATime) {
+        float4 y[kAtATime][F];
+        float z[kAtATime], mx = m;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kAtATime; ++i) {
             const size_t at = row_of(min(i0 + i, np - 1));
             z[i] = __ldcg(p.part_lse + at);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                y[i][k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kC) + 32 * k + lane);
+            for (int k = 0; k < F; ++k)
+                if (i0 + i < np) y[i][k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kC) + 32 * k + at4);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kAtATime; ++i)
             if (i0 + i < np) mx = fmaxf(mx, z[i]);
         const float ref = mx == ninf_f() ? 0.f : mx, f = ex2(m - ref);
         sum *= f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < F; ++k) {
             acc[k].x *= f;
             acc[k].y *= f;
             acc[k].z *= f;
             acc[k].w *= f;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kAtATime; ++i) {
             if (i0 + i >= np) break;
             const float w = ex2(z[i] - ref);
             sum += w;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < F; ++k) {
                 acc[k].x += w * y[i][k].x;
                 acc[k].y += w * y[i][k].y;
                 acc[k].z += w * y[i][k].z;
@@ -808,11 +822,11 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const size_t row = (size_t)d.x * p.S * p.H + r.first + x;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        reinterpret_cast<uint2*>(p.o + row * kC)[32 * k + lane] =
+    for (int k = 0; k < F; ++k)
+        reinterpret_cast<uint2*>(p.o + row * kC)[32 * k + at4] =
             make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
                        pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
-    if (lane == 0)
+    if (at4 == 0)
         p.lse[row] = sum == 0.f ? ninf_f() : ((m == ninf_f() ? 0.f : m) + lg2(sum)) * kLn2;
 }
 
@@ -927,6 +941,8 @@ cpa_status cpa_latent_decode(const void* q_c, int64_t qc_token_stride, int64_t q
     p.n_pairs = p.n_rt / p.cl;
     p.n_cta = n_sm;
     p.n_grp = n_sm / p.cl;
+    const long long units = (long long)B * p.n_pairs;
+    p.by_unit = units <= p.n_grp;
     p.scale_log2 = sm_scale * kLog2e;
     if (!make_heads_map(&p.cmap, q_c, kC, H, (uint64_t)B * S, qc_head_stride, qc_token_stride, p.heads,
                         p.toks) ||
@@ -942,10 +958,15 @@ cpa_status cpa_latent_decode(const void* q_c, int64_t qc_token_stride, int64_t q
     if (launch_overlapped(latent_kernel, dim3((unsigned)p.n_cta), kThreads, smem, s, p) !=
         cudaSuccess)
         return CPA_ERR_LAUNCH;
-    return launch_overlapped(latent_join_kernel, dim3((unsigned)p.n_cta, (unsigned)(rows + 7) / 8), 256, 0, s,
-                             p) == cudaSuccess
-               ? CPA_OK
-               : CPA_ERR_LAUNCH;
+    // A unit has about n_grp / units parts: where they are many they are read many at a time, by
+    // more warps (one request of 777 tokens 14.5 -> 10.2 us; 64 units of three parts 39.7 -> 41.1).
+    const bool many = units * 4 <= p.n_grp;
+    const int per_block = many ? join_rows(1) : join_rows(4);
+    const dim3 grid((unsigned)((p.by_unit ? (int)units : p.n_grp) * p.cl + 1),
+                    (unsigned)((rows + per_block - 1) / per_block));
+    const cudaError_t e = many ? launch_overlapped(latent_join_kernel<1>, grid, kJoinWarps * 32, 0, s, p)
+                               : launch_overlapped(latent_join_kernel<4>, grid, kJoinWarps * 32, 0, s, p);
+    return e == cudaSuccess ? CPA_OK : CPA_ERR_LAUNCH;
 }
 
 }  // extern "C"
