@@ -52,12 +52,17 @@ constexpr uint32_t kQBytes = 3 * kSlotBytes;
 constexpr uint32_t kOffQ = 1024;
 constexpr uint32_t kOffRing = kOffQ + 2 * kQBytes;
 constexpr uint32_t kSmem = kOffRing + kSlots * kSlotBytes + 1024;  // (aligned up inside)
-// What a unit costs besides its tiles, in tiles (see cpa_window.cu).
+// What a unit costs besides its tiles, in tiles; nothing in a call of few tiles, which lasts as
+// long as its longest chain of them (448 tiles 24.0 -> 20.5 us, 1300 tiles 31.7 -> 31.0; up to
+// twelve tiles a block: 38.2 -> 41.3 for 1400 tiles in 250 units).
 constexpr int kUnitCost = 3;
+constexpr int kFewTiles = 6;  // of a block
 constexpr int kMinTiles = 2;  // fewest tiles of a block where units have a cost
-constexpr int kWholeUnits = 6;       // units a block from which they are handed out whole
-constexpr int kMostHeads = 8;        // that are handed out side by side,
-constexpr int kSharedKeys = 65536;   // as long as their keys are no more than these (32 MB)
+// Units a block from which they are handed out whole (12 chunks with 5 units a block 533 -> 497 us,
+// 2 x 2000 tokens with 3 units a block 104 -> 96 us, six chunks with 3 units a block 328 us both).
+constexpr int kWholeUnits = 2;
+constexpr int kMostHeads = 8;       // that are handed out side by side,
+constexpr int kSharedKeys = 65536;  // as long as their keys are no more than these (32 MB)
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
 static_assert(kSmem <= 232448, "shared memory of one block");
 
@@ -128,7 +133,7 @@ struct Ctrl {
     uint32_t tmem_base;
     volatile uint32_t abort_flag;
     uint32_t bad;
-    int unit_cost;            // kUnitCost, or 0 where no block takes more than two tiles
+    int unit_cost;            // kUnitCost, or 0 where no block takes more than kFewTiles
     long long t0, left, per;  // this block's range, in tiles of cost
     int b, h, qt, off;        // where it begins: a unit, and how far into its cost
     Piece piece[kPieces];
@@ -227,7 +232,7 @@ __device__ void schedule(const ExpandedParams& p, Ctrl* c, long long* sums) {
         total += sums[w];
         total_units += sums[kWarps + w];
     }
-    const int unit_cost = total <= 2 * p.n_cta ? 0 : kUnitCost;
+    const int unit_cost = total <= kFewTiles * p.n_cta ? 0 : kUnitCost;
     total += unit_cost * total_units;
     before += unit_cost * units_before;
     mine += unit_cost * units;
