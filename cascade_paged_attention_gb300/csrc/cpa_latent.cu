@@ -358,7 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             uint32_t q_loads = 0;
             for (; w.more(); w.next(p)) {
                 const Rows r(p, w.pair * p.cl + rank);
-                if (q_loads > 0 && !wait_warp(&ctrl->q_empty, (q_loads - 1) & 1u, ctrl)) break;
+                // (this wait lasts as long as the unit: others find out if the pipeline is broken)
+                if (q_loads > 0 &&
+                    !__all_sync(0xffffffffu, mbar_wait(&ctrl->q_empty, (q_loads - 1) & 1u, &ctrl->abort_flag,
+                                                       &ctrl->bad, 100 * kWaitLimitNs)))
+                    break;
                 if (lane == 0) mbar_arrive_expect_tx(&ctrl->q_full, q_bytes);
                 __syncwarp();
                 if (lane < 9)

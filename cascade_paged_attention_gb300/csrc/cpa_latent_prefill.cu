@@ -129,7 +129,7 @@ struct Ctrl {
     uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: weights of keys 0..63, 64..127
     uint64_t turn[2];   // the issuing warps' turns
     uint64_t mma_done;
-    volatile uint64_t redo_ns;  // when a row that is done again last began a run of keys
+    volatile uint64_t alive_ns;  // the last sign of work that others may wait for (see wait_on)
     uint32_t tmem_base;
     volatile uint32_t abort_flag;
     uint32_t bad;
@@ -138,9 +138,9 @@ struct Ctrl {
     int b, h, qt, off;        // where it begins: a unit, and how far into its cost
     Piece piece[kPieces];
 };
-// mbar_wait() of cpa_device.cuh, with a limit that a redo puts off: the rows that are not
-// finite are done again key by key while the other warps wait, for as long as their caches
-// are, and tell the time with every key tile.
+// mbar_wait() of cpa_device.cuh, with a limit that signs of work put off: rows that are not
+// finite are done again key by key while the other warps wait, and a warp without a part in a
+// unit waits until it ends, for as long as the sequence is.
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Ctrl* c) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
@@ -148,7 +148,7 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Ctrl* c)
         if (mbar_try_wait(bar, parity)) return true;
         if (n & 63u) continue;
         if (c->abort_flag) return false;
-        const uint64_t since = max(t0, (uint64_t)c->redo_ns);
+        const uint64_t since = max(t0, (uint64_t)c->alive_ns);
         if ((int64_t)(globaltimer_ns() - since) > (int64_t)kWaitLimitNs) {
             atomicOr(&c->bad, CPA_DEV_TIMEOUT);
             c->abort_flag = 1u;
@@ -392,7 +392,7 @@ __device__ __forceinline__ float slow_row(const ExpandedParams& p, Ctrl* c, size
     o[0] = o[1] = o[2] = o[3] = 0.f;
     // four keys at a time, so that their loads and sums overlap
     for (int k4 = k0; k4 < k1; k4 += 4) {
-        if (lane == 0 && ((k4 - k0) & 127) == 0) c->redo_ns = globaltimer_ns();
+        if (lane == 0 && ((k4 - k0) & 127) == 0) c->alive_ns = globaltimer_ns();
         float s[4];
         uint2 v[4];
 #pragma unroll
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             mbar_init(&ctrl->turn[i], 1);
         }
         mbar_init(&ctrl->mma_done, 2);
-        ctrl->redo_ns = 0;
+        ctrl->alive_ns = 0;
         ctrl->abort_flag = 0;
         ctrl->bad = 0;
         fence_barrier_init();
@@ -517,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                     const long long last = ctrl->t0 + ctrl->left + x.nt - x.j1 - 1;
                     desc = make_int4(x.t0, x.ntok, x.h, (int)(last / ctrl->per - blockIdx.x) + 1);
                 }
-                for (int j = x.j0; j < x.j1 && ok; ++j)
+                for (int j = x.j0; j < x.j1 && ok; ++j) {
+                    if (lane == 0 && (j & 1023) == 0) ctrl->alive_ns = globaltimer_ns();
                     for (int i = 0; i < 5; ++i, ++g) {
                         const uint32_t st = g % kSlots;
                         if (g >= kSlots) {
@@ -539,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                         }
                         __syncwarp();
                     }
+                }
                 x = next;
             }
             // no copy may be in flight when the block leaves

@@ -237,6 +237,41 @@ def test_streams_and_graphs():
             against(q_c, q_r, pages, table, lens, S, *out, P)
 
 
+def test_calls_one_after_the_other():
+    """Appends, decodes and copies of one stream in a graph, each reading what the one before wrote,
+    with one workspace: launches that overlap change nothing."""
+    H, P, B = 32, 16, 5
+    lens = [70, 300, 5, 1000, 64]
+    q_c, q_r, pages, table, dl = make([x + 8 for x in lens], 1, H, P, 14, width=64)
+    dl.copy_(i32(lens))
+    ws = torch.empty(cpa.cpa_latent_decode_workspace_size(B, 1, H), dtype=torch.uint8, device="cuda")
+    start = i32(range(B + 1))
+    steps = 4
+    g = ref.gen(15)
+    c, r = randn(steps, B, C, g=g), randn(steps, B, R, g=g)
+    qc, qr = q_c.clone(), q_r.clone()
+    outs = []
+    graph = torch.cuda.CUDAGraph()
+    before = pages.clone()
+    with torch.cuda.graph(graph):
+        for i in range(steps):
+            dl.add_(1)
+            cpa.cpa_latent_append(c[i], r[i], pages, table, start, dl, workspace=ws)
+            o, lse = cpa.cpa_latent_decode(qc, qr, pages, table, dl, max_seq_len=1024, workspace=ws)
+            outs.append((qc.clone(), qr.clone(), o, lse, dl.clone()))
+            qc.copy_(o)                       # the next step's queries come from this one's output
+            qr.copy_(o[..., :R])
+    for _ in range(2):
+        pages.copy_(before)
+        dl.copy_(i32(lens))
+        qc.copy_(q_c)
+        qr.copy_(q_r)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, o, lse, n in outs:
+            against(a, b, pages, table, n.tolist(), 1, o, lse, P)
+
+
 def test_binding_refuses():
     q_c, q_r, pages, table, dl = make([20, 30], 2, 8, 16, 0)
     for bad in (dict(S=1), dict(S=3), dict(S=0)):
@@ -388,6 +423,37 @@ def test_prefill_bad_starts_are_reported():
     ws.fill_(0xFF)
     got = cpa.cpa_latent_prefill(none, nope, rope, v, i32([0, 0, 0]), i32(ks), workspace=ws, check=True)
     assert got[0].shape == (0, 2, D)
+
+
+@pytest.mark.parametrize("news,lens,H", [
+    ([2500], [2500], 32), ([300, 0, 1, 700, 1500], [400, 7, 3000, 700, 1500], 32),
+    ([900, 70], [1000, 4000], 96), ([40] * 130, [41] * 130, 16)])
+def test_prefill_units_handed_out_whole(news, lens, H):
+    """Enough rows that blocks take whole units, a few heads at a time."""
+    assert sum(news) * H >= 2 * 152 * 256
+    check_prefill(news, lens, H, seed=H, lead=1, trail=2, k_lead=3, k_trail=1)
+
+
+def test_prefill_units_handed_out_whole_in_a_graph():
+    """Captured behind a copy, replayed: each replay hands out its units from the first."""
+    news, lens, H = [1300, 1300], [1300, 1500], 32
+    q, nope, rope, v, qs, ks = make_prefill(news, lens, H, 3)
+    src, dq, dk = torch.empty_like(q), i32(qs), i32(ks)
+    ws = torch.full((cpa.cpa_latent_prefill_workspace_size(2, q.shape[0], rope.shape[0], H),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    cpa.cpa_latent_prefill(q, nope, rope, v, dq, dk, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.copy_(src)
+        out = cpa.cpa_latent_prefill(q, nope, rope, v, dq, dk, workspace=ws)
+        again = cpa.cpa_latent_prefill(q, nope, rope, v, dq, dk, workspace=ws)
+    for seed in (1, 2):
+        src.copy_(randn(*q.shape, g=ref.gen(seed)))
+        ws.fill_(0x5A)
+        graph.replay()
+        against_prefill(src, nope, rope, v, qs, ks, *out)
+        assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
 
 
 def test_prefill_many_requests():
