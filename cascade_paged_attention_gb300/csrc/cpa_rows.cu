@@ -6,8 +6,9 @@
 // ties to even, cut at +-448; what is read back is bf16(code * scale), the product
 // in 32 bits.
 //
-// What bounds it: HBM for prompts (a row is read once and written once), latency for
-// the tokens of a decode step.
+// What bounds it: HBM for prompts, where a row is read once and written once (128k tokens of 8 heads
+// of 128, bf16: 1.05 GB in 156 us, 0.99 of the copy rate; to FP8 pages 0.79 GB in 134 us, 0.87, from
+// them in 120 us, 0.97), latency for the tokens of a decode step (4.4 us).
 //
 // A warp takes up to 32 tokens and a segment of a row, up to 32 pieces (a piece is eight
 // elements: 16 bytes of a row in bf16, 8 codes in an FP8 page).  Its lanes first look up the slots of the
@@ -16,6 +17,9 @@
 // than a warp (128 bytes in a latent's row, whose nine are then alike) shares it with the next
 // tokens.  There are more blocks than run at a time: the lookups of those that begin hide behind
 // the rows of the others.
+//
+// A lane's registers hold few rows, so a warp first asks the rows that it will read into L2: an
+// append before its lookups, which rows need none of.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -31,13 +35,21 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
-// Tokens in flight a lane, blocks an SM (their registers), tokens of a warp in a call with many.
-// (Prompts of 41k tokens to FP8 pages: 4, 3, 32 58.8 us; 4, 3, 24 60.2; 4, 4, 32 66.8; 8, 3, 32
-// 66.9.  74k tokens of FP8 pages to rows: 8, 3, 32 82.9 us; 6, 4, 24 81.9; 4, 3, 32 93.0.
-// Copies: 4, 3, 16 as 6, 3, 24, 2 % before 4, 4, 32.  A loop over runs in as many blocks as run
-// at a time: 1.2 to 1.5 times as long.)
+// Tokens in flight a lane, blocks an SM (their registers).  (41k tokens to FP8 pages: 4, 3 49.5 us;
+// 4, 4 57.0; 2, 3 58.8; 8, 3 57.8.  74k tokens of FP8 pages to rows: 8, 3 75.9; 8, 4 76.5; 4, 3
+// 76.9.  Copies of 41k tokens: 4, 3 55.9; 2, 3 56.7; 8, 3 56.8; 8, 2 58.9.  A loop over runs in as
+// many blocks as run at a time: 1.2 to 1.5 times as long.)
 constexpr int unroll_of(bool fp8, bool gather) { return fp8 && gather ? 8 : 4; }
-constexpr int tokens_of(bool fp8) { return fp8 ? 32 : 16; }
+// Tokens of a warp in a call with many, by rows side by side in it, and how many of them are asked
+// into L2 ahead of their load.  (To FP8 pages 32 and 6 49.5 us, 4 49.1, 8 50.4, 12 53.1, all 61.4,
+// none 59.4; 16 and all 56.1; 128k tokens 32 and 6 133.7, 4 134.0, none 164.  From them 16 and all
+// 75.9, 32 and 8 77.4, none 83.5.  Copies 8 and all 55.9, 4 57.0, 16 58.0, 32 63.3, none 61.4;
+// latents read back 32 and all 17.3, 16 17.9, 8 23.0, none 19.5.)
+CPA_HD int tokens_of(bool fp8, bool gather, int sub) {
+    const int n = (fp8 ? (gather ? 16 : 32) : 8) * sub;
+    return n < 32 ? n : 32;
+}
+CPA_HD int ahead_of(bool fp8, bool gather, int sub) { return fp8 && !gather ? 6 * sub : 32; }
 constexpr int kMinBlocks = 3;
 constexpr int kLatentC = 512, kLatentR = 64;  // elements of a latent's two parts
 
@@ -115,6 +127,10 @@ __device__ __forceinline__ int slot_of_token(const RowParams& p, int t0, int n, 
         return -1;
     }
     return (int)(((uint32_t)pg << p.lp) + ((uint32_t)pos & ((1u << p.lp) - 1u)));
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -223,8 +239,30 @@ __global__ void __launch_bounds__(kRowThreads, kMinBlocks) rows_kernel(const __g
         uint8_t* const pages = p.pages[part] + (size_t)piece * (FP8 ? 8 : 16);
         const size_t row_bytes = p.row_bytes[part], slot_bytes = p.slot_bytes[part];
         const int n = min(p.tokens, p.T - (int)t0);
+        // asks tokens i and on, 32 >> log_lines of them, into L2
+        const int width = min(p.pieces[part] - (seg << log_lanes), 1 << log_lanes) * (GATHER && FP8 ? 8 : 16);
+        const int log_lines = max(log_lanes - (GATHER && FP8 ? 4 : 3), 0);
+        const int line = (lane & ((1 << log_lines) - 1)) * 128;
+        const uint8_t* const first = (GATHER ? p.pages[part] : p.rows[part]) +
+                                     (size_t)(seg << log_lanes) * (GATHER && FP8 ? 8 : 16) + line;
+        auto ask = [&](int i, int end, int slot) {
+            i += lane >> log_lines;
+            const int at = GATHER ? __shfl_sync(0xffffffffu, slot, i & 31) : 0;
+            if (i < end && at >= 0 && line < width)
+                prefetch_l2(first + (GATHER ? (size_t)at * slot_bytes : (size_t)(t0 + i) * row_bytes));
+        };
+        const int asked = 32 >> log_lines, ahead = ahead_of(FP8, GATHER, sub);
+        const int begin = min(n, ahead);
+        if (!GATHER)
+            for (int i = 0; i < begin; i += asked) ask(i, begin, 0);
         const int slot = slot_of_token<GATHER>(p, (int)t0, n, bad);
+        if (GATHER)
+            for (int i = 0; i < begin; i += asked) ask(i, begin, slot);
         for (int i0 = 0; i0 < n; i0 += sub * kUnroll) {
+            if (FP8 && !GATHER) {
+                const int end = min(n, i0 + ahead + sub * kUnroll);
+                for (int i = i0 + ahead; i < end; i += asked) ask(i, end, 0);
+            }
             uint4 x[kUnroll];
             int at[kUnroll];
 #pragma unroll
@@ -336,7 +374,7 @@ cpa_status launch_rows(RowParams& p, cudaStream_t s) {
     if (n_sm <= 0) return CPA_ERR_CUDA;
     const long long per_group = p.segments[0] + p.segments[1];
     // few tokens: fewer to a warp, so that all SMs take part
-    p.tokens = tokens_of(FP8);
+    p.tokens = tokens_of(FP8, GATHER, 32 >> p.log_lanes[0]);
     while (p.tokens > 4 && p.T / p.tokens * per_group < (long long)n_sm * 16) p.tokens /= 2;
     const long long warps = ((long long)p.T + p.tokens - 1) / p.tokens * per_group;
     const long long blocks = (warps + kRowWarps - 1) / kRowWarps;
