@@ -7,7 +7,8 @@
 // mbarrier.try_wait, and after kWaitLimitNs of wall time (read from
 // %globaltimer) it records CPA_DEV_TIMEOUT in the caller's status word, raises
 // the CTA's abort flag and returns false, so that no kernel can hang the GPU.
-// (cpa_window.cu has its own form, whose limit counts from the last sign of work.)
+// (cpa_window.cu and cpa_latent_prefill.cu have their own form, whose limit counts from the last
+// sign of work.)
 #pragma once
 #include <cstdint>
 #include <cuda.h>

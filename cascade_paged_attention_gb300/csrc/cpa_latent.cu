@@ -12,8 +12,9 @@
 // and V^T comes straight from the tile, whose rows are keys.  P is the only operand that
 // goes through shared memory.
 //
-// The order of the products is S(i) PV(i-1): while one tile's scores go through the
-// softmax, the next tile's are made.
+// The order of the products: while one tile's scores go through the softmax, the next
+// tile's are made.  What is ready goes first, values before scores where both are (they
+// give the ring its places back).
 //
 // Warps (7): 0-3 softmax and output, 4 loads the tiles and 6 Q, 5 issues the products.  Every
 // warp finds the block's range by itself, before the barriers are ready.  Scores lie 16 rows
@@ -30,6 +31,14 @@
 // Split.  As in cpa_decode the key tiles of all units lie end to end, every block takes a
 // range of equal cost, and a unit cut by a range's end is joined by a second kernel in the
 // order of its parts.
+//
+// What bounds it.  Up to 32 rows: HBM (64 x 2000 tokens, 16 heads: 39.7 us, 3.7 TB/s with the
+// launches in it; 64 x 16000: 195 us, 6.05 TB/s, 0.89 of the copy rate).  64 rows: the ring.  It
+// holds two tiles, and a tile stays in it for its load (2100 cycles), its scores (1220), the
+// softmax (1000) and its values (810), some of them behind another tile's: 3230 cycles a tile,
+// where shared memory needs 2490 for what the products read and the loads write, HBM 3072 when
+// no other block shares the tile and the products alone 2030 (64 x 16000 tokens, 64 heads: 202 us;
+// 32 ragged requests of 128 heads: 114 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -57,14 +66,15 @@ constexpr int kMaxTokens = 64;  // S: the mask of a request's last tokens is one
 constexpr uint32_t kBox = 9u * 1024u;
 constexpr uint32_t kSlotBytes = 4 * kBox;
 constexpr int kMaxSlots = 5;
-// Halves that are asked into L2 ahead of their load.  (None: 64 x 2000 tokens 40.5 us in place of
-// 41.1, 64 x 16000 205 in place of 198, 32 ragged requests with 128 heads 128 in place of 119;
-// two to eight: 0.5 to 4 us longer for the first, no shorter for the others.)
+// Halves that are asked into L2 ahead of their load.  (None, one, two: 64 x 2000 tokens 39.6, 39.8,
+// 40.1 us; 64 x 16000 199, 195, 192, with 64 heads 217, 202, 201; 32 ragged requests of 128 heads
+// 117.8, 113.7, 113.8; five tokens a request 53.9, 53.0, 53.3.)
 constexpr int kAhead = 1;
 constexpr uint32_t kOffQ = 1024;
 constexpr uint32_t kMaxSmem = 232448;
 constexpr uint32_t kColS = 256;  // TMEM: O^T in columns 0 .. 255, the scores of two tiles
-// What a unit costs besides its tiles, in tiles.
+// What a unit costs besides its tiles, in tiles.  (1, 2, 3: 64 x 2000 tokens 39.1, 39.8, 40.5 us, 32
+// ragged requests of 128 heads 115.1, 113.7, 114.1, five tokens a request 54.1, 53.0, 54.3.)
 constexpr int kUnitCost = 2;
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
 
@@ -388,8 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             const uint64_t v_desc = sdesc_sw128(sbase + o_k, 1024, kBox);  // chunk after chunk, keys as rows
             const uint64_t p_desc = sdesc_sw128(sbase + o_p, 16, 1024);
             // Two walks over the same tiles: scores g, and the values of tile d behind it.  What is
-            // ready goes first; the scores where both are (the softmax then has work while the
-            // values' products run).
+            // ready goes first; the values where both are, whose places the next loads wait for.
             uint32_t g = 0, d = 0, d_pieces = 0;
             int ks = 0, vs = 0;  // slots of their first halves
             uint32_t kpar = 0, qpar = 0;

@@ -26,6 +26,14 @@
 // units, and the others read them from a ring in shared memory.
 //
 // Values that are not numbers: as in cpa_window.cu.
+//
+// What bounds it: the tensor cores.  2 x 8192 tokens of 32 heads take 870 to 910 us on their own,
+// 1.51 to 1.58 PFLOP/s of products that the mask leaves, 0.80 to 0.84 of the measured rate; a round
+// of both query tiles takes 2920 cycles where its products need 2560 at the nominal rate (scores
+// read Q and K from shared memory, which the loads write and the weights do not leave alone), a
+// unit's end 7600.  Six chunks of 200 to 640 tokens behind contexts: 328 us, 0.60, because a
+// request's last unit may hold one query tile, which has nothing to take turns with (3800 cycles a
+// key tile).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -819,10 +827,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                 const int row_o = lane & 1 ? (active ? row : -1) : row_x;
                 float check = lse2 == ninf_f() ? 0.f : lse2;
                 float4* po = p.part_o + slot * 32 * kRows + R;
-                // (Two lanes exchange halves, so that they write 64 bytes of a row together:
-                // 355 -> 350 us against 32 bytes of a row by each; 128 or 256 bytes together
-                // would give 1 us more before the cost of the exchange.  Through shared memory
-                // the whole lines cost as much, and the 32 KB that the third K stage needs.)
+                // (Two lanes exchange halves, so that they write 64 bytes of a row together, as in
+                // cpa_window.cu.)
 #pragma unroll 1
                 for (int c0 = 0; c0 < 128; c0 += 32) {
                     uint32_t v[32];

@@ -32,7 +32,9 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--case", choices=["cascade", "naive", "pass_a", "pass_b", "prefill", "tree",
                                        "tree_pass_b", "shared", "cascade_fp8", "decode",
-                                       "decode_fp8", "window", "copy_pages"],
+                                       "decode_fp8", "window", "copy_pages", "append",
+                                       "append_fp8", "gather", "gather_fp8", "latent_append",
+                                       "latent_gather", "latent_decode", "latent_prefill"],
                     default="cascade")
     ap.add_argument("--config", default="pages_example")
     ap.add_argument("--hit", type=float, default=0.5, help="prefill: cached fraction h")
@@ -41,6 +43,9 @@ def main():
                     help="decode, decode_fp8, window: the last tokens seen (0: all)")
     ap.add_argument("--sinks", type=int, default=0, help="the first tokens that stay seen")
     ap.add_argument("--batch", type=int, default=0, help="override B")
+    ap.add_argument("--heads", type=int, default=16, help="latent_decode, latent_prefill: heads")
+    ap.add_argument("--tokens", type=int, default=1,
+                    help="latent_decode: last tokens of a request that have queries")
     ap.add_argument("--warmup", type=int, default=2)
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--graph", action="store_true",
@@ -110,6 +115,82 @@ def main():
                 cpa.cpa_decode(q, kp, vp, pt, lens, **kw)
         work = (f"{args.config} window={args.window}: KV "
                 f"{int(wl.prefix_lens.sum()) * wl.kv_bytes_per_token() / 1e6:.1f} MB")
+    elif args.case in ("append", "append_fp8", "gather", "gather_fp8"):
+        # whole prompts, written to the pages that they are read from otherwise
+        cfg = dict(cpa_synth.VERIFY_CONFIGS[args.config], topk=1, S=1)
+        if args.batch:
+            cfg["B"] = args.batch
+        fp8 = args.case.endswith("fp8")
+        wl = cpa_synth.make_verify_fp8(scales=args.scales, **cfg) if fp8 else \
+            cpa_synth.make_verify(**cfg)
+        pt, lens = i32(wl.prefix_page_table), i32(wl.prefix_lens)
+        start = i32(np.concatenate([[0], np.cumsum(wl.prefix_lens)]))
+        T = int(wl.prefix_lens.sum())
+        if fp8:
+            pool = [torch.from_numpy(np.ascontiguousarray(a)).to(dev) for a in (
+                wl.k_pages, wl.v_pages, wl.k_scale.astype(np.float32),
+                wl.v_scale.astype(np.float32))]
+        else:
+            pool = [bf(wl.k_pages), bf(wl.v_pages)]
+        rows = [torch.zeros((T, wl.H_kv, pool[0].shape[3]), dtype=torch.bfloat16, device=dev)
+                for _ in range(2)]
+        if args.case == "append":
+            def call():
+                cpa.cpa_cache_append(*rows, *pool, pt, start, lens)
+        elif args.case == "append_fp8":
+            def call():
+                cpa.cpa_cache_append_fp8(*rows, *pool, pt, start, lens)
+        elif args.case == "gather":
+            def call():
+                cpa.cpa_cache_gather(*pool, pt, start, k_out=rows[0], v_out=rows[1])
+        else:
+            def call():
+                cpa.cpa_cache_gather_fp8(*pool, pt, start, k_out=rows[0], v_out=rows[1])
+        n = 2 * rows[0].numel()
+        work = f"{args.config}: {T} tokens, {2 * n / 1e6:.1f} MB as rows, " \
+               f"{(1 if fp8 else 2) * n / 1e6:.1f} MB in pages"
+    elif args.case == "latent_prefill":
+        B, N, H = args.batch or 2, cpa_synth.PREFILL_CONFIG["N"], args.heads
+        gen = torch.Generator(device=dev).manual_seed(21)
+
+        def rows(*shape):
+            return torch.randn(shape, generator=gen, device=dev, dtype=torch.bfloat16)
+        q, kv = rows(B * N, H, cpa.NOPE_DIM + cpa.ROPE_DIM), rows(B * N, H, 2 * cpa.NOPE_DIM)
+        k_rope, start = rows(B * N, cpa.ROPE_DIM), i32(np.arange(B + 1) * N)
+
+        def call():
+            cpa.cpa_latent_prefill(q, kv[..., :cpa.NOPE_DIM], k_rope, kv[..., cpa.NOPE_DIM:], start,
+                                   start)
+        flops = 2 * (2 * cpa.NOPE_DIM + cpa.ROPE_DIM) * B * H * N * (N + 1) // 2
+        work = f"B={B} N={N} H={H}: {flops / 1e12:.2f} TFLOP"
+    elif args.case in ("latent_append", "latent_gather", "latent_decode"):
+        cfg = dict(cpa_synth.VERIFY_CONFIGS[args.config], topk=1, S=1, H_q=1, H_kv=1)
+        if args.batch:
+            cfg["B"] = args.batch
+        wl = cpa_synth.make_verify(**cfg)  # (its table and lengths)
+        pt, lens = i32(wl.prefix_page_table), i32(wl.prefix_lens)
+        start = i32(np.concatenate([[0], np.cumsum(wl.prefix_lens)]))
+        T, S, width = int(wl.prefix_lens.sum()), args.tokens, cpa.LATENT_DIM + cpa.ROPE_DIM
+        gen = torch.Generator(device=dev).manual_seed(22)
+
+        def rows(*shape):
+            return torch.randn(shape, generator=gen, device=dev, dtype=torch.bfloat16)
+        pool = rows(wl.num_pages, wl.page_size, width)
+        if args.case == "latent_append":
+            c, r = rows(T, cpa.LATENT_DIM), rows(T, cpa.ROPE_DIM)
+
+            def call():
+                cpa.cpa_latent_append(c, r, pool, pt, start, lens)
+        elif args.case == "latent_gather":
+            def call():
+                cpa.cpa_latent_gather(pool, pt, start, T)
+        else:
+            q_c = rows(wl.B * S, args.heads, cpa.LATENT_DIM)
+            q_r = rows(wl.B * S, args.heads, cpa.ROPE_DIM)
+
+            def call():
+                cpa.cpa_latent_decode(q_c, q_r, pool, pt, lens, S=S, max_seq_len=wl.max_prefix_len)
+        work = f"{args.config} S={S} H={args.heads}: latents {T * width * 2 / 1e6:.1f} MB"
     elif args.case == "copy_pages":
         cfg = dict(cpa_synth.VERIFY_CONFIGS[args.config])
         wl = cpa_synth.make_verify(**cfg)

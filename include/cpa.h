@@ -45,7 +45,10 @@
  *     two kernels (cpa_cascade_verify_shared when its shared prefix ends inside
  *     a page, the cpa_decode calls, cpa_window_prefill, cpa_cache_fork,
  *     cpa_cache_free where n * pt_stride is above 1024, cpa_cache_compact in
- *     place or where B * max_keep is above 4096): they check every argument
+ *     place or where B * max_keep is above 4096, cpa_latent_decode,
+ *     cpa_latent_prefill with a memset before them in a call of many units, the
+ *     appends and gathers where B is above 8192 or T / page_size above 16384):
+ *     they check every argument
  *     before the first, so only CPA_ERR_LAUNCH or CPA_ERR_CUDA from the second
  *     launch can follow a launch already made.
  *   - Errors: arguments that can be checked on the host return a status
