@@ -32,8 +32,8 @@
 // of both query tiles takes 2920 cycles where its products need 2560 at the nominal rate (scores
 // read Q and K from shared memory, which the loads write and the weights do not leave alone), a
 // unit's end 7600.  Six chunks of 200 to 640 tokens behind contexts: 328 us, 0.60, because a
-// request's last unit may hold one query tile, which has nothing to take turns with (3800 cycles a
-// key tile).
+// request's last unit may hold one query tile: it loads 80 KB a key tile for half the products (3800
+// cycles; with the key tiles shared out to both pipelines no fewer).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
