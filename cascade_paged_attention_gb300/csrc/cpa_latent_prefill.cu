@@ -21,8 +21,8 @@
 // of equal cost, and a second kernel joins the units that a range's end cuts.  With heads that
 // share no keys that order has every head's K and V in use at a time, more than L2 holds
 // (2 x 8192 tokens, 32 heads: 3.8 GB read from DRAM in place of 0.6).  A call with many units
-// therefore hands them out whole, a few heads at a time, the longest of these heads first, so
-// that what is left at the end is short.  Either way the warp that loads K and V finds the
+// therefore hands them out whole, a few heads at a time, the longest of these heads first and
+// long requests before short ones, so that what is left at the end is short.  Either way the warp that loads K and V finds the
 // units, and the others read them from a ring in shared memory.
 //
 // Values that are not numbers: as in cpa_window.cu.
@@ -69,6 +69,9 @@ constexpr int kMinTiles = 2;  // fewest tiles of a block where units have a cost
 // Units a block from which they are handed out whole (12 chunks with 5 units a block 533 -> 497 us,
 // 2 x 2000 tokens with 3 units a block 104 -> 96 us, six chunks with 3 units a block 328 us both).
 constexpr int kWholeUnits = 2;
+// Requests are handed out whole in the order of their lengths, by classes of an eighth of the
+// longest: in the order of the batch blocks were at work for 327 to 655 thousand cycles.  (MEASURED)
+constexpr int kClasses = 8;
 constexpr int kMostHeads = 8;       // that are handed out side by side,
 constexpr int kSharedKeys = 65536;  // as long as their keys are no more than these (32 MB)
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
@@ -119,6 +122,11 @@ __device__ __forceinline__ int tiles_of(const Request& r, int qt) {
     return (r.L - r.m + min(r.m, (qt + 1) * kRows) + kTile - 1) / kTile;
 }
 
+// The class of a request's length, the highest that of the longest.
+__device__ __forceinline__ int class_of(const Request& r, int most) {
+    return (tiles_of(r, units_of(r) - 1) * kClasses - 1) / most;
+}
+
 // A unit, or the part [j0, j1) of its tiles that a block does; j0 == j1: no more.
 struct Piece {
     int t0, ntok;  // rows of q
@@ -141,6 +149,7 @@ struct Ctrl {
     uint32_t tmem_base;
     volatile uint32_t abort_flag;
     uint32_t bad;
+    int most_tiles;           // of a unit
     int unit_cost;            // kUnitCost, or 0 where no block takes more than kFewTiles
     long long t0, left, per;  // this block's range, in tiles of cost
     int b, h, qt, off;        // where it begins: a unit, and how far into its cost
@@ -208,13 +217,17 @@ __device__ void schedule(const ExpandedParams& p, Ctrl* c, long long* sums) {
     const int per_thread = (p.B + kThreads - 1) / kThreads, b0 = (int)threadIdx.x * per_thread;
     uint32_t bad = 0;
     long long mine = 0, units = 0;
+    int most = 0;
     for (int i = 0; i < per_thread; ++i) {
         Request r = {0, 0, 0, 0};
         if (b0 + i < p.B) r = request_of(p, b0 + i, bad);
         mine += lane_tiles(r) * p.H;
         units += (long long)units_of(r) * p.H;
+        if (r.m > 0) most = max(most, tiles_of(r, units_of(r) - 1));
     }
     if (bad) atomicOr(&c->bad, bad);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0 && most > 0) atomicMax(&c->most_tiles, most);
     long long incl = mine, incl_units = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -299,7 +312,7 @@ struct Finder {
     Request r;
     int b, h, qt, unit_cost;
     long long left;  // cost of the range after this piece
-    int base;        // whole units: the first of request b
+    int base, cls;   // whole units: the first of request b, and its class
     bool first;
     __device__ __forceinline__ Piece piece(int j0, int j1) const {
         const int m0 = qt * kRows;
@@ -318,12 +331,37 @@ struct Finder {
         unit_cost = c->unit_cost;
         uint32_t bad = 0;
         base = 0;
+        cls = kClasses - 1;
         // (a block without a range has no place where it begins)
         const bool range = !p.whole && left > 0;
-        b = range ? c->b : 0;
+        b = range ? c->b : -1;
         h = range ? c->h : 0;
         qt = range ? c->qt : 0;
-        r = request_of(p, b, bad);
+        r = {0, 0, 0, 0};
+        if (range) r = request_of(p, b, bad);
+    }
+    // The next request of this class, then of those below; false: none.
+    __device__ __forceinline__ bool advance(const ExpandedParams& p, const Ctrl* c) {
+        const int lane = threadIdx.x & 31;
+        uint32_t bad = 0;
+        for (; cls >= 0; --cls, b = -1) {
+            for (int b0 = b + 1; b0 < p.B; b0 += 32) {
+                Request q = {0, 0, 0, 0};
+                if (b0 + lane < p.B) q = request_of(p, b0 + lane, bad);
+                const uint32_t here =
+                    __ballot_sync(0xffffffffu, q.m > 0 && class_of(q, c->most_tiles) == cls);
+                if (here == 0u) continue;
+                const int src = __ffs((int)here) - 1;
+                b = b0 + src;
+                r.t0 = __shfl_sync(0xffffffffu, q.t0, src);
+                r.m = __shfl_sync(0xffffffffu, q.m, src);
+                r.k0 = __shfl_sync(0xffffffffu, q.k0, src);
+                r.L = __shfl_sync(0xffffffffu, q.L, src);
+                return true;
+            }
+        }
+        r.m = 0;
+        return false;
     }
     __device__ __forceinline__ Piece next(const ExpandedParams& p, const Ctrl* c) {
         uint32_t bad = 0;
@@ -338,12 +376,7 @@ struct Finder {
             }
             while (u - base >= units_of(r) * p.H) {
                 base += units_of(r) * p.H;
-                if (++b == p.B) {
-                    b = p.B - 1;  // (no unit is at or past here)
-                    r.m = 0;
-                    return none;
-                }
-                r = request_of(p, b, bad);
+                if (!advance(p, c)) return none;
             }
             // as many heads at a time as kSharedKeys allows, the last query tokens first
             const int nq = units_of(r);
@@ -475,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
         ctrl->alive_ns = 0;
         ctrl->abort_flag = 0;
         ctrl->bad = 0;
+        ctrl->most_tiles = 0;
         fence_barrier_init();
         prefetch_tmap(&p.qmap);
         prefetch_tmap(&p.kmap);
