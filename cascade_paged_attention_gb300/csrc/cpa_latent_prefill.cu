@@ -31,7 +31,7 @@
 // 1.51 to 1.58 PFLOP/s of products that the mask leaves, 0.80 to 0.84 of the measured rate; a round
 // of both query tiles takes 2920 cycles where its products need 2560 at the nominal rate (scores
 // read Q and K from shared memory, which the loads write and the weights do not leave alone), a
-// unit's end 7600.  Six chunks of 200 to 640 tokens behind contexts: 328 us, 0.60, because a
+// unit's end 7600.  Six chunks of 200 to 640 tokens behind contexts: 295 us, 0.67, because a
 // request's last unit may hold one query tile: it loads 80 KB a key tile for half the products (3800
 // cycles; with the key tiles shared out to both pipelines no fewer).
 #include <cuda_bf16.h>
@@ -69,8 +69,10 @@ constexpr int kMinTiles = 2;  // fewest tiles of a block where units have a cost
 // Units a block from which they are handed out whole (12 chunks with 5 units a block 533 -> 497 us,
 // 2 x 2000 tokens with 3 units a block 104 -> 96 us, six chunks with 3 units a block 328 us both).
 constexpr int kWholeUnits = 2;
-// Requests are handed out whole in the order of their lengths, by classes of an eighth of the
-// longest: in the order of the batch blocks were at work for 327 to 655 thousand cycles.  (MEASURED)
+// Whole units are handed out in the order of their requests' lengths, in classes of an eighth of the
+// longest.  (Six chunks in the order of the batch 326 us, blocks at work for 327 to 655 thousand
+// cycles; so 295, 446 to 559 thousand; with 4 or 16 classes 293 and 297.  12 chunks 491 -> 455 us,
+// 16 chunks 906 -> 829.)
 constexpr int kClasses = 8;
 constexpr int kMostHeads = 8;       // that are handed out side by side,
 constexpr int kSharedKeys = 65536;  // as long as their keys are no more than these (32 MB)

@@ -434,6 +434,44 @@ def test_prefill_units_handed_out_whole(news, lens, H):
     check_prefill(news, lens, H, seed=H, lead=1, trail=2, k_lead=3, k_trail=1)
 
 
+def test_prefill_last_query_tiles_alone():
+    """Whole units of one query tile with one key tile and with many, odd and even in number, one
+    after another and between those of two: every request's result, the same in each run."""
+    g = torch.Generator().manual_seed(7)
+    news = [1, 128, 127, 300, 100, 129, 64, 5, 257, 380, 128, 40] * 2
+    lens = [m + int(torch.randint(0, 1400, (1,), generator=g)) * (i % 4 != 0) for i, m in enumerate(news)]
+    H = 32
+    assert sum(news) * H >= 2 * 152 * 256
+    q, nope, rope, v, qs, ks = make_prefill(news, lens, H, 5)
+    args = (q, nope, rope, v, i32(qs), i32(ks))
+    first = cpa.cpa_latent_prefill(*args, check=True)
+    against_prefill(q, nope, rope, v, qs, ks, *first)
+    for _ in range(20):
+        o, lse = cpa.cpa_latent_prefill(*args)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    cpa.cpa_latent_prefill(*args, check=True)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_prefill_values_that_are_not_numbers_in_whole_units(value):
+    """Behind the first rows of a query tile that is its unit's only one, in an even and in an odd key
+    tile: the rows that see it have it in that column, the others are as without it."""
+    news, lens, H = [70, 2400], [700, 2400], 32
+    assert sum(news) * H >= 2 * 152 * 256
+    for at in (690, 635):  # key tiles 5 and 4; rows 630 and on
+        q, nope, rope, v, qs, ks = make_prefill(news, lens, H, 11)
+        want, want_lse = cpa.cpa_latent_prefill(q, nope, rope, v, i32(qs), i32(ks), check=True)
+        v[at, 2, 9] = value
+        o, lse = cpa.cpa_latent_prefill(q, nope, rope, v, i32(qs), i32(ks), check=True)
+        bad = ~torch.isfinite(o.float())
+        hit = torch.arange(630, 700, device="cuda") >= at
+        assert bool(bad[:70][hit][:, 2, 9].all()) and int(bad.sum()) == int(hit.sum())
+        v[at, 2, 9] = 0.0
+        seen = ref.seen(torch.arange(630, 700)[~hit.cpu()].tolist(), 700, 0, 0, "cuda")
+        ref.close(o[:70][~hit], lse[:70][~hit], lref.expanded(q[:70][~hit], nope[:700], rope[:700], v[:700], seen))
+        assert torch.equal(o[70:], want[70:]) and torch.equal(lse[70:], want_lse[70:])
+
+
 def test_prefill_units_handed_out_whole_in_a_graph():
     """Captured behind a copy, replayed: each replay hands out its units from the first."""
     news, lens, H = [1300, 1300], [1300, 1500], 32
