@@ -742,6 +742,15 @@ def _new(shape, dtype, dev: int, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _out(t, name: str, shape, dtype, dev: int, stream):
+    """An output: the caller's, checked, or a new one."""
+    if t is None:
+        return _new(shape, dtype, dev, stream)
+    _want(t, name, dtype, len(shape), dev)
+    _shape(t, name, shape)
+    return t
+
+
 # PyTorch's current stream of a device as an integer (the first without making a Stream of it)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -1120,13 +1129,8 @@ def _gather(name, k_pages, v_pages, scales, page_table, out_start, T, first, k_o
     dev, (num_pages, P, H_kv, d), dtype = _row_pools(k_pages, v_pages, scales is not None)
     B, stride = _request_args(page_table, out_start, first, "first", dev)
     shape = (_out_rows(T, (k_out, v_out)), H_kv, d)
-    if k_out is None:
-        k_out = _new(shape, dtype, dev, stream)
-    if v_out is None:
-        v_out = _new(shape, dtype, dev, stream)
-    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
-        _want(t, nm, dtype, 3, dev)
-        _shape(t, nm, shape)
+    k_out = _out(k_out, "k_out", shape, dtype, dev, stream)
+    v_out = _out(v_out, "v_out", shape, dtype, dev, stream)
     pools = (k_pages.data_ptr(), v_pages.data_ptr())
     requests = (page_table.data_ptr(), stride, out_start.data_ptr(),
                 None if first is None else first.data_ptr(), B, shape[0])
@@ -1192,13 +1196,8 @@ def cpa_latent_gather(pages, page_table, out_start, T: Optional[int] = None, fir
     dev, num_pages, P = _latent_pool(pages)
     B, stride = _request_args(page_table, out_start, first, "first", dev)
     T = _out_rows(T, (c_out, r_out))
-    if c_out is None:
-        c_out = _new((T, LATENT_DIM), torch.bfloat16, dev, stream)
-    if r_out is None:
-        r_out = _new((T, ROPE_DIM), torch.bfloat16, dev, stream)
-    for t, nm, width in ((c_out, "c_out", LATENT_DIM), (r_out, "r_out", ROPE_DIM)):
-        _want(t, nm, torch.bfloat16, 2, dev)
-        _shape(t, nm, (T, width))
+    c_out = _out(c_out, "c_out", (T, LATENT_DIM), torch.bfloat16, dev, stream)
+    r_out = _out(r_out, "r_out", (T, ROPE_DIM), torch.bfloat16, dev, stream)
     args = (pages.data_ptr(), page_table.data_ptr(), stride, out_start.data_ptr(),
             None if first is None else first.data_ptr(), B, T, LATENT_DIM, ROPE_DIM, P, num_pages,
             c_out.data_ptr(), r_out.data_ptr())
@@ -1212,8 +1211,9 @@ def _heads_of(t, name: str, shape, dev: int):
     if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and \
             t.shape == shape:
         st = t.stride()
-        if st[2] == 1 and shape[0] > 1 and shape[1] > 1:
-            return st[0], st[1]
+        n, H, w = shape
+        if st[2] == 1:
+            return st[0] if n > 1 else H * w, st[1] if H > 1 else w
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
@@ -1255,14 +1255,8 @@ def cpa_latent_decode(q_c, q_r, pages, page_table, seq_lens, S: int = 1,
     qc = _heads_of(q_c, "q_c", (n, H, LATENT_DIM), dev)
     qr = _heads_of(q_r, "q_r", (n, H, ROPE_DIM), dev)
     stride = page_table.shape[1]
-    if o is None:
-        o = _new((n, H, LATENT_DIM), torch.bfloat16, dev, stream)
-    if lse is None:
-        lse = _new((n, H), torch.float32, dev, stream)
-    _want(o, "o", torch.bfloat16, 3, dev)
-    _want(lse, "lse", torch.float32, 2, dev)
-    _shape(o, "o", (n, H, LATENT_DIM))
-    _shape(lse, "lse", (n, H))
+    o = _out(o, "o", (n, H, LATENT_DIM), torch.bfloat16, dev, stream)
+    lse = _out(lse, "lse", (n, H), torch.float32, dev, stream)
     args = (q_c.data_ptr(), *qc, q_r.data_ptr(), *qr, pages.data_ptr(), page_table.data_ptr(),
             stride, seq_lens.data_ptr(), B, S, H, LATENT_DIM, ROPE_DIM, P, num_pages,
             _max_len(max_seq_len, stride, P),
@@ -1299,14 +1293,8 @@ def cpa_latent_prefill(q, k_nope, k_rope, v, q_start, k_start, sm_scale: Optiona
     ks = _heads_of(k_nope, "k_nope", (T_k, H, NOPE_DIM), dev)
     vs = _heads_of(v, "v", (T_k, H, NOPE_DIM), dev)
     rs = _rows_of(k_rope, "k_rope", torch.bfloat16, (T_k, ROPE_DIM), dev)
-    if o is None:
-        o = _new((T, H, NOPE_DIM), torch.bfloat16, dev, stream)
-    if lse is None:
-        lse = _new((T, H), torch.float32, dev, stream)
-    _want(o, "o", torch.bfloat16, 3, dev)
-    _want(lse, "lse", torch.float32, 2, dev)
-    _shape(o, "o", (T, H, NOPE_DIM))
-    _shape(lse, "lse", (T, H))
+    o = _out(o, "o", (T, H, NOPE_DIM), torch.bfloat16, dev, stream)
+    lse = _out(lse, "lse", (T, H), torch.float32, dev, stream)
     args = (q.data_ptr(), k_nope.data_ptr(), *ks, k_rope.data_ptr(), rs, v.data_ptr(), *vs,
             q_start.data_ptr(), k_start.data_ptr(), B, T, T_k, H, NOPE_DIM, ROPE_DIM, NOPE_DIM,
             (NOPE_DIM + ROPE_DIM) ** -0.5 if sm_scale is None else float(sm_scale), o.data_ptr(),
