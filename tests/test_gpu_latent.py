@@ -427,7 +427,8 @@ def test_prefill_bad_starts_are_reported():
 
 @pytest.mark.parametrize("news,lens,H", [
     ([2500], [2500], 32), ([300, 0, 1, 700, 1500], [400, 7, 3000, 700, 1500], 32),
-    ([900, 70], [1000, 4000], 96), ([40] * 130, [41] * 130, 16)])
+    ([900, 70], [1000, 4000], 96), ([40] * 130, [41] * 130, 16),
+    ([37 * i % 61 for i in range(75)], [37 * i % 61 + 53 * i % 900 for i in range(75)], 40)])
 def test_prefill_units_handed_out_whole(news, lens, H):
     """Enough rows that blocks take whole units, a few heads at a time."""
     assert sum(news) * H >= 2 * 152 * 256
