@@ -165,11 +165,77 @@ struct Reciprocals {
     }
 };
 
+// Every row of every request that is right, request by request, by one block.  The search above takes
+// starts to be ascending; where one is not it may pass over requests that are, and this block moves
+// their rows.  (Rows that the search did find get the same bytes twice.)  Slow: one SM copies.
+template <bool FP8, bool GATHER>
+__device__ __noinline__ uint32_t move_request_by_request(const RowParams& p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t bad = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        RowRequest mine = {0, 0, 0, false};
+        if (b0 + lane < p.B) mine = row_request<GATHER>(p, b0 + lane);
+        for (uint32_t todo = __ballot_sync(0xffffffffu, mine.ok && mine.s1 > mine.s0); todo; todo &= todo - 1) {
+            const int src = __ffs((int)todo) - 1;
+            const int s0 = __shfl_sync(0xffffffffu, mine.s0, src), s1 = __shfl_sync(0xffffffffu, mine.s1, src);
+            const int first = (int)__shfl_sync(0xffffffffu, mine.pos, src);
+            const int32_t* const table = p.table + (size_t)(b0 + src) * p.stride;
+            for (int t = s0 + ((warp - src) & (kRowWarps - 1)); t < s1; t += kRowWarps) {
+                const int pos = first + (t - s0), pg = __ldg(table + (pos >> p.lp));
+                if (pg < 0 || pg >= p.num_pages) {
+                    bad |= CPA_DEV_BAD_PAGE;
+                    continue;
+                }
+                const size_t slot = ((size_t)pg << p.lp) + (pos & ((1 << p.lp) - 1));
+                for (int part = 0; part < 2; ++part) {
+                    for (int piece = lane; piece < p.pieces[part]; piece += 32) {
+                        uint4* const row = reinterpret_cast<uint4*>(
+                            p.rows[part] + (size_t)t * p.row_bytes[part] + (size_t)piece * 16);
+                        uint8_t* const page = p.pages[part] + slot * p.slot_bytes[part] + (size_t)piece * (FP8 ? 8 : 16);
+                        if (!FP8) {
+                            if (GATHER)
+                                *row = *reinterpret_cast<const uint4*>(page);
+                            else
+                                *reinterpret_cast<uint4*>(page) = *row;
+                            continue;
+                        }
+                        const float* const scale = p.scale[part] + (p.per_channel ? piece * 8 : 0);
+                        const int step = p.per_channel ? 1 : 0;
+                        if (GATHER) {
+                            const uint2 c = *reinterpret_cast<const uint2*>(page);
+                            uint32_t o[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t h = e4m3x2_to_f16x2(k < 2 ? c.x : c.y, k & 1);
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                                o[k] = pack_bf16x2(f.x * __ldg(scale + 2 * k * step),
+                                                   f.y * __ldg(scale + (2 * k + 1) * step));
+                            }
+                            *row = make_uint4(o[0], o[1], o[2], o[3]);
+                        } else {
+                            float f[8];
+                            bf16x8_to_f32(*row, f);
+                            uint32_t c[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                c[k] = e4m3x2(f[2 * k] / __ldg(scale + 2 * k * step),
+                                              f[2 * k + 1] / __ldg(scale + (2 * k + 1) * step));
+                            *reinterpret_cast<uint2*>(page) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    return bad;
+}
+
 // What is wrong with a call, by one block: every request, and every page that it names.
-template <bool GATHER>
+template <bool FP8, bool GATHER>
 __device__ void look_over(const RowParams& p) {
     const int lane = threadIdx.x & 31;
     uint32_t bad = 0;
+    bool descends = false;
     // up to 32 requests to a warp at a time, fewer so that all warps have some: a request for
     // each lane, then the pages of each by the warp
     const int chunk = min(32, (p.B + kRowWarps - 1) / kRowWarps);
@@ -177,6 +243,7 @@ __device__ void look_over(const RowParams& p) {
         int first = 0, n = 0;
         if (lane < chunk && b0 + lane < p.B) {
             const RowRequest r = row_request<GATHER>(p, b0 + lane);
+            descends |= r.s1 < r.s0;
             if (!r.ok) {
                 bad |= CPA_DEV_BAD_LENGTH;
             } else if (r.s1 > r.s0) {
@@ -201,6 +268,7 @@ __device__ void look_over(const RowParams& p) {
     const bool len = __syncthreads_or((int)(bad & CPA_DEV_BAD_LENGTH));
     if (threadIdx.x == 0)
         *p.status = (page ? CPA_DEV_BAD_PAGE : 0u) | (len ? CPA_DEV_BAD_LENGTH : 0u);
+    if (len && __syncthreads_or((int)descends)) move_request_by_request<FP8, GATHER>(p);
 }
 
 template <bool FP8, bool GATHER>
@@ -209,7 +277,7 @@ __global__ void __launch_bounds__(kRowThreads, kMinBlocks) rows_kernel(const __g
     const int lane = threadIdx.x & 31;
     uint32_t bad = 0;
     if (p.status_block && blockIdx.x == 0) {
-        look_over<GATHER>(p);
+        look_over<FP8, GATHER>(p);
         return;
     }
     const int block = (int)blockIdx.x - p.status_block;
@@ -221,9 +289,15 @@ __global__ void __launch_bounds__(kRowThreads, kMinBlocks) rows_kernel(const __g
     const long long t0 = w / per_group * p.tokens;
     if (!p.status_block) {
         wait_for_clear();
-        if (block == 0)
-            for (int b = threadIdx.x; b < p.B; b += kRowThreads)
-                if (!row_request<GATHER>(p, b).ok) bad |= CPA_DEV_BAD_LENGTH;
+        if (block == 0) {
+            bool descends = false;
+            for (int b = threadIdx.x; b < p.B; b += kRowThreads) {
+                const RowRequest r = row_request<GATHER>(p, b);
+                descends |= r.s1 < r.s0;
+                if (!r.ok) bad |= CPA_DEV_BAD_LENGTH;
+            }
+            if (__syncthreads_or((int)descends)) bad |= move_request_by_request<FP8, GATHER>(p);
+        }
     }
     if (t0 < p.T) {
         const int log_lanes = p.log_lanes[part], sub = 32 >> log_lanes;

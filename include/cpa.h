@@ -593,7 +593,8 @@ cpa_status cpa_cache_compact(void* k_pages, void* v_pages, const int32_t* src_ta
  * tokens of one of them at most (cpa_cache_fork shares whole pages only).
  * A new_start that is not ascending or leaves [0, T] or a length out of range sets
  * CPA_DEV_BAD_LENGTH, a page id outside [0, num_pages) CPA_DEV_BAD_PAGE; such a
- * request's, or such a page's, tokens are not written, all others are.
+ * request's, or such a page's, tokens are not written, all others are (a request is
+ * judged by its own start, end and length; a call whose starts do not ascend is slow).
  * T up to 2^30.  Workspace: cpa_status_workspace_size().
  */
 cpa_status cpa_cache_append(const void* k_new, const void* v_new, size_t k_stride_bytes,
@@ -625,7 +626,8 @@ cpa_status cpa_cache_append_fp8(const void* k_new, const void* v_new, size_t k_s
  * 16-byte aligned, not over any input).  first NULL: position 0.  Rows of no
  * request, and those whose request or page sets a bit of the status word (as for
  * cpa_cache_append, with first[b] + n_b in the place of the length), are left as
- * they were.  Workspace: cpa_status_workspace_size().
+ * they were; one that starts that do not ascend give to two requests holds values of
+ * theirs.  Workspace: cpa_status_workspace_size().
  */
 cpa_status cpa_cache_gather(const void* k_pages, const void* v_pages, const int32_t* page_table,
                             int pt_stride, const int32_t* out_start, const int32_t* first, int B,

@@ -181,6 +181,100 @@ def test_what_is_wrong_is_reported_and_left_out(big):
         go(table, i32(s), i32(lens), 8)
 
 
+def rows_of_valid_requests(st, lens, T, most):
+    """(request, first row, tokens) of each request whose own start, end and length are in range."""
+    return [(b, s0, s1 - s0) for b, (s0, s1) in enumerate(zip(st, st[1:]))
+            if 0 <= s0 <= s1 <= T and 0 <= lens[b] - (s1 - s0) and lens[b] <= most]
+
+
+def _one_bad_start():
+    st = list(range(0, 404, 4))
+    st[64] = 0  # requests 63 (descending) and 64 (longer than its sequence) are wrong
+    return st, [4 + b % 30 for b in range(100)]
+
+
+def _starts_past_the_rows():
+    st = list(range(0, 153, 3))
+    st[7], st[20], st[41] = 10 ** 9, -5, 2 ** 31 - 1
+    return st, [3 + b for b in range(50)]
+
+
+BAD_STARTS = [_one_bad_start(), ([0, 10, 0, 30], [50, 30, 20]), ([0, 10, 0, 30], [50, 30, 40]),
+              _starts_past_the_rows(), ([9, 9, 40, 12, 33, 33, 50], [5, 31, 28, 21, 3, 60])]
+
+
+@pytest.mark.parametrize("kind", ["copy", "fp8", "latent"])
+@pytest.mark.parametrize("case", range(len(BAD_STARTS)))
+@pytest.mark.parametrize("big", [False, True])
+def test_starts_that_are_not_ascending(kind, case, big):
+    """Requests beside a wrong start: every row of those that are right is moved, whatever the
+    search by start would find, and nothing else is.  (big: the form whose warps report by
+    themselves.)"""
+    st, lens = (list(x) for x in BAD_STARTS[case])
+    P, H = 8, 2
+    if big:
+        lens += [1] * 9000
+        st += list(range(st[-1] + 1, st[-1] + 9001))
+    T = st[-1] + 2
+    g = ref.gen(case)
+    table, pool = ref.table_of(lens, P, g)
+    most = table.shape[1] * P
+    valid = rows_of_valid_requests(st, lens, T, most)
+    assert 0 < len(valid) < len(lens) and sorted(st) != st
+    rows = torch.cat([torch.arange(s0, s0 + m, device="cuda") for _, s0, m in valid])
+    req = torch.repeat_interleave(i32([b for b, _, _ in valid]).long(), i32([m for _, _, m in valid]).long())
+    pos = rows - i32([s0 for _, s0, m in valid for _ in range(m)]).long() + \
+        i32([lens[b] - m for b, _, m in valid for _ in range(m)]).long()
+    at = table[req, pos // P].long() * P + pos % P
+    ws = torch.full((256,), 0xA5, dtype=torch.uint8, device="cuda")
+    scale = [torch.rand(H, 128, generator=g, device="cuda") * 0.02 + 0.001 for _ in "kv"]
+    widths = (512, 64) if kind == "latent" else (H * 128, H * 128)
+    new = [torch.randn(T, w, generator=g, device="cuda").to(torch.bfloat16) for w in widths]
+    args = (table, i32(st), i32(lens))
+    if kind == "latent":
+        pages = torch.full((pool, P, 576), 7.0, device="cuda").to(torch.bfloat16)
+        want = pages.clone()
+        want.view(-1, 576)[at] = torch.cat(new, 1)[rows]
+        cpa.cpa_latent_append(*new, pages, *args, workspace=ws)
+        got, want = [pages], [want]
+    else:
+        kv = [x.view(T, H, 128) for x in new]
+        kind_of = torch.uint8 if kind == "fp8" else torch.bfloat16
+        got = [torch.full((pool, P, H, 128), 7, dtype=kind_of, device="cuda") for _ in "kv"]
+        want = [x.clone() for x in got]
+        for w, x, s in zip(want, kv, scale):
+            w.view(-1, H, 128)[at] = quantised(x[rows], s) if kind == "fp8" else x[rows]
+        if kind == "fp8":
+            cpa.cpa_cache_append_fp8(*kv, *got, *scale, *args, workspace=ws)
+        else:
+            cpa.cpa_cache_append(*kv, *got, *args, workspace=ws)
+    assert cpa.cpa_get_device_status(ws)[0] == 8
+    for x, w in zip(got, want):
+        assert torch.equal(bits(x), bits(w))
+    # and back: rows of one valid request have its slots, rows of none are as they were
+    first = i32([lens[b] - (s1 - s0) if abs(s1 - s0) < 2 ** 20 else 0 for b, (s0, s1) in enumerate(zip(st, st[1:]))])
+    out = [torch.full((T, w) if kind == "latent" else (T, H, 128), 5.0, device="cuda").to(torch.bfloat16) for w in widths]
+    kw = dict(first=first, workspace=ws)
+    if kind == "latent":
+        cpa.cpa_latent_gather(*got, table, i32(st), c_out=out[0], r_out=out[1], **kw)
+    elif kind == "fp8":
+        cpa.cpa_cache_gather_fp8(*got, *scale, table, i32(st), k_out=out[0], v_out=out[1], **kw)
+    else:
+        cpa.cpa_cache_gather(*got, table, i32(st), k_out=out[0], v_out=out[1], **kw)
+    assert cpa.cpa_get_device_status(ws)[0] == 8
+    times = torch.bincount(rows, minlength=T)
+    one = times[rows] == 1
+    for i, o in enumerate(out):
+        if kind == "latent":
+            src = got[0].view(-1, 576)[at][:, :512] if i == 0 else got[0].view(-1, 576)[at][:, 512:]
+        else:
+            src = got[i].view(-1, H, 128)[at]
+            if kind == "fp8":
+                src = (src.view(torch.float8_e4m3fn).float() * scale[i]).to(torch.bfloat16)
+        assert torch.equal(bits(o[rows[one]]), bits(src[one]))
+        assert bool((o[times == 0] == 5).all())
+
+
 @pytest.mark.parametrize("B", [5000, 9000])
 def test_many_requests_and_empty_ones(B):
     g = ref.gen(9)
