@@ -106,17 +106,21 @@ struct ExpandedParams {
 struct Request {
     int t0, m, k0, L;
 };
-__device__ __forceinline__ Request request_of(const ExpandedParams& p, int b, uint32_t& bad) {
-    const int s0 = __ldg(p.q_start + b), s1 = __ldg(p.q_start + b + 1);
-    const int k0 = __ldg(p.k_start + b), k1 = __ldg(p.k_start + b + 1);
+__device__ __forceinline__ Request request_of(const int32_t* q_start, const int32_t* k_start, int T, int T_k,
+                                              int b, uint32_t& bad) {
+    const int s0 = __ldg(q_start + b), s1 = __ldg(q_start + b + 1);
+    const int k0 = __ldg(k_start + b), k1 = __ldg(k_start + b + 1);
     Request r = {s0, 0, k0, 0};
-    if (s0 < 0 || s1 < s0 || s1 > p.T || k0 < 0 || k1 < k0 || k1 > p.T_k || s1 - s0 > k1 - k0) {
+    if (s0 < 0 || s1 < s0 || s1 > T || k0 < 0 || k1 < k0 || k1 > T_k || s1 - s0 > k1 - k0) {
         bad |= CPA_DEV_BAD_LENGTH;
     } else {
         r.m = s1 - s0;
         r.L = k1 - k0;
     }
     return r;
+}
+__device__ __forceinline__ Request request_of(const ExpandedParams& p, int b, uint32_t& bad) {
+    return request_of(p.q_start, p.k_start, p.T, p.T_k, b, bad);
 }
 __device__ __forceinline__ int units_of(const Request& r) { return (r.m + kRows - 1) / kRows; }
 // Tiles of a request's query tokens qt * kRows and on.
@@ -1026,6 +1030,15 @@ __global__ void __launch_bounds__(256) expanded_join_kernel(const __grid_constan
         p.lse[row] = sum == 0.f ? ninf_f() : ((m == ninf_f() ? 0.f : m) + lg2(sum)) * kLn2;
 }
 
+// All that a call without new tokens does: its starts are looked at.
+__global__ void __launch_bounds__(256) starts_kernel(const int32_t* q_start, const int32_t* k_start, int B,
+                                                     int T_k, uint32_t* status) {
+    uint32_t bad = 0;
+    for (int b = threadIdx.x; b < B; b += 256) request_of(q_start, k_start, 0, T_k, b, bad);
+    const bool any = __syncthreads_or((int)bad);
+    if (threadIdx.x == 0) *status = any ? CPA_DEV_BAD_LENGTH : 0u;
+}
+
 struct ExpandedWs {
     size_t counter, bad, desc, part_lse, part_o, total;
 };
@@ -1088,7 +1101,10 @@ cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token
     if (!workspace || workspace_bytes < kStatusBytes) return CPA_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return CPA_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (T == 0) return cudaMemsetAsync(workspace, 0, 4, s) == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
+    if (T == 0) {
+        starts_kernel<<<1, 256, 0, s>>>(q_start, k_start, B, T_k, static_cast<uint32_t*>(workspace));
+        return cudaGetLastError() == cudaSuccess ? CPA_OK : CPA_ERR_LAUNCH;
+    }
     const int n_sm = sm_count();
     if (n_sm <= 0) return CPA_ERR_CUDA;
     const ExpandedWs w = expanded_ws(n_sm);

@@ -443,7 +443,6 @@ cpa_status rows_ready(RowParams& p, const int32_t* table, int stride, const int3
 
 template <bool FP8, bool GATHER>
 cpa_status launch_rows(RowParams& p, cudaStream_t s) {
-    if (p.T == 0) return clear_status(p.status, s);
     const int n_sm = sm_count();
     if (n_sm <= 0) return CPA_ERR_CUDA;
     const long long per_group = p.segments[0] + p.segments[1];
@@ -455,7 +454,8 @@ cpa_status launch_rows(RowParams& p, cudaStream_t s) {
     // One block more looks a call over while the others move rows; where it would take longer
     // than they do, every warp reports into a cleared word.
     p.status_block = p.B <= 8192 && (p.T >> p.lp) <= 16384 ? 1 : 0;
-    const dim3 grid((unsigned)(blocks + p.status_block));
+    // (a call without rows has one block all the same, for its starts and lengths)
+    const dim3 grid((unsigned)(blocks > 0 ? blocks + p.status_block : 1));
     if (!p.status_block)
         return launch_cleared(rows_kernel<FP8, GATHER>, grid, kRowThreads, s, p.status, p);
     rows_kernel<FP8, GATHER><<<grid, kRowThreads, 0, s>>>(p);

@@ -425,6 +425,23 @@ def test_prefill_bad_starts_are_reported():
     assert got[0].shape == (0, 2, D)
 
 
+def test_prefill_without_rows_looks_its_requests_over():
+    _, nope, rope, v, _, ks = make_prefill([4, 3], [6, 5], 2, 1)
+    none = torch.empty(0, 2, D + R, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(cpa.cpa_latent_prefill_workspace_size(2, 0, 11, 2), dtype=torch.uint8, device="cuda")
+    for a, b, status in (([0, 0, 0], ks, 0), ([0, 0, 5], ks, 8), ([0, -1, 0], ks, 8), ([0, 5, 0], ks, 8),
+                         ([0, 0, 0], [0, 6, 12], 8), ([0, 0, 0], [0, 6, 5], 8), ([0, 0, 0], [-1, 6, 11], 8)):
+        ws.fill_(0xFF)
+        cpa.cpa_latent_prefill(none, nope, rope, v, i32(a), i32(b), workspace=ws)
+        assert cpa.cpa_get_device_status(ws)[0] == status, (a, b)
+    many = i32([0] * 5001)
+    ws.fill_(0xFF)
+    cpa.cpa_latent_prefill(none, nope, rope, v, many, many, workspace=ws, check=True)
+    many[4000] = 1
+    cpa.cpa_latent_prefill(none, nope, rope, v, i32([0] * 5001), many, workspace=ws)
+    assert cpa.cpa_get_device_status(ws)[0] == 8
+
+
 @pytest.mark.parametrize("news,lens,H", [
     ([2500], [2500], 32), ([300, 0, 1, 700, 1500], [400, 7, 3000, 700, 1500], 32),
     ([900, 70], [1000, 4000], 96), ([40] * 130, [41] * 130, 16),

@@ -383,3 +383,41 @@ def test_binding_refuses():
         cpa.cpa_cache_append(odd, new, k, k, t, s, n)
     with pytest.raises(ValueError, match="576"):
         cpa.cpa_latent_gather(k.view(4, 16, 256), t, s, T=3)
+
+
+@pytest.mark.parametrize("B", [3, 9000])
+def test_a_call_without_rows_looks_its_requests_over(B):
+    """T = 0: starts and lengths are looked at all the same, and nothing is written."""
+    k = torch.full((4, 16, 1, 128), 3.0, device="cuda").to(torch.bfloat16)
+    lat = torch.full((4, 16, 576), 3.0, device="cuda").to(torch.bfloat16)
+    one = torch.ones(1, device="cuda")
+    none = torch.empty(0, 1, 128, dtype=torch.bfloat16, device="cuda")
+    c, r = none.new_empty(0, 512), none.new_empty(0, 64)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    table = torch.full((B, 1), -1, dtype=torch.int32, device="cuda")
+    good, lens = i32([0] * (B + 1)), i32([0, 16] + [5] * (B - 2))
+
+    def status(start, n):
+        out = []
+        for call in (lambda: cpa.cpa_cache_append(none, none, k, k, table, start, n, workspace=ws),
+                     lambda: cpa.cpa_cache_append_fp8(none, none, k.view(torch.uint8)[..., :128].contiguous(),
+                                                      k.view(torch.uint8)[..., :128].contiguous(), one, one, table,
+                                                      start, n, workspace=ws),
+                     lambda: cpa.cpa_latent_append(c, r, lat, table, start, n, workspace=ws),
+                     lambda: cpa.cpa_cache_gather(k, k, table, start, T=0, first=n, workspace=ws),
+                     lambda: cpa.cpa_latent_gather(lat, table, start, T=0, first=n, workspace=ws)):
+            ws.fill_(0xFF)
+            call()
+            out.append(cpa.cpa_get_device_status(ws)[0])
+        return out
+
+    assert status(good, lens) == [0] * 5
+    for at, x in ((B, 5), (0, -1), (B // 2, 1), (B // 2, -1)):
+        bad = good.clone()
+        bad[at] = x
+        assert status(bad, lens) == [8] * 5, (at, x)
+    for x in (-1, 17, 2 ** 31 - 1, -2 ** 31):
+        n = lens.clone()
+        n[B - 1] = x
+        assert status(good, n) == [8] * 5, x
+    assert bool((k == 3).all()) and bool((lat == 3).all())
