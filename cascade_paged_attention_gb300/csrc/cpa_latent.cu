@@ -25,8 +25,9 @@
 // Values that are not numbers.  A masked key has weight 0, but 0 times a NaN in V is a
 // NaN in a matrix product.  Slots past a sequence's end are cleared in shared memory.  Of
 // keys that some rows of the request see and others do not (the last S - 1 at most)
-// elements that are not finite are cleared too, and added to the rows that see them when
-// the output is written.
+// elements that are not finite are cleared too, and the rows that see them get NaN in those
+// columns when the output is written: such an element is part of the key, whose score is
+// infinite or NaN with it, so that the row is NaN throughout or the weight 0, and 0 times it NaN.
 //
 // Split.  As in cpa_decode the key tiles of all units lie end to end, every block takes a
 // range of equal cost, and a unit cut by a range's end is joined by a second kernel in the
@@ -721,16 +722,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                         const size_t at = (((size_t)pg << p.lp) + (k & ((1 << p.lp) - 1))) * kSlot;
                         for (int blk = 0; blk < 4; ++blk) {
                             const int col = blk * 128 + warp * 32 + lane;
-                            const float y = __bfloat162float(p.pages[at + col]);
-                            if (isfinite(y)) continue;
+                            if (isfinite(__bfloat162float(p.pages[at + col]))) continue;
+                            const float nan = __int_as_float(0x7fffffff);
                             // token i + 1 of the request is at position k
                             for (int x = max(0, (i + 1 - r.s0) * p.heads); x < r.n; ++x) {
-                                if (split) {
-                                    p.part_o[(slot * kRows + x) * kC + col] += y;
-                                } else {
-                                    __nv_bfloat16* out = p.o + (row0 + x) * kC + col;
-                                    *out = __float2bfloat16(__bfloat162float(*out) + y);
-                                }
+                                if (split)
+                                    p.part_o[(slot * kRows + x) * kC + col] = nan;
+                                else
+                                    p.o[(row0 + x) * kC + col] = __float2bfloat16(nan);
                             }
                         }
                     }

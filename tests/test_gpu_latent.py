@@ -162,6 +162,40 @@ def test_values_that_are_not_numbers(value, lens):
     assert not bool(torch.isfinite(lse[2:4])[torch.isnan(x) | (x > 0)].any())
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("L", [3, 65, 300, 5000])
+def test_an_infinite_latent_is_the_same_wherever_it_lies(value, L):
+    """Its score is infinite.  Minus infinity: weight 0, and 0 x infinity in its own column, whether
+    all of a request's tokens see the key or only the last ones; plus infinity: the whole row."""
+    S, H, P = 4, 20, 16
+    lens = [L, 40]
+    for at in sorted({1, L - 1, L - 2, L - 3, L - 4, L // 2} & set(range(1, L))):
+        q_c, q_r, pages, table, dl = make(lens, S, H, P, 13)
+        where = (table[0, at // P].long(), at % P, 9)
+        pages[where] = 0.0
+        pos = torch.arange(L, device="cuda")
+        lat = pages[table[0].long()[pos // P], pos % P].clone()
+        pages[where] = value
+        o, lse = cpa.cpa_latent_decode(q_c, q_r, pages, table, dl, S=S, check=True)
+        last = cpa.cpa_latent_decode(q_c[S - 1::S], q_r[S - 1::S], pages, table, dl, check=True)
+        seen = torch.arange(L - S, L, device="cuda")[:, None] >= at
+        score = q_c[:S, :, 9].float() * value
+        lost, kept = seen & (score > 0), ~(seen & (score > 0))
+        assert bool(torch.isnan(o[:S][lost]).all()) and not bool(torch.isfinite(lse[:S][lost]).any())
+        hit = seen & (score < 0)
+        assert bool(torch.isnan(o[:S, :, 9][hit]).all())
+        # all else is as without the key
+        mask = visible(L, S) & (pos != at)
+        want = lref.absorbed(q_c[:S], q_r[:S], lat, mask)
+        got, ref_o = o[:S].clone(), want[0]
+        got[:, :, 9][hit] = 0.0
+        ref_o[:, :, 9][hit] = 0.0
+        ref.close(got[kept], lse[:S][kept], [x[kept] for x in want])
+        assert torch.equal(torch.isnan(last[0][0]), torch.isnan(o[S - 1]))
+        assert torch.equal(torch.isinf(last[0][0]), torch.isinf(o[S - 1]))
+        against(q_c[S:], q_r[S:], pages, table[1:], lens[1:], S, o[S:], lse[S:], P)
+
+
 def test_unseen_infinite_score():
     """A key whose score is minus infinity has weight 0, in any tile."""
     lens, P = [200], 16
