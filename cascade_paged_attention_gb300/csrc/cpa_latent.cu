@@ -356,6 +356,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     }
                 }
             }
+            // (a wait gave up: the units that begin in the rest of the range have entries all the
+            // same, with nothing to join)
+            if (p.by_unit && rank == 0)
+                for (; w.more(); w.next(p))
+                    if (lane == 0 && w.j0 == 0) p.desc[w.b * p.n_pairs + w.pair] = make_int4(w.b, w.pair, 1, grp);
             // no copy may be in flight when the block leaves
             for (uint32_t i = 0; i < (uint32_t)n_slots; ++i)
                 if (i < h)
@@ -780,7 +785,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const __gr
     }
     const int rank = blockIdx.x % p.cl;
     const int4 d = __ldcg(p.desc + blockIdx.x / p.cl);
-    if (d.x < 0 || d.z < 2) return;
+    if (!join_in_range(d.x, d.y, d.z, d.w, p.B, p.n_pairs, p.n_grp)) return;
     const Rows r(p, d.y * p.cl + rank);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, np = d.z;
     const int x = blockIdx.y * join_rows(F) + warp * F / 4;

@@ -57,4 +57,13 @@ CPA_HD int split_slot(int64_t total, int n, int c, int64_t u_start, bool fast32 
     return 2 * c + ((split_begin(total, n, c, fast32) < u_start) ? 1 : 0);
 }
 
+// Whether an entry of a join's list names a unit of the call (request b, pair of its n_pairs)
+// and parts that exist: `parts` of them, more than one, in the slots of the groups from `group`
+// on.  A block that gave up a wait may leave entries and parts unwritten; what a join reads and
+// writes stays in bounds whatever they hold.
+CPA_HD bool join_in_range(int b, int pair, int parts, int group, int B, int n_pairs, int n_grp) {
+    return b >= 0 && b < B && pair >= 0 && pair < n_pairs && parts > 1 && group >= 0 &&
+           group < n_grp && parts <= n_grp - group;
+}
+
 }  // namespace cpa

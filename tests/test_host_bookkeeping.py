@@ -65,3 +65,57 @@ def test_per_device_setup_runs_once_per_device(tmp_path):
                    check=True, capture_output=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "ok", (r.returncode, r.stdout, r.stderr)
+
+
+JOINS = r"""
+#include <cstdint>
+#include <cstdio>
+#include <cstdlib>
+#include "cpa_types.h"
+
+int main() {
+    // whatever an entry holds: what passes names a unit of the call and parts that exist
+    std::srand(7);
+    auto word = [] {
+        const uint32_t r = (uint32_t)std::rand() * 2654435761u;
+        switch (r % 5) {
+            case 0: return (int)r;
+            case 1: return (int)(r >> 8) % 160 - 4;
+            case 2: return (int)0xA5A5A5A5u;
+            case 3: return 0x7fffffff;
+            default: return (int)(r >> 16) % 9 - 1;
+        }
+    };
+    long long passed = 0;
+    for (int i = 0; i < 3000000; ++i) {
+        const int B = 1 + std::abs(word() % 200), n_pairs = 1 + std::abs(word() % 7), n_grp = i & 1 ? 152 : 76;
+        const int b = word(), pair = word(), parts = word(), group = word();
+        if (!cpa::join_in_range(b, pair, parts, group, B, n_pairs, n_grp)) continue;
+        ++passed;
+        if (b < 0 || b >= B || pair < 0 || pair >= n_pairs || parts < 2) return 1;
+        if (group < 0 || (long long)group + parts > n_grp) return 2;
+    }
+    if (passed < 100) return 3;
+    // what a call writes passes
+    if (!cpa::join_in_range(0, 0, 152, 0, 1, 1, 152) || !cpa::join_in_range(63, 1, 2, 150, 64, 2, 152)) return 4;
+    // units that are whole, or begin nowhere, are nobody's to join
+    if (cpa::join_in_range(0, 0, 1, 0, 1, 1, 152) || cpa::join_in_range(-1, 0, 0, 0, 1, 1, 152)) return 5;
+    std::printf("ok\n");
+    return 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs a host C++ compiler")
+def test_a_join_stays_in_bounds_whatever_its_entry_holds(tmp_path):
+    src, exe = tmp_path / "joins.cpp", tmp_path / "joins"
+    src.write_text(JOINS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-I", CSRC, "-I", os.path.join(ROOT, "include"), str(src),
+                    "-o", str(exe)], check=True, capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", (r.returncode, r.stdout, r.stderr)
+    # and the join whose entries a block may have left unwritten looks at nothing before it asks
+    with open(os.path.join(CSRC, "cpa_latent.cu")) as f:
+        text = f.read()
+    join = text[text.index("latent_join_kernel(const"):]
+    assert join.index("join_in_range(d.x, d.y, d.z, d.w") < join.index("const Rows r(p, d.y")
