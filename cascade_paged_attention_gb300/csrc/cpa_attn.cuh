@@ -670,6 +670,7 @@ __global__ void __launch_bounds__(Cfg<NUM_MT>::kThreads, 1)
             long long g = 0;
             int pst = 0;          // stage of tile g
             uint32_t pkpar = 0;   // parity of that stage's current use
+            int q_loads = 0;
             bool ok = true;
             while (w.left > 0 && ok) {
                 const Unit x = get_unit(p, w.u);
@@ -691,6 +692,7 @@ __global__ void __launch_bounds__(Cfg<NUM_MT>::kThreads, 1)
                                         &ctrl->q_full[qb], pol_q);
                         }
                     }
+                    ++q_loads;
                 }
                 // block-table window: lane l holds the page of box (wbase + l)
                 const int key_base = x.tile_base * kBN;
@@ -846,10 +848,15 @@ __global__ void __launch_bounds__(Cfg<NUM_MT>::kThreads, 1)
             for (int st = 0; st < p.n_stages; ++st) {
                 if (st < filled) {
                     const long long last = st + ((filled - 1 - st) / p.n_stages) * p.n_stages;
-                    mbar_wait(&ctrl->kv_full[st], (uint32_t)((last / p.n_stages) & 1), abort_flag,
-                              p.status);
+                    if (!mbar_wait(&ctrl->kv_full[st], (uint32_t)((last / p.n_stages) & 1), abort_flag,
+                                   p.status))
+                        mbar_drain(&ctrl->kv_full[st], (uint32_t)((last / p.n_stages) & 1));
                 }
             }
+            // (Q's too where the block gives up; else the products have waited for them)
+            if (!C::kQInTmem && *abort_flag)
+                for (int qb = 0; qb < p.n_qbufs && qb < q_loads; ++qb)
+                    mbar_drain(&ctrl->q_full[qb], (uint32_t)(((q_loads - 1 - qb) / p.n_qbufs) & 1));
         } else if (warp == kMmaWarp) {
             // ============================== MMA issuer
             // The work is a sequence of items, one per (tile, M tile): item i uses S
@@ -1002,7 +1009,7 @@ __global__ void __launch_bounds__(Cfg<NUM_MT>::kThreads, 1)
                     }
                 }
                 umma_commit(&ctrl->mma_done);
-                mbar_wait(&ctrl->mma_done, 0, abort_flag, p.status);
+                if (!mbar_wait(&ctrl->mma_done, 0, abort_flag, p.status)) mbar_drain(&ctrl->mma_done, 0);
                 CPA_TRACE_CTA(3, globaltimer_ns());
             }
             __syncwarp();
@@ -1712,6 +1719,7 @@ __global__ void __launch_bounds__(Cfg<NUM_MT>::kThreads, 1)
                             const bool okm = bar_and(1, 128, mbar_wait(&ctrl->merge_full, 0,
                                                                        abort_flag, p.status));
                             if (!okm) {
+                                mbar_drain(&ctrl->merge_full, 0);
                                 ok = false;
                                 break;
                             }

@@ -104,7 +104,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     }
 }
 
-// The same wait, with one decision for the whole warp: a warp never splits
+// For a role whose last wait, for its own copies or products, found that the block has given up:
+// they may still be in flight, and may not be when the block leaves (they take microseconds; one
+// whose other arrivals never come is left after kDrainLimitNs).
+constexpr uint64_t kDrainLimitNs = 100ull * 1000ull * 1000ull;  // 100 ms
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kDrainLimitNs) {
+    }
+}
+
+// mbar_wait() with one decision for the whole warp: a warp never splits
 // into lanes that continue and lanes that gave up.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
                                                volatile uint32_t* abort_flag, uint32_t* status) {

@@ -363,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     if (lane == 0 && w.j0 == 0) p.desc[w.b * p.n_pairs + w.pair] = make_int4(w.b, w.pair, 1, grp);
             // no copy may be in flight when the block leaves
             for (uint32_t i = 0; i < (uint32_t)n_slots; ++i)
-                if (i < h)
-                    mbar_wait(&ctrl->k_full[i], ((h - 1 - i) / n_slots) & 1u, &ctrl->abort_flag,
-                              &ctrl->bad);
+                if (i < h && !mbar_wait(&ctrl->k_full[i], ((h - 1 - i) / n_slots) & 1u, &ctrl->abort_flag,
+                                        &ctrl->bad))
+                    mbar_drain(&ctrl->k_full[i], ((h - 1 - i) / n_slots) & 1u);
             __syncwarp();
         } else if (warp == 6) {
             // ============================== loads of Q
@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 ++q_loads;
             }
             // (no copy may be in flight when the block leaves)
-            mbar_wait(&ctrl->q_full, (q_loads - 1) & 1u, &ctrl->abort_flag, &ctrl->bad);
+            if (!mbar_wait(&ctrl->q_full, (q_loads - 1) & 1u, &ctrl->abort_flag, &ctrl->bad))
+                mbar_drain(&ctrl->q_full, (q_loads - 1) & 1u);
             __syncwarp();
         } else if (warp == 5) {
             // ============================== products
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 }
             }
             commit(lead, &ctrl->mma_done);
-            wait_warp(&ctrl->mma_done, 0, ctrl);
+            if (!wait_warp(&ctrl->mma_done, 0, ctrl)) mbar_drain(&ctrl->mma_done, 0);
         } else {
             // ============================== softmax and output
             // Scores: rows 16 warp + lane / 4 (a) and 8 more (b), columns 8 i + 2 (lane % 4) and

@@ -593,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             }
             // no copy may be in flight when the block leaves
             for (uint32_t s = 0; s < kSlots; ++s)
-                if (s < g) wait_on(&ctrl->full[s], ((g - 1 - s) / kSlots) & 1u, ctrl);
+                if (s < g && !wait_on(&ctrl->full[s], ((g - 1 - s) / kSlots) & 1u, ctrl))
+                    mbar_drain(&ctrl->full[s], ((g - 1 - s) / kSlots) & 1u);
             __syncwarp();
         } else if (warp == 9) {
             // ============================== loads of Q
@@ -625,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
                     prefetch_3d(&p.qmap, lane % 3 * 64, w.x.h, w.x.t0 + lane / 3 * kTile);
             }
             for (int mt = 0; mt < 2; ++mt)
-                if (q_loads[mt] > 0) wait_on(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u, ctrl);
+                if (q_loads[mt] > 0 && !wait_on(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u, ctrl))
+                    mbar_drain(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u);
             __syncwarp();
         } else if (warp >= 10) {
             // ============================== products of query tile mt
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             }
             if (ok && kg > 0) round(0, false, false);
             commit(lead, &ctrl->mma_done);
-            wait_warp(&ctrl->mma_done, 0, ctrl);
+            if (!wait_warp(&ctrl->mma_done, 0, ctrl)) mbar_drain(&ctrl->mma_done, 0);
         } else {
             // ============================== softmax and output
             const int mt = warp >> 2;

@@ -621,13 +621,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                 }
             }
             for (int mt = 0; mt < 2; ++mt)
-                if (q_loads[mt] > 0)
-                    wait_on(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u, ctrl);
+                if (q_loads[mt] > 0 && !wait_on(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u, ctrl))
+                    mbar_drain(&ctrl->q_full[mt], (q_loads[mt] - 1) & 1u);
             // no copy may be in flight when the block leaves
             for (int s = 0; s < n_stages; ++s)
                 if (s < g) {
                     const long long last = s + (g - 1 - s) / n_stages * n_stages;
-                    wait_on(&full[s], (uint32_t)((last / n_stages) & 1), ctrl);
+                    if (!wait_on(&full[s], (uint32_t)((last / n_stages) & 1), ctrl))
+                        mbar_drain(&full[s], (uint32_t)((last / n_stages) & 1));
                 }
             __syncwarp();
         } else if (warp >= 10) {
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
                     round(w.tiles_q(p), j == w.j0, j == w.j1 - 1);
             if (ok) round(0, false, false);
             commit(lead, &ctrl->mma_done);
-            wait_warp(&ctrl->mma_done, 0, ctrl);
+            if (!wait_warp(&ctrl->mma_done, 0, ctrl)) mbar_drain(&ctrl->mma_done, 0);
         } else if (warp < 8) {
             // ============================== softmax and output
             const int mt = warp >> 2;

@@ -23,3 +23,18 @@ def test_shared_arrays_read_as_vectors_are_aligned(name):
             for c in re.finditer(r"reinterpret_cast<(?:const\s+)?(\w+)\s*\*>\(\s*&?" + var + r"\b", text):
                 need = VECTOR_BYTES.get(c.group(1), 1)
                 assert given >= need, f"{var}: {given}-byte aligned, read as {c.group(1)}"
+
+
+@pytest.mark.parametrize("name", sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))))
+def test_a_block_that_gave_up_waits_for_its_copies_and_products(name):
+    """The waits of a kernel return at once when its block has given up one of them; what is in flight
+    then is waited for by mbar_drain()."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = re.sub(r"//[^\n]*", lambda m: m.group(0) if "in flight when" in m.group(0) else "", f.read())
+    for m in re.finditer(r"\bwait_warp\(&ctrl->mma_done|\bmbar_wait\(&ctrl->(?:mma_done|merge_full)", text):
+        assert "mbar_drain(&ctrl->" in text[m.end():m.end() + 350], text[m.start():m.end()]
+    for m in re.finditer(r"in flight when", text):
+        block = text[m.end():m.end() + 700]
+        assert "wait" in block and "mbar_drain(&" in block
+    loads = len(re.findall(r"\b(?:tma_load_[23]d|bulk_load)\(smem", text))
+    assert loads == 0 or "mbar_drain(&" in text
