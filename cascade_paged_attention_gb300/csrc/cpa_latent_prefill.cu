@@ -22,8 +22,10 @@
 // share no keys that order has every head's K and V in use at a time, more than L2 holds
 // (2 x 8192 tokens, 32 heads: 3.8 GB read from DRAM in place of 0.6).  A call with many units
 // therefore hands them out whole, a few heads at a time, the longest of these heads first and
-// long requests before short ones, so that what is left at the end is short.  Either way the warp that loads K and V finds the
-// units, and the others read them from a ring in shared memory.
+// long requests before short ones, so that what is left at the end is short; unless a few long units,
+// or a last wave of like ones, would keep some blocks at work for long after the others.  Either
+// way the warp that loads K and V finds the units, and the others read them from a ring in shared
+// memory.
 //
 // Values that are not numbers: as in cpa_window.cu.
 //
@@ -66,14 +68,24 @@ constexpr uint32_t kSmem = kOffRing + kSlots * kSlotBytes + 1024;  // (aligned u
 constexpr int kUnitCost = 3;
 constexpr int kFewTiles = 6;  // of a block
 constexpr int kMinTiles = 2;  // fewest tiles of a block where units have a cost
-// Units a block from which they are handed out whole (12 chunks with 5 units a block 533 -> 497 us,
-// 2 x 2000 tokens with 3 units a block 104 -> 96 us, six chunks with 3 units a block 328 us both).
+// Units a block from which they may be handed out whole (12 chunks with 5 units a block 533 -> 497
+// us, 2 x 2000 tokens with 3 units a block 104 -> 96 us, six chunks with 3 units a block 328 us both):
+// the most that q's rows can hold, which the host knows.
 constexpr int kWholeUnits = 2;
+// They are where that keeps the blocks about as busy as equal ranges do.  Of the units of s tiles and
+// more some block has the average number, rounded up, and the call is at least as long as these: a
+// fifth more than a range is let pass, since whole units find K and V in L2.  (Whole against ranges,
+// and the bound over a range: one chunk of 2560 tokens behind 30000 1200 and 998 us, 1.33; ten of 256 behind 8000
+// 360 and 298, 1.43; 32 tokens behind 131072 beside a prompt of 2400 1397 and 459, 4.2; three of 100
+// behind 4000 in a buffer of 8192 rows 71 and 67, 1.6.  One chunk of 4096 behind 30000 1676 and 1696,
+// 1.1; ten of 512 behind 2000 205 and 213, 1.1; 2 x 2000 tokens 98 and 102, 0.8; six chunks 297 and 324,
+// 0.8; 64 tokens behind 20000 beside two prompts of 4000 301 and 326, 1.0.)
+constexpr int kEvenPart = 5;  // a fifth
 // Whole units are handed out in the order of their requests' lengths, in classes of an eighth of the
 // longest.  (Six chunks in the order of the batch 326 us, blocks at work for 327 to 655 thousand
 // cycles; so 295, 446 to 559 thousand; with 4 or 16 classes 293 and 297.  12 chunks 491 -> 455 us,
 // 16 chunks 906 -> 829.)
-constexpr int kClasses = 8;
+constexpr int kClasses = 8;  // (and the lengths of units that the rule above looks at)
 constexpr int kMostHeads = 8;       // that are handed out side by side,
 constexpr int kSharedKeys = 65536;  // as long as their keys are no more than these (32 MB)
 constexpr float kRescale = 8.0f;  // O is rescaled when a row's maximum grew by more than 2^8
@@ -98,7 +110,7 @@ struct ExpandedParams {
     size_t k_token, k_head, r_token, v_token, v_head;  // strides in elements
     uint32_t* counter;  // units handed out beyond the blocks' first ones
     int B, T, T_k, H, n_cta;
-    int whole;          // units are handed out whole
+    int may_whole;      // units may be handed out whole
     float scale_log2;
 };
 
@@ -126,6 +138,12 @@ __device__ __forceinline__ int units_of(const Request& r) { return (r.m + kRows 
 // Tiles of a request's query tokens qt * kRows and on.
 __device__ __forceinline__ int tiles_of(const Request& r, int qt) {
     return (r.L - r.m + min(r.m, (qt + 1) * kRows) + kTile - 1) / kTile;
+}
+
+// Units of a request of at least t tiles.
+__device__ __forceinline__ int units_at_least(const Request& r, int t) {
+    const int need = t * kTile - (kTile - 1) - (r.L - r.m);  // query tokens up to the unit's end
+    return r.m < max(need, 1) ? 0 : units_of(r) + 1 - max(1, (need + kRows - 1) / kRows);
 }
 
 // The class of a request's length, the highest that of the longest.
@@ -156,6 +174,8 @@ struct Ctrl {
     volatile uint32_t abort_flag;
     uint32_t bad;
     int most_tiles;           // of a unit
+    int at_least[kClasses];   // units of at least so many eighths of it
+    int whole;                // units are handed out whole
     int unit_cost;            // kUnitCost, or 0 where no block takes more than kFewTiles
     long long t0, left, per;  // this block's range, in tiles of cost
     int b, h, qt, off;        // where it begins: a unit, and how far into its cost
@@ -264,6 +284,28 @@ __device__ void schedule(const ExpandedParams& p, Ctrl* c, long long* sums) {
     before += unit_cost * units_before;
     mine += unit_cost * units;
     long long per = (total + p.n_cta - 1) / p.n_cta;
+    int whole = 0;
+    if (p.may_whole) {
+        auto eighths = [&](int k) { return (c->most_tiles * (k + 1) + kClasses - 1) / kClasses; };
+        int n[kClasses] = {};
+        for (int i = 0; i < per_thread && b0 + i < p.B; ++i) {
+            const Request r = request_of(p, b0 + i, bad);
+#pragma unroll
+            for (int k = 0; k < kClasses; ++k) n[k] += units_at_least(r, eighths(k));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kClasses; ++k) {
+            const int sum = __reduce_add_sync(0xffffffffu, n[k] * p.H);
+            if (lane == 0 && sum != 0) atomicAdd(&c->at_least[k], sum);
+        }
+        __syncthreads();
+        long long longest = 0;
+#pragma unroll
+        for (int k = 0; k < kClasses; ++k)
+            longest = max(longest, (long long)((c->at_least[k] + p.n_cta - 1) / p.n_cta) * (eighths(k) + unit_cost));
+        whole = longest - per <= per / kEvenPart;
+    }
     if (unit_cost) per = max(per, (long long)(kMinTiles + kUnitCost));
     const long long t0 = per * blockIdx.x;
     if (threadIdx.x == 0) {
@@ -271,6 +313,7 @@ __device__ void schedule(const ExpandedParams& p, Ctrl* c, long long* sums) {
         c->unit_cost = unit_cost;
         c->t0 = t0;
         c->left = t0 < total ? min(per, total - t0) : 0;
+        c->whole = whole;
     }
     // the warp whose requests hold position t0 looks through them
     const uint32_t here = __ballot_sync(0xffffffffu, before <= t0 && t0 < before + mine);
@@ -319,7 +362,7 @@ struct Finder {
     int b, h, qt, unit_cost;
     long long left;  // cost of the range after this piece
     int base, cls;   // whole units: the first of request b, and its class
-    bool first;
+    bool first, whole;
     __device__ __forceinline__ Piece piece(int j0, int j1) const {
         const int m0 = qt * kRows;
         return {r.t0 + m0, min(kRows, r.m - m0), r.L - r.m + m0, r.k0, r.L, h, tiles_of(r, qt), j0, j1};
@@ -338,8 +381,9 @@ struct Finder {
         uint32_t bad = 0;
         base = 0;
         cls = kClasses - 1;
+        whole = c->whole;
         // (a block without a range has no place where it begins)
-        const bool range = !p.whole && left > 0;
+        const bool range = !whole && left > 0;
         b = range ? c->b : -1;
         h = range ? c->h : 0;
         qt = range ? c->qt : 0;
@@ -374,7 +418,7 @@ struct Finder {
         const Piece none = {};
         const bool begin = first;
         first = false;
-        if (p.whole) {
+        if (whole) {
             int u = blockIdx.x;
             if (!begin) {
                 if ((threadIdx.x & 31) == 0) u = p.n_cta + (int)atomicAdd(p.counter, 1u);
@@ -515,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
         ctrl->abort_flag = 0;
         ctrl->bad = 0;
         ctrl->most_tiles = 0;
+        for (int i = 0; i < kClasses; ++i) ctrl->at_least[i] = 0;
         fence_barrier_init();
         prefetch_tmap(&p.qmap);
         prefetch_tmap(&p.kmap);
@@ -1150,8 +1195,8 @@ cpa_status cpa_latent_prefill(const void* q, const void* k_nope, int64_t k_token
         !make_rows_map(&p.rmap, kr, kRope, keys, rope_token_stride, 128))
         return CPA_ERR_CUDA;
     if (raise_smem_once() != cudaSuccess) return CPA_ERR_CUDA;
-    p.whole = (long long)T * H >= (long long)kWholeUnits * n_sm * kRows;
-    if (p.whole && cudaMemsetAsync(p.counter, 0, 4, s) != cudaSuccess) return CPA_ERR_CUDA;
+    p.may_whole = (long long)T * H >= (long long)kWholeUnits * n_sm * kRows;
+    if (p.may_whole && cudaMemsetAsync(p.counter, 0, 4, s) != cudaSuccess) return CPA_ERR_CUDA;
     if (launch_overlapped(expanded_kernel, dim3((unsigned)n_sm), kThreads, kSmem, s, p) != cudaSuccess)
         return CPA_ERR_LAUNCH;
     return launch_overlapped(expanded_join_kernel,

@@ -546,6 +546,76 @@ def test_prefill_units_handed_out_whole_in_a_graph():
         assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
 
 
+@pytest.mark.parametrize("news,lens,H,trail", [
+    ([20, 2420], [20000, 2420], 32, 0),           # one long context beside a prompt
+    ([2430, 1, 17], [2430, 9000, 12000], 32, 3),
+    ([2500], [7000], 32, 0), ([256] * 10, [2300] * 10, 32, 5),  # a last wave of like units
+    ([40, 0, 33, 27], [300, 5, 900, 700], 32, 2400),          # few tokens in a large buffer
+    ([1300, 1300], [1300, 1300], 32, 0), ([600] * 9, [900] * 9, 32, 0)])
+def test_prefill_whole_units_and_ranges(news, lens, H, trail):
+    """Calls of enough rows for whole units, some of which are shared out in ranges all the same."""
+    assert (sum(news) + trail) * H >= 2 * 152 * 256
+    check_prefill(news, lens, H, seed=len(news), trail=trail, k_trail=2)
+
+
+def test_prefill_replays_that_change_how_units_are_shared_out():
+    """One captured call, whose starts make it one of whole units, of ranges, of little work and of
+    none."""
+    H = 32
+    q, nope, rope, v, qs, ks = make_prefill([1250, 1250], [6000, 6000], H, 17)
+    dq, dk = i32(qs), i32(ks)
+    o = torch.zeros((2500, H, D), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((2500, H), device="cuda")
+    ws = torch.full((cpa.cpa_latent_prefill_workspace_size(2, 2500, 12000, H),), 0xA5, dtype=torch.uint8, device="cuda")
+    cpa.cpa_latent_prefill(q, nope, rope, v, dq, dk, o=o, lse=lse, workspace=ws, check=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cpa.cpa_latent_prefill(q, nope, rope, v, dq, dk, o=o, lse=lse, workspace=ws)
+    for a, b in (([0, 1250, 2500], [0, 1300, 2600]), ([0, 2490, 2500], [0, 2490, 12000]), ([5, 45, 70], [0, 900, 1000]),
+                 ([0, 0, 0], [0, 0, 9]), ([0, 2500, 2500], [0, 12000, 12000]), ([0, 1250, 2500], [0, 1300, 2600])):
+        dq.copy_(i32(a))
+        dk.copy_(i32(b))
+        o.fill_(7)
+        lse.fill_(7)
+        graph.replay()
+        assert cpa.cpa_get_device_status(ws) == (0, 0)
+        against_prefill(q, nope, rope, v, a, b, o, lse)
+        for r in (slice(0, a[0]), slice(a[-1], 2500)):
+            assert bool((o[r] == 7).all()) and bool((lse[r] == 7).all())
+
+
+def test_prefill_with_one_long_context_is_shared_out():
+    """A few tokens behind a long context beside a prompt take no more than twice as long as the two
+    one after the other (a unit of the long one on each of a few blocks: three times)."""
+    news, lens, H = [32, 2400], [100000, 2400], 32
+    q, nope, rope, v, qs, ks = make_prefill(news, lens, H, 19)
+    both = (i32(qs), i32(ks))
+    ws = torch.empty(cpa.cpa_latent_prefill_workspace_size(2, q.shape[0], rope.shape[0], H), dtype=torch.uint8, device="cuda")
+
+    def together():
+        cpa.cpa_latent_prefill(q, nope, rope, v, *both, workspace=ws)
+
+    parts = [(slice(qs[b], qs[b + 1]), slice(ks[b], ks[b + 1]), i32([0, news[b]]), i32([0, lens[b]])) for b in range(2)]
+
+    def one_by_one():
+        for a, b, x, y in parts:
+            cpa.cpa_latent_prefill(q[a], nope[b], rope[b], v[b], x, y, workspace=ws)
+
+    def us(f):
+        best = 1e9
+        for _ in range(8):
+            t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            t0.record()
+            f()
+            t1.record()
+            torch.cuda.synchronize()
+            best = min(best, t0.elapsed_time(t1) * 1e3)
+        return best
+
+    a, b = us(together), us(one_by_one)
+    assert a <= 2 * b, (a, b)
+
+
 def test_prefill_many_requests():
     g = torch.Generator().manual_seed(3)
     news = torch.randint(0, 5, (900,), generator=g).tolist()
