@@ -443,11 +443,13 @@ cpa_status rows_ready(RowParams& p, const int32_t* table, int stride, const int3
 
 template <bool FP8, bool GATHER>
 cpa_status launch_rows(RowParams& p, cudaStream_t s) {
+    const long long per_group = p.segments[0] + p.segments[1];
+    p.tokens = tokens_of(FP8, GATHER, 32 >> p.log_lanes[0]);
+    // (a grid has no more blocks than that)
+    if ((p.T / p.tokens + 1) * per_group / kRowWarps >= 0x7ffffffe) return CPA_ERR_UNSUPPORTED;
     const int n_sm = sm_count();
     if (n_sm <= 0) return CPA_ERR_CUDA;
-    const long long per_group = p.segments[0] + p.segments[1];
     // few tokens: fewer to a warp, so that all SMs take part
-    p.tokens = tokens_of(FP8, GATHER, 32 >> p.log_lanes[0]);
     while (p.tokens > 4 && p.T / p.tokens * per_group < (long long)n_sm * 16) p.tokens /= 2;
     const long long warps = ((long long)p.T + p.tokens - 1) / p.tokens * per_group;
     const long long blocks = (warps + kRowWarps - 1) / kRowWarps;

@@ -595,7 +595,7 @@ cpa_status cpa_cache_compact(void* k_pages, void* v_pages, const int32_t* src_ta
  * CPA_DEV_BAD_LENGTH, a page id outside [0, num_pages) CPA_DEV_BAD_PAGE; such a
  * request's, or such a page's, tokens are not written, all others are (a request is
  * judged by its own start, end and length; a call whose starts do not ascend is slow).
- * T up to 2^30.  Workspace: cpa_status_workspace_size().
+ * T up to 2^30, T * token_bytes below 2^45.  Workspace: cpa_status_workspace_size().
  */
 cpa_status cpa_cache_append(const void* k_new, const void* v_new, size_t k_stride_bytes,
                             size_t v_stride_bytes, void* k_pages, void* v_pages,

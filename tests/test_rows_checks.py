@@ -96,6 +96,14 @@ def test_row_limits(L, p):
     assert call(L, p, "latent_decode", max_len=(1 << 30) + 1, stride=1 << 27) == 2
 
 
+@pytest.mark.parametrize("fn", ["cache_append", "cache_append_fp8", "cache_gather", "cache_gather_fp8"])
+def test_more_rows_than_a_grid_has_blocks_for(L, p, fn):
+    """Rows may overlap (a stride of 0), so their number is not bounded by memory alone."""
+    wide = dict(channels=1 << 19) if "fp8" in fn else dict(token=1 << 20)
+    small = dict(ks=0, vs=0) if "append" in fn else {}
+    assert call(L, p, fn, T=1 << 30, **wide, **small) == 2
+
+
 def test_workspace_sizes(L):
     for bad in ((0, 1, 8, 512, 64, 16), (1, 0, 8, 512, 64, 16), (1, 1, 0, 512, 64, 16),
                 (1, 1, 8, 256, 64, 16), (1, 1, 8, 512, 32, 16), (1, 1, 8, 512, 64, 7),
