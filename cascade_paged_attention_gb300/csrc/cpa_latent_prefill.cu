@@ -236,6 +236,36 @@ __device__ __forceinline__ long long lane_tiles(const Request& r) {
     return sum;
 }
 
+// Whether whole units keep the blocks about as busy as ranges of cost `per` (see kEvenPart); every
+// thread.  (Not inlined: a few prompt tokens, which have no use for it, took 0.7 of 20.4 us more with it
+// in the way.)
+__device__ __noinline__ int whole_units(const ExpandedParams& p, Ctrl* c, long long per, int unit_cost) {
+    const int lane = threadIdx.x & 31;
+    const int per_thread = (p.B + kThreads - 1) / kThreads, b0 = (int)threadIdx.x * per_thread;
+    // (the average rounded up is at most one unit more than it: short units need no count)
+    if (c->most_tiles + unit_cost <= per / kEvenPart) return 1;
+    uint32_t bad = 0;  // (known by now)
+    auto eighths = [&](int k) { return (c->most_tiles * (k + 1) + kClasses - 1) / kClasses; };
+    int n[kClasses] = {};
+    for (int i = 0; i < per_thread && b0 + i < p.B; ++i) {
+        const Request r = request_of(p, b0 + i, bad);
+#pragma unroll
+        for (int k = 0; k < kClasses; ++k) n[k] += units_at_least(r, eighths(k));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kClasses; ++k) {
+        const int sum = __reduce_add_sync(0xffffffffu, n[k] * p.H);
+        if (lane == 0 && sum != 0) atomicAdd(&c->at_least[k], sum);
+    }
+    __syncthreads();
+    long long longest = 0;
+#pragma unroll
+    for (int k = 0; k < kClasses; ++k)
+        longest = max(longest, (long long)((c->at_least[k] + p.n_cta - 1) / p.n_cta) * (eighths(k) + unit_cost));
+    return longest - per <= per / kEvenPart;
+}
+
 // Every thread: the problem's cost, this block's range, and the unit where it begins.  Each
 // thread sums a run of requests; one scan over the block follows.
 __device__ void schedule(const ExpandedParams& p, Ctrl* c, long long* sums) {
@@ -284,28 +314,7 @@ __device__ void schedule(const ExpandedParams& p, Ctrl* c, long long* sums) {
     before += unit_cost * units_before;
     mine += unit_cost * units;
     long long per = (total + p.n_cta - 1) / p.n_cta;
-    int whole = 0;
-    if (p.may_whole) {
-        auto eighths = [&](int k) { return (c->most_tiles * (k + 1) + kClasses - 1) / kClasses; };
-        int n[kClasses] = {};
-        for (int i = 0; i < per_thread && b0 + i < p.B; ++i) {
-            const Request r = request_of(p, b0 + i, bad);
-#pragma unroll
-            for (int k = 0; k < kClasses; ++k) n[k] += units_at_least(r, eighths(k));
-        }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < kClasses; ++k) {
-            const int sum = __reduce_add_sync(0xffffffffu, n[k] * p.H);
-            if (lane == 0 && sum != 0) atomicAdd(&c->at_least[k], sum);
-        }
-        __syncthreads();
-        long long longest = 0;
-#pragma unroll
-        for (int k = 0; k < kClasses; ++k)
-            longest = max(longest, (long long)((c->at_least[k] + p.n_cta - 1) / p.n_cta) * (eighths(k) + unit_cost));
-        whole = longest - per <= per / kEvenPart;
-    }
+    const int whole = p.may_whole ? whole_units(p, c, per, unit_cost) : 0;
     if (unit_cost) per = max(per, (long long)(kMinTiles + kUnitCost));
     const long long t0 = per * blockIdx.x;
     if (threadIdx.x == 0) {
