@@ -90,6 +90,33 @@ def test_batches_and_splits(lens, S, H):
     check(lens, S, H, 16, seed=len(lens) + H)
 
 
+def test_thousands_of_requests():
+    """More requests than blocks and warps, none to a few tokens each, two tokens of queries."""
+    B, S, H, P = 4099, 2, 3, 8
+    g = ref.gen(21)
+    lens = torch.randint(0, 12, (B,), generator=g, device="cuda").tolist()
+    q_c, q_r, pages, table, dl = make(lens, S, H, P, 22)
+    o, lse = cpa.cpa_latent_decode(q_c, q_r, pages, table, dl, S=S, check=True)
+    pos = torch.arange(12, device="cuda")
+    page = table[:, (pos // P).clamp(max=table.shape[1] - 1)].long().clamp(min=0)
+    lat = pages[page, pos % P].double()                                   # [B, 12, C + R]
+    q = torch.cat([q_c, q_r], 2).double().view(B, S, H, C + R)
+    p = dl.long()[:, None] - S + torch.arange(S, device="cuda")[None]
+    mask = pos[None, None] <= p[..., None]                                # [B, S, 12]
+    x = torch.einsum("bshd,bjd->bshj", q, lat) * lref.SCALE
+    big = torch.einsum("bshd,bjd->bshj", q.abs(), lat.abs()) * lref.SCALE
+    x = x.masked_fill(~mask[:, :, None], float("-inf"))
+    ds = big.masked_fill(~mask[:, :, None], 0.0).amax(-1) * (C + R) * 2.0 ** -23
+    z = torch.logsumexp(x, -1)
+    w = torch.exp(x - torch.where(z == float("-inf"), 0.0, z)[..., None])
+    want = torch.einsum("bshj,bjc->bshc", w, lat[..., :C])
+    size = torch.einsum("bshj,bjc->bshc", w, lat[..., :C].abs())
+    tol = ref.U_BF16 * want.abs() + (ref.E_P_BF16 + 2 * ds + 2.0 ** -18)[..., None] * size
+    tol_l = ds + 2.0 ** -20 * (1 + torch.where(z == float("-inf"), 0.0, z).abs())
+    ref.close(o, lse, [y.reshape(B * S, *y.shape[2:]) for y in (want, z, tol, tol_l)])
+
+
+
 def test_bounds_given_and_repeat():
     """The same call twice gives the same bits, whatever its workspace held."""
     lens = [1000, 3, 900, 5000]
@@ -621,6 +648,16 @@ def test_prefill_many_requests():
     news = torch.randint(0, 5, (900,), generator=g).tolist()
     lens = [m + int(torch.randint(0, 9, (1,), generator=g)) for m in news]
     check_prefill(news, lens, 1, seed=2)
+
+
+@pytest.mark.parametrize("H,m", [(1, 300), (32, 2500)])
+def test_prefill_among_empty_requests(H, m):
+    """Thousands of requests without new tokens before, between and behind a few that have some."""
+    news = [0] * 5000 + [m] + [0] * 3000 + [1] + [0] * 2000
+    lens = [1] * 5000 + [m + 50] + [0] * 3000 + [70] + [2] * 2000
+    q, nope, rope, v, qs, ks = make_prefill(news, lens, H, 5)
+    o, lse = cpa.cpa_latent_prefill(q, nope, rope, v, i32(qs), i32(ks), check=True)
+    against_prefill(q, nope, rope, v, qs, ks, o, lse, which=[5000, 8001])
 
 
 def test_prefill_offsets_past_32_bits():

@@ -421,3 +421,62 @@ def test_a_call_without_rows_looks_its_requests_over(B):
         n[B - 1] = x
         assert status(good, n) == [8] * 5, x
     assert bool((k == 3).all()) and bool((lat == 3).all())
+
+
+EDGE_SCALES = [0.0, -0.0, float("inf"), float("-inf"), float("nan"), 2.0 ** -120, -2.0 ** -120, 2.0 ** 120,
+               -2.0 ** 120, 2.0 ** -149, 3.0e38, 2.0 ** -100, 2.0 ** 100, -0.013, -1.0, -3.0, 2.0 ** -7, 0.5, 1.0,
+               3.0, 0.007, 0.25, 1.1, 2.0 ** -9]
+
+
+def test_fp8_scales_of_every_kind():
+    """0, infinities, NaN, scales too far from 1 for their reciprocal, negative ones; powers of two and
+    others side by side in one group of channels; over values of every kind."""
+    g = ref.gen(31)
+    H, P, T = 2, 16, 600
+    scale = [torch.empty(H, 128, device="cuda") for _ in "kv"]
+    for i, s in enumerate(scale):
+        order = torch.randint(0, len(EDGE_SCALES), (H * 128,), generator=g, device="cuda")
+        order[:len(EDGE_SCALES)] = torch.arange(len(EDGE_SCALES), device="cuda")
+        s.copy_(torch.tensor(EDGE_SCALES, device="cuda")[order].view(H, 128))
+        s[1, 64:] = torch.rand(64, generator=g, device="cuda") * 0.02 + 0.001
+        s[1, 64::3] = 2.0 ** -6
+    new = [torch.randn(T, H, 128, generator=g, device="cuda").to(torch.bfloat16) for _ in "kv"]
+    special = torch.tensor([0.0, -0.0, 1e30, -1e30, float("inf"), float("-inf"), float("nan"), 1e-30, -1e-30, 1e-38,
+                            448.0, 1.0], device="cuda").to(torch.bfloat16)
+    for x in new:
+        x[:len(special)] = special[:, None, None]
+    check_fp8(new, scale, P)
+    for one in EDGE_SCALES:  # one scale for all channels
+        check_fp8(new, [torch.tensor([one], device="cuda"), torch.tensor([-one], device="cuda")], P)
+
+
+def test_fp8_values_beside_the_borders_of_codes():
+    """The bf16 values nearest to (the middle between two codes) x scale, and those beside them."""
+    P, H = 16, 1
+    g = ref.gen(32)
+    codes = torch.arange(0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).float()
+    mid = (codes[1:] + codes[:-1]) / 2                                  # 126 of them
+    scale = torch.exp(torch.randn(128, generator=g, device="cuda") * 3)
+    scale[::9] = torch.exp2(torch.randint(-12, 12, scale[::9].shape, generator=g, device="cuda").float())
+    x = (mid[:, None] * scale).to(torch.bfloat16).view(torch.int16)     # positive: bit patterns ascend
+    x = torch.cat([x + i for i in (-1, 0, 1)]).view(torch.bfloat16)
+    x = torch.cat([x, -x]).view(-1, H, 128)
+    check_fp8([x, x.flip(0)], [scale.view(H, 128), scale.view(H, 128)], P)
+
+
+def check_fp8(new, scale, P):
+    """Appended and read back, against PyTorch's quotient and product."""
+    T, H = new[0].shape[:2]
+    n = (T + P - 1) // P
+    table, st, lens = i32([list(range(n))[::-1]]), i32([0, T]), i32([T])
+    pages = [torch.zeros(n, P, H, 128, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    cpa.cpa_cache_append_fp8(*new, *pages, *scale, table, st, lens, check=True)
+    pos = torch.arange(T, device="cuda")
+    codes = [p[table[0].long()[pos // P], pos % P] for p in pages]
+    for c, x, s in zip(codes, new, scale):
+        same_codes(c, quantised(x, s))
+    back = cpa.cpa_cache_gather_fp8(*pages, *scale, table, st, T=T, check=True)
+    for o, c, s in zip(back, codes, scale):
+        w = (c.view(torch.float8_e4m3fn).float() * s).to(torch.bfloat16)
+        assert torch.equal(torch.isnan(o), torch.isnan(w))
+        assert torch.equal(o[~torch.isnan(w)], w[~torch.isnan(w)])
