@@ -37,8 +37,8 @@
 // launches in it; 64 x 16000: 195 us, 6.05 TB/s, 0.89 of the copy rate).  64 rows: the ring.  It
 // holds two tiles, and a tile stays in it for its load (2100 cycles), its scores (1220), the
 // softmax (1000) and its values (810), some of them behind another tile's: 3230 cycles a tile,
-// where shared memory needs 2490 for what the products read and the loads write, HBM 3100 when
-// no other block shares the tile and the products alone 2030 (64 x 16000 tokens, 64 heads: 202 us;
+// where shared memory needs 2490 for what the products of one SM read and the loads write, HBM 3100
+// when no other block shares the tile and the products alone 2030 (64 x 16000 tokens, 64 heads: 202 us;
 // 32 ragged requests of 128 heads: 114 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -29,13 +29,14 @@
 //
 // Values that are not numbers: as in cpa_window.cu.
 //
-// What bounds it: the tensor cores.  2 x 8192 tokens of 32 heads take 870 to 910 us on their own,
-// 1.51 to 1.58 PFLOP/s of products that the mask leaves, 0.80 to 0.84 of the measured rate; a round
-// of both query tiles takes 2920 cycles where its products need 2560 at the nominal rate (scores
-// read Q and K from shared memory, which the loads write and the weights do not leave alone), a
-// unit's end 7600.  Six chunks of 200 to 640 tokens behind contexts: 295 us, 0.67, because a
-// request's last unit may hold one query tile: it loads 80 KB a key tile for half the products (3800
-// cycles; with the key tiles shared out to both pipelines no fewer).
+// What bounds it: the tensor cores.  2 x 8192 tokens of 32 heads take 870 to 910 us in a captured
+// graph, 1.51 to 1.58 PFLOP/s of products that the mask leaves, 0.80 to 0.84 of the measured rate, and
+// 900 to 915 as a program calls it; a round of both query tiles takes 2920 cycles where its products
+// need 2560 at the nominal rate (scores read Q and K from shared memory, which the loads write and the
+// weights do not leave alone), a unit's end 7600.  Six chunks of 200 to 640 tokens behind contexts: 300
+// us, 0.66 (317 and 0.62 as a program calls it), because a request's last unit may hold one query tile:
+// it loads 80 KB a key tile for half the products (3800 cycles; with the key tiles shared out to both
+// pipelines no fewer).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -75,8 +76,8 @@ constexpr int kWholeUnits = 2;
 // They are where that keeps the blocks about as busy as equal ranges do.  Of the units of s tiles and
 // more some block has the average number, rounded up, and the call is at least as long as these: a
 // fifth more than a range is let pass, since whole units find K and V in L2.  (Whole against ranges,
-// and the bound over a range: one chunk of 2560 tokens behind 30000 1200 and 998 us, 1.33; ten of 256 behind 8000
-// 360 and 298, 1.43; 32 tokens behind 131072 beside a prompt of 2400 1397 and 459, 4.2; three of 100
+// and the bound over a range: one chunk of 2560 tokens behind 30000 1200 and 998 us, 1.3; ten of 256 behind 8000
+// 360 and 298, 1.4; 32 tokens behind 131072 beside a prompt of 2400 1397 and 459, 4.2; three of 100
 // behind 4000 in a buffer of 8192 rows 71 and 67, 1.6.  One chunk of 4096 behind 30000 1676 and 1696,
 // 1.1; ten of 512 behind 2000 205 and 213, 1.1; 2 x 2000 tokens 98 and 102, 0.8; six chunks 297 and 324,
 // 0.8; 64 tokens behind 20000 beside two prompts of 4000 301 and 326, 1.0.)
