@@ -400,12 +400,17 @@ struct Finder {
         r = {0, 0, 0, 0};
         if (range) r = request_of(p, b, bad);
     }
+    // (the warps that wait for the next piece may wait for as long as there are requests to pass over)
+    static __device__ __forceinline__ void passed(Ctrl* c, int b) {
+        if ((threadIdx.x & 31) == 0 && (b & 0xffff) < 32) c->alive_ns = globaltimer_ns();
+    }
     // The next request of this class, then of those below; false: none.
-    __device__ __forceinline__ bool advance(const ExpandedParams& p, const Ctrl* c) {
+    __device__ __forceinline__ bool advance(const ExpandedParams& p, Ctrl* c) {
         const int lane = threadIdx.x & 31;
         uint32_t bad = 0;
         for (; cls >= 0; --cls, b = -1) {
             for (int b0 = b + 1; b0 < p.B; b0 += 32) {
+                passed(c, b0);
                 Request q = {0, 0, 0, 0};
                 if (b0 + lane < p.B) q = request_of(p, b0 + lane, bad);
                 const uint32_t here =
@@ -423,7 +428,7 @@ struct Finder {
         r.m = 0;
         return false;
     }
-    __device__ __forceinline__ Piece next(const ExpandedParams& p, const Ctrl* c) {
+    __device__ __forceinline__ Piece next(const ExpandedParams& p, Ctrl* c) {
         uint32_t bad = 0;
         const Piece none = {};
         const bool begin = first;
@@ -453,8 +458,10 @@ struct Finder {
             qt = 0;
             if (++h == p.H) {
                 h = 0;
-                do r = request_of(p, ++b, bad);
-                while (r.m == 0);  // (cost is left, so a request with tokens is)
+                do {  // (cost is left, so a request with tokens is)
+                    r = request_of(p, ++b, bad);
+                    if ((b & 0xffff) == 0) passed(c, b);
+                } while (r.m == 0);
             }
         }
         return cut(0);

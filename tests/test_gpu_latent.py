@@ -660,6 +660,17 @@ def test_prefill_among_empty_requests(H, m):
     against_prefill(q, nope, rope, v, qs, ks, o, lse, which=[5000, 8001])
 
 
+def test_prefill_walks_over_millions_of_empty_requests():
+    """What one warp takes seconds to pass over puts off the limit of the other warps' waits."""
+    H, m, n = 16, 5000, 1 << 24
+    q, nope, rope, v, qs, ks = make_prefill([m, 3], [m, 40], H, 3)
+    a, b = (torch.full((n + 3,), m, dtype=torch.int32, device="cuda") for _ in "qk")
+    a[0], a[-1], b[0], b[-1] = 0, m + 3, 0, m + 40
+    ws = torch.empty(cpa.cpa_latent_prefill_workspace_size(n + 2, m + 3, m + 40, H), dtype=torch.uint8, device="cuda")
+    o, lse = cpa.cpa_latent_prefill(q, nope, rope, v, a, b, workspace=ws, check=True)
+    against_prefill(q, nope, rope, v, [0, m, m + 3], [0, m, m + 40], o, lse)
+
+
 def test_prefill_offsets_past_32_bits():
     """Keys past 2^31 elements of the expanded array."""
     H, g = 64, ref.gen(2)
